@@ -15,6 +15,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace hyb {
+
 hyb_status fail(hyb_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -29,6 +33,19 @@ hyb_status ok() {
   g_last_error.clear();
   return HYB_OK;
 }
+
+hyb_status hip_status(hipError_t e, const char* what) {
+  if (e == hipSuccess) return ok();
+  return fail(HYB_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace hyb
+
+namespace {
+
+using hyb::fail;
+using hyb::hip_status;
+using hyb::ok;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -137,11 +154,6 @@ hyb_status check_mfma_limits(int32_t m, int64_t ldx) {
     return fail(HYB_ERR_UNSUPPORTED, "matrix-core kernel needs ldx < 4194304 elements");
   if ((int64_t(m) + 15) / 16 > 65535 * 8) return fail(HYB_ERR_UNSUPPORTED, "m = %d too large for one launch", m);
   return HYB_OK;
-}
-
-hyb_status hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(HYB_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 // Workspace of the split-K launches of hyb_gemm and hyb_gemm_lowrank, held

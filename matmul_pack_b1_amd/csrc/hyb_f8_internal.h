@@ -1,0 +1,38 @@
+// Internal interface between the host-side checks of the 8-bit entry points
+// (hyb_f8_api.cpp) and their kernels (hyb_f8.hip).  Everything reaching a
+// launcher has been validated.
+#pragma once
+
+#include "../../include/hyb_f8.h"
+#include "hyb_internal.h"
+
+namespace hyb {
+
+// Columns of one step, and its bytes per 16-row panel.
+constexpr int64_t kF8Step = 128;
+constexpr int64_t kPanelStep = 2048;
+// Largest k: a panel's byte offsets within a 16-panel tile stay below 2^31.
+constexpr int64_t kF8MaxK = int64_t(1) << 22;
+constexpr int64_t kF8MaxRows = (int64_t(1) << 31) - 16;
+
+inline int64_t f8_steps(int64_t k) { return (k + kF8Step - 1) / kF8Step; }
+inline int64_t f8_rows16(int64_t rows) { return (rows + 15) / 16 * 16; }
+
+// How a product runs.
+struct F8Route {
+  int ap, bp;  // panels of w and of x per workgroup
+  int waves;   // register-fed: wavefronts cutting k; LDS-fed: 0
+  int parts;   // k cut over this many workgroups per tile (1: not)
+};
+F8Route f8_route(int64_t n, int64_t k, int64_t m, int64_t cus);
+size_t f8_workspace_bytes(const F8Route& r, int64_t n, int64_t m);
+
+hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k, int64_t lda, int kind,
+                              const hyb_f8& dst, hipStream_t s);
+hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void* a, int dtype, int64_t lda,
+                                hipStream_t s);
+// ws NULL runs the route unsplit.
+hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x, int64_t m, void* y, int y_dtype,
+                          int64_t ldy, float* ws, hipStream_t s);
+
+}  // namespace hyb

@@ -26,6 +26,12 @@ constexpr int kGemvCrossoverM = 4;
 // Matrices per grouped decode launch (HYB_MAX_GROUP in hyb.h).
 constexpr int kMaxGroup = HYB_MAX_GROUP;
 
+// Status of a host call: fail() leaves the message for hyb_last_error, ok()
+// clears it, hip_status() turns a runtime error into HYB_ERR_HIP.
+hyb_status fail(hyb_status st, const char* fmt, ...);
+hyb_status ok();
+hyb_status hip_status(hipError_t e, const char* what);
+
 hipError_t launch_pack(const hyb_layout& L, const void* w, int64_t ldw, const hyb_packed& P,
                        hipStream_t s);
 hipError_t launch_unpack(const hyb_layout& L, const hyb_packed& P, void* w, int64_t ldw,

@@ -1,0 +1,272 @@
+// Matrix product of two operands held in panels, Y[j, i] = sum_k A[i, k] B[j, k],
+// shared by the 8-bit block-scaled product and the cross entropy's gradients.
+//
+// A panel is 16 rows; a step of a panel is 2 KiB: 128 columns of 8-bit codes
+// or 64 columns of 16-bit values, in two halves of 1 KiB of which lane L of a
+// wavefront owns the 16 bytes at 16 L:
+//   row L%16, columns 64 h + 16 (L/16) + 0..15   (8 bits, half h)
+//   row L%16, columns 32 h +  8 (L/16) + 0..7    (16 bits, half h)
+// The halves are the operand registers of the 16x16x128 (two halves) and
+// 16x16x32 (one half) matrix instructions, so a tile goes from memory to LDS
+// as it lies and every LDS read is 64 lanes over 1 KiB without a bank
+// conflict.  (Which columns a lane holds does not matter to the sum as long
+// as both operands agree.)  Panel p's steps are contiguous, at
+// (p * steps + s) * 2048.
+//
+// 8-bit operands carry one exponent byte per row and step (E8M0: 2^(byte -
+// 127)), four steps to a 32-bit word, word (s / 4) * rows16 + row; the matrix
+// instruction takes the word of its lane's row as it is and multiplies the
+// products of a step by both operands' powers of two.
+#ifndef HYB_PANEL_H_
+#define HYB_PANEL_H_
+
+#include "hyb_device.h"
+
+namespace hyb {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+typedef __attribute__((ext_vector_type(4))) int srd4_t;
+
+// Element kinds of a panel product beside HYB_F16 and HYB_BF16: 8-bit codes
+// through the scaled 8-bit instruction, or widened (exactly) to bf16, scale
+// included, for the 16-bit one.
+//
+// Why both.  The 8-bit instruction (the scaled form as well as the plain
+// 16x16x32 one) does not sum its products to fp32 accuracy: over random codes
+// of all exponents its result is off by up to 2^-11 of the largest product of
+// the 128 (5e-5 of the result in the 2-norm); over products within a
+// 15-bit window it is exact, so bits of a product far below the largest one
+// are dropped.  The 16-bit instruction has no such loss, at half the rate.
+// Outputs that keep fp32 take the wide kind, 16-bit outputs (whose rounding is
+// 2^-8 or 2^-11 of the result) the fast one.
+constexpr int kF8 = 0;
+constexpr int kF8Wide = -1;
+constexpr bool is_f8(int kind) { return kind <= 0; }
+
+struct PanelOperand {
+  const char* data;
+  const uint32_t* scale;  // 8-bit operands only
+  int32_t rows16;         // rows rounded up to 16 (the panels that exist)
+};
+
+__device__ __forceinline__ srd4_t panel_srd(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return srd4_t{__builtin_amdgcn_readfirstlane(int(a & 0xFFFFFFFFu)),
+                __builtin_amdgcn_readfirstlane(int((a >> 32) & 0xFFFFu)),
+                __builtin_amdgcn_readfirstlane(int(bytes)), kBufDword3};
+}
+
+// 16 bytes per lane from srd + voffset into LDS at lds + 16 * lane; past the
+// resource's end zeros are written.  Issued from inline assembly so that
+// the compiler does not tie LDS reads to transfers of a later step; the
+// caller waits (panel_wait) before its barrier.
+__device__ __forceinline__ void panel_dma16(srd4_t srd, uint32_t lds, int voffset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset), "s"(srd)
+               : "memory", "m0");
+}
+
+template <int N>
+__device__ __forceinline__ void panel_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t panel_lds_addr(const void* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char*)(p)));
+}
+
+// Registers of one panel's step: as loaded, or widened to bf16.
+template <int KIND>
+struct PanelRegs {
+  u32x4_t v[KIND == kF8Wide ? 4 : 2];
+};
+
+// The loaded halves of a step as operand registers; `scale` is the lane's
+// scale word.  (v_cvt_scalef32_pk_bf16_fp8 reads only the exponent of its
+// scale; 4 significant bits and a power of two are exact in bf16.)
+template <int KIND, int BYTE>
+__device__ __forceinline__ PanelRegs<KIND> panel_regs(u32x4_t h0, u32x4_t h1, uint32_t scale) {
+  PanelRegs<KIND> r;
+  if constexpr (KIND == kF8Wide) {
+    const float f = __builtin_bit_cast(float, ((scale >> (8 * BYTE)) & 0xFFu) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h0[i], f, false));
+      r.v[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h0[i], f, true));
+      r.v[2 + (i >> 1)][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h1[i], f, false));
+      r.v[2 + (i >> 1)][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h1[i], f, true));
+    }
+  } else {
+    r.v[0] = h0;
+    r.v[1] = h1;
+  }
+  return r;
+}
+
+// One step's product of a panel pair: 128 (8-bit) or 64 (16-bit) columns.
+template <int KIND, int BYTE>
+__device__ __forceinline__ f32x4_t panel_mfma(const PanelRegs<KIND>& ar, const PanelRegs<KIND>& br, f32x4_t c,
+                                              uint32_t sa, uint32_t sb) {
+  const auto& a = ar.v;
+  const auto& b = br.v;
+  if constexpr (KIND == kF8Wide) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = mfma16x16x32<HYB_BF16>(__builtin_bit_cast(uint4, a[i]), __builtin_bit_cast(uint4, b[i]), c);
+    return c;
+  } else if constexpr (KIND == kF8) {
+    const i32x8_t av = {int(a[0][0]), int(a[0][1]), int(a[0][2]), int(a[0][3]),
+                        int(a[1][0]), int(a[1][1]), int(a[1][2]), int(a[1][3])};
+    const i32x8_t bv = {int(b[0][0]), int(b[0][1]), int(b[0][2]), int(b[0][3]),
+                        int(b[1][0]), int(b[1][1]), int(b[1][2]), int(b[1][3])};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 0, 0, BYTE, int(sa), BYTE, int(sb));
+  } else {
+    c = mfma16x16x32<KIND>(__builtin_bit_cast(uint4, a[0]), __builtin_bit_cast(uint4, b[0]), c);
+    return mfma16x16x32<KIND>(__builtin_bit_cast(uint4, a[1]), __builtin_bit_cast(uint4, b[1]), c);
+  }
+}
+
+// Workgroups run round-robin over the 8 XCDs (id L on XCD L % 8), each with
+// its own L2.  XCD x takes a contiguous range of an order in which 4 A blocks
+// are swept across all B blocks before the next 4, so workgroups that run
+// together on one XCD share A and B panels in its L2.
+__device__ __forceinline__ void panel_block(int32_t id, int32_t total, int32_t na, int32_t nb, int32_t& ab,
+                                            int32_t& bb) {
+  constexpr int32_t kXcd = 8, kGroup = 4;
+  const int32_t xcd = id % kXcd, per = total / kXcd, extra = total % kXcd;
+  const int32_t g = xcd * per + (xcd < extra ? xcd : extra) + id / kXcd;
+  const int32_t first = g / (kGroup * nb) * kGroup;
+  const int32_t width = na - first < kGroup ? na - first : kGroup;
+  const int32_t r = g - first * nb;
+  bb = r / width;
+  ab = first + r % width;
+}
+
+// LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, two LDS
+// stages of one step each.
+template <int KIND, int AP, int BP, int WA, int WB>
+struct PanelTile {
+  static constexpr int kWaves = WA * WB;
+  static constexpr int kA = AP / WA, kB = BP / WB;  // panels per wavefront
+  static constexpr int kStage = (AP + BP) * 2048;
+  static constexpr int kScaleStage = is_f8(KIND) ? (AP + BP) * 64 : 0;  // a word per row, four steps
+  static constexpr int kLds = 2 * kStage + 2 * kScaleStage;
+  static constexpr int kLoads = (AP + BP) * 2 / kWaves;  // 1 KiB transfers per wavefront and step
+  static_assert(AP % WA == 0 && BP % WB == 0 && (AP + BP) * 2 % kWaves == 0, "even split");
+
+  // Sums of steps [s0, s1) of A panels pa.. and B panels pb..; wavefront
+  // (wa, wb) ends with acc[i][j] of its panels pa + wa kA + i, pb + wb kB + j
+  // (lane L: A rows 4 (L/16) + 0..3, B row L%16).
+  __device__ static void run(const PanelOperand& A, const PanelOperand& B, int32_t steps, int32_t pa, int32_t pb,
+                             int32_t s0, int32_t s1, char* smem, f32x4_t (&acc)[kA][kB]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wa = wave % WA, wb = wave / WA;
+    const int64_t pitch = int64_t(steps) * 2048;
+    // Resources end with the operand's last panel: panels behind it read as zeros.
+    const int32_t va = A.rows16 / 16 - pa < AP ? A.rows16 / 16 - pa : AP;
+    const int32_t vb = B.rows16 / 16 - pb < BP ? B.rows16 / 16 - pb : BP;
+    const srd4_t ra = panel_srd(A.data + pa * pitch, uint32_t(va * pitch));
+    const srd4_t rb = panel_srd(B.data + pb * pitch, uint32_t(vb * pitch));
+    const uint32_t base = panel_lds_addr(smem);
+
+    auto issue = [&](int32_t s, int stage) {
+      const uint32_t dst = base + stage * kStage;
+#pragma unroll
+      for (int t = 0; t < kLoads; ++t) {
+        const int c = wave * kLoads + t;  // 1 KiB piece: panel c / 2, half c % 2
+        const int p = c >> 1;
+        const bool is_a = p < AP;
+        const int32_t off = int32_t((is_a ? p : p - AP) * pitch) + s * 2048 + (c & 1) * 1024;
+        if (is_a)
+          panel_dma16(ra, dst + c * 1024, off + lane * 16);
+        else
+          panel_dma16(rb, dst + c * 1024, off + lane * 16);
+      }
+      if constexpr (is_f8(KIND)) {
+        // the scale words of steps s .. s+3, once per four steps (s counts
+        // from a multiple of four): AP * 64 + BP * 64 bytes in 1 KiB pieces
+        if ((s & 3) == 0 || s == s0) {
+          const uint32_t sdst = base + 2 * kStage + ((s >> 2) & 1) * kScaleStage;
+          const int64_t word = int64_t(s >> 2);
+          if (wave == 0) {
+            const srd4_t sa = panel_srd(A.scale + word * A.rows16 + pa * 16, uint32_t(va * 64));
+            for (int c = 0; c * 1024 < AP * 64; ++c)
+              if (lane * 16 + c * 1024 < AP * 64) panel_dma16(sa, sdst + c * 1024, lane * 16 + c * 1024);
+          }
+          if (wave == kWaves - 1) {
+            const srd4_t sb = panel_srd(B.scale + word * B.rows16 + pb * 16, uint32_t(vb * 64));
+            for (int c = 0; c * 1024 < BP * 64; ++c)
+              if (lane * 16 + c * 1024 < BP * 64)
+                panel_dma16(sb, sdst + AP * 64 + c * 1024, lane * 16 + c * 1024);
+          }
+        }
+      }
+    };
+
+#pragma unroll
+    for (int i = 0; i < kA; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    uint32_t sca[kA], scb[kB];
+#pragma unroll
+    for (int i = 0; i < kA; ++i) sca[i] = 0;
+#pragma unroll
+    for (int j = 0; j < kB; ++j) scb[j] = 0;
+
+    auto compute = [&](int32_t s, int stage, auto byte) {
+      constexpr int kByte = decltype(byte)::value;
+      const char* src = smem + stage * kStage + lane * 16;
+      if constexpr (is_f8(KIND)) {
+        if (kByte == 0 || s == s0) {
+          const char* sc = smem + 2 * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
+#pragma unroll
+          for (int i = 0; i < kA; ++i) sca[i] = *reinterpret_cast<const uint32_t*>(sc + (wa * kA + i) * 64);
+#pragma unroll
+          for (int j = 0; j < kB; ++j) scb[j] = *reinterpret_cast<const uint32_t*>(sc + (AP + wb * kB + j) * 64);
+        }
+      }
+      PanelRegs<KIND> b[kB];
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        const char* p = src + (AP + wb * kB + j) * 2048;
+        b[j] = panel_regs<KIND, kByte>(*reinterpret_cast<const u32x4_t*>(p),
+                                       *reinterpret_cast<const u32x4_t*>(p + 1024), scb[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < kA; ++i) {
+        const char* p = src + (wa * kA + i) * 2048;
+        const PanelRegs<KIND> a = panel_regs<KIND, kByte>(*reinterpret_cast<const u32x4_t*>(p),
+                                                          *reinterpret_cast<const u32x4_t*>(p + 1024), sca[i]);
+#pragma unroll
+        for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(a, b[j], acc[i][j], sca[i], scb[j]);
+      }
+    };
+
+    issue(s0, s0 & 1);
+    // Unrolled by four so that a step's scale byte is an immediate of its
+    // matrix instruction.  A step waits for its own transfers, meets the
+    // other wavefronts (whose reads of the other stage are then done too),
+    // starts the next step's transfers into the other stage and multiplies.
+    for (int32_t q = s0 & ~3; q < s1; q += 4) {
+      auto one = [&](auto byte) {
+        const int32_t s = q + decltype(byte)::value;
+        if (s < s0 || s >= s1) return;
+        panel_wait<0>();
+        __syncthreads();
+        if (s + 1 < s1) issue(s + 1, (s + 1) & 1);
+        compute(s, s & 1, byte);
+      };
+      one(std::integral_constant<int, 0>());
+      one(std::integral_constant<int, 1>());
+      one(std::integral_constant<int, 2>());
+      one(std::integral_constant<int, 3>());
+    }
+  }
+};
+
+}  // namespace
+}  // namespace hyb
+
+#endif  // HYB_PANEL_H_

@@ -1,0 +1,209 @@
+"""8-bit block-scaled matrices and their product: ctypes binding over the
+entry points of include/hyb_f8.h.
+
+    Q = f8.pack(w)          # weight, n x k: one scale per 128 x 128 block
+    y = f8.gemm(Q, x)       # y = x Q^T, x quantised per 1 x 128 block in the call
+    X = f8.quant(x)         # quantise once for several products
+    y = f8.gemm(Q, X)
+    w8 = f8.unpack(Q)       # the values the codes stand for
+
+Argument marshalling only, as in binding.py: torch tensors supply device
+memory and the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+from . import binding as hb
+
+WEIGHT, ROWS = 1, 2   # HYB_F8_WEIGHT, HYB_F8_ROWS
+EXPORTED = ("hyb_f8_size", "hyb_f8_quantize", "hyb_f8_dequantize", "hyb_f8_gemm_workspace_size", "hyb_f8_gemm")
+KIND_NAMES = {WEIGHT: "weight", ROWS: "rows"}
+
+
+class HybF8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+_ready = False
+
+
+def lib() -> ctypes.CDLL:
+    global _ready
+    L = hb.lib()
+    if not _ready:
+        P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        SZ, M = ctypes.c_size_t, ctypes.POINTER(HybF8)
+        L.hyb_f8_size.argtypes = [I64, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+        L.hyb_f8_quantize.argtypes = [P, I32, I64, I64, I64, I32, M, P]
+        L.hyb_f8_dequantize.argtypes = [M, I64, I64, P, I32, I64, P]
+        L.hyb_f8_gemm_workspace_size.argtypes = [I64, I64, I32, ctypes.POINTER(SZ)]
+        L.hyb_f8_gemm.argtypes = [M, I64, I64, M, I32, P, I32, I64, P, SZ, P]
+        for name in EXPORTED:
+            getattr(L, name).restype = I32
+        _ready = True
+    return L
+
+
+def _code(dtype) -> int:
+    torch = hb._torch()
+    try:
+        return {torch.float16: hb.HYB_F16, torch.bfloat16: hb.HYB_BF16, torch.float32: hb.HYB_F32}[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}: float16, bfloat16 or float32") from None
+
+
+def _pitch(t, k) -> int:
+    """Row stride of a 2-D tensor (k where it has at most one row)."""
+    return int(t.stride(0)) if t.numel() and t.shape[0] > 1 else int(k)
+
+
+def sizes(rows: int, k: int) -> tuple[int, int]:
+    """Bytes of the codes and of the scales of a rows x k matrix."""
+    a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    hb.check(lib().hyb_f8_size(int(rows), int(k), ctypes.byref(a), ctypes.byref(b)), "hyb_f8_size")
+    return int(a.value), int(b.value)
+
+
+@dataclass
+class F8Matrix:
+    """A quantised matrix: kind WEIGHT or ROWS, its shape, the dtype it was
+    made from, and two device buffers."""
+    kind: int
+    shape: tuple
+    dtype: object
+    codes: object
+    scales: object
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def struct(self) -> HybF8:
+        return HybF8(hb._ptr(self.codes), hb._ptr(self.scales))
+
+    def weight_bytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _check_matrix(Q, kind, name):
+    if not isinstance(Q, F8Matrix):
+        raise TypeError(f"{name} must be an F8Matrix")
+    if Q.kind != kind:
+        raise TypeError(f"{name} is quantised as {KIND_NAMES[Q.kind]}, expected {KIND_NAMES[kind]}")
+    need = sizes(*Q.shape)
+    if (Q.codes.numel(), Q.scales.numel()) != need:
+        raise ValueError(f"{name}: buffers of {(Q.codes.numel(), Q.scales.numel())} bytes, its shape needs {need}")
+
+
+def _quantize(a, kind, out, name):
+    torch = hb._torch()
+    hb._check_2d(a, name)
+    code = _code(a.dtype)
+    rows, k = a.shape
+    nc, ns = sizes(rows, k)
+    if out is not None:
+        _check_matrix(out, kind, "out")
+        if tuple(out.shape) != (rows, k):
+            raise ValueError(f"out is {tuple(out.shape)}, expected {(rows, k)}")
+    hb._check_gpu(a, name)
+    if out is None:
+        out = F8Matrix(kind, (rows, k), a.dtype, torch.empty(nc, dtype=torch.uint8, device=a.device),
+                       torch.empty(ns, dtype=torch.uint8, device=a.device))
+    else:
+        if out.codes.device != a.device:
+            raise ValueError(f"out is on {out.codes.device}, {name} on {a.device}")
+        out.dtype = a.dtype
+    with torch.cuda.device(a.device):
+        hb.check(lib().hyb_f8_quantize(hb._ptr(a), code, rows, k, _pitch(a, k), kind, ctypes.byref(out.struct()),
+                                       hb._stream(a.device)), "hyb_f8_quantize")
+    return out
+
+
+def pack(w, out: F8Matrix | None = None) -> F8Matrix:
+    """Quantise a weight (n x k; float16, bfloat16 or float32; unit column
+    stride) with one scale per 128 x 128 block.  `out` reuses buffers."""
+    return _quantize(w, WEIGHT, out, "w")
+
+
+def quant(x, out: F8Matrix | None = None) -> F8Matrix:
+    """Quantise activations (m x k) with one scale per 1 x 128 block, once for
+    every product that reads them."""
+    return _quantize(x, ROWS, out, "x")
+
+
+def unpack(Q: F8Matrix, out_dtype=None, out=None):
+    """The values the codes of Q stand for (default dtype: that of the matrix
+    it was made from, which holds them exactly)."""
+    torch = hb._torch()
+    if not isinstance(Q, F8Matrix):
+        raise TypeError("Q must be an F8Matrix")
+    _check_matrix(Q, Q.kind, "Q")
+    rows, k = Q.shape
+    if out is not None and out_dtype is None:
+        out_dtype = out.dtype
+    tdt = out_dtype if out_dtype is not None else Q.dtype
+    code = _code(tdt)
+    if out is None:
+        out = torch.empty((rows, k), dtype=tdt, device=Q.device)
+    hb._check_out(out, (rows, k), tdt)
+    hb._check_gpu(out, "out", Q.device)
+    with torch.cuda.device(Q.device):
+        hb.check(lib().hyb_f8_dequantize(ctypes.byref(Q.struct()), rows, k, hb._ptr(out), code, _pitch(out, k),
+                                         hb._stream(Q.device)), "hyb_f8_dequantize")
+    return out
+
+
+def workspace_bytes(Q: F8Matrix, m: int) -> int:
+    """Workspace bytes of hyb_f8_gemm for m tokens on the current device."""
+    nbytes = ctypes.c_size_t(0)
+    hb.check(lib().hyb_f8_gemm_workspace_size(Q.shape[0], Q.shape[1], int(m), ctypes.byref(nbytes)),
+             "hyb_f8_gemm_workspace_size")
+    return int(nbytes.value)
+
+
+def gemm(Q: F8Matrix, x, out_dtype=None, out=None, workspace=None):
+    """Y = X Q^T for any number of tokens (fp32 by default, or float16 /
+    bfloat16).  x: activations (m x k; quantised here, for this call) or what
+    quant() gave.  The workspace of a product that cuts k comes from torch's
+    allocator unless `workspace` (a contiguous device tensor of at least
+    workspace_bytes(Q, m) bytes) is given."""
+    torch = hb._torch()
+    _check_matrix(Q, WEIGHT, "Q")
+    n, k = Q.shape
+    if not isinstance(x, F8Matrix):
+        hb._check_2d(x, "x")
+        _code(x.dtype)
+    else:
+        _check_matrix(x, ROWS, "x")
+    if x.shape[1] != k:
+        raise ValueError(f"x has {x.shape[1]} columns, the weight has k = {k}")
+    m = x.shape[0]
+    if out is not None and out_dtype is None:
+        out_dtype = out.dtype
+    tdt = out_dtype if out_dtype is not None else torch.float32
+    code = _code(tdt)
+    if out is not None:
+        hb._check_out(out, (m, n), tdt)
+    if isinstance(x, F8Matrix):
+        if x.device != Q.device:
+            raise ValueError(f"x is on {x.device}, Q on {Q.device}")
+    else:
+        hb._check_gpu(x, "x", Q.device)
+    if out is None:
+        out = torch.empty((m, n), dtype=tdt, device=Q.device)
+    hb._check_gpu(out, "out", Q.device)
+    X = x if isinstance(x, F8Matrix) else quant(x)
+    with torch.cuda.device(Q.device):
+        if workspace is None:
+            need = workspace_bytes(Q, m)
+            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+        else:
+            hb._check_gpu(workspace, "workspace", Q.device)
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+        nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        hb.check(lib().hyb_f8_gemm(ctypes.byref(Q.struct()), n, k, ctypes.byref(X.struct()), m, hb._ptr(out), code,
+                                   _pitch(out, n), hb._ptr(workspace), nbytes, hb._stream(Q.device)), "hyb_f8_gemm")
+    return out

@@ -1,0 +1,147 @@
+"""8-bit block-scaled matrices without a GPU: the oracle's own pins, the C
+ABI's sizes and refusals (include/hyb_f8.h), and the binding's checks.  Every
+call below fails validation or does host work only."""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from matmul_pack_b1_amd import binding as hb
+from matmul_pack_b1_amd import f8
+from oracle import f8_oracle as fo
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_oracle_table_and_rounding_match_torch():
+    codes = torch.arange(256, dtype=torch.uint8)
+    assert np.array_equal(fo.e4m3_table(), codes.view(torch.float8_e4m3fn).double().numpy(), equal_nan=True)
+    rng = np.random.default_rng(0)
+    v = np.clip(rng.standard_normal(20000) * np.exp(3 * rng.standard_normal(20000)), -448, 448).astype(np.float32)
+    grid = fo.e4m3_table()[:127]
+    mid = (grid[1:] + grid[:-1]) / 2                       # every halfway point, and its neighbours
+    v = np.concatenate([v, mid, np.nextafter(mid, 0), np.nextafter(mid, 500), -mid, [0.0, -0.0, np.nan]])
+    v32 = v.astype(np.float32)
+    want = torch.from_numpy(v32).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(fo.encode(v32.astype(np.float64)), want)
+
+
+@pytest.mark.parametrize("top,e", [(0.0, 0), (448.0, 0), (448.5, 1), (1.0, -8), (0.875, -9), (0.876, -8), (1.75, -8),
+                                   (1.7500001, -7), (np.inf, 0), (2.0 ** -149, -127), (3.0e38, 120)])
+def test_oracle_scale(top, e):
+    codes, exps = fo.quantise(np.array([[0.0, top]]), 1)
+    assert exps[0, 0] == e
+    assert codes[0, 1] == 255 if np.isinf(top) else True
+    if np.isfinite(top) and top:
+        assert np.abs(fo.values(codes, exps)[0, 1]) <= 448 * 2.0 ** e
+
+
+def test_exports_match_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "hyb_f8.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(hyb_[a-z0-9_]+)\s*\(", text))
+    assert names == set(f8.EXPORTED)
+    out = subprocess.run(["nm", "-D", "--defined-only", hb.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (hyb_\w+)", out))
+
+
+@pytest.mark.parametrize("rows,k", [(0, 0), (0, 5), (5, 0), (1, 1), (16, 128), (17, 129), (300, 513), (2 ** 20, 8192)])
+def test_sizes(rows, k):
+    rows16, steps = -(-rows // 16) * 16, -(-k // 128)
+    want = (rows16 * steps * 128, rows16 * -(-steps // 4) * 4) if rows and k else (0, 0)
+    assert f8.sizes(rows, k) == want
+    if 0 < rows <= 300 and k:
+        cb, sb = fo.buffers(np.zeros((rows, k), np.uint8), np.zeros((rows, steps), np.int64))
+        assert (cb.size, sb.size) == want
+
+
+def _status(call):
+    with pytest.raises(hb.HybError) as e:
+        hb.check(call, "call")
+    return e.value.status
+
+
+P16 = 1 << 20  # any 16-byte aligned non-null address: never followed
+
+
+def _m(codes=P16, scales=P16):
+    return ctypes.byref(f8.HybF8(codes, scales))
+
+
+def test_size_refusals():
+    n = ctypes.c_size_t(0)
+    L = f8.lib()
+    assert _status(L.hyb_f8_size(-1, 8, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_size(8, -1, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_size(8, (1 << 22) + 1, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_size(1 << 31, 8, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_size(8, 8, None, ctypes.byref(n))) == 1
+    assert _status(L.hyb_f8_gemm_workspace_size(8, 8, -1, ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_gemm_workspace_size(8, 8, 1, None)) == 1
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(dtype=7), 3), (dict(kind=0), 1), (dict(rows=-1), 2), (dict(k=-3), 2), (dict(a=None), 1),
+    (dict(a=P16 + 1), 1), (dict(lda=7), 1), (dict(lda=-8), 1), (dict(lda=(1 << 31) + 1), 4), (dict(codes=None), 1),
+    (dict(scales=None), 1), (dict(codes=P16 + 8), 1), (dict(scales=P16 + 4), 1),
+])
+def test_quantise_refusals(args, status):
+    d = dict(a=P16, dtype=hb.HYB_BF16, rows=4, k=8, lda=8, kind=f8.ROWS, codes=P16, scales=P16)
+    d.update(args)
+    L = f8.lib()
+    dst = _m(d["codes"], d["scales"])
+    assert _status(L.hyb_f8_quantize(d["a"], d["dtype"], d["rows"], d["k"], d["lda"], d["kind"], dst, None)) == status
+    if "kind" not in args:
+        assert _status(L.hyb_f8_dequantize(dst, d["rows"], d["k"], d["a"], d["dtype"], d["lda"], None)) == status
+    assert hb.last_error()
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(y_dtype=0), 3), (dict(n=-1), 2), (dict(k=-1), 2), (dict(m=-1), 2), (dict(y=None), 1), (dict(y=P16 + 2), 1),
+    (dict(ldy=7), 1), (dict(w=(None, P16)), 1), (dict(x=(P16, None)), 1), (dict(w=(P16 + 1, P16)), 1),
+    (dict(ws=None, nbytes=64), 1), (dict(ws=P16 + 8, nbytes=64), 1), (dict(n=2 ** 31 - 16, m=2 ** 31 - 1, ldy=2 ** 31), 4),
+])
+def test_gemm_refusals(args, status):
+    d = dict(w=(P16, P16), n=8, k=256, x=(P16, P16), m=2, y=P16, y_dtype=hb.HYB_F32, ldy=8, ws=None, nbytes=0)
+    d.update(args)
+    st = f8.lib().hyb_f8_gemm(_m(*d["w"]), d["n"], d["k"], _m(*d["x"]), d["m"], d["y"], d["y_dtype"], d["ldy"], d["ws"],
+                              d["nbytes"], None)
+    assert _status(st) == status
+
+
+def test_empty_calls_do_nothing():
+    L = f8.lib()
+    assert L.hyb_f8_quantize(None, hb.HYB_F32, 0, 8, 8, f8.ROWS, None, None) == 0
+    assert L.hyb_f8_quantize(None, hb.HYB_F32, 8, 0, 0, f8.ROWS, None, None) == 0
+    assert L.hyb_f8_gemm(None, 8, 8, None, 0, None, hb.HYB_F32, 8, None, 0, None) == 0
+    assert L.hyb_f8_gemm(None, 0, 8, None, 3, None, hb.HYB_F32, 0, None, 0, None) == 0
+
+
+def _fake(kind, rows, k, dtype=torch.bfloat16):
+    nc, ns = f8.sizes(rows, k)
+    return f8.F8Matrix(kind, (rows, k), dtype, torch.empty(nc, dtype=torch.uint8), torch.empty(ns, dtype=torch.uint8))
+
+
+def test_binding_refusals():
+    w = torch.zeros(8, 256, dtype=torch.bfloat16)
+    for call, err in [
+        (lambda: f8.pack(w.double()), TypeError), (lambda: f8.pack(w[0]), ValueError),
+        (lambda: f8.pack(w.t()), ValueError), (lambda: f8.pack(w), ValueError),              # not on a GPU
+        (lambda: f8.quant(w, out=_fake(f8.WEIGHT, 8, 256)), TypeError),
+        (lambda: f8.pack(w, out=_fake(f8.WEIGHT, 8, 128)), ValueError),
+        (lambda: f8.unpack(w), TypeError), (lambda: f8.unpack(_fake(f8.ROWS, 2, 3), out_dtype=torch.int8), TypeError),
+        (lambda: f8.gemm(_fake(f8.ROWS, 8, 256), w), TypeError),
+        (lambda: f8.gemm(_fake(f8.WEIGHT, 8, 256), _fake(f8.WEIGHT, 8, 256)), TypeError),
+        (lambda: f8.gemm(_fake(f8.WEIGHT, 8, 128), w), ValueError),
+        (lambda: f8.gemm(_fake(f8.WEIGHT, 8, 256), w, out=torch.zeros(8, 9)), ValueError),
+        (lambda: f8.gemm(_fake(f8.WEIGHT, 8, 256), w.int()), TypeError),
+    ]:
+        with pytest.raises(err):
+            call()
+    short = _fake(f8.WEIGHT, 8, 256)
+    short.codes = short.codes[:-1]
+    with pytest.raises(ValueError, match="buffers"):
+        f8.gemm(short, w)
