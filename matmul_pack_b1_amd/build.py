@@ -19,7 +19,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libhyb.so")
 SOURCES = ["hyb_api.cpp", "hyb_route.cpp", "hyb_pack.hip", "hyb_gemv.hip", "hyb_gemm.hip", "hyb_lowrank.hip",
-           "hyb_f8_api.cpp", "hyb_f8_route.cpp", "hyb_f8.hip"]
+           "hyb_f8_api.cpp", "hyb_f8_route.cpp", "hyb_f8.hip",
+           "hyb_xent_api.cpp", "hyb_xent_plan.cpp", "hyb_xent.hip"]
 ARCH = os.environ.get("HYB_ARCH", "gfx950")
 
 

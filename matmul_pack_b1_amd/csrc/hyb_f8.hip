@@ -43,11 +43,12 @@ __device__ __forceinline__ void load16(const void* a, int64_t base, int32_t c0, 
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    if (c0 + i >= k) break;
-    if constexpr (DT == HYB_F32)
-      v[i] = static_cast<const float*>(a)[base + c0 + i];
-    else
-      v[i] = widen16<DT>(static_cast<const uint16_t*>(a)[base + c0 + i]);
+    if (c0 + i < k) {
+      if constexpr (DT == HYB_F32)
+        v[i] = static_cast<const float*>(a)[base + c0 + i];
+      else
+        v[i] = widen16<DT>(static_cast<const uint16_t*>(a)[base + c0 + i]);
+    }
   }
 }
 
@@ -274,11 +275,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
       for (int h = 0; h < 2; ++h)
         a[t][h] = __builtin_bit_cast(
             u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (s + t) * 2048 + h * 1024 + lane * 16, 0, HYB_W_AUX));
-    const uint32_t sa = W.scale[int64_t(s >> 2) * W.rows16 + pw * 16 + (lane & 15)];
+    const uint32_t sa = W.scale[int64_t(s >> 2) * W.scale_pitch + pw * 16 + (lane & 15)];
 #pragma unroll
     for (int j = 0; j < BP; ++j) {
       const int32_t xr = (px + j) * 16 + (lane & 15);
-      const uint32_t sb = X.scale[int64_t(s >> 2) * X.rows16 + (xr < X.rows16 ? xr : 0)];
+      const uint32_t sb = X.scale[int64_t(s >> 2) * X.scale_pitch + (xr < X.rows16 ? xr : 0)];
       auto step = [&](auto byte) {
         constexpr int t = decltype(byte)::value;
         u32x4_t b[2];
@@ -406,9 +407,9 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
     return hipGetLastError();
   }
   const PanelOperand W{static_cast<const char*>(w.codes), static_cast<const uint32_t*>(w.scales),
-                       int32_t(f8_rows16(n))};
+                       int32_t(f8_rows16(n)), f8_rows16(n)};
   const PanelOperand X{static_cast<const char*>(x.codes), static_cast<const uint32_t*>(x.scales),
-                       int32_t(f8_rows16(m))};
+                       int32_t(f8_rows16(m)), f8_rows16(m)};
   const int32_t steps = int32_t(f8_steps(k));
   const F8Route r = f8_route(n, k, m, device_cus());
   (void)ws;

@@ -48,6 +48,7 @@ struct PanelOperand {
   const char* data;
   const uint32_t* scale;  // 8-bit operands only
   int32_t rows16;         // rows rounded up to 16 (the panels that exist)
+  int64_t scale_pitch;    // words from four steps' scales to the next four's
 };
 
 __device__ __forceinline__ srd4_t panel_srd(const void* base, uint32_t bytes) {
@@ -154,7 +155,8 @@ struct PanelTile {
   static constexpr int kLoads = (AP + BP) * 2 / kWaves;  // 1 KiB transfers per wavefront and step
   static_assert(AP % WA == 0 && BP % WB == 0 && (AP + BP) * 2 % kWaves == 0, "even split");
 
-  // Sums of steps [s0, s1) of A panels pa.. and B panels pb..; wavefront
+  // Sums of steps [s0, s1), s0 a multiple of four, of A panels pa.. and B
+  // panels pb..; wavefront
   // (wa, wb) ends with acc[i][j] of its panels pa + wa kA + i, pb + wb kB + j
   // (lane L: A rows 4 (L/16) + 0..3, B row L%16).
   __device__ static void run(const PanelOperand& A, const PanelOperand& B, int32_t steps, int32_t pa, int32_t pb,
@@ -186,16 +188,16 @@ struct PanelTile {
       if constexpr (is_f8(KIND)) {
         // the scale words of steps s .. s+3, once per four steps (s counts
         // from a multiple of four): AP * 64 + BP * 64 bytes in 1 KiB pieces
-        if ((s & 3) == 0 || s == s0) {
+        if ((s & 3) == 0) {
           const uint32_t sdst = base + 2 * kStage + ((s >> 2) & 1) * kScaleStage;
           const int64_t word = int64_t(s >> 2);
           if (wave == 0) {
-            const srd4_t sa = panel_srd(A.scale + word * A.rows16 + pa * 16, uint32_t(va * 64));
+            const srd4_t sa = panel_srd(A.scale + word * A.scale_pitch + pa * 16, uint32_t(va * 64));
             for (int c = 0; c * 1024 < AP * 64; ++c)
               if (lane * 16 + c * 1024 < AP * 64) panel_dma16(sa, sdst + c * 1024, lane * 16 + c * 1024);
           }
           if (wave == kWaves - 1) {
-            const srd4_t sb = panel_srd(B.scale + word * B.rows16 + pb * 16, uint32_t(vb * 64));
+            const srd4_t sb = panel_srd(B.scale + word * B.scale_pitch + pb * 16, uint32_t(vb * 64));
             for (int c = 0; c * 1024 < BP * 64; ++c)
               if (lane * 16 + c * 1024 < BP * 64)
                 panel_dma16(sb, sdst + AP * 64 + c * 1024, lane * 16 + c * 1024);
@@ -219,7 +221,7 @@ struct PanelTile {
       constexpr int kByte = decltype(byte)::value;
       const char* src = smem + stage * kStage + lane * 16;
       if constexpr (is_f8(KIND)) {
-        if (kByte == 0 || s == s0) {
+        if (kByte == 0) {
           const char* sc = smem + 2 * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
 #pragma unroll
           for (int i = 0; i < kA; ++i) sca[i] = *reinterpret_cast<const uint32_t*>(sc + (wa * kA + i) * 64);
@@ -244,19 +246,21 @@ struct PanelTile {
       }
     };
 
-    issue(s0, s0 & 1);
-    // Unrolled by four so that a step's scale byte is an immediate of its
-    // matrix instruction.  A step waits for its own transfers, meets the
-    // other wavefronts (whose reads of the other stage are then done too),
-    // starts the next step's transfers into the other stage and multiplies.
-    for (int32_t q = s0 & ~3; q < s1; q += 4) {
+    // A step waits for its own transfers, meets the other wavefronts (whose
+    // reads of the other stage are then done too), starts the next step's
+    // transfers into the other stage and multiplies.  Unrolled by four so
+    // that stage and scale byte are immediates.
+    if (s0 >= s1) return;
+    issue(s0, 0);
+    for (int32_t q = s0; q < s1; q += 4) {
       auto one = [&](auto byte) {
-        const int32_t s = q + decltype(byte)::value;
-        if (s < s0 || s >= s1) return;
+        constexpr int kByte = decltype(byte)::value;
+        const int32_t s = q + kByte;
+        if (s >= s1) return;
         panel_wait<0>();
         __syncthreads();
-        if (s + 1 < s1) issue(s + 1, (s + 1) & 1);
-        compute(s, s & 1, byte);
+        if (s + 1 < s1) issue(s + 1, (kByte + 1) & 1);
+        compute(s, kByte & 1, byte);
       };
       one(std::integral_constant<int, 0>());
       one(std::integral_constant<int, 1>());

@@ -1,0 +1,812 @@
+// Kernels of the cross entropy over a vocabulary projection
+// (include/hyb_xent.h).
+//
+// The vocabulary is cut into pieces.  Loss: each 256-entry x 256-token tile of
+// Z = W' X^T leaves, per token, the maximum and the sum of exponentials of
+// its entries (and the target's logit); a second kernel joins them to lse.
+// Gradient: the same tiles, recomputed, become G = softmax - onehot in
+// registers and leave as 16-bit panels, once with tokens as rows (for dX = G
+// W', summed over pieces in fp32) and once with entries as rows (for dW =
+// G^T X).  All products run on the panel tiles of hyb_panel.h; what they
+// need in the other orientation (W'^T, X^T) is transposed panel by panel.
+#include <type_traits>
+
+#include "hyb_panel.h"
+#include "hyb_xent_internal.h"
+
+namespace hyb {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// exp(a - b) for a <= b where both may be -inf (an empty sum): 0.
+__device__ __forceinline__ float rescale(float a, float b) { return a == b ? 1.f : fast_exp(a - b); }
+
+// Factor that lifts probabilities into fp16's normal range (bf16 needs none).
+template <int DT>
+constexpr float g_scale() {
+  return DT == HYB_F16 ? 16384.f : 1.f;
+}
+
+// ------------------------------------------------------------ operand forms --
+
+// x (m x k, row-major) as panels; rows of ignored tokens and behind m zero.
+__global__ __launch_bounds__(256) void k_xent_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m,
+                                                     int32_t steps, const int64_t* __restrict__ target, int64_t ignore,
+                                                     char* __restrict__ out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t panel = blockIdx.x;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps) return;
+  const int64_t row = panel * 16 + (lane & 15);
+  const bool live = row < m && target[row] != ignore;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (live) u = *reinterpret_cast<const uint4*>(x + row * ldx + s * 64 + h * 32 + (lane >> 4) * 8);
+    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16) = u;
+  }
+}
+
+// Sixteen columns 16 q.. of a row (q = lane / 16) as the two 16-byte pieces of
+// the panel order: half q / 2, lane groups 2 (q % 2) and 2 (q % 2) + 1.
+__device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t (&e)[8]) {
+  const int q = lane >> 4;
+  char* p = step + (q >> 1) * 1024 + (2 * (q & 1)) * 256 + (lane & 15) * 16;
+  *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
+  *reinterpret_cast<uint4*>(p + 256) = make_uint4(e[4], e[5], e[6], e[7]);
+}
+
+// Rows v0.. of a packed matrix as panels (one wavefront per panel and step):
+// a dense tile's chunks already are in panel order, a sparse chunk is
+// expanded from its values and codes.  Rows from n_vocab on are zero.
+__global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ dense, const uint4* __restrict__ val,
+                                                     const uint16_t* __restrict__ meta,
+                                                     const int32_t* __restrict__ tidx, int b1, int b2, int meta_kind,
+                                                     int32_t tiles_k, int32_t n_dense, int32_t n_sparse, int64_t v0,
+                                                     int64_t n_vocab, int32_t steps, char* __restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps) return;
+  const int64_t r0 = v0 + int64_t(blockIdx.x) * 16;  // first row of the panel
+  const int64_t tn = r0 / b1;
+  const int rs = int(r0 - tn * b1) / 16;              // slab within the tile
+  const int spt = b2 / 64, c = s % spt;
+  const int32_t ti = tidx[tn * tiles_k + s / spt];
+  char* dst = out + (int64_t(blockIdx.x) * steps + s) * kPanelStep;
+  const bool row_ok = r0 + (lane & 15) < n_vocab;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (ti >= 0 && ti < n_dense) {
+    const uint4* src = dense + (int64_t(ti) * b1 * b2 + int64_t(rs) * 16 * b2 + c * 1024) / 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint4*>(dst + h * 1024 + lane * 16) = row_ok ? src[h * 64 + lane] : zero;
+    return;
+  }
+  uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (ti < 0 && ~ti < n_sparse && row_ok) {
+    const int64_t slot = ~ti;
+    const uint4 u = val[(slot * b1 * b2 / 2 + int64_t(rs) * 8 * b2 + c * 512) / 8 + lane];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t code = meta[slot * b1 * b2 / 16 + int64_t(rs) * b2 + lane * (b2 / 64) + c];
+    if (meta_kind == HYB_META_MASK8) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          e[4 * g + j] = __builtin_amdgcn_perm(w[2 * g + 1], w[2 * g], expand8_selector((code >> (8 * g)) & 0xFFu, j));
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t i0, i1;
+        nibble_positions((code >> (4 * g)) & 0xFu, meta_kind, i0, i1);
+        e[2 * g] = __builtin_amdgcn_perm(0u, w[g], scatter_selector(0, i0, i1));
+        e[2 * g + 1] = __builtin_amdgcn_perm(0u, w[g], scatter_selector(2, i0, i1));
+      }
+    }
+  }
+  store_row16(dst, lane, e);
+}
+
+// Largest exponent byte of an 8-bit head's scales (rows < n_vocab), for the
+// fp16 form of its values; *top starts at 0.
+__global__ __launch_bounds__(256) void k_xent_top_scale(const uint32_t* __restrict__ scales, int64_t rows16,
+                                                        int64_t n_vocab, int32_t steps, uint32_t* __restrict__ top) {
+  const int64_t row = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  uint32_t t = 0;
+  if (row < n_vocab) {
+    const int32_t s0 = int32_t(blockIdx.y) * 4;
+    const uint32_t w = scales[int64_t(blockIdx.y) * rows16 + row];
+    for (int i = 0; i < 4; ++i)
+      if (s0 + i < steps) {
+        const uint32_t b = (w >> (8 * i)) & 0xFFu;
+        t = b > t ? b : t;
+      }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_xor(t, d);
+    t = o > t ? o : t;
+  }
+  if ((threadIdx.x & 63) == 0 && t > 0) atomicMax(top, t);
+}
+
+// Rows v0.. of an 8-bit head as 16-bit panels.  bf16 holds every value
+// exactly.  fp16 holds it divided by 2^(top - 133), top the head's largest
+// exponent byte: at most 448 * 64, and exact for blocks whose scale is
+// within 2^21 of the largest (smaller ones lose bits of values that are below
+// 2^-30 of the head's largest).
+template <int DT>
+__global__ __launch_bounds__(256) void k_xent_widen(const char* __restrict__ codes, const uint32_t* __restrict__ scales,
+                                                    int32_t rows16, int64_t v0, int64_t n_vocab, int32_t steps,
+                                                    const uint32_t* __restrict__ top, char* __restrict__ out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps) return;
+  const int64_t row = v0 + int64_t(blockIdx.x) * 16 + (lane & 15);
+  const int64_t panel = v0 / 16 + blockIdx.x;
+  const bool row_ok = row < n_vocab;
+  uint32_t byte = row_ok ? (scales[int64_t(s >> 2) * rows16 + row] >> (8 * (s & 3))) & 0xFFu : 127u;
+  if constexpr (DT == HYB_F16) {
+    const int b = int(byte) - int(*top) + 133;
+    byte = uint32_t(b < 1 ? 1 : b);
+  }
+  const float f = __builtin_bit_cast(float, byte << 23);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row_ok) {
+      const uint4 u = *reinterpret_cast<const uint4*>(codes + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == HYB_BF16) {
+          e[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, false));
+          e[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, true));
+        } else {
+          e[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], f, false));
+          e[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], f, true));
+        }
+      }
+    }
+    store_row16(out + (int64_t(blockIdx.x) * 2 * steps + 2 * s + h) * kPanelStep, lane, e);
+  }
+}
+
+// Panels of A (rows16 rows, `steps` steps of 64 columns) as panels of A^T:
+// 64 * steps rows of ceil(rows16 / 64) steps, zeros behind A's rows.  One
+// workgroup per 64 x 64 block, through LDS; the row pitch of 136 bytes puts
+// the four lane groups of a column read on different banks.
+__global__ __launch_bounds__(256) void k_xent_transpose(const char* __restrict__ in, int32_t rows16, int32_t steps,
+                                                        char* __restrict__ out, int32_t out_steps) {
+  constexpr int kPitch = 136;
+  __shared__ __attribute__((aligned(16))) char tile[64 * kPitch];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t rb = int32_t(blockIdx.x), s = int32_t(blockIdx.y);
+  const int64_t panel = int64_t(rb) * 4 + wave;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (panel * 16 < rows16) u = *reinterpret_cast<const uint4*>(in + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16);
+    char* p = tile + (wave * 16 + (lane & 15)) * kPitch + h * 64 + (lane >> 4) * 16;
+    *reinterpret_cast<uint2*>(p) = make_uint2(u.x, u.y);
+    *reinterpret_cast<uint2*>(p + 8) = make_uint2(u.z, u.w);
+  }
+  __syncthreads();
+  const int64_t orow = int64_t(s) * 4 + wave;  // output panel: columns 16 wave.. of this step
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const char* p = tile + (h * 32 + (lane >> 4) * 8 + 2 * i) * kPitch + (wave * 16 + (lane & 15)) * 2;
+      e[i] = *reinterpret_cast<const uint16_t*>(p) | uint32_t(*reinterpret_cast<const uint16_t*>(p + kPitch)) << 16;
+    }
+    *reinterpret_cast<uint4*>(out + (orow * out_steps + rb) * kPanelStep + h * 1024 + lane * 16) =
+        make_uint4(e[0], e[1], e[2], e[3]);
+  }
+}
+
+// --------------------------------------------------------------- the logits --
+
+struct XentTile {
+  int64_t v0;       // first vocabulary row of the piece
+  int64_t n_vocab, ignore;
+  const int64_t* target;
+  int32_t m, m16;
+  // loss
+  float2* part;     // [chunk][m16]: maximum, sum of exponentials
+  float* zt;        // target's logit
+  // gradient
+  const float* lse;
+  const float* grad;
+  const float* gtop;  // power of two >= max |grad|
+  char* g;            // panels of G: tokens x entries of the piece (or NULL)
+  char* gt;           // panels of G^T diag(grad / gtop): entries x tokens (or NULL)
+  int32_t g_steps, gt_steps;
+};
+
+// One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
+// leaves the softmax sums, true the two forms of G.
+template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, int32_t steps,
+                                                            XentTile t) {
+  typedef PanelTile<KIND, AP, BP, WA, WB> T;
+  extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
+  const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  int32_t ab, bb;
+  panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
+  f32x4_t acc[T::kA][T::kB];
+  T::run(W, X, steps, ab * AP, bb * BP, 0, steps, xent_smem, acc);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wa = wave % WA, wb = wave / WA;
+  // entry of acc[i][.][e]: vbase + 16 i + e; token of acc[.][j]: tbase + 16 j
+  const int64_t vbase = t.v0 + int64_t(ab * AP + wa * T::kA) * 16 + (lane >> 4) * 4;
+  const int32_t tbase = (bb * BP + wb * T::kB) * 16 + (lane & 15);
+  __syncthreads();  // the tile's LDS stages are free
+  if constexpr (!GRAD) {
+    float2* sums = reinterpret_cast<float2*>(xent_smem);  // [WA][16 BP]
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j) {
+      const int32_t tok = tbase + 16 * j;
+      const int64_t want = tok < t.m ? t.target[tok] : -1;
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t v = vbase + 16 * i + e;
+          if (v >= t.n_vocab) acc[i][j][e] = -__builtin_inff();
+          if (v == want && v < t.n_vocab && tok < t.m) t.zt[tok] = acc[i][j][e];
+          // a NaN logit makes the maximum NaN, and with it the loss
+          top = acc[i][j][e] > top || acc[i][j][e] != acc[i][j][e] ? acc[i][j][e] : top;
+        }
+#pragma unroll
+      for (int d = 16; d < 64; d *= 2) {
+        const float o = __shfl_xor(top, d);
+        top = o > top || o != o ? o : top;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += rescale(acc[i][j][e], top) * (acc[i][j][e] == -__builtin_inff() ? 0.f : 1.f);
+#pragma unroll
+      for (int d = 16; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+      if (lane < 16) sums[wa * (BP * 16) + (wb * T::kB + j) * 16 + lane] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < BP * 16; c += 64 * WA * WB) {
+      const int32_t tok = bb * BP * 16 + c;
+      if (tok >= t.m16) continue;
+      float2 r = sums[c];
+#pragma unroll
+      for (int a = 1; a < WA; ++a) {
+        const float2 o = sums[a * (BP * 16) + c];
+        const float top = o.x > r.x || o.x != o.x ? o.x : r.x;
+        r = make_float2(top, r.y * rescale(r.x, top) + o.y * rescale(o.x, top));
+      }
+      t.part[(t.v0 / (16 * AP) + ab) * t.m16 + tok] = r;
+    }
+  } else {
+    const float gtop = *t.gtop;
+    // per wavefront: 16 entries x 32 tokens of G^T, 80-byte rows
+    constexpr int kPitch = 80;
+    char* turn = xent_smem + wave * 16 * kPitch;
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j) {
+      const int32_t tok = tbase + 16 * j;
+      const int64_t want = tok < t.m ? t.target[tok] : t.ignore;
+      const bool seen = tok < t.m && want != t.ignore;
+      const bool valid = want >= 0 && want < t.n_vocab;
+      const float lse = seen ? t.lse[tok] : 0.f;
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i) {
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t v = vbase + 16 * i + e;
+          float p = fast_exp(acc[i][j][e] - lse) - (v == want ? 1.f : 0.f);
+          if (!valid) p = __builtin_nanf("");
+          if (!seen || v >= t.n_vocab) p = 0.f;
+          acc[i][j][e] = p;
+          h[e] = round16<DT>(p * g_scale<DT>());
+        }
+        // row tok % 16 of token panel tok / 16, entries 16 i.. of this wavefront
+        const int32_t col = (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4;
+        if (t.g && tok < t.m16 && col < t.g_steps * 64)
+          *reinterpret_cast<uint2*>(t.g + (int64_t(tok >> 4) * t.g_steps + (col >> 6)) * kPanelStep +
+                                    ((col & 32) >> 5) * 1024 + ((col & 31) >> 3) * 256 + (tok & 15) * 16 + (col & 7) * 2) =
+              make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+      }
+    }
+    if (t.gt) {
+#pragma unroll
+      for (int jj = 0; jj < T::kB; jj += 2) {
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int32_t tok = tbase + 16 * (jj + j);
+          const bool seen = tok < t.m && t.target[tok < t.m ? tok : 0] != t.ignore;
+          f[j] = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
+        }
+        const int32_t tok0 = (bb * BP + wb * T::kB + jj) * 16;
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // an ignored token's 0 stays 0 whatever its grad
+              *reinterpret_cast<uint16_t*>(turn + ((lane >> 4) * 4 + e) * kPitch + (16 * j + (lane & 15)) * 2) =
+                  round16<DT>(acc[i][jj + j][e] * f[j]);
+            }
+          // one wavefront writes and reads `turn`: its own accesses done suffices
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          const int32_t row = (ab * AP + wa * T::kA + i) * 16;
+          const uint4 u = *reinterpret_cast<const uint4*>(turn + (lane & 15) * kPitch + (lane >> 4) * 16);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          if (row < W.rows16 && tok0 < t.gt_steps * 64)
+            *reinterpret_cast<uint4*>(t.gt + (int64_t(row >> 4) * t.gt_steps + (tok0 >> 6)) * kPanelStep +
+                                      ((tok0 & 32) >> 5) * 1024 + lane * 16) = u;
+        }
+      }
+    }
+  }
+}
+
+// Softmax sums of rows of fp32 logits (few tokens), one workgroup per chunk of
+// 2048 entries and token.
+__global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
+  __shared__ float2 sums[4];
+  const int32_t tok = int32_t(blockIdx.y);
+  const int64_t v0 = int64_t(blockIdx.x) * 2048;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t want = t.target[tok];
+  float v[8];
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = v0 + i * 256 + threadIdx.x;
+    v[i] = c < t.n_vocab ? z[tok * ldz + c] : -__builtin_inff();
+    if (c == want && c < t.n_vocab) t.zt[tok] = v[i];
+    top = v[i] > top || v[i] != v[i] ? v[i] : top;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const float o = __shfl_xor(top, d);
+    top = o > top || o != o ? o : top;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += rescale(v[i], top) * (v[i] == -__builtin_inff() ? 0.f : 1.f);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+  if (lane == 0) sums[wave] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float2 r = sums[0];
+    for (int a = 1; a < 4; ++a) {
+      const float2 o = sums[a];
+      const float m = o.x > r.x || o.x != o.x ? o.x : r.x;
+      r = make_float2(m, r.y * rescale(r.x, m) + o.y * rescale(o.x, m));
+    }
+    t.part[blockIdx.x * int64_t(t.m16) + tok] = r;
+  }
+}
+
+// Joins a token's partial sums: 16 tokens per workgroup, 64 threads each, in a
+// fixed order.
+__global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ part, int64_t chunks, int32_t m,
+                                                    int32_t m16, const float* __restrict__ zt,
+                                                    const int64_t* __restrict__ target, int64_t ignore,
+                                                    int64_t n_vocab, float* __restrict__ loss,
+                                                    float* __restrict__ lse) {
+  __shared__ float2 sums[64][16];
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int32_t tok = int32_t(blockIdx.x) * 16 + l;
+  float2 r = make_float2(-__builtin_inff(), 0.f);
+  auto join = [](float2 a, float2 o) {
+    const float top = o.x > a.x || o.x != o.x ? o.x : a.x;
+    return make_float2(top, a.y * rescale(a.x, top) + o.y * rescale(o.x, top));
+  };
+  if (tok < m)
+    for (int64_t c = g; c < chunks; c += 64) r = join(r, part[c * m16 + tok]);
+  sums[g][l] = r;
+  for (int d = 32; d > 0; d /= 2) {
+    __syncthreads();
+    if (g < d) sums[g][l] = join(sums[g][l], sums[g + d][l]);
+  }
+  if (g == 0 && tok < m) {
+    const float2 f = sums[0][l];
+    const float total = f.x + logf(f.y);
+    const int64_t want = target[tok];
+    if (want == ignore) {
+      loss[tok] = 0.f;
+      lse[tok] = 0.f;
+    } else {
+      loss[tok] = want >= 0 && want < n_vocab ? total - zt[tok] : __builtin_nanf("");
+      lse[tok] = total;
+    }
+  }
+}
+
+// ------------------------------------------------------------ the gradients --
+
+// Smallest power of two >= the largest finite |grad| of a token that counts
+// (1 if there is none); also clears *top.
+__global__ __launch_bounds__(1024) void k_xent_grad_top(const float* __restrict__ grad,
+                                                        const int64_t* __restrict__ target, int64_t ignore, int32_t m,
+                                                        float* __restrict__ gtop, uint32_t* __restrict__ top) {
+  __shared__ uint32_t tops[16];
+  uint32_t u = 0;
+  for (int32_t i = threadIdx.x; i < m; i += 1024) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, grad[i]) & 0x7FFFFFFFu;
+    if (target[i] != ignore && b < 0x7F800000u && b > u) u = b;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_xor(u, d);
+    u = o > u ? o : u;
+  }
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = u;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) u = tops[i] > u ? tops[i] : u;
+    u = (u + 0x7FFFFFu) & 0x7F800000u;
+    // grad / gtop and the product with gtop stay in range: 2^-100 .. 2^100
+    if (u < 0x0D800000u) u = 0x0D800000u;
+    if (u > 0x71800000u) u = 0x71800000u;
+    *gtop = __builtin_bit_cast(float, u);
+    *top = 0;
+  }
+}
+
+struct XentOut {
+  float* acc;        // dX: [part][row][ld] fp32
+  int64_t ld, part;  // floats
+  int first;         // store (first piece) or add
+  uint16_t* y;       // dW: 16-bit rows of the head's type
+  int64_t ldy;
+  const float* gtop;
+  int32_t rows, cols;  // rows of B and columns (rows of A) that exist
+  int64_t live;        // dW: rows from here on are padding, zero
+  int vec;
+};
+
+// Y[b, a] = sum over steps of A's panels with B's; DX: fp32, this workgroup's
+// part of the steps, stored or added; else 16-bit, scaled back by gtop.
+template <int DT, bool DX, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
+                                                               int parts, XentOut o) {
+  typedef PanelTile<DT, AP, BP, WA, WB> T;
+  extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
+  const int32_t na = (A.rows16 + 16 * AP - 1) / (16 * AP), nb = (B.rows16 + 16 * BP - 1) / (16 * BP);
+  int32_t ab, bb;
+  const int32_t part = int32_t(blockIdx.y);
+  panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
+  const int32_t quads = (steps + 3) / 4;  // a part is a whole number of four steps
+  const int32_t s0 = int32_t(int64_t(quads) * part / parts) * 4;
+  const int32_t s1 = part + 1 == parts ? steps : int32_t(int64_t(quads) * (part + 1) / parts) * 4;
+  f32x4_t acc[T::kA][T::kB];
+  T::run(A, B, steps, ab * AP, bb * BP, s0, s1, xent_smem, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wa = wave % WA, wb = wave / WA;
+  const float back = DX ? 1.f : *o.gtop / g_scale<DT>();
+#pragma unroll
+  for (int j = 0; j < T::kB; ++j) {
+    const int32_t row = (bb * BP + wb * T::kB + j) * 16 + (lane & 15);
+    if (row >= o.rows) continue;
+#pragma unroll
+    for (int i = 0; i < T::kA; ++i) {
+      const int32_t col = (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4;
+      if constexpr (DX) {
+        if (col >= o.ld) continue;
+        f32x4_t* p = reinterpret_cast<f32x4_t*>(o.acc + part * o.part + row * o.ld + col);
+        f32x4_t v = acc[i][j];
+        if (!o.first) {
+          const f32x4_t u = *p;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += u[e];
+        }
+        *p = v;
+      } else {
+        if (col >= o.cols) continue;
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = row < o.live ? round16<DT>(acc[i][j][e] * back) : uint16_t(0);
+        uint16_t* p = o.y + row * o.ldy + col;
+        if (o.vec && col + 4 <= o.cols) {
+          *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < o.cols) p[e] = h[e];
+        }
+      }
+    }
+  }
+}
+
+// dX = grad * sum of the parts (in order), rounded once; ignored tokens 0.
+template <int DT, bool F8>
+__global__ __launch_bounds__(256) void k_xent_dx(const float* __restrict__ acc, int64_t ld, int64_t part, int parts,
+                                                 int32_t m, int32_t k, const int64_t* __restrict__ target,
+                                                 int64_t ignore, const float* __restrict__ grad,
+                                                 const uint32_t* __restrict__ top, uint16_t* __restrict__ dx,
+                                                 int64_t lddx) {
+  const int64_t tok = blockIdx.x;
+  const int32_t col = (int32_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  if (col >= k) return;
+  const bool seen = target[tok] != ignore;
+  f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (seen) {
+    for (int p = 0; p < parts; ++p) {
+      const f32x4_t u = *reinterpret_cast<const f32x4_t*>(acc + p * part + tok * ld + col);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += u[e];
+    }
+    float f = grad[tok] / g_scale<DT>();
+    // the fp16 form of an 8-bit head was divided by 2^(top - 133)
+    const int lift = F8 && DT == HYB_F16 ? int(*top) - 133 : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e] * f, lift);
+  }
+  uint16_t* p = dx + tok * lddx + col;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < k) p[e] = round16<DT>(v[e]);
+}
+
+// Rows r0.. of dW set to zero (an empty batch).
+__global__ __launch_bounds__(256) void k_xent_zero(uint16_t* __restrict__ dw, int64_t ld, int32_t k) {
+  const int32_t c = int32_t(blockIdx.y) * 256 + threadIdx.x;
+  if (c < k) dw[int64_t(blockIdx.x) * ld + c] = 0;
+}
+
+// ----------------------------------------------------------------- launches --
+
+template <typename F>
+hipError_t allow_lds(F* fn, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
+hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, int32_t steps, const XentTile& t, hipStream_t s) {
+  typedef PanelTile<KIND, AP, BP, WA, WB> T;
+  const hipError_t e = allow_lds(&k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>, T::kLds);
+  if (e != hipSuccess) return e;
+  const int64_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  hipLaunchKernelGGL((k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB),
+                     T::kLds, s, W, X, steps, t);
+  return hipGetLastError();
+}
+
+template <int DT, bool GRAD>
+hipError_t run_tiles(bool f8, int bp, const PanelOperand& W, const PanelOperand& X, int32_t steps, const XentTile& t,
+                     hipStream_t s) {
+  if (f8)
+    return bp == 16 ? run_tile<kF8Wide, DT, GRAD, 16, 16, 2, 4>(W, X, steps, t, s)
+                    : run_tile<kF8Wide, DT, GRAD, 16, 4, 4, 2>(W, X, steps, t, s);
+  return bp == 16 ? run_tile<DT, DT, GRAD, 16, 16, 2, 4>(W, X, steps, t, s)
+                  : run_tile<DT, DT, GRAD, 16, 4, 4, 2>(W, X, steps, t, s);
+}
+
+template <int DT, bool DX, int AP, int BP, int WA, int WB>
+hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
+                       hipStream_t s) {
+  typedef PanelTile<DT, AP, BP, WA, WB> T;
+  const hipError_t e = allow_lds(&k_xent_product<DT, DX, AP, BP, WA, WB>, T::kLds);
+  if (e != hipSuccess) return e;
+  const int64_t na = (A.rows16 + 16 * AP - 1) / (16 * AP), nb = (B.rows16 + 16 * BP - 1) / (16 * BP);
+  hipLaunchKernelGGL((k_xent_product<DT, DX, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
+                     dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
+  return hipGetLastError();
+}
+
+// The piece of `rows` vocabulary rows from v0 as 16-bit panels in `out`.
+template <int DT>
+hipError_t piece_panels(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t v0, int64_t rows,
+                        const uint32_t* top, char* out, hipStream_t s) {
+  const unsigned panels = unsigned((rows + 15) / 16);
+  if (p.f8) {
+    hipLaunchKernelGGL((k_xent_widen<DT>), dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
+                       static_cast<const char*>(head.f8->codes), static_cast<const uint32_t*>(head.f8->scales),
+                       int32_t(f8_rows16(p.n)), v0, n_vocab, int32_t(p.steps), top, out);
+  } else {
+    const hyb_layout& L = *head.layout;
+    const hyb_packed& P = *head.packed;
+    hipLaunchKernelGGL(k_xent_expand, dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
+                       static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
+                       static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
+                       int32_t(L.n_dense), int32_t(L.n_sparse), v0, n_vocab, int32_t(p.steps), out);
+  }
+  return hipGetLastError();
+}
+
+// x as the B operand of the logits product.
+hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtype, int64_t ldx, const int64_t* target,
+                     int64_t ignore, char* ws, hipStream_t s, PanelOperand* out) {
+  if (p.f8) {
+    const hyb_f8 X{ws + p.x, ws + p.xs};
+    *out = PanelOperand{ws + p.x, reinterpret_cast<const uint32_t*>(ws + p.xs), int32_t(p.m16), p.m16};
+    return launch_f8_quantize(x, dtype, p.m, p.k, ldx, HYB_F8_ROWS, X, s);
+  }
+  *out = PanelOperand{ws + p.x, nullptr, int32_t(p.m16), 0};
+  hipLaunchKernelGGL(k_xent_pack_x, dim3(unsigned(p.m16 / 16), unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
+                     static_cast<const uint16_t*>(x), ldx, p.m, int32_t(p.steps), target, ignore, ws + p.x);
+  return hipGetLastError();
+}
+
+// The A operand of the logits product for a piece: an 8-bit head's own
+// panels, a packed head's expanded ones.
+PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t v0, int64_t rows, const char* panels) {
+  const int32_t rows16 = int32_t((rows + 15) / 16 * 16);
+  if (!p.f8) return PanelOperand{panels, nullptr, rows16, 0};
+  return PanelOperand{static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep,
+                      static_cast<const uint32_t*>(head.f8->scales) + v0, rows16, f8_rows16(p.n)};
+}
+
+#define HYB_TRY(call)                      \
+  do {                                     \
+    const hipError_t e_ = (call);          \
+    if (e_ != hipSuccess) return e_;       \
+  } while (0)
+
+template <int DT>
+hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int64_t ldx, XentTile t,
+                      float* loss, float* lse, char* ws, hipStream_t s) {
+  int64_t chunks = 0;
+  if (p.rows) {
+    float* z = reinterpret_cast<float*>(ws + p.logits);
+    const int64_t ldz = (p.n + 3) / 4 * 4;
+    if (p.f8) {
+      PanelOperand X;
+      HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+      HYB_TRY(launch_f8_gemm(*head.f8, p.n, p.k, hyb_f8{ws + p.x, ws + p.xs}, p.m, z, HYB_F32, ldz, nullptr, s));
+    } else if (p.m <= kGemvCrossoverM || (p.m <= kMaxGemvM && gemv_preferred(*head.layout, int(p.m)))) {
+      HYB_TRY(launch_gemv(*head.layout, *head.packed, x, int(p.m), ldx, z, HYB_F32, ldz, s));
+    } else {
+      HYB_TRY(launch_gemm(*head.layout, *head.packed, x, int(p.m), ldx, z, HYB_F32, ldz, s, nullptr, 0));
+    }
+    chunks = (n_vocab + 2047) / 2048;
+    hipLaunchKernelGGL(k_xent_rows, dim3(unsigned(chunks), unsigned(p.m)), dim3(256), 0, s, z, ldz, t);
+    HYB_TRY(hipGetLastError());
+  } else {
+    PanelOperand X;
+    HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+    const int64_t step = p.f8 ? n_vocab : p.piece;
+    for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
+      const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
+      if (!p.f8) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, nullptr, ws + p.w, s));
+      t.v0 = v0;
+      const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
+      HYB_TRY((run_tiles<DT, false>(p.f8, p.bp, W, X, int32_t(p.steps), t, s)));
+      chunks = v0 / 256 + (W.rows16 + 255) / 256;
+    }
+  }
+  hipLaunchKernelGGL(k_xent_join, dim3(unsigned(p.m16 / 16)), dim3(1024), 0, s, t.part, chunks, t.m, t.m16, t.zt,
+                     t.target, t.ignore, n_vocab, loss, lse);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int64_t ldx,
+                          XentTile t, void* dx, int64_t lddx, void* dw, int64_t lddw, char* ws, hipStream_t s) {
+  float* gtop = reinterpret_cast<float*>(ws + p.misc);
+  uint32_t* top = reinterpret_cast<uint32_t*>(ws + p.misc + 64);
+  hipLaunchKernelGGL(k_xent_grad_top, dim3(1), dim3(1024), 0, s, t.grad, t.target, t.ignore, t.m, gtop, top);
+  HYB_TRY(hipGetLastError());
+  t.gtop = gtop;
+  if (p.f8 && dx && DT == HYB_F16) {
+    hipLaunchKernelGGL(k_xent_top_scale, dim3(unsigned((n_vocab + 255) / 256), unsigned((p.steps + 3) / 4)), dim3(256),
+                       0, s, static_cast<const uint32_t*>(head.f8->scales), f8_rows16(p.n), n_vocab, int32_t(p.steps),
+                       top);
+    HYB_TRY(hipGetLastError());
+  }
+  PanelOperand X;
+  HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+  const int32_t krows = int32_t(p.ksteps16 * 64);
+  if (dw) {
+    hipLaunchKernelGGL(k_xent_transpose, dim3(unsigned(p.m64 / 64), unsigned(p.ksteps16)), dim3(256), 0, s, ws + p.x,
+                       int32_t(p.m16), int32_t(p.ksteps16), ws + p.xt, int32_t(p.m64 / 64));
+    HYB_TRY(hipGetLastError());
+  }
+  t.g = dx ? ws + p.g : nullptr;
+  t.gt = dw ? ws + p.gt : nullptr;
+  t.gt_steps = int32_t(p.m64 / 64);
+  // dX runs over the vocabulary that counts, dW over every row of the head.
+  const int64_t end = dw ? p.n : n_vocab;
+  for (int64_t v0 = 0; v0 < end; v0 += p.piece) {
+    const int64_t rows = end - v0 < p.piece ? end - v0 : p.piece;
+    const int32_t vsteps = int32_t((rows + 63) / 64);
+    t.v0 = v0;
+    t.g_steps = vsteps;
+    if (!p.f8 || dx) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, top, ws + p.w, s));
+    const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
+    HYB_TRY((run_tiles<DT, true>(p.f8, p.bp, W, X, int32_t(p.steps), t, s)));
+    if (dx) {
+      hipLaunchKernelGGL(k_xent_transpose, dim3(unsigned(vsteps), unsigned(p.ksteps16)), dim3(256), 0, s, ws + p.w,
+                         int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), ws + p.wt, vsteps);
+      HYB_TRY(hipGetLastError());
+      XentOut o{};
+      o.acc = reinterpret_cast<float*>(ws + p.dx);
+      o.ld = krows;
+      o.part = p.m * int64_t(krows);
+      o.first = v0 == 0;
+      o.rows = int32_t(p.m);
+      o.cols = krows;
+      const PanelOperand A{ws + p.wt, nullptr, krows, 0}, B{ws + p.g, nullptr, int32_t(p.m16), 0};
+      HYB_TRY(p.bp == 16 ? (run_product<DT, true, 16, 16, 2, 4>(A, B, vsteps, p.parts, o, s))
+                         : (run_product<DT, true, 16, 4, 4, 2>(A, B, vsteps, p.parts, o, s)));
+    }
+    if (dw) {
+      XentOut o{};
+      o.y = static_cast<uint16_t*>(dw) + v0 * lddw;
+      o.ldy = lddw;
+      o.gtop = gtop;
+      o.rows = int32_t(rows);
+      o.cols = int32_t(p.k);
+      o.live = n_vocab - v0;
+      o.vec = reinterpret_cast<uintptr_t>(dw) % 8 == 0 && lddw % 4 == 0;
+      const PanelOperand A{ws + p.xt, nullptr, krows, 0},
+          B{ws + p.gt, nullptr, int32_t((rows + 15) / 16 * 16), 0};
+      HYB_TRY((run_product<DT, false, 16, 16, 2, 4>(A, B, int32_t(p.m64 / 64), 1, o, s)));
+    }
+  }
+  if (dx) {
+    const dim3 grid(unsigned(p.m), unsigned((p.k + 1023) / 1024));
+    const float* acc = reinterpret_cast<const float*>(ws + p.dx);
+    if (p.f8)
+      hipLaunchKernelGGL((k_xent_dx<DT, true>), grid, dim3(256), 0, s, acc, int64_t(krows), p.m * int64_t(krows),
+                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, t.grad, top, static_cast<uint16_t*>(dx), lddx);
+    else
+      hipLaunchKernelGGL((k_xent_dx<DT, false>), grid, dim3(256), 0, s, acc, int64_t(krows), p.m * int64_t(krows),
+                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, t.grad, top, static_cast<uint16_t*>(dx), lddx);
+    HYB_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_xent(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype, int64_t ldx,
+                       const int64_t* target, int64_t ignore, float* loss, float* lse, char* ws, hipStream_t s) {
+  XentTile t{};
+  t.n_vocab = n_vocab;
+  t.ignore = ignore;
+  t.target = target;
+  t.m = int32_t(p.m);
+  t.m16 = int32_t(p.m16);
+  t.part = reinterpret_cast<float2*>(ws + p.part);
+  t.zt = reinterpret_cast<float*>(ws + p.zt);
+  return dtype == HYB_BF16 ? loss_typed<HYB_BF16>(head, p, n_vocab, x, ldx, t, loss, lse, ws, s)
+                           : loss_typed<HYB_F16>(head, p, n_vocab, x, ldx, t, loss, lse, ws, s);
+}
+
+hipError_t launch_xent_backward(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype,
+                                int64_t ldx, const int64_t* target, int64_t ignore, const float* lse,
+                                const float* grad, void* dx, int64_t lddx, void* dw, int64_t lddw, char* ws,
+                                hipStream_t s) {
+  if (p.m == 0) {
+    hipLaunchKernelGGL(k_xent_zero, dim3(unsigned(p.n), unsigned((p.k + 255) / 256)), dim3(256), 0, s,
+                       static_cast<uint16_t*>(dw), lddw, int32_t(p.k));
+    return hipGetLastError();
+  }
+  XentTile t{};
+  t.n_vocab = n_vocab;
+  t.ignore = ignore;
+  t.target = target;
+  t.m = int32_t(p.m);
+  t.m16 = int32_t(p.m16);
+  t.lse = lse;
+  t.grad = grad;
+  return dtype == HYB_BF16 ? backward_typed<HYB_BF16>(head, p, n_vocab, x, ldx, t, dx, lddx, dw, lddw, ws, s)
+                           : backward_typed<HYB_F16>(head, p, n_vocab, x, ldx, t, dx, lddx, dw, lddw, ws, s);
+}
+
+}  // namespace hyb

@@ -1,0 +1,76 @@
+// Host planning of the cross entropy: pieces of the vocabulary, tile shapes
+// and the workspace.
+#include "hyb_xent_internal.h"
+
+namespace hyb {
+
+namespace {
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+
+}  // namespace
+
+XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
+  XentPlan p{};
+  p.f8 = head.f8 != nullptr;
+  p.n = p.f8 ? head.n : head.layout->n;
+  p.k = p.f8 ? head.k : head.layout->k;
+  p.m = m;
+  p.m16 = up(m, 16);
+  p.m64 = up(m, 64);
+  p.steps = p.f8 ? f8_steps(p.k) : p.k / 64;
+  p.ksteps16 = p.f8 ? 2 * p.steps : p.steps;
+  const bool dx = what & HYB_XENT_DX, dw = what & HYB_XENT_DW;
+  p.rows = !dx && !dw && m <= 64;
+  p.bp = m <= 64 ? 4 : 16;
+  // A piece's 16-bit dz takes at most 256 MiB.
+  p.piece = int64_t(256) << 20;
+  p.piece = p.piece / (2 * (p.m64 > 0 ? p.m64 : 64)) / 256 * 256;
+  if (p.piece < 256) p.piece = 256;
+  if (p.piece > 32768) p.piece = 32768;
+  if (p.piece > up(p.n, 256)) p.piece = up(p.n, 256);
+  p.chunks = p.rows ? up(p.n, 2048) / 2048 : up(p.n, 256) / 256;
+  p.parts = 1;
+  if (dx) {
+    // The dX product has (k / 256) x (m / 256) tiles; its vocabulary is cut
+    // until the tiles fill the compute units.
+    const int64_t tiles = up(p.ksteps16 * 64, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp));
+    while (tiles * p.parts * 2 <= cus && p.parts < 32) p.parts *= 2;
+  }
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at += size_t(up(bytes, 256));
+    return here;
+  };
+  const int64_t krows = p.ksteps16 * 64;
+  if (p.f8) {
+    p.x = take(p.m16 * p.steps * 128);
+    p.xs = take((p.steps + 3) / 4 * p.m16 * 4);
+  } else if (!p.rows) {
+    p.x = take(p.m16 * p.k * 2);
+  }
+  p.misc = take(256);
+  if (!dx && !dw) {
+    p.part = take(p.chunks * p.m16 * 8);
+    p.zt = take(p.m16 * 4);
+  }
+  if (p.rows) {
+    p.logits = take(m * up(p.n, 4) * 4);
+  } else if (!p.f8 || dx) {
+    p.w = take(p.piece * krows * 2);
+  }
+  if (dx) {
+    p.wt = take(p.piece * krows * 2);
+    p.g = take(p.m16 * p.piece * 2);
+    p.dx = take(int64_t(p.parts) * m * krows * 4);
+  }
+  if (dw) {
+    p.gt = take(p.piece * p.m64 * 2);
+    p.xt = take(krows * p.m64 * 2);
+  }
+  p.total = at;
+  return p;
+}
+
+}  // namespace hyb
