@@ -23,9 +23,10 @@
  * [0, n_vocab) makes that token's loss and dX row, and dW, NaN.
  *
  * Products are exact and summed in fp32, softmax sums are fp32.  In the
- * backward pass dz / grad is rounded once to the 16-bit type of the
- * products (bf16, or fp16 scaled by 2^14 so that probabilities down to 4e-9
- * keep 11 bits) and both gradients are summed in fp32 and rounded once.
+ * backward pass dz is rounded once to the 16-bit type of the products (bf16;
+ * or fp16, scaled by 2^14 over the largest |grad| rounded up to a power of two,
+ * so that a dz of 4e-9 of that grad keeps 11 bits) and both gradients are
+ * summed in fp32 and rounded once.
  * The vocabulary is worked through in pieces; the logits of a piece live in
  * registers (or, for few tokens, in the workspace).
  *

@@ -250,11 +250,11 @@ __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, 
 // from memory to the operand registers.  Bound by the read of w, so the wide
 // kind costs nothing here and serves every output type.
 template <int BP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOperand X, int32_t steps, F8Out out) {
+__global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOperand X, F8Out out) {
   __shared__ f32x4_t part[WAVES][BP][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t pw = int32_t(blockIdx.x), px = int32_t(blockIdx.y) * BP;
+  const int32_t pw = int32_t(blockIdx.x), px = int32_t(blockIdx.y) * BP, steps = W.steps;
   const int64_t pitch = int64_t(steps) * kPanelStep;
   // One resource per panel, ending with it: steps behind the last are zeros.
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(W.data + pw * pitch, int32_t(pitch));
@@ -313,14 +313,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
 }
 
 template <int KIND, int AP, int BP, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelOperand X, int32_t steps, F8Out out) {
+__global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelOperand X, F8Out out) {
   typedef PanelTile<KIND, AP, BP, WA, WB> T;
   extern __shared__ __attribute__((aligned(1024))) char f8_smem[];
   const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
   int32_t ab, bb;
   panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
   f32x4_t acc[T::kA][T::kB];
-  T::run(W, X, steps, ab * AP, bb * BP, 0, steps, f8_smem, acc);
+  T::run(W, X, ab * AP, bb * BP, 0, W.steps, f8_smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave % WA, wb = wave / WA;
 #pragma unroll
@@ -338,14 +338,13 @@ __global__ __launch_bounds__(256) void k_f8_zero(F8Out o) {
 }
 
 template <int KIND, int AP, int BP, int WA, int WB>
-hipError_t launch_tile(const PanelOperand& W, const PanelOperand& X, int32_t steps, const F8Out& o, hipStream_t s) {
+hipError_t launch_tile(const PanelOperand& W, const PanelOperand& X, const F8Out& o, hipStream_t s) {
   typedef PanelTile<KIND, AP, BP, WA, WB> T;
   const void* fn = reinterpret_cast<const void*>(&k_f8_tile<KIND, AP, BP, WA, WB>);
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
-  hipLaunchKernelGGL((k_f8_tile<KIND, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB), T::kLds, s, W, X, steps,
-                     o);
+  hipLaunchKernelGGL((k_f8_tile<KIND, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB), T::kLds, s, W, X, o);
   return hipGetLastError();
 }
 
@@ -406,27 +405,27 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
     hipLaunchKernelGGL(k_f8_zero, dim3(unsigned((n * m + 255) / 256)), dim3(256), 0, s, o);
     return hipGetLastError();
   }
-  const PanelOperand W{static_cast<const char*>(w.codes), static_cast<const uint32_t*>(w.scales),
-                       int32_t(f8_rows16(n)), f8_rows16(n)};
-  const PanelOperand X{static_cast<const char*>(x.codes), static_cast<const uint32_t*>(x.scales),
-                       int32_t(f8_rows16(m)), f8_rows16(m)};
   const int32_t steps = int32_t(f8_steps(k));
+  const PanelOperand W{static_cast<const char*>(w.codes), int32_t(f8_rows16(n)), steps,
+                       static_cast<const uint32_t*>(w.scales), f8_rows16(n)};
+  const PanelOperand X{static_cast<const char*>(x.codes), int32_t(f8_rows16(m)), steps,
+                       static_cast<const uint32_t*>(x.scales), f8_rows16(m)};
   const F8Route r = f8_route(n, k, m, device_cus());
   (void)ws;
   if (r.waves) {
     const dim3 grid(unsigned(W.rows16 / 16), unsigned((X.rows16 / 16 + r.bp - 1) / r.bp));
     if (r.bp == 1)
-      hipLaunchKernelGGL((k_f8_rows<1, 8>), grid, dim3(512), 0, s, W, X, steps, o);
+      hipLaunchKernelGGL((k_f8_rows<1, 8>), grid, dim3(512), 0, s, W, X, o);
     else if (r.bp == 2)
-      hipLaunchKernelGGL((k_f8_rows<2, 8>), grid, dim3(512), 0, s, W, X, steps, o);
+      hipLaunchKernelGGL((k_f8_rows<2, 8>), grid, dim3(512), 0, s, W, X, o);
     else
-      hipLaunchKernelGGL((k_f8_rows<4, 8>), grid, dim3(512), 0, s, W, X, steps, o);
+      hipLaunchKernelGGL((k_f8_rows<4, 8>), grid, dim3(512), 0, s, W, X, o);
     return hipGetLastError();
   }
   const bool wide = y_dtype == HYB_F32;  // kF8Wide
   if (r.ap == 16)
-    return wide ? launch_tile<kF8Wide, 16, 16, 2, 4>(W, X, steps, o, s) : launch_tile<kF8, 16, 16, 2, 4>(W, X, steps, o, s);
-  return wide ? launch_tile<kF8Wide, 8, 8, 2, 2>(W, X, steps, o, s) : launch_tile<kF8, 8, 8, 2, 2>(W, X, steps, o, s);
+    return wide ? launch_tile<kF8Wide, 16, 16, 2, 4>(W, X, o, s) : launch_tile<kF8, 16, 16, 2, 4>(W, X, o, s);
+  return wide ? launch_tile<kF8Wide, 8, 8, 2, 2>(W, X, o, s) : launch_tile<kF8, 8, 8, 2, 2>(W, X, o, s);
 }
 
 }  // namespace hyb

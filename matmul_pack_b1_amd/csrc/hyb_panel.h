@@ -1,22 +1,31 @@
 // Matrix product of two operands held in panels, Y[j, i] = sum_k A[i, k] B[j, k],
-// shared by the 8-bit block-scaled product and the cross entropy's gradients.
+// shared by the 8-bit block-scaled product and the cross entropy.
 //
 // A panel is 16 rows; a step of a panel is 2 KiB: 128 columns of 8-bit codes
-// or 64 columns of 16-bit values, in two halves of 1 KiB of which lane L of a
-// wavefront owns the 16 bytes at 16 L:
-//   row L%16, columns 64 h + 16 (L/16) + 0..15   (8 bits, half h)
-//   row L%16, columns 32 h +  8 (L/16) + 0..7    (16 bits, half h)
-// The halves are the operand registers of the 16x16x128 (two halves) and
-// 16x16x32 (one half) matrix instructions, so a tile goes from memory to LDS
-// as it lies and every LDS read is 64 lanes over 1 KiB without a bank
-// conflict.  (Which columns a lane holds does not matter to the sum as long
-// as both operands agree.)  Panel p's steps are contiguous, at
-// (p * steps + s) * 2048.
+// or 64 columns of 16-bit values, in two halves of 1 KiB of four 256-byte
+// units g of 16 bytes for each row r:
+//   8 bits   half h, unit g, row r: columns 64 h + 16 g + 0..15 at 256 g + 16 r
+//   16 bits  columns 32 h + 8 g + 0..7 at 256 g + 16 (r ^ 8 (g & 1))
+// Lane L of a wavefront takes row L%16 and unit L/16, which makes a half the
+// operand of a 16x16x32 matrix instruction (16 bits) and two halves that of a
+// 16x16x128 one (8 bits): a tile goes from memory to LDS as it lies and every
+// LDS read is 64 lanes over 1 KiB without a bank conflict.  (Which columns a
+// lane holds does not matter to the sum as long as both operands agree.)
+// Panel p's steps are contiguous, at (p * steps + s) * 2048.
+//
+// A 16-bit operand may also be read the other way round, its columns as the
+// product's rows and its rows as the summed index, with the transposing LDS
+// read (ds_read_b64_tr_b16: of 16 lanes, lane 4 i + c points at the four
+// columns 4 c.. of row i and lane j receives column j of rows 0..3).  The
+// exchange of rows 0..7 and 8..15 in odd units puts the eight 64-byte pieces
+// of 32 lanes on different banks.  A lane then holds, of the 32 rows of a
+// half step, rows 16 (q/2) + 4 (q%2) + {0..3, 8..11}, q = L/16; where the other
+// operand is read straight, its columns are stored in that order.
 //
 // 8-bit operands carry one exponent byte per row and step (E8M0: 2^(byte -
-// 127)), four steps to a 32-bit word, word (s / 4) * rows16 + row; the matrix
-// instruction takes the word of its lane's row as it is and multiplies the
-// products of a step by both operands' powers of two.
+// 127)), four steps to a 32-bit word, word (s / 4) * scale_pitch + row; the
+// matrix instruction takes the word of its lane's row as it is and multiplies
+// the products of a step by both operands' powers of two.
 #ifndef HYB_PANEL_H_
 #define HYB_PANEL_H_
 
@@ -46,8 +55,9 @@ constexpr bool is_f8(int kind) { return kind <= 0; }
 
 struct PanelOperand {
   const char* data;
-  const uint32_t* scale;  // 8-bit operands only
   int32_t rows16;         // rows rounded up to 16 (the panels that exist)
+  int32_t steps;          // steps per panel
+  const uint32_t* scale;  // 8-bit operands only
   int64_t scale_pitch;    // words from four steps' scales to the next four's
 };
 
@@ -143,64 +153,142 @@ __device__ __forceinline__ void panel_block(int32_t id, int32_t total, int32_t n
   ab = first + r % width;
 }
 
+// Byte offset of a lane's 16 bytes within a half.
+template <int KIND>
+__device__ __forceinline__ int panel_lane(int lane) {
+  return is_f8(KIND) ? lane * 16 : (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
+}
+
+typedef __attribute__((ext_vector_type(4))) short i16x4_t;
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
 // LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, two LDS
-// stages of one step each.
-template <int KIND, int AP, int BP, int WA, int WB>
+// stages of one step each.  TA / TB: that operand is read transposed (its
+// "panels" here are blocks of 16 of its columns).
+template <int KIND, int AP, int BP, int WA, int WB, bool TA = false, bool TB = false>
 struct PanelTile {
   static constexpr int kWaves = WA * WB;
   static constexpr int kA = AP / WA, kB = BP / WB;  // panels per wavefront
   static constexpr int kStage = (AP + BP) * 2048;
   static constexpr int kScaleStage = is_f8(KIND) ? (AP + BP) * 64 : 0;  // a word per row, four steps
   static constexpr int kLds = 2 * kStage + 2 * kScaleStage;
-  static constexpr int kLoads = (AP + BP) * 2 / kWaves;  // 1 KiB transfers per wavefront and step
-  static_assert(AP % WA == 0 && BP % WB == 0 && (AP + BP) * 2 % kWaves == 0, "even split");
+  static constexpr int kLoadsA = AP * 2 / kWaves, kLoadsB = BP * 2 / kWaves;  // 1 KiB transfers per wavefront and step
+  static_assert(AP % WA == 0 && BP % WB == 0 && AP * 2 % kWaves == 0 && BP * 2 % kWaves == 0, "even split");
+  static_assert(!(TA || TB) || !is_f8(KIND), "8-bit operands are read straight");
+
+  // One operand's transfers of step s into its part of a stage.
+  template <bool T, int P, int LOADS>
+  struct Feed {
+    srd4_t rsrc;
+    const char* data;
+    int64_t pitch, total;
+    int32_t first;
+
+    // Straight: panels p0.., the resource ends with the last panel (panels
+    // behind it read as zeros).  Transposed: columns 16 p0.. of all panels; a
+    // step is four panels, the resource moves with it and ends with the
+    // operand (rows behind the last panel read as zeros; columns behind the
+    // last step are the next panel's, of outputs that do not exist).
+    __device__ Feed(const PanelOperand& o, int32_t p0) {
+      pitch = int64_t(o.steps) * 2048;
+      data = o.data;
+      first = p0;
+      total = int64_t(o.rows16 / 16) * pitch;
+      if constexpr (!T) {
+        const int32_t n = o.rows16 / 16 - p0 < P ? o.rows16 / 16 - p0 : P;
+        rsrc = panel_srd(data + p0 * pitch, uint32_t(n * pitch));
+      }
+    }
+    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
+      if constexpr (T) {
+        constexpr int kChunks = P / 2;  // 32-column halves per panel
+        const int64_t off = s * 4 * pitch + first * 512;
+        const int64_t left = total - off;
+        const srd4_t r = panel_srd(data + off, uint32_t(left < 0 ? 0 : left < (int64_t(1) << 31) ? left : (int64_t(1) << 31)));
+#pragma unroll
+        for (int t = 0; t < LOADS; ++t) {
+          const int c = wave * LOADS + t;
+          panel_dma16(r, dst + c * 1024, int32_t(c / kChunks * pitch) + c % kChunks * 1024 + lane * 16);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < LOADS; ++t) {
+          const int c = wave * LOADS + t;  // panel c / 2, half c % 2
+          panel_dma16(rsrc, dst + c * 1024, int32_t((c >> 1) * pitch) + s * 2048 + (c & 1) * 1024 + lane * 16);
+        }
+      }
+    }
+  };
+
+  // The two halves of panel p (of P) of a staged step.
+  struct Halves {
+    u32x4_t v[2];
+  };
+  template <bool T, int P>
+  __device__ __forceinline__ static Halves read(const char* src, int p, int lane_off, int turn0, int turn1) {
+    Halves r;
+    if constexpr (T) {
+      const char* c = src + (p >> 1) * 1024 + (p & 1) * 512;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const char* b = c + 2 * h * (P / 2) * 1024;
+        const uint2 lo = __builtin_bit_cast(
+            uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(const_cast<char*>(b + turn0))));
+        const uint2 hi = __builtin_bit_cast(
+            uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(const_cast<char*>(b + turn1))));
+        r.v[h] = u32x4_t{lo.x, lo.y, hi.x, hi.y};
+      }
+    } else {
+      const char* b = src + p * 2048 + lane_off;
+      r.v[0] = *reinterpret_cast<const u32x4_t*>(b);
+      r.v[1] = *reinterpret_cast<const u32x4_t*>(b + 1024);
+    }
+    return r;
+  }
+
+  // Lane offsets of the two transposing reads of a half: panel q/2 of the
+  // half's two, rows 4 (q%2) + i (+ 8), columns 4 c.. of the block's 16.
+  template <int P>
+  __device__ __forceinline__ static int turn(int lane, int part) {
+    const int q = lane >> 4, i = (lane & 15) >> 2, c = lane & 3;
+    return (q >> 1) * (P / 2) * 1024 + (c >> 1) * 256 + (4 * (q & 1) + i + 8 * (part ^ (c >> 1))) * 16 + (c & 1) * 8;
+  }
 
   // Sums of steps [s0, s1), s0 a multiple of four, of A panels pa.. and B
-  // panels pb..; wavefront
-  // (wa, wb) ends with acc[i][j] of its panels pa + wa kA + i, pb + wb kB + j
-  // (lane L: A rows 4 (L/16) + 0..3, B row L%16).
-  __device__ static void run(const PanelOperand& A, const PanelOperand& B, int32_t steps, int32_t pa, int32_t pb,
-                             int32_t s0, int32_t s1, char* smem, f32x4_t (&acc)[kA][kB]) {
+  // panels pb..; wavefront (wa, wb) ends with acc[i][j] of its panels
+  // pa + wa kA + i, pb + wb kB + j (lane L: A rows 4 (L/16) + 0..3, B row L%16).
+  __device__ static void run(const PanelOperand& A, const PanelOperand& B, int32_t pa, int32_t pb, int32_t s0,
+                             int32_t s1, char* smem, f32x4_t (&acc)[kA][kB]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wa = wave % WA, wb = wave / WA;
-    const int64_t pitch = int64_t(steps) * 2048;
-    // Resources end with the operand's last panel: panels behind it read as zeros.
-    const int32_t va = A.rows16 / 16 - pa < AP ? A.rows16 / 16 - pa : AP;
-    const int32_t vb = B.rows16 / 16 - pb < BP ? B.rows16 / 16 - pb : BP;
-    const srd4_t ra = panel_srd(A.data + pa * pitch, uint32_t(va * pitch));
-    const srd4_t rb = panel_srd(B.data + pb * pitch, uint32_t(vb * pitch));
+    const Feed<TA, AP, kLoadsA> fa(A, pa);
+    const Feed<TB, BP, kLoadsB> fb(B, pb);
     const uint32_t base = panel_lds_addr(smem);
+    const int straight = panel_lane<KIND>(lane);
+    const int ta0 = turn<AP>(lane, 0), ta1 = turn<AP>(lane, 1);
+    const int tb0 = turn<BP>(lane, 0), tb1 = turn<BP>(lane, 1);
 
     auto issue = [&](int32_t s, int stage) {
       const uint32_t dst = base + stage * kStage;
-#pragma unroll
-      for (int t = 0; t < kLoads; ++t) {
-        const int c = wave * kLoads + t;  // 1 KiB piece: panel c / 2, half c % 2
-        const int p = c >> 1;
-        const bool is_a = p < AP;
-        const int32_t off = int32_t((is_a ? p : p - AP) * pitch) + s * 2048 + (c & 1) * 1024;
-        if (is_a)
-          panel_dma16(ra, dst + c * 1024, off + lane * 16);
-        else
-          panel_dma16(rb, dst + c * 1024, off + lane * 16);
-      }
+      fa.issue(s, dst, wave, lane);
+      fb.issue(s, dst + AP * 2048, wave, lane);
       if constexpr (is_f8(KIND)) {
-        // the scale words of steps s .. s+3, once per four steps (s counts
-        // from a multiple of four): AP * 64 + BP * 64 bytes in 1 KiB pieces
+        // the scale words of steps s .. s+3: AP * 64 + BP * 64 bytes
         if ((s & 3) == 0) {
           const uint32_t sdst = base + 2 * kStage + ((s >> 2) & 1) * kScaleStage;
           const int64_t word = int64_t(s >> 2);
           if (wave == 0) {
-            const srd4_t sa = panel_srd(A.scale + word * A.scale_pitch + pa * 16, uint32_t(va * 64));
+            const int32_t n = A.rows16 - pa * 16 < AP * 16 ? A.rows16 - pa * 16 : AP * 16;
+            const srd4_t sa = panel_srd(A.scale + word * A.scale_pitch + pa * 16, uint32_t(n * 4));
             for (int c = 0; c * 1024 < AP * 64; ++c)
               if (lane * 16 + c * 1024 < AP * 64) panel_dma16(sa, sdst + c * 1024, lane * 16 + c * 1024);
           }
           if (wave == kWaves - 1) {
-            const srd4_t sb = panel_srd(B.scale + word * B.scale_pitch + pb * 16, uint32_t(vb * 64));
+            const int32_t n = B.rows16 - pb * 16 < BP * 16 ? B.rows16 - pb * 16 : BP * 16;
+            const srd4_t sb = panel_srd(B.scale + word * B.scale_pitch + pb * 16, uint32_t(n * 4));
             for (int c = 0; c * 1024 < BP * 64; ++c)
-              if (lane * 16 + c * 1024 < BP * 64)
-                panel_dma16(sb, sdst + AP * 64 + c * 1024, lane * 16 + c * 1024);
+              if (lane * 16 + c * 1024 < BP * 64) panel_dma16(sb, sdst + AP * 64 + c * 1024, lane * 16 + c * 1024);
           }
         }
       }
@@ -217,9 +305,14 @@ struct PanelTile {
 #pragma unroll
     for (int j = 0; j < kB; ++j) scb[j] = 0;
 
-    auto compute = [&](int32_t s, int stage, auto byte) {
+    // Multiplies the staged step s and, once its first reads are under way,
+    // starts the next step's transfers.  The reads of A panel i + 1 are issued
+    // ahead of panel i's products, so that an LDS round trip hides behind
+    // them (the scheduling barriers keep the compiler from moving them back).
+    auto compute = [&](int32_t s, int stage, auto byte, bool more) {
       constexpr int kByte = decltype(byte)::value;
-      const char* src = smem + stage * kStage + lane * 16;
+      const char* src = smem + stage * kStage;
+      const char* srcb = src + AP * 2048;
       if constexpr (is_f8(KIND)) {
         if (kByte == 0) {
           const char* sc = smem + 2 * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
@@ -229,27 +322,29 @@ struct PanelTile {
           for (int j = 0; j < kB; ++j) scb[j] = *reinterpret_cast<const uint32_t*>(sc + (AP + wb * kB + j) * 64);
         }
       }
+      Halves a = read<TA, AP>(src, wa * kA, straight, ta0, ta1);
+      Halves braw[kB];
+#pragma unroll
+      for (int j = 0; j < kB; ++j) braw[j] = read<TB, BP>(srcb, wb * kB + j, straight, tb0, tb1);
+      if (more) issue(s + 1, stage ^ 1);
       PanelRegs<KIND> b[kB];
 #pragma unroll
-      for (int j = 0; j < kB; ++j) {
-        const char* p = src + (AP + wb * kB + j) * 2048;
-        b[j] = panel_regs<KIND, kByte>(*reinterpret_cast<const u32x4_t*>(p),
-                                       *reinterpret_cast<const u32x4_t*>(p + 1024), scb[j]);
-      }
+      for (int j = 0; j < kB; ++j) b[j] = panel_regs<KIND, kByte>(braw[j].v[0], braw[j].v[1], scb[j]);
 #pragma unroll
       for (int i = 0; i < kA; ++i) {
-        const char* p = src + (wa * kA + i) * 2048;
-        const PanelRegs<KIND> a = panel_regs<KIND, kByte>(*reinterpret_cast<const u32x4_t*>(p),
-                                                          *reinterpret_cast<const u32x4_t*>(p + 1024), sca[i]);
+        const Halves was = a;
+        if (i + 1 < kA) a = read<TA, AP>(src, wa * kA + i + 1, straight, ta0, ta1);
+        const PanelRegs<KIND> now = panel_regs<KIND, kByte>(was.v[0], was.v[1], sca[i]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(a, b[j], acc[i][j], sca[i], scb[j]);
+        for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(now, b[j], acc[i][j], sca[i], scb[j]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // A step waits for its own transfers, meets the other wavefronts (whose
-    // reads of the other stage are then done too), starts the next step's
-    // transfers into the other stage and multiplies.  Unrolled by four so
-    // that stage and scale byte are immediates.
+    // A step waits for its own transfers and meets the other wavefronts (whose
+    // reads of the other stage are then done too).  Unrolled by four so that
+    // stage and scale byte are immediates.
     if (s0 >= s1) return;
     issue(s0, 0);
     for (int32_t q = s0; q < s1; q += 4) {
@@ -259,8 +354,7 @@ struct PanelTile {
         if (s >= s1) return;
         panel_wait<0>();
         __syncthreads();
-        if (s + 1 < s1) issue(s + 1, (kByte + 1) & 1);
-        compute(s, kByte & 1, byte);
+        compute(s, kByte & 1, byte, s + 1 < s1);
       };
       one(std::integral_constant<int, 0>());
       one(std::integral_constant<int, 1>());

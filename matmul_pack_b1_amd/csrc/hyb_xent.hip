@@ -5,10 +5,10 @@
 // Z = W' X^T leaves, per token, the maximum and the sum of exponentials of
 // its entries (and the target's logit); a second kernel joins them to lse.
 // Gradient: the same tiles, recomputed, become G = softmax - onehot in
-// registers and leave as 16-bit panels, once with tokens as rows (for dX = G
-// W', summed over pieces in fp32) and once with entries as rows (for dW =
-// G^T X).  All products run on the panel tiles of hyb_panel.h; what they
-// need in the other orientation (W'^T, X^T) is transposed panel by panel.
+// registers and leave as 16-bit panels, from which dX = G W' (summed over
+// pieces in fp32) and dW = G^T X follow.  All products run on the panel tiles
+// of hyb_panel.h; the operands that the gradients need the other way round
+// (W', X and, for dW, G) are transposed on their way out of LDS.
 #include <type_traits>
 
 #include "hyb_panel.h"
@@ -46,17 +46,17 @@ __global__ __launch_bounds__(256) void k_xent_pack_x(const uint16_t* __restrict_
   for (int h = 0; h < 2; ++h) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (live) u = *reinterpret_cast<const uint4*>(x + row * ldx + s * 64 + h * 32 + (lane >> 4) * 8);
-    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16) = u;
+    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + panel_lane<HYB_BF16>(lane)) = u;
   }
 }
 
 // Sixteen columns 16 q.. of a row (q = lane / 16) as the two 16-byte pieces of
-// the panel order: half q / 2, lane groups 2 (q % 2) and 2 (q % 2) + 1.
+// the panel order: half q / 2, units 2 (q % 2) and 2 (q % 2) + 1.
 __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t (&e)[8]) {
-  const int q = lane >> 4;
-  char* p = step + (q >> 1) * 1024 + (2 * (q & 1)) * 256 + (lane & 15) * 16;
-  *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
-  *reinterpret_cast<uint4*>(p + 256) = make_uint4(e[4], e[5], e[6], e[7]);
+  const int q = lane >> 4, r = lane & 15;
+  char* p = step + (q >> 1) * 1024 + (2 * (q & 1)) * 256;
+  *reinterpret_cast<uint4*>(p + r * 16) = make_uint4(e[0], e[1], e[2], e[3]);
+  *reinterpret_cast<uint4*>(p + 256 + (r ^ 8) * 16) = make_uint4(e[4], e[5], e[6], e[7]);
 }
 
 // Rows v0.. of a packed matrix as panels (one wavefront per panel and step):
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ d
     const uint4* src = dense + (int64_t(ti) * b1 * b2 + int64_t(rs) * 16 * b2 + c * 1024) / 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint4*>(dst + h * 1024 + lane * 16) = row_ok ? src[h * 64 + lane] : zero;
+      *reinterpret_cast<uint4*>(dst + h * 1024 + panel_lane<HYB_BF16>(lane)) = row_ok ? src[h * 64 + lane] : zero;
     return;
   }
   uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -176,40 +176,6 @@ __global__ __launch_bounds__(256) void k_xent_widen(const char* __restrict__ cod
   }
 }
 
-// Panels of A (rows16 rows, `steps` steps of 64 columns) as panels of A^T:
-// 64 * steps rows of ceil(rows16 / 64) steps, zeros behind A's rows.  One
-// workgroup per 64 x 64 block, through LDS; the row pitch of 136 bytes puts
-// the four lane groups of a column read on different banks.
-__global__ __launch_bounds__(256) void k_xent_transpose(const char* __restrict__ in, int32_t rows16, int32_t steps,
-                                                        char* __restrict__ out, int32_t out_steps) {
-  constexpr int kPitch = 136;
-  __shared__ __attribute__((aligned(16))) char tile[64 * kPitch];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t rb = int32_t(blockIdx.x), s = int32_t(blockIdx.y);
-  const int64_t panel = int64_t(rb) * 4 + wave;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (panel * 16 < rows16) u = *reinterpret_cast<const uint4*>(in + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16);
-    char* p = tile + (wave * 16 + (lane & 15)) * kPitch + h * 64 + (lane >> 4) * 16;
-    *reinterpret_cast<uint2*>(p) = make_uint2(u.x, u.y);
-    *reinterpret_cast<uint2*>(p + 8) = make_uint2(u.z, u.w);
-  }
-  __syncthreads();
-  const int64_t orow = int64_t(s) * 4 + wave;  // output panel: columns 16 wave.. of this step
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const char* p = tile + (h * 32 + (lane >> 4) * 8 + 2 * i) * kPitch + (wave * 16 + (lane & 15)) * 2;
-      e[i] = *reinterpret_cast<const uint16_t*>(p) | uint32_t(*reinterpret_cast<const uint16_t*>(p + kPitch)) << 16;
-    }
-    *reinterpret_cast<uint4*>(out + (orow * out_steps + rb) * kPanelStep + h * 1024 + lane * 16) =
-        make_uint4(e[0], e[1], e[2], e[3]);
-  }
-}
-
 // --------------------------------------------------------------- the logits --
 
 struct XentTile {
@@ -224,31 +190,29 @@ struct XentTile {
   const float* lse;
   const float* grad;
   const float* gtop;  // power of two >= max |grad|
-  char* g;            // panels of G: tokens x entries of the piece (or NULL)
-  char* gt;           // panels of G^T diag(grad / gtop): entries x tokens (or NULL)
-  int32_t g_steps, gt_steps;
+  char* g;            // panels of diag(grad / gtop) G: tokens x entries of the piece
+  int32_t g_steps;
 };
 
 // One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
-// leaves the softmax sums, true the two forms of G.
+// leaves the softmax sums, true G.
 template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, int32_t steps,
-                                                            XentTile t) {
+__global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, XentTile t) {
   typedef PanelTile<KIND, AP, BP, WA, WB> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
   int32_t ab, bb;
   panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
   f32x4_t acc[T::kA][T::kB];
-  T::run(W, X, steps, ab * AP, bb * BP, 0, steps, xent_smem, acc);
+  T::run(W, X, ab * AP, bb * BP, 0, W.steps, xent_smem, acc);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave % WA, wb = wave / WA;
   // entry of acc[i][.][e]: vbase + 16 i + e; token of acc[.][j]: tbase + 16 j
   const int64_t vbase = t.v0 + int64_t(ab * AP + wa * T::kA) * 16 + (lane >> 4) * 4;
   const int32_t tbase = (bb * BP + wb * T::kB) * 16 + (lane & 15);
-  __syncthreads();  // the tile's LDS stages are free
   if constexpr (!GRAD) {
+    __syncthreads();  // the tile's LDS stages are free
     float2* sums = reinterpret_cast<float2*>(xent_smem);  // [WA][16 BP]
 #pragma unroll
     for (int j = 0; j < T::kB; ++j) {
@@ -294,9 +258,6 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
     }
   } else {
     const float gtop = *t.gtop;
-    // per wavefront: 16 entries x 32 tokens of G^T, 80-byte rows
-    constexpr int kPitch = 80;
-    char* turn = xent_smem + wave * 16 * kPitch;
 #pragma unroll
     for (int j = 0; j < T::kB; ++j) {
       const int32_t tok = tbase + 16 * j;
@@ -304,56 +265,28 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
       const bool seen = tok < t.m && want != t.ignore;
       const bool valid = want >= 0 && want < t.n_vocab;
       const float lse = seen ? t.lse[tok] : 0.f;
+      const float f = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
 #pragma unroll
       for (int i = 0; i < T::kA; ++i) {
         uint16_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t v = vbase + 16 * i + e;
-          float p = fast_exp(acc[i][j][e] - lse) - (v == want ? 1.f : 0.f);
+          float p = (fast_exp(acc[i][j][e] - lse) - (v == want ? 1.f : 0.f)) * f;
           if (!valid) p = __builtin_nanf("");
           if (!seen || v >= t.n_vocab) p = 0.f;
-          acc[i][j][e] = p;
-          h[e] = round16<DT>(p * g_scale<DT>());
+          h[e] = round16<DT>(p);
         }
-        // row tok % 16 of token panel tok / 16, entries 16 i.. of this wavefront
-        const int32_t col = (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4;
-        if (t.g && tok < t.m16 && col < t.g_steps * 64)
+        // Row tok % 16 of panel tok / 16.  The four entries 16 i + 4 q + e,
+        // q = lane / 16, lie where a lane of the dX product that reads W'
+        // transposed holds the same rows of W': unit 2 (i % 2) + q % 2, half
+        // q / 2 of its 16 bytes.
+        const int32_t col = (ab * AP + wa * T::kA + i) * 16;
+        const int q = lane >> 4, u = 2 * ((col >> 4) & 1) + (q & 1);
+        if (tok < t.m16 && col < t.g_steps * 64)
           *reinterpret_cast<uint2*>(t.g + (int64_t(tok >> 4) * t.g_steps + (col >> 6)) * kPanelStep +
-                                    ((col & 32) >> 5) * 1024 + ((col & 31) >> 3) * 256 + (tok & 15) * 16 + (col & 7) * 2) =
+                                    ((col & 32) >> 5) * 1024 + u * 256 + ((tok & 15) ^ (8 * (u & 1))) * 16 + (q >> 1) * 8) =
               make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
-      }
-    }
-    if (t.gt) {
-#pragma unroll
-      for (int jj = 0; jj < T::kB; jj += 2) {
-        float f[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int32_t tok = tbase + 16 * (jj + j);
-          const bool seen = tok < t.m && t.target[tok < t.m ? tok : 0] != t.ignore;
-          f[j] = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
-        }
-        const int32_t tok0 = (bb * BP + wb * T::kB + jj) * 16;
-#pragma unroll
-        for (int i = 0; i < T::kA; ++i) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // an ignored token's 0 stays 0 whatever its grad
-              *reinterpret_cast<uint16_t*>(turn + ((lane >> 4) * 4 + e) * kPitch + (16 * j + (lane & 15)) * 2) =
-                  round16<DT>(acc[i][jj + j][e] * f[j]);
-            }
-          // one wavefront writes and reads `turn`: its own accesses done suffices
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          const int32_t row = (ab * AP + wa * T::kA + i) * 16;
-          const uint4 u = *reinterpret_cast<const uint4*>(turn + (lane & 15) * kPitch + (lane >> 4) * 16);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          if (row < W.rows16 && tok0 < t.gt_steps * 64)
-            *reinterpret_cast<uint4*>(t.gt + (int64_t(row >> 4) * t.gt_steps + (tok0 >> 6)) * kPanelStep +
-                                      ((tok0 & 32) >> 5) * 1024 + lane * 16) = u;
-        }
       }
     }
   }
@@ -478,14 +411,17 @@ struct XentOut {
   int vec;
 };
 
-// Y[b, a] = sum over steps of A's panels with B's; DX: fp32, this workgroup's
-// part of the steps, stored or added; else 16-bit, scaled back by gtop.
+// DX: Y[token, column] = sum over the piece's entries of G W' (A = W' read
+// transposed, B = G), fp32, this workgroup's part of the steps, stored or
+// added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
+// transposed), 16-bit, scaled back by gtop.
 template <int DT, bool DX, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
-  typedef PanelTile<DT, AP, BP, WA, WB> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, true, !DX> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
-  const int32_t na = (A.rows16 + 16 * AP - 1) / (16 * AP), nb = (B.rows16 + 16 * BP - 1) / (16 * BP);
+  const int32_t na = (A.steps * 4 + AP - 1) / AP;
+  const int32_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
   int32_t ab, bb;
   const int32_t part = int32_t(blockIdx.y);
   panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
@@ -493,13 +429,15 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
   const int32_t s0 = int32_t(int64_t(quads) * part / parts) * 4;
   const int32_t s1 = part + 1 == parts ? steps : int32_t(int64_t(quads) * (part + 1) / parts) * 4;
   f32x4_t acc[T::kA][T::kB];
-  T::run(A, B, steps, ab * AP, bb * BP, s0, s1, xent_smem, acc);
+  T::run(A, B, ab * AP, bb * BP, s0, s1, xent_smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave % WA, wb = wave / WA;
   const float back = DX ? 1.f : *o.gtop / g_scale<DT>();
 #pragma unroll
   for (int j = 0; j < T::kB; ++j) {
-    const int32_t row = (bb * BP + wb * T::kB + j) * 16 + (lane & 15);
+    // dW: G's entries 4..7 and 8..11 of 16 have changed places
+    const int r16 = DX ? lane & 15 : (lane & 3) | (lane & 4) << 1 | (lane & 8) >> 1;
+    const int32_t row = (bb * BP + wb * T::kB + j) * 16 + r16;
     if (row >= o.rows) continue;
 #pragma unroll
     for (int i = 0; i < T::kA; ++i) {
@@ -532,11 +470,11 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
   }
 }
 
-// dX = grad * sum of the parts (in order), rounded once; ignored tokens 0.
+// dX = gtop * sum of the parts (in order), rounded once; ignored tokens 0.
 template <int DT, bool F8>
 __global__ __launch_bounds__(256) void k_xent_dx(const float* __restrict__ acc, int64_t ld, int64_t part, int parts,
                                                  int32_t m, int32_t k, const int64_t* __restrict__ target,
-                                                 int64_t ignore, const float* __restrict__ grad,
+                                                 int64_t ignore, const float* __restrict__ gtop,
                                                  const uint32_t* __restrict__ top, uint16_t* __restrict__ dx,
                                                  int64_t lddx) {
   const int64_t tok = blockIdx.x;
@@ -550,7 +488,7 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float* __restrict__ acc, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += u[e];
     }
-    float f = grad[tok] / g_scale<DT>();
+    const float f = *gtop / g_scale<DT>();
     // the fp16 form of an 8-bit head was divided by 2^(top - 133)
     const int lift = F8 && DT == HYB_F16 ? int(*top) - 133 : 0;
 #pragma unroll
@@ -576,33 +514,33 @@ hipError_t allow_lds(F* fn, int bytes) {
 }
 
 template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
-hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, int32_t steps, const XentTile& t, hipStream_t s) {
+hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
   typedef PanelTile<KIND, AP, BP, WA, WB> T;
   const hipError_t e = allow_lds(&k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
   hipLaunchKernelGGL((k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB),
-                     T::kLds, s, W, X, steps, t);
+                     T::kLds, s, W, X, t);
   return hipGetLastError();
 }
 
 template <int DT, bool GRAD>
-hipError_t run_tiles(bool f8, int bp, const PanelOperand& W, const PanelOperand& X, int32_t steps, const XentTile& t,
-                     hipStream_t s) {
+hipError_t run_tiles(bool f8, int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
   if (f8)
-    return bp == 16 ? run_tile<kF8Wide, DT, GRAD, 16, 16, 2, 4>(W, X, steps, t, s)
-                    : run_tile<kF8Wide, DT, GRAD, 16, 4, 4, 2>(W, X, steps, t, s);
-  return bp == 16 ? run_tile<DT, DT, GRAD, 16, 16, 2, 4>(W, X, steps, t, s)
-                  : run_tile<DT, DT, GRAD, 16, 4, 4, 2>(W, X, steps, t, s);
+    return bp == 16 ? run_tile<kF8Wide, DT, GRAD, 16, 16, 2, 4>(W, X, t, s)
+                    : run_tile<kF8Wide, DT, GRAD, 16, 4, 4, 2>(W, X, t, s);
+  return bp == 16 ? run_tile<DT, DT, GRAD, 16, 16, 2, 4>(W, X, t, s)
+                  : run_tile<DT, DT, GRAD, 16, 4, 4, 2>(W, X, t, s);
 }
 
 template <int DT, bool DX, int AP, int BP, int WA, int WB>
 hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                        hipStream_t s) {
-  typedef PanelTile<DT, AP, BP, WA, WB> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, true, !DX> T;
   const hipError_t e = allow_lds(&k_xent_product<DT, DX, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
-  const int64_t na = (A.rows16 + 16 * AP - 1) / (16 * AP), nb = (B.rows16 + 16 * BP - 1) / (16 * BP);
+  const int64_t na = (A.steps * 4 + AP - 1) / AP;
+  const int64_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
   hipLaunchKernelGGL((k_xent_product<DT, DX, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
                      dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
   return hipGetLastError();
@@ -633,10 +571,10 @@ hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtyp
                      int64_t ignore, char* ws, hipStream_t s, PanelOperand* out) {
   if (p.f8) {
     const hyb_f8 X{ws + p.x, ws + p.xs};
-    *out = PanelOperand{ws + p.x, reinterpret_cast<const uint32_t*>(ws + p.xs), int32_t(p.m16), p.m16};
+    *out = PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.steps), reinterpret_cast<const uint32_t*>(ws + p.xs), p.m16};
     return launch_f8_quantize(x, dtype, p.m, p.k, ldx, HYB_F8_ROWS, X, s);
   }
-  *out = PanelOperand{ws + p.x, nullptr, int32_t(p.m16), 0};
+  *out = PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.steps), nullptr, 0};
   hipLaunchKernelGGL(k_xent_pack_x, dim3(unsigned(p.m16 / 16), unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(x), ldx, p.m, int32_t(p.steps), target, ignore, ws + p.x);
   return hipGetLastError();
@@ -646,9 +584,9 @@ hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtyp
 // panels, a packed head's expanded ones.
 PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t v0, int64_t rows, const char* panels) {
   const int32_t rows16 = int32_t((rows + 15) / 16 * 16);
-  if (!p.f8) return PanelOperand{panels, nullptr, rows16, 0};
-  return PanelOperand{static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep,
-                      static_cast<const uint32_t*>(head.f8->scales) + v0, rows16, f8_rows16(p.n)};
+  if (!p.f8) return PanelOperand{panels, rows16, int32_t(p.steps), nullptr, 0};
+  return PanelOperand{static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep, rows16,
+                      int32_t(p.steps), static_cast<const uint32_t*>(head.f8->scales) + v0, f8_rows16(p.n)};
 }
 
 #define HYB_TRY(call)                      \
@@ -685,7 +623,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
       if (!p.f8) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, nullptr, ws + p.w, s));
       t.v0 = v0;
       const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
-      HYB_TRY((run_tiles<DT, false>(p.f8, p.bp, W, X, int32_t(p.steps), t, s)));
+      HYB_TRY((run_tiles<DT, false>(p.f8, p.bp, W, X, t, s)));
       chunks = v0 / 256 + (W.rows16 + 255) / 256;
     }
   }
@@ -711,14 +649,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
   PanelOperand X;
   HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
   const int32_t krows = int32_t(p.ksteps16 * 64);
-  if (dw) {
-    hipLaunchKernelGGL(k_xent_transpose, dim3(unsigned(p.m64 / 64), unsigned(p.ksteps16)), dim3(256), 0, s, ws + p.x,
-                       int32_t(p.m16), int32_t(p.ksteps16), ws + p.xt, int32_t(p.m64 / 64));
-    HYB_TRY(hipGetLastError());
-  }
-  t.g = dx ? ws + p.g : nullptr;
-  t.gt = dw ? ws + p.gt : nullptr;
-  t.gt_steps = int32_t(p.m64 / 64);
+  t.g = ws + p.g;
   // dX runs over the vocabulary that counts, dW over every row of the head.
   const int64_t end = dw ? p.n : n_vocab;
   for (int64_t v0 = 0; v0 < end; v0 += p.piece) {
@@ -728,11 +659,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     t.g_steps = vsteps;
     if (!p.f8 || dx) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, top, ws + p.w, s));
     const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
-    HYB_TRY((run_tiles<DT, true>(p.f8, p.bp, W, X, int32_t(p.steps), t, s)));
+    HYB_TRY((run_tiles<DT, true>(p.f8, p.bp, W, X, t, s)));
+    // G: tokens x entries, vsteps steps; W': entries x columns
+    const PanelOperand G{ws + p.g, int32_t(p.m16), vsteps, nullptr, 0};
     if (dx) {
-      hipLaunchKernelGGL(k_xent_transpose, dim3(unsigned(vsteps), unsigned(p.ksteps16)), dim3(256), 0, s, ws + p.w,
-                         int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), ws + p.wt, vsteps);
-      HYB_TRY(hipGetLastError());
       XentOut o{};
       o.acc = reinterpret_cast<float*>(ws + p.dx);
       o.ld = krows;
@@ -740,9 +670,9 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.first = v0 == 0;
       o.rows = int32_t(p.m);
       o.cols = krows;
-      const PanelOperand A{ws + p.wt, nullptr, krows, 0}, B{ws + p.g, nullptr, int32_t(p.m16), 0};
-      HYB_TRY(p.bp == 16 ? (run_product<DT, true, 16, 16, 2, 4>(A, B, vsteps, p.parts, o, s))
-                         : (run_product<DT, true, 16, 4, 4, 2>(A, B, vsteps, p.parts, o, s)));
+      const PanelOperand A{ws + p.w, int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), nullptr, 0};
+      HYB_TRY(p.bp == 16 ? (run_product<DT, true, 16, 16, 2, 4>(A, G, vsteps, p.parts, o, s))
+                         : (run_product<DT, true, 16, 4, 4, 2>(A, G, vsteps, p.parts, o, s)));
     }
     if (dw) {
       XentOut o{};
@@ -753,9 +683,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.cols = int32_t(p.k);
       o.live = n_vocab - v0;
       o.vec = reinterpret_cast<uintptr_t>(dw) % 8 == 0 && lddw % 4 == 0;
-      const PanelOperand A{ws + p.xt, nullptr, krows, 0},
-          B{ws + p.gt, nullptr, int32_t((rows + 15) / 16 * 16), 0};
-      HYB_TRY((run_product<DT, false, 16, 16, 2, 4>(A, B, int32_t(p.m64 / 64), 1, o, s)));
+      HYB_TRY((run_product<DT, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
     }
   }
   if (dx) {
@@ -763,10 +691,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     const float* acc = reinterpret_cast<const float*>(ws + p.dx);
     if (p.f8)
       hipLaunchKernelGGL((k_xent_dx<DT, true>), grid, dim3(256), 0, s, acc, int64_t(krows), p.m * int64_t(krows),
-                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, t.grad, top, static_cast<uint16_t*>(dx), lddx);
+                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, gtop, top, static_cast<uint16_t*>(dx), lddx);
     else
       hipLaunchKernelGGL((k_xent_dx<DT, false>), grid, dim3(256), 0, s, acc, int64_t(krows), p.m * int64_t(krows),
-                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, t.grad, top, static_cast<uint16_t*>(dx), lddx);
+                         p.parts, t.m, int32_t(p.k), t.target, t.ignore, gtop, top, static_cast<uint16_t*>(dx), lddx);
     HYB_TRY(hipGetLastError());
   }
   return hipSuccess;

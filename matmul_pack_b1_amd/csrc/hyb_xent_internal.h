@@ -22,7 +22,7 @@ struct XentPlan {
   bool rows;           // few tokens, loss only: logits through the library's product
   int64_t chunks;      // partial softmax sums per token
   int parts;           // cuts of the vocabulary in the dX product
-  size_t x, xs, part, zt, logits, w, wt, g, gt, xt, dx, misc, total;
+  size_t x, xs, part, zt, logits, w, g, dx, misc, total;
 };
 XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus);
 

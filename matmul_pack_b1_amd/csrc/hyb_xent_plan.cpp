@@ -60,15 +60,8 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   } else if (!p.f8 || dx) {
     p.w = take(p.piece * krows * 2);
   }
-  if (dx) {
-    p.wt = take(p.piece * krows * 2);
-    p.g = take(p.m16 * p.piece * 2);
-    p.dx = take(int64_t(p.parts) * m * krows * 4);
-  }
-  if (dw) {
-    p.gt = take(p.piece * p.m64 * 2);
-    p.xt = take(krows * p.m64 * 2);
-  }
+  if (dx || dw) p.g = take(p.m16 * p.piece * 2);
+  if (dx) p.dx = take(int64_t(p.parts) * m * krows * 4);
   p.total = at;
   return p;
 }

@@ -6,10 +6,11 @@ Bounds, from the rounding steps of the calculation (h is half a step of the
   z     fp32 sums of exact products: ez = k 2^-23 max_v sum_c |x w|
   loss  2 ez; exponentials and their fp32 sums, at most 2^-17 of the sum (about
         a hundred roundings), and the roundings of lse and z: 2^-22 |lse|
-  dX    each entry of G = softmax - onehot is off by h |G| (its rounding,
-        plus 2^-39 where fp16 scaled by 2^14 is subnormal, and 2^-126 in any
-        type: the exponential's result and a matrix operand below the smallest
-        normal fp32 or bf16 number count as zero) and p (ez + 2^-17);
+  dX    each entry of dz = grad (softmax - onehot) is off by h |dz| (its
+        rounding, plus, over the largest |grad| rounded up to a power of two,
+        2^-39 where fp16 scaled by 2^14 is subnormal, and 2^-126 in any type:
+        the exponential's result and a matrix operand below the smallest
+        normal fp32 or bf16 number count as zero) and |grad| p (ez + 2^-17);
         fp32 sums n_vocab 2^-23; the result's own rounding h
   dW    the same with X in place of W and m in place of n_vocab"""
 import numpy as np
@@ -68,11 +69,11 @@ def bounds(xv, wv, x, target, grad, n_vocab, k):
     p = np.exp(z - lse[:, None]) * seen[:, None]
     G = p.copy()
     G[np.flatnonzero(seen), t[seen]] -= 1.0
-    eg = (np.abs(G) * (h + n_vocab * 2.0 ** -23) + p * (ez + 2.0 ** -17)[:, None] + sub) * seen[:, None]
-    tol_dx = (eg @ ws) * np.abs(g)[:, None] + h * np.abs(dx) + tiny
-    # dW's fp16 form is scaled by the largest |grad|: its subnormal step too
-    eg = (np.abs(G) * (h + len(t) * 2.0 ** -23) + p * (ez + 2.0 ** -17)[:, None]) * np.abs(g)[:, None] * seen[:, None]
-    eg += 2 * sub * np.abs(g[seen]).max(initial=0.0) * seen[:, None]
+    ag = np.abs(g)[:, None]
+    low = 2 * sub * np.abs(g[seen]).max(initial=0.0)
+    eg = ((np.abs(G) * (h + n_vocab * 2.0 ** -23) + p * (ez + 2.0 ** -17)[:, None]) * ag + low) * seen[:, None]
+    tol_dx = eg @ ws + h * np.abs(dx) + tiny
+    eg = ((np.abs(G) * (h + len(t) * 2.0 ** -23) + p * (ez + 2.0 ** -17)[:, None]) * ag + low) * seen[:, None]
     tol_dw = np.zeros_like(wv)
     tol_dw[:n_vocab] = eg.T @ xs
     tol_dw += h * np.abs(dw) + tiny
