@@ -56,8 +56,8 @@ typedef struct {
 } hyb_f8;
 
 /* Bytes of the two buffers of a rows x k matrix (the same for both kinds;
- * 0 when rows or k is 0).  Host only.  rows >= 0, 0 <= k <= 2^22, at most
- * 2^31 - 16 rows, else HYB_ERR_SHAPE. */
+ * 0 when rows or k is 0).  Host only.  0 <= rows <= 2^27 - 16, 0 <= k <= 2^22,
+ * else HYB_ERR_SHAPE. */
 hyb_status hyb_f8_size(int64_t rows, int64_t k, size_t* code_bytes, size_t* scale_bytes);
 
 /* Quantise A (rows x k of `dtype`, HYB_F16, HYB_BF16 or HYB_F32, row stride
@@ -86,6 +86,15 @@ hyb_status hyb_f8_dequantize(const hyb_f8* src, int64_t rows, int64_t k, void* a
 hyb_status hyb_f8_gemm_workspace_size(int64_t n, int64_t k, int32_t m, size_t* bytes);
 hyb_status hyb_f8_gemm(const hyb_f8* w, int64_t n, int64_t k, const hyb_f8* x, int32_t m, void* y, int32_t y_dtype,
                        int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* hyb_f8_quantize of x (m x k of x_dtype, row stride ldx) and hyb_f8_gemm in
+ * one call, for activations that one product reads.  The workspace (bytes of
+ * hyb_f8_linear_workspace_size, 16-byte aligned, as above) is needed: it holds
+ * the codes as well.  The result is bitwise that of the two calls. */
+hyb_status hyb_f8_linear_workspace_size(int64_t n, int64_t k, int32_t m, size_t* bytes);
+hyb_status hyb_f8_linear(const hyb_f8* w, int64_t n, int64_t k, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
+                         void* y, int32_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 #ifdef __cplusplus
 }

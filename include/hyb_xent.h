@@ -66,7 +66,8 @@ hyb_status hyb_xent_workspace_size(const hyb_head* head, int32_t m, int32_t what
  *           type), row stride ldx >= k; 16-byte aligned with ldx % 8 == 0
  *           for a packed head, element-aligned for an 8-bit one
  *   target  device int64[m]
- * 0 <= m <= 2^22 tokens; a head has 1 <= n <= 2^30 and 1 <= k <= 2^21. */
+ * 0 <= m <= 2^22 tokens; a head has 1 <= n <= 2^27 - 16 and
+ * 1 <= k <= 2^21. */
 hyb_status hyb_xent(const hyb_head* head, int64_t n_vocab, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
                     const int64_t* target, int64_t ignore_index, float* loss, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream);

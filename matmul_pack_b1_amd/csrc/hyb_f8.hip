@@ -10,46 +10,93 @@ namespace {
 
 // ------------------------------------------------------ quantise, read back --
 
-// 16 columns c0.. of one row as fp32; zeros behind the row's end.  `vec`:
-// every row starts 16-byte aligned.
+// Eight columns c0.. of one row, as loaded (two elements to a word, or one
+// for fp32); zeros behind the row's end.  `vec`: every row starts 16-byte
+// aligned.
 template <int DT>
-__device__ __forceinline__ void load16(const void* a, int64_t base, int32_t c0, int32_t k, bool row_ok, bool vec,
-                                       float (&v)[16]) {
+struct Eight {
+  uint32_t w[DT == HYB_F32 ? 8 : 4];
+};
+
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8(const void* a, int64_t base, int32_t c0, int32_t k, bool vec) {
+  Eight<DT> r;
+  constexpr int kWords = DT == HYB_F32 ? 8 : 4;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  if (!row_ok || c0 >= k) return;
-  if (vec && c0 + 16 <= k) {
-    if constexpr (DT == HYB_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a) + base + c0);
+  for (int i = 0; i < kWords; ++i) r.w[i] = 0;
+  if (c0 >= k) return r;
+  if (vec && c0 + 8 <= k) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a) + (base + c0) * (DT == HYB_F32 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = p[i];
-        v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
-      }
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a) + base + c0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 u = p[i];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = widen16<DT>(w[j] & 0xFFFFu);
-          v[8 * i + 2 * j + 1] = widen16<DT>(w[j] >> 16);
-        }
-      }
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 u = p[i];
+      r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
     }
-    return;
+    return r;
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i)
     if (c0 + i < k) {
       if constexpr (DT == HYB_F32)
-        v[i] = static_cast<const float*>(a)[base + c0 + i];
+        r.w[i] = static_cast<const uint32_t*>(a)[base + c0 + i];
       else
-        v[i] = widen16<DT>(static_cast<const uint16_t*>(a)[base + c0 + i]);
+        r.w[i / 2] |= uint32_t(static_cast<const uint16_t*>(a)[base + c0 + i]) << (16 * (i & 1));
     }
+  return r;
+}
+
+// Element i as fp32.
+template <int DT>
+__device__ __forceinline__ float elem(const Eight<DT>& r, int i) {
+  if constexpr (DT == HYB_F32) return __builtin_bit_cast(float, r.w[i]);
+  return widen16<DT>((r.w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+}
+
+constexpr uint32_t kF32Inf = 0x7F800000u;
+
+// fp32 bits of the largest magnitude; a NaN or an infinity gives at least
+// kF32Inf.  (Magnitudes of one type order as their bits.)
+template <int DT>
+__device__ __forceinline__ uint32_t top_of(const Eight<DT>& r) {
+  if constexpr (DT == HYB_F32) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = r.w[i] & 0x7FFFFFFFu;
+      t = u > t ? u : t;
+    }
+    return t;
+  } else {
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
+    u16x2_t t = __builtin_bit_cast(u16x2_t, r.w[0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2_t, r.w[i] & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, widen16<DT>(t[0] > t[1] ? t[0] : t[1]));
   }
+}
+
+// The same over finite elements only.
+template <int DT>
+__device__ __forceinline__ uint32_t top_finite(const Eight<DT>& r) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, elem<DT>(r, i)) & 0x7FFFFFFFu;
+    t = u < kF32Inf && u > t ? u : t;
+  }
+  return t;
+}
+
+// Largest of the 16 lanes of a row of lanes, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xF, 0xF, false));  // row_ror:8
+  v = o > v ? o : v;
+  o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x124, 0xF, 0xF, false));
+  v = o > v ? o : v;
+  o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x122, 0xF, 0xF, false));
+  v = o > v ? o : v;
+  o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x121, 0xF, 0xF, false));
+  return o > v ? o : v;
 }
 
 // Exponent byte of a block whose largest finite magnitude has the bits
@@ -68,101 +115,102 @@ __device__ __forceinline__ float exp2_byte(uint32_t byte) {
   return __builtin_bit_cast(float, byte == 0 ? 0x00400000u : byte << 23);
 }
 
-constexpr uint32_t kF32Inf = 0x7F800000u;
-
-// Magnitude bits of the largest finite element.
-__device__ __forceinline__ uint32_t top_finite(const float (&v)[16], uint32_t top) {
+// Eight codes of a / 2^(e - 127); `mark` makes elements that are not finite
+// the NaN code (the conversion is only given finite ones).
+template <int DT>
+__device__ __forceinline__ uint2 codes8(const Eight<DT>& r, uint32_t e, bool mark) {
+  const float inv = exp2_byte(254u - e);
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
-    top = u < kF32Inf && u > top ? u : top;
-  }
-  return top;
-}
-
-// 16 codes of elements already divided by the scale (|.| <= 448, or not
-// finite: made NaN first, the conversion leaves NaN as the NaN code).
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float inv) {
-  uint32_t w[4];
+  for (int i = 0; i < 2; ++i) {
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(elem<DT>(r, 4 * i) * inv, elem<DT>(r, 4 * i + 1) * inv, 0, false);
+    w[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(elem<DT>(r, 4 * i + 2) * inv, elem<DT>(r, 4 * i + 3) * inv, lo, true));
+    if (mark) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = v[4 * i + j];
-      const bool finite = (__builtin_bit_cast(uint32_t, a) & 0x7FFFFFFFu) < kF32Inf;
-      f[j] = finite ? a * inv : __builtin_nanf("");
+      for (int j = 0; j < 4; ++j)
+        if ((__builtin_bit_cast(uint32_t, elem<DT>(r, 4 * i + j)) & 0x7FFFFFFFu) >= kF32Inf) w[i] |= 0xFFu << (8 * j);
     }
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-    w[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint2(w[0], w[1]);
 }
 
-// One wavefront per panel and four steps (512 columns): lane L holds, of each
-// step, its row's columns 16 (L/16) + 0..15 of both halves, so the codes
-// leave as 1 KiB stores in panel order and a row's maximum needs the four
-// lanes of that row.  A weight block is eight panels: a workgroup of eight
-// wavefronts, whose maxima meet in LDS.  Bound by memory (one read of the
-// matrix, half or a quarter as many bytes written).
+// One wavefront per panel and four steps: a load covers 512 columns of one row
+// (8 per lane, 16 lanes to a step), so a row's maximum is one over 16 lanes;
+// the codes go through LDS into panel order and leave as 1 KiB stores.  A
+// weight block is eight panels: a workgroup of eight wavefronts, whose maxima
+// meet in LDS.  Bound by memory: one read of the matrix, half or a quarter as
+// many bytes written (28672 x 8192 bf16: see the measurements).
 template <int DT, bool WEIGHT>
-__global__ __launch_bounds__(512) void k_f8_quantize(const void* __restrict__ a, int64_t rows, int32_t k, int64_t lda,
-                                                     int vec, char* __restrict__ codes, uint32_t* __restrict__ scales,
-                                                     int32_t panels, int32_t steps) {
+__global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* __restrict__ a, int64_t rows,
+                                                                    int32_t k, int64_t lda, int vec,
+                                                                    char* __restrict__ codes,
+                                                                    char* __restrict__ scales, int32_t panels,
+                                                                    int32_t steps) {
+  constexpr int kWaves = WEIGHT ? 8 : 4;
+  __shared__ __attribute__((aligned(16))) char turn_lds[kWaves][8192];
   __shared__ uint32_t top_lds[8][4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4;
-  const int64_t panel = int64_t(blockIdx.x) * 8 + wave;
-  const int32_t s0 = int32_t(blockIdx.y) * 4;
-  const int64_t row = panel * 16 + (lane & 15);
-  const bool live = panel < panels;
-  const int64_t base = row * lda;
-  float v[4][2][16];
-  uint32_t top[4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // a weight's wavefronts take the panels of a block, a row matrix's the quads
+  const int64_t panel = WEIGHT ? int64_t(blockIdx.x) * 8 + wave : blockIdx.x;
+  const int32_t s0 = (WEIGHT ? int32_t(blockIdx.y) : int32_t(blockIdx.y) * 4 + wave) * 4;
+  const int64_t r0 = panel * 16;
+  const int32_t c0 = s0 * 128 + lane * 8;
+  const bool live = panel < panels && s0 < steps;
+  Eight<DT> v[16];
+  uint32_t top[16];
+  uint32_t all = 0;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      load16<DT>(a, base, (s0 + s) * 128 + h * 64 + q * 16, k, row < rows, vec, v[s][h]);
+  for (int r = 0; r < 16; ++r) {
+    v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0, vec);
   }
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    uint32_t t = top_finite(v[s][0], 0u);
-    t = top_finite(v[s][1], t);
-    uint32_t o = __shfl_xor(t, 16);
-    t = o > t ? o : t;
-    o = __shfl_xor(t, 32);
-    top[s] = o > t ? o : t;
+  for (int r = 0; r < 16; ++r) {
+    top[r] = top_of<DT>(v[r]);
+    all = top[r] > all ? top[r] : all;
+  }
+  const bool mark = __any(all >= kF32Inf);
+  if (mark) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top[r] = top_finite<DT>(v[r]);
   }
   if constexpr (WEIGHT) {
+    uint32_t t = 0;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-#pragma unroll
-      for (int d = 1; d < 16; d *= 2) {
-        const uint32_t o = __shfl_xor(top[s], d);
-        top[s] = o > top[s] ? o : top[s];
-      }
-      if (lane == 0) top_lds[wave][s] = top[s];
-    }
+    for (int r = 0; r < 16; ++r) t = top[r] > t ? top[r] : t;
+    t = max16(t);
+    if ((lane & 15) == 0) top_lds[wave][lane >> 4] = t;
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int w = 0; w < 8; ++w) t = top_lds[w][lane >> 4] > t ? top_lds[w][lane >> 4] : t;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) top[s] = top_lds[w][s] > top[s] ? top_lds[w][s] : top[s];
+    for (int r = 0; r < 16; ++r) top[r] = t;
   }
   if (!live) return;
-  uint32_t word = 0;
+  // Columns 8 j.. (j = lane % 16) of a step: half j / 8, unit (j % 8) / 2, one
+  // half of its row's 16 bytes.  Rows are rotated within a unit so that the
+  // units, all multiples of 256 bytes, are written through different banks.
+  char* turn = turn_lds[wave];
+  const int j = lane & 15;
+  const int unit = (lane >> 4) * 8 + (j >> 1);  // 256-byte unit of the 8 KiB
+  uint32_t mine = 127;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint32_t e = s0 + s < steps ? block_exponent(top[s]) : 127u;
-    word |= e << (8 * s);
-    if (s0 + s >= steps) continue;
-    const float inv = exp2_byte(254u - e);
-    char* dst = codes + (panel * steps + s0 + s) * kPanelStep + lane * 16;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(dst + h * 1024) = codes16(v[s][h], inv);
+  for (int r = 0; r < 16; ++r) {
+    if constexpr (!WEIGHT) top[r] = max16(top[r]);
+    const uint32_t e = block_exponent(top[r]);
+    if (r == j) mine = r0 + r < rows && s0 + (lane >> 4) < steps ? e : 127u;
+    *reinterpret_cast<uint2*>(turn + unit * 256 + ((r + unit) & 15) * 16 + (j & 1) * 8) = codes8<DT>(v[r], e, mark);
   }
-  if (q == 0) scales[int64_t(s0 / 4) * panels * 16 + row] = row < rows ? word : 0x7F7F7F7Fu;
+  // one wavefront writes and reads `turn`: its own accesses done suffices
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    if (s0 + p / 2 >= steps) break;
+    const int u = p * 4 + (lane >> 4);
+    *reinterpret_cast<uint4*>(codes + (panel * steps + s0) * kPanelStep + p * 1024 + lane * 16) =
+        *reinterpret_cast<const uint4*>(turn + u * 256 + ((j + u) & 15) * 16);
+  }
+  scales[((int64_t(s0 / 4) * panels * 16) + r0 + j) * 4 + (lane >> 4)] = char(mine);
 }
 
 template <int DT>
@@ -176,12 +224,20 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ 
   if (panel >= panels || row >= rows) return;
   const int32_t s0 = int32_t(blockIdx.y) * 4;
   const uint32_t word = scales[int64_t(s0 / 4) * panels * 16 + row];
-  for (int s = 0; s < 4 && s0 + s < steps; ++s) {
+  uint4 all[4][2];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      all[s][h] = s0 + s < steps ? *reinterpret_cast<const uint4*>(codes + (panel * steps + s0 + s) * kPanelStep +
+                                                                   h * 1024 + lane * 16)
+                                 : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
     const float scale = exp2_byte((word >> (8 * s)) & 0xFFu);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 u = *reinterpret_cast<const uint4*>(codes + (panel * steps + s0 + s) * kPanelStep + h * 1024 + lane * 16);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint32_t w[4] = {all[s][h].x, all[s][h].y, all[s][h].z, all[s][h].w};
       float f[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -312,17 +368,36 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
   }
 }
 
-template <int KIND, int AP, int BP, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelOperand X, F8Out out) {
-  typedef PanelTile<KIND, AP, BP, WA, WB> T;
+// More tokens: AP x BP panels per workgroup through LDS.  The first `whole`
+// tiles (whole rounds of the compute units) run over all of k; each of the
+// rest is cut into `parts`, whose sums are left in `ws` (wavefront by
+// wavefront, as they lie in registers) for k_f8_sum.
+template <int KIND, int AP, int BP, int WA, int WB, int STAGES>
+__global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelOperand X, F8Out out,
+                                                          int32_t whole, int parts, f32x4_t* __restrict__ ws) {
+  typedef PanelTile<KIND, AP, BP, WA, WB, STAGES> T;
   extern __shared__ __attribute__((aligned(1024))) char f8_smem[];
   const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
-  int32_t ab, bb;
-  panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
+  const int32_t id = int32_t(blockIdx.x), rest = id - whole;
+  int32_t ab, bb, s0 = 0, s1 = W.steps;
+  panel_block(rest < 0 ? panel_order(id, whole) : whole + rest / parts, na, nb, ab, bb);
   f32x4_t acc[T::kA][T::kB];
-  T::run(W, X, ab * AP, bb * BP, 0, W.steps, f8_smem, acc);
+  if (rest >= 0) {
+    const int32_t part = rest % parts, quads = (W.steps + 3) / 4;  // a part is a whole number of four steps
+    s0 = int32_t(int64_t(quads) * part / parts) * 4;
+    if (part + 1 < parts) s1 = int32_t(int64_t(quads) * (part + 1) / parts) * 4;
+  }
+  T::run(W, X, ab * AP, bb * BP, s0, s1, f8_smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave % WA, wb = wave / WA;
+  if (rest >= 0) {
+    f32x4_t* p = ws + int64_t(rest) * (AP * BP * 64) + wave * (T::kA * T::kB * 64) + lane;
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j)
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i) p[(i * T::kB + j) * 64] = acc[i][j];
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < T::kB; ++j)
 #pragma unroll
@@ -331,21 +406,58 @@ __global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelO
                 (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4, acc[i][j]);
 }
 
-// Zeros (k = 0).
-__global__ __launch_bounds__(256) void k_f8_zero(F8Out o) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i < int64_t(o.n) * o.m) store_out(o.y, o.ydt, i / o.n * o.ldy + i % o.n, 0.f);
+// Adds the parts of a tile in order and stores the outputs: one workgroup per
+// four of a tile's AP x BP panel products.
+template <int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(256) void k_f8_sum(const f32x4_t* __restrict__ ws, int32_t na, int32_t nb, int32_t whole,
+                                                int parts, F8Out out) {
+  constexpr int kA = AP / WA, kB = BP / WB;
+  const int lane = threadIdx.x & 63;
+  const int c = int(blockIdx.y) * 4 + (threadIdx.x >> 6);  // wavefront, i, j of the tile
+  const int wave = c / (kA * kB), i = c % (kA * kB) / kB, j = c % kB;
+  int32_t ab, bb;
+  panel_block(whole + int32_t(blockIdx.x), na, nb, ab, bb);
+  const f32x4_t* p = ws + int64_t(blockIdx.x) * parts * (AP * BP * 64) + c * 64 + lane;
+  f32x4_t v = p[0];
+  for (int t = 1; t < parts; ++t) {
+    const f32x4_t u = p[int64_t(t) * (AP * BP * 64)];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += u[e];
+  }
+  f8_store4(out, int64_t(bb * BP + wave / WA * kB + j) * 16 + (lane & 15),
+            (ab * AP + wave % WA * kA + i) * 16 + (lane >> 4) * 4, v);
 }
 
-template <int KIND, int AP, int BP, int WA, int WB>
-hipError_t launch_tile(const PanelOperand& W, const PanelOperand& X, const F8Out& o, hipStream_t s) {
-  typedef PanelTile<KIND, AP, BP, WA, WB> T;
-  const void* fn = reinterpret_cast<const void*>(&k_f8_tile<KIND, AP, BP, WA, WB>);
+// Zeros (k = 0).
+__global__ __launch_bounds__(256) void k_f8_zero(F8Out o) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < int64_t(o.n) * o.m; i += int64_t(gridDim.x) * 256)
+    store_out(o.y, o.ydt, i / o.n * o.ldy + i % o.n, 0.f);
+}
+
+template <int KIND, int AP, int BP, int WA, int WB, int STAGES>
+hipError_t launch_tile(const PanelOperand& W, const PanelOperand& X, const F8Out& o, const F8Route& r, float* ws,
+                       hipStream_t s) {
+  typedef PanelTile<KIND, AP, BP, WA, WB, STAGES> T;
+  const void* fn = reinterpret_cast<const void*>(&k_f8_tile<KIND, AP, BP, WA, WB, STAGES>);
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
-  hipLaunchKernelGGL((k_f8_tile<KIND, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB), T::kLds, s, W, X, o);
+  const int64_t whole = ws && r.parts > 1 ? r.whole : na * nb, rest = na * nb - whole;
+  f32x4_t* sums = reinterpret_cast<f32x4_t*>(ws);
+  hipLaunchKernelGGL((k_f8_tile<KIND, AP, BP, WA, WB, STAGES>), dim3(unsigned(whole + rest * r.parts)),
+                     dim3(64 * WA * WB), T::kLds, s, W, X, o, int32_t(whole), r.parts, sums);
+  if (rest > 0)
+    hipLaunchKernelGGL((k_f8_sum<AP, BP, WA, WB>), dim3(unsigned(rest), AP * BP / 4), dim3(256), 0, s, sums,
+                       int32_t(na), int32_t(nb), int32_t(whole), r.parts, o);
   return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_route(const F8Route& r, const PanelOperand& W, const PanelOperand& X, const F8Out& o, float* ws,
+                        hipStream_t s) {
+  if (r.ap == 16 && r.bp == 16) return launch_tile<KIND, 16, 16, 2, 4, 2>(W, X, o, r, ws, s);
+  if (r.ap == 16) return launch_tile<KIND, 16, 8, 4, 2, 2>(W, X, o, r, ws, s);
+  return launch_tile<KIND, 8, 8, 2, 4, 4>(W, X, o, r, ws, s);
 }
 
 }  // namespace
@@ -355,15 +467,16 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
   const int32_t panels = int32_t(f8_rows16(rows) / 16), steps = int32_t(f8_steps(k));
   const int esize = dtype == HYB_F32 ? 4 : 2;
   const int vec = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda * esize % 16 == 0;
-  const dim3 grid(unsigned((panels + 7) / 8), unsigned((steps + 3) / 4));
+  const unsigned quads = unsigned((steps + 3) / 4);
+  const dim3 grid = kind == HYB_F8_WEIGHT ? dim3(unsigned((panels + 7) / 8), quads) : dim3(unsigned(panels), (quads + 3) / 4);
   char* codes = static_cast<char*>(dst.codes);
-  uint32_t* scales = static_cast<uint32_t*>(dst.scales);
+  char* scales = static_cast<char*>(dst.scales);
 #define HYB_F8_QUANT(DT)                                                                                             \
   if (kind == HYB_F8_WEIGHT)                                                                                         \
     hipLaunchKernelGGL((k_f8_quantize<DT, true>), grid, dim3(512), 0, s, a, rows, int32_t(k), lda, vec, codes,       \
                        scales, panels, steps);                                                                       \
   else                                                                                                               \
-    hipLaunchKernelGGL((k_f8_quantize<DT, false>), grid, dim3(512), 0, s, a, rows, int32_t(k), lda, vec, codes,      \
+    hipLaunchKernelGGL((k_f8_quantize<DT, false>), grid, dim3(256), 0, s, a, rows, int32_t(k), lda, vec, codes,      \
                        scales, panels, steps)
   if (dtype == HYB_F32) {
     HYB_F8_QUANT(HYB_F32);
@@ -402,7 +515,8 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
   const F8Out o{y,      ldy, int32_t(n), int32_t(m), y_dtype,
                 reinterpret_cast<uintptr_t>(y) % (4 * esize) == 0 && ldy % 4 == 0};
   if (k == 0) {
-    hipLaunchKernelGGL(k_f8_zero, dim3(unsigned((n * m + 255) / 256)), dim3(256), 0, s, o);
+    const int64_t blocks = (n * m + 255) / 256;
+    hipLaunchKernelGGL(k_f8_zero, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, o);
     return hipGetLastError();
   }
   const int32_t steps = int32_t(f8_steps(k));
@@ -410,8 +524,7 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
                        static_cast<const uint32_t*>(w.scales), f8_rows16(n)};
   const PanelOperand X{static_cast<const char*>(x.codes), int32_t(f8_rows16(m)), steps,
                        static_cast<const uint32_t*>(x.scales), f8_rows16(m)};
-  const F8Route r = f8_route(n, k, m, device_cus());
-  (void)ws;
+  const F8Route r = f8_route(n, k, m, y_dtype == HYB_F32, device_cus());
   if (r.waves) {
     const dim3 grid(unsigned(W.rows16 / 16), unsigned((X.rows16 / 16 + r.bp - 1) / r.bp));
     if (r.bp == 1)
@@ -422,10 +535,7 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
       hipLaunchKernelGGL((k_f8_rows<4, 8>), grid, dim3(512), 0, s, W, X, o);
     return hipGetLastError();
   }
-  const bool wide = y_dtype == HYB_F32;  // kF8Wide
-  if (r.ap == 16)
-    return wide ? launch_tile<kF8Wide, 16, 16, 2, 4>(W, X, o, s) : launch_tile<kF8, 16, 16, 2, 4>(W, X, o, s);
-  return wide ? launch_tile<kF8Wide, 8, 8, 2, 2>(W, X, o, s) : launch_tile<kF8, 8, 8, 2, 2>(W, X, o, s);
+  return y_dtype == HYB_F32 ? launch_route<kF8Wide>(r, W, X, o, ws, s) : launch_route<kF8>(r, W, X, o, ws, s);
 }
 
 }  // namespace hyb

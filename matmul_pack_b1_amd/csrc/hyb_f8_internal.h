@@ -13,19 +13,26 @@ constexpr int64_t kF8Step = 128;
 constexpr int64_t kPanelStep = 2048;
 // Largest k: a panel's byte offsets within a 16-panel tile stay below 2^31.
 constexpr int64_t kF8MaxK = int64_t(1) << 22;
-constexpr int64_t kF8MaxRows = (int64_t(1) << 31) - 16;
+// Launch limits: 512 threads per panel of w, or per tile, stay below 2^32 in
+// one grid dimension.
+constexpr int64_t kF8MaxRows = (int64_t(1) << 27) - 16;
+constexpr int64_t kF8MaxPanelPairs = int64_t(1) << 29;
 
 inline int64_t f8_steps(int64_t k) { return (k + kF8Step - 1) / kF8Step; }
 inline int64_t f8_rows16(int64_t rows) { return (rows + 15) / 16 * 16; }
 
 // How a product runs.
 struct F8Route {
-  int ap, bp;  // panels of w and of x per workgroup
-  int waves;   // register-fed: wavefronts cutting k; LDS-fed: 0
-  int parts;   // k cut over this many workgroups per tile (1: not)
+  int ap, bp;     // panels of w and of x per workgroup
+  int waves;      // register-fed: wavefronts cutting k; LDS-fed: 0
+  int64_t whole;  // LDS-fed: tiles that run over all of k ...
+  int parts;      // ... and the parts each of the others is cut into (1: all run whole)
 };
-F8Route f8_route(int64_t n, int64_t k, int64_t m, int64_t cus);
+// `wide`: the product of an fp32 output (kF8Wide).
+F8Route f8_route(int64_t n, int64_t k, int64_t m, bool wide, int64_t cus);
 size_t f8_workspace_bytes(const F8Route& r, int64_t n, int64_t m);
+// Bytes that serve both kinds.
+size_t f8_workspace_bytes(int64_t n, int64_t k, int64_t m, int64_t cus);
 
 hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k, int64_t lda, int kind,
                               const hyb_f8& dst, hipStream_t s);

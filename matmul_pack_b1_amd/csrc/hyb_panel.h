@@ -141,11 +141,13 @@ __device__ __forceinline__ f32x4_t panel_mfma(const PanelRegs<KIND>& ar, const P
 // its own L2.  XCD x takes a contiguous range of an order in which 4 A blocks
 // are swept across all B blocks before the next 4, so workgroups that run
 // together on one XCD share A and B panels in its L2.
-__device__ __forceinline__ void panel_block(int32_t id, int32_t total, int32_t na, int32_t nb, int32_t& ab,
-                                            int32_t& bb) {
-  constexpr int32_t kXcd = 8, kGroup = 4;
+__device__ __forceinline__ int32_t panel_order(int32_t id, int32_t total) {
+  constexpr int32_t kXcd = 8;
   const int32_t xcd = id % kXcd, per = total / kXcd, extra = total % kXcd;
-  const int32_t g = xcd * per + (xcd < extra ? xcd : extra) + id / kXcd;
+  return xcd * per + (xcd < extra ? xcd : extra) + id / kXcd;
+}
+__device__ __forceinline__ void panel_block(int32_t g, int32_t na, int32_t nb, int32_t& ab, int32_t& bb) {
+  constexpr int32_t kGroup = 4;
   const int32_t first = g / (kGroup * nb) * kGroup;
   const int32_t width = na - first < kGroup ? na - first : kGroup;
   const int32_t r = g - first * nb;
@@ -162,16 +164,18 @@ __device__ __forceinline__ int panel_lane(int lane) {
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
-// LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, two LDS
-// stages of one step each.  TA / TB: that operand is read transposed (its
-// "panels" here are blocks of 16 of its columns).
-template <int KIND, int AP, int BP, int WA, int WB, bool TA = false, bool TB = false>
+// LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, STAGES LDS
+// stages of one step each (transfers run STAGES - 1 steps ahead).  TA / TB:
+// that operand is read transposed (its "panels" here are blocks of 16 of its
+// columns).
+template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false>
 struct PanelTile {
+  static_assert(STAGES == 2 || STAGES == 4, "a step's stage is an immediate of the loop unrolled by four");
   static constexpr int kWaves = WA * WB;
   static constexpr int kA = AP / WA, kB = BP / WB;  // panels per wavefront
   static constexpr int kStage = (AP + BP) * 2048;
   static constexpr int kScaleStage = is_f8(KIND) ? (AP + BP) * 64 : 0;  // a word per row, four steps
-  static constexpr int kLds = 2 * kStage + 2 * kScaleStage;
+  static constexpr int kLds = STAGES * kStage + 2 * kScaleStage;
   static constexpr int kLoadsA = AP * 2 / kWaves, kLoadsB = BP * 2 / kWaves;  // 1 KiB transfers per wavefront and step
   static_assert(AP % WA == 0 && BP % WB == 0 && AP * 2 % kWaves == 0 && BP * 2 % kWaves == 0, "even split");
   static_assert(!(TA || TB) || !is_f8(KIND), "8-bit operands are read straight");
@@ -276,7 +280,7 @@ struct PanelTile {
       if constexpr (is_f8(KIND)) {
         // the scale words of steps s .. s+3: AP * 64 + BP * 64 bytes
         if ((s & 3) == 0) {
-          const uint32_t sdst = base + 2 * kStage + ((s >> 2) & 1) * kScaleStage;
+          const uint32_t sdst = base + STAGES * kStage + ((s >> 2) & 1) * kScaleStage;
           const int64_t word = int64_t(s >> 2);
           if (wave == 0) {
             const int32_t n = A.rows16 - pa * 16 < AP * 16 ? A.rows16 - pa * 16 : AP * 16;
@@ -306,7 +310,7 @@ struct PanelTile {
     for (int j = 0; j < kB; ++j) scb[j] = 0;
 
     // Multiplies the staged step s and, once its first reads are under way,
-    // starts the next step's transfers.  The reads of A panel i + 1 are issued
+    // starts the transfers of step s + STAGES - 1.  The reads of A panel i + 1 are issued
     // ahead of panel i's products, so that an LDS round trip hides behind
     // them (the scheduling barriers keep the compiler from moving them back).
     auto compute = [&](int32_t s, int stage, auto byte, bool more) {
@@ -315,7 +319,7 @@ struct PanelTile {
       const char* srcb = src + AP * 2048;
       if constexpr (is_f8(KIND)) {
         if (kByte == 0) {
-          const char* sc = smem + 2 * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
+          const char* sc = smem + STAGES * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
 #pragma unroll
           for (int i = 0; i < kA; ++i) sca[i] = *reinterpret_cast<const uint32_t*>(sc + (wa * kA + i) * 64);
 #pragma unroll
@@ -326,7 +330,7 @@ struct PanelTile {
       Halves braw[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) braw[j] = read<TB, BP>(srcb, wb * kB + j, straight, tb0, tb1);
-      if (more) issue(s + 1, stage ^ 1);
+      if (more) issue(s + STAGES - 1, (stage + STAGES - 1) % STAGES);
       PanelRegs<KIND> b[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) b[j] = panel_regs<KIND, kByte>(braw[j].v[0], braw[j].v[1], scb[j]);
@@ -342,19 +346,26 @@ struct PanelTile {
       }
     };
 
-    // A step waits for its own transfers and meets the other wavefronts (whose
-    // reads of the other stage are then done too).  Unrolled by four so that
-    // stage and scale byte are immediates.
+    // A step waits for its own transfers (those of the STAGES - 2 steps after it
+    // may be under way; the few scale transfers only make that wait
+    // stricter) and meets the other wavefronts, whose reads of the stage
+    // that is filled next are then done too.  Unrolled by four so that stage
+    // and scale byte are immediates.
     if (s0 >= s1) return;
-    issue(s0, 0);
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t)
+      if (s0 + t < s1) issue(s0 + t, t);
     for (int32_t q = s0; q < s1; q += 4) {
       auto one = [&](auto byte) {
         constexpr int kByte = decltype(byte)::value;
         const int32_t s = q + kByte;
         if (s >= s1) return;
-        panel_wait<0>();
+        if (STAGES > 2 && s + STAGES - 2 < s1)
+          panel_wait<(STAGES - 2) * (kLoadsA + kLoadsB)>();
+        else
+          panel_wait<0>();
         __syncthreads();
-        compute(s, kByte & 1, byte, s + 1 < s1);
+        compute(s, kByte % STAGES, byte, s + STAGES - 1 < s1);
       };
       one(std::integral_constant<int, 0>());
       one(std::integral_constant<int, 1>());

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
   int32_t ab, bb;
-  panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
   f32x4_t acc[T::kA][T::kB];
   T::run(W, X, ab * AP, bb * BP, 0, W.steps, xent_smem, acc);
   const int lane = threadIdx.x & 63;
@@ -418,13 +418,13 @@ struct XentOut {
 template <int DT, bool DX, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
-  typedef PanelTile<DT, AP, BP, WA, WB, true, !DX> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (A.steps * 4 + AP - 1) / AP;
   const int32_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
   int32_t ab, bb;
   const int32_t part = int32_t(blockIdx.y);
-  panel_block(int32_t(blockIdx.x), na * nb, na, nb, ab, bb);
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
   const int32_t quads = (steps + 3) / 4;  // a part is a whole number of four steps
   const int32_t s0 = int32_t(int64_t(quads) * part / parts) * 4;
   const int32_t s1 = part + 1 == parts ? steps : int32_t(int64_t(quads) * (part + 1) / parts) * 4;
@@ -500,10 +500,11 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float* __restrict__ acc, 
     if (col + e < k) p[e] = round16<DT>(v[e]);
 }
 
-// Rows r0.. of dW set to zero (an empty batch).
-__global__ __launch_bounds__(256) void k_xent_zero(uint16_t* __restrict__ dw, int64_t ld, int32_t k) {
+// dW of an empty batch.
+__global__ __launch_bounds__(256) void k_xent_zero(uint16_t* __restrict__ dw, int64_t n, int64_t ld, int32_t k) {
   const int32_t c = int32_t(blockIdx.y) * 256 + threadIdx.x;
-  if (c < k) dw[int64_t(blockIdx.x) * ld + c] = 0;
+  for (int64_t r = blockIdx.x; r < n; r += gridDim.x)
+    if (c < k) dw[r * ld + c] = 0;
 }
 
 // ----------------------------------------------------------------- launches --
@@ -536,7 +537,7 @@ hipError_t run_tiles(bool f8, int bp, const PanelOperand& W, const PanelOperand&
 template <int DT, bool DX, int AP, int BP, int WA, int WB>
 hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                        hipStream_t s) {
-  typedef PanelTile<DT, AP, BP, WA, WB, true, !DX> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX> T;
   const hipError_t e = allow_lds(&k_xent_product<DT, DX, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (A.steps * 4 + AP - 1) / AP;
@@ -721,8 +722,8 @@ hipError_t launch_xent_backward(const hyb_head& head, const XentPlan& p, int64_t
                                 const float* grad, void* dx, int64_t lddx, void* dw, int64_t lddw, char* ws,
                                 hipStream_t s) {
   if (p.m == 0) {
-    hipLaunchKernelGGL(k_xent_zero, dim3(unsigned(p.n), unsigned((p.k + 255) / 256)), dim3(256), 0, s,
-                       static_cast<uint16_t*>(dw), lddw, int32_t(p.k));
+    hipLaunchKernelGGL(k_xent_zero, dim3(unsigned(p.n < 4096 ? p.n : 4096), unsigned((p.k + 255) / 256)), dim3(256), 0,
+                       s, static_cast<uint16_t*>(dw), p.n, lddw, int32_t(p.k));
     return hipGetLastError();
   }
   XentTile t{};

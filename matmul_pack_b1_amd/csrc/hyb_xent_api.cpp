@@ -10,7 +10,7 @@ using hyb::ok;
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Largest rows x k the kernels' 32-bit panel and tile numbers cover.
-constexpr int64_t kMaxVocab = int64_t(1) << 30;
+constexpr int64_t kMaxVocab = hyb::kF8MaxRows;
 constexpr int32_t kMaxTokens = 1 << 22;
 constexpr int64_t kMaxK = int64_t(1) << 21;
 
@@ -48,7 +48,7 @@ hyb_status check_head(const hyb_head* h, bool streams) {
     }
   }
   if (n < 1 || n > kMaxVocab || k < 1 || k > kMaxK)
-    return fail(HYB_ERR_SHAPE, "head %lld x %lld: need 1 <= n <= 2^30 and 1 <= k <= 2^21", (long long)n, (long long)k);
+    return fail(HYB_ERR_SHAPE, "head %lld x %lld: need 1 <= n <= 2^27 - 16 and 1 <= k <= 2^21", (long long)n, (long long)k);
   return HYB_OK;
 }
 
@@ -63,6 +63,8 @@ hyb_status check_call(const hyb_head* h, int64_t n_vocab, const void* x, int32_t
   if (h->layout && dt != h->layout->dtype)
     return fail(HYB_ERR_DTYPE, "x_dtype %d differs from the head's type %d", dt, h->layout->dtype);
   if (m < 0 || m > kMaxTokens) return fail(HYB_ERR_SHAPE, "m = %d outside [0, %d]", m, kMaxTokens);
+  if (h->f8 && (n + 255) / 256 * ((int64_t(m) + 63) / 64) >= (int64_t(1) << 23))
+    return fail(HYB_ERR_UNSUPPORTED, "n x m = %lld x %d is too large for one launch", (long long)n, m);
   if (m == 0) return HYB_OK;
   const uintptr_t align = h->f8 ? 2 : 16;
   if (!x || !aligned(x, align)) return fail(HYB_ERR_INVALID_ARG, "x is NULL or not %d-byte aligned", int(align));

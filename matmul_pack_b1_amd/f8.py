@@ -12,13 +12,18 @@ memory and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
+
+import torch
 
 from . import binding as hb
 
 WEIGHT, ROWS = 1, 2   # HYB_F8_WEIGHT, HYB_F8_ROWS
-EXPORTED = ("hyb_f8_size", "hyb_f8_quantize", "hyb_f8_dequantize", "hyb_f8_gemm_workspace_size", "hyb_f8_gemm")
+EXPORTED = ("hyb_f8_size", "hyb_f8_quantize", "hyb_f8_dequantize", "hyb_f8_gemm_workspace_size", "hyb_f8_gemm",
+            "hyb_f8_linear_workspace_size", "hyb_f8_linear")
 KIND_NAMES = {WEIGHT: "weight", ROWS: "rows"}
 
 
@@ -40,18 +45,36 @@ def lib() -> ctypes.CDLL:
         L.hyb_f8_dequantize.argtypes = [M, I64, I64, P, I32, I64, P]
         L.hyb_f8_gemm_workspace_size.argtypes = [I64, I64, I32, ctypes.POINTER(SZ)]
         L.hyb_f8_gemm.argtypes = [M, I64, I64, M, I32, P, I32, I64, P, SZ, P]
+        L.hyb_f8_linear_workspace_size.argtypes = [I64, I64, I32, ctypes.POINTER(SZ)]
+        L.hyb_f8_linear.argtypes = [M, I64, I64, P, I32, I32, I64, P, I32, I64, P, SZ, P]
         for name in EXPORTED:
             getattr(L, name).restype = I32
         _ready = True
     return L
 
 
+_CODES = {torch.float16: hb.HYB_F16, torch.bfloat16: hb.HYB_BF16, torch.float32: hb.HYB_F32}
+
+
 def _code(dtype) -> int:
-    torch = hb._torch()
-    try:
-        return {torch.float16: hb.HYB_F16, torch.bfloat16: hb.HYB_BF16, torch.float32: hb.HYB_F32}[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype}: float16, bfloat16 or float32") from None
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: float16, bfloat16 or float32")
+    return code
+
+
+def _on(device):
+    """Makes `device` current for a call (a decode step's calls are short: no
+    switch where it is already)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+# torch's current-stream handle without building a Stream object (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device):
+    return _raw_stream(device.index) if _raw_stream else hb._stream(device)
 
 
 def _pitch(t, k) -> int:
@@ -64,6 +87,21 @@ def sizes(rows: int, k: int) -> tuple[int, int]:
     a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
     hb.check(lib().hyb_f8_size(int(rows), int(k), ctypes.byref(a), ctypes.byref(b)), "hyb_f8_size")
     return int(a.value), int(b.value)
+
+
+@lru_cache(maxsize=4096)
+def _sizes(rows, k):
+    return sizes(rows, k)
+
+
+@lru_cache(maxsize=4096)
+def _ws_bytes(linear, n, k, m, index):
+    """Workspace bytes of a product on device `index` (a function of the shape
+    and the device's compute units)."""
+    nbytes = ctypes.c_size_t(0)
+    name = "hyb_f8_linear_workspace_size" if linear else "hyb_f8_gemm_workspace_size"
+    hb.check(getattr(lib(), name)(n, k, m, ctypes.byref(nbytes)), name)
+    return int(nbytes.value)
 
 
 @dataclass
@@ -92,17 +130,16 @@ def _check_matrix(Q, kind, name):
         raise TypeError(f"{name} must be an F8Matrix")
     if Q.kind != kind:
         raise TypeError(f"{name} is quantised as {KIND_NAMES[Q.kind]}, expected {KIND_NAMES[kind]}")
-    need = sizes(*Q.shape)
+    need = _sizes(*Q.shape)
     if (Q.codes.numel(), Q.scales.numel()) != need:
         raise ValueError(f"{name}: buffers of {(Q.codes.numel(), Q.scales.numel())} bytes, its shape needs {need}")
 
 
 def _quantize(a, kind, out, name):
-    torch = hb._torch()
     hb._check_2d(a, name)
     code = _code(a.dtype)
     rows, k = a.shape
-    nc, ns = sizes(rows, k)
+    nc, ns = _sizes(rows, k)
     if out is not None:
         _check_matrix(out, kind, "out")
         if tuple(out.shape) != (rows, k):
@@ -115,9 +152,9 @@ def _quantize(a, kind, out, name):
         if out.codes.device != a.device:
             raise ValueError(f"out is on {out.codes.device}, {name} on {a.device}")
         out.dtype = a.dtype
-    with torch.cuda.device(a.device):
-        hb.check(lib().hyb_f8_quantize(hb._ptr(a), code, rows, k, _pitch(a, k), kind, ctypes.byref(out.struct()),
-                                       hb._stream(a.device)), "hyb_f8_quantize")
+    with _on(a.device):
+        hb.check(lib().hyb_f8_quantize(hb._ptr(a), code, rows, k, _pitch(a, k), kind, out.struct(),
+                                       _stream(a.device)), "hyb_f8_quantize")
     return out
 
 
@@ -136,7 +173,6 @@ def quant(x, out: F8Matrix | None = None) -> F8Matrix:
 def unpack(Q: F8Matrix, out_dtype=None, out=None):
     """The values the codes of Q stand for (default dtype: that of the matrix
     it was made from, which holds them exactly)."""
-    torch = hb._torch()
     if not isinstance(Q, F8Matrix):
         raise TypeError("Q must be an F8Matrix")
     _check_matrix(Q, Q.kind, "Q")
@@ -149,34 +185,33 @@ def unpack(Q: F8Matrix, out_dtype=None, out=None):
         out = torch.empty((rows, k), dtype=tdt, device=Q.device)
     hb._check_out(out, (rows, k), tdt)
     hb._check_gpu(out, "out", Q.device)
-    with torch.cuda.device(Q.device):
-        hb.check(lib().hyb_f8_dequantize(ctypes.byref(Q.struct()), rows, k, hb._ptr(out), code, _pitch(out, k),
-                                         hb._stream(Q.device)), "hyb_f8_dequantize")
+    with _on(Q.device):
+        hb.check(lib().hyb_f8_dequantize(Q.struct(), rows, k, hb._ptr(out), code, _pitch(out, k),
+                                         _stream(Q.device)), "hyb_f8_dequantize")
     return out
 
 
-def workspace_bytes(Q: F8Matrix, m: int) -> int:
-    """Workspace bytes of hyb_f8_gemm for m tokens on the current device."""
-    nbytes = ctypes.c_size_t(0)
-    hb.check(lib().hyb_f8_gemm_workspace_size(Q.shape[0], Q.shape[1], int(m), ctypes.byref(nbytes)),
-             "hyb_f8_gemm_workspace_size")
-    return int(nbytes.value)
+def workspace_bytes(Q: F8Matrix, m: int, quantised: bool = False) -> int:
+    """Workspace bytes of gemm() for m tokens on the current device; with
+    `quantised`, for activations that quant() gave."""
+    return _ws_bytes(not quantised, Q.shape[0], Q.shape[1], int(m), torch.cuda.current_device()
+                     if torch.cuda.is_available() else -1)
 
 
 def gemm(Q: F8Matrix, x, out_dtype=None, out=None, workspace=None):
     """Y = X Q^T for any number of tokens (fp32 by default, or float16 /
     bfloat16).  x: activations (m x k; quantised here, for this call) or what
-    quant() gave.  The workspace of a product that cuts k comes from torch's
-    allocator unless `workspace` (a contiguous device tensor of at least
-    workspace_bytes(Q, m) bytes) is given."""
-    torch = hb._torch()
+    quant() gave.  The workspace comes from torch's allocator unless
+    `workspace` (a contiguous device tensor of at least workspace_bytes(Q, m)
+    bytes) is given."""
     _check_matrix(Q, WEIGHT, "Q")
     n, k = Q.shape
-    if not isinstance(x, F8Matrix):
-        hb._check_2d(x, "x")
-        _code(x.dtype)
-    else:
+    quantised = isinstance(x, F8Matrix)
+    if quantised:
         _check_matrix(x, ROWS, "x")
+    else:
+        hb._check_2d(x, "x")
+        xcode = _code(x.dtype)
     if x.shape[1] != k:
         raise ValueError(f"x has {x.shape[1]} columns, the weight has k = {k}")
     m = x.shape[0]
@@ -184,26 +219,32 @@ def gemm(Q: F8Matrix, x, out_dtype=None, out=None, workspace=None):
         out_dtype = out.dtype
     tdt = out_dtype if out_dtype is not None else torch.float32
     code = _code(tdt)
+    device = Q.codes.device
     if out is not None:
         hb._check_out(out, (m, n), tdt)
-    if isinstance(x, F8Matrix):
-        if x.device != Q.device:
-            raise ValueError(f"x is on {x.device}, Q on {Q.device}")
+    if quantised:
+        if x.device != device:
+            raise ValueError(f"x is on {x.device}, Q on {device}")
     else:
-        hb._check_gpu(x, "x", Q.device)
+        hb._check_gpu(x, "x", device)
     if out is None:
-        out = torch.empty((m, n), dtype=tdt, device=Q.device)
-    hb._check_gpu(out, "out", Q.device)
-    X = x if isinstance(x, F8Matrix) else quant(x)
-    with torch.cuda.device(Q.device):
+        out = torch.empty((m, n), dtype=tdt, device=device)
+    hb._check_gpu(out, "out", device)
+    with _on(device):
         if workspace is None:
-            need = workspace_bytes(Q, m)
-            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+            nbytes = _ws_bytes(not quantised, n, k, m, device.index)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         else:
-            hb._check_gpu(workspace, "workspace", Q.device)
+            hb._check_gpu(workspace, "workspace", device)
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
-        nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        hb.check(lib().hyb_f8_gemm(ctypes.byref(Q.struct()), n, k, ctypes.byref(X.struct()), m, hb._ptr(out), code,
-                                   _pitch(out, n), hb._ptr(workspace), nbytes, hb._stream(Q.device)), "hyb_f8_gemm")
+            nbytes = workspace.numel() * workspace.element_size()
+        ws, stream = hb._ptr(workspace), _stream(device)
+        if quantised:
+            st = lib().hyb_f8_gemm(Q.struct(), n, k, x.struct(), m, hb._ptr(out), code, _pitch(out, n), ws, nbytes, stream)
+        else:
+            st = lib().hyb_f8_linear(Q.struct(), n, k, hb._ptr(x), xcode, m, _pitch(x, k), hb._ptr(out), code,
+                                     _pitch(out, n), ws, nbytes, stream)
+    if st:
+        hb.check(st, "hyb_f8_gemm" if quantised else "hyb_f8_linear")
     return out

@@ -114,11 +114,11 @@ def loss(P, x, target, n_vocab=None, ignore_index=-100, workspace=None):
     head, n, k, m, n_vocab = _check(P, x, target, n_vocab)
     out = torch.empty(m, dtype=torch.float32, device=x.device)
     lse = torch.empty(m, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
+    with f8._on(x.device):
         ws, nbytes = _workspace(P, m, False, False, workspace, x.device)
         hb.check(lib().hyb_xent(ctypes.byref(head), n_vocab, hb._ptr(x), f8._code(x.dtype), m, f8._pitch(x, k),
                                 hb._ptr(target), int(ignore_index), hb._ptr(out), hb._ptr(lse), hb._ptr(ws), nbytes,
-                                hb._stream(x.device)), "hyb_xent")
+                                f8._stream(x.device)), "hyb_xent")
     return out, lse
 
 
@@ -143,11 +143,11 @@ def backward(P, x, target, lse, grad, n_vocab=None, ignore_index=-100, need_dx=T
         if t is not None:
             hb._check_out(t, shape, x.dtype, name)
             hb._check_gpu(t, name, x.device)
-    with torch.cuda.device(x.device):
+    with f8._on(x.device):
         ws, nbytes = _workspace(P, m, need_dx, need_dw, workspace, x.device)
         hb.check(lib().hyb_xent_backward(
             ctypes.byref(head), n_vocab, hb._ptr(x), f8._code(x.dtype), m, f8._pitch(x, k), hb._ptr(target),
             int(ignore_index), hb._ptr(lse), hb._ptr(grad), hb._ptr(dx), f8._pitch(dx, k) if need_dx else 0,
-            hb._ptr(dw), f8._pitch(dw, k) if need_dw else 0, hb._ptr(ws), nbytes, hb._stream(x.device)),
+            hb._ptr(dw), f8._pitch(dw, k) if need_dw else 0, hb._ptr(ws), nbytes, f8._stream(x.device)),
             "hyb_xent_backward")
     return dx, dw

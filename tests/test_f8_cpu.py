@@ -77,7 +77,7 @@ def test_size_refusals():
     assert _status(L.hyb_f8_size(-1, 8, ctypes.byref(n), ctypes.byref(n))) == 2
     assert _status(L.hyb_f8_size(8, -1, ctypes.byref(n), ctypes.byref(n))) == 2
     assert _status(L.hyb_f8_size(8, (1 << 22) + 1, ctypes.byref(n), ctypes.byref(n))) == 2
-    assert _status(L.hyb_f8_size(1 << 31, 8, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_f8_size(1 << 27, 8, ctypes.byref(n), ctypes.byref(n))) == 2
     assert _status(L.hyb_f8_size(8, 8, None, ctypes.byref(n))) == 1
     assert _status(L.hyb_f8_gemm_workspace_size(8, 8, -1, ctypes.byref(n))) == 2
     assert _status(L.hyb_f8_gemm_workspace_size(8, 8, 1, None)) == 1
@@ -102,7 +102,7 @@ def test_quantise_refusals(args, status):
 @pytest.mark.parametrize("args,status", [
     (dict(y_dtype=0), 3), (dict(n=-1), 2), (dict(k=-1), 2), (dict(m=-1), 2), (dict(y=None), 1), (dict(y=P16 + 2), 1),
     (dict(ldy=7), 1), (dict(w=(None, P16)), 1), (dict(x=(P16, None)), 1), (dict(w=(P16 + 1, P16)), 1),
-    (dict(ws=None, nbytes=64), 1), (dict(ws=P16 + 8, nbytes=64), 1), (dict(n=2 ** 31 - 16, m=2 ** 31 - 1, ldy=2 ** 31), 4),
+    (dict(ws=None, nbytes=64), 1), (dict(ws=P16 + 8, nbytes=64), 1), (dict(n=2 ** 27 - 16, m=2 ** 20, ldy=2 ** 31), 4),
 ])
 def test_gemm_refusals(args, status):
     d = dict(w=(P16, P16), n=8, k=256, x=(P16, P16), m=2, y=P16, y_dtype=hb.HYB_F32, ldy=8, ws=None, nbytes=0)
@@ -112,8 +112,24 @@ def test_gemm_refusals(args, status):
     assert _status(st) == status
 
 
+@pytest.mark.parametrize("args,status", [
+    (dict(dt=0), 3), (dict(y_dtype=9), 3), (dict(n=-1), 2), (dict(k=(1 << 22) + 1), 2), (dict(m=-1), 2),
+    (dict(x=None), 1), (dict(x=P16 + 1), 1), (dict(ldx=255), 1), (dict(y=None), 1), (dict(ldy=7), 1),
+    (dict(w=(None, P16)), 1), (dict(ws=None), 1), (dict(ws=P16 + 8), 1), (dict(nbytes=4000), 1),
+])
+def test_linear_refusals(args, status):
+    d = dict(w=(P16, P16), n=8, k=256, x=P16, dt=hb.HYB_BF16, m=2, ldx=256, y=P16, y_dtype=hb.HYB_F32, ldy=8, ws=P16,
+             nbytes=1 << 30)
+    d.update(args)
+    st = f8.lib().hyb_f8_linear(_m(*d["w"]), d["n"], d["k"], d["x"], d["dt"], d["m"], d["ldx"], d["y"], d["y_dtype"],
+                                d["ldy"], d["ws"], d["nbytes"], None)
+    assert _status(st) == status
+
+
 def test_empty_calls_do_nothing():
     L = f8.lib()
+    assert L.hyb_f8_linear(None, 8, 8, None, hb.HYB_BF16, 0, 8, None, hb.HYB_F32, 8, None, 0, None) == 0
+    assert L.hyb_f8_linear(None, 0, 8, None, hb.HYB_BF16, 4, 8, None, hb.HYB_F32, 0, None, 0, None) == 0
     assert L.hyb_f8_quantize(None, hb.HYB_F32, 0, 8, 8, f8.ROWS, None, None) == 0
     assert L.hyb_f8_quantize(None, hb.HYB_F32, 8, 0, 0, f8.ROWS, None, None) == 0
     assert L.hyb_f8_gemm(None, 8, 8, None, 0, None, hb.HYB_F32, 8, None, 0, None) == 0

@@ -256,3 +256,19 @@ def test_two_streams():
     torch.cuda.synchronize()
     for i, w_ in enumerate(want):
         assert all(torch.equal(g, w_) for g in got[i]), i
+
+
+@pytest.mark.parametrize("m", [1, 16, 70, 300, 2100])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_one_call_is_quantise_then_product(m, dtype):
+    n, k = 1100, 3000
+    x, w = normal(m, m, k, dtype), normal(3, n, k, dtype, 0.05)
+    Q = f8.pack(w)
+    for dt in (torch.float32, torch.bfloat16):
+        want = f8.gemm(Q, f8.quant(x), out_dtype=dt)
+        assert torch.equal(f8.gemm(Q, x, out_dtype=dt), want)
+        ws = torch.full((f8.workspace_bytes(Q, m),), 0xFF, dtype=torch.uint8, device="cuda")
+        assert torch.equal(f8.gemm(Q, x, out_dtype=dt, workspace=ws), want)
+        wide = torch.zeros(m, k + 3, dtype=DT[dtype], device="cuda")
+        wide[:, :k] = x
+        assert torch.equal(f8.gemm(Q, wide[:, :k], out_dtype=dt), want)

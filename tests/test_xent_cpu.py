@@ -83,7 +83,8 @@ BOTH_REFUSALS = [
     (dict(head=lambda: packed_head(streams=False)), 1), (dict(head=lambda: f8_head(codes=None)), 1),
     (dict(head=lambda: f8_head(codes=P16 + 4)), 1), (dict(head=lambda: f8_head(n=0)), 2),
     (dict(head=lambda: f8_head(k=0)), 2), (dict(head=lambda: f8_head(k=(1 << 21) + 1)), 2),
-    (dict(head=lambda: f8_head(n=(1 << 30) + 1)), 2), (dict(head=lambda: xent.HybHead()), 1),
+    (dict(head=lambda: f8_head(n=(1 << 27))), 2), (dict(head=lambda: xent.HybHead()), 1),
+    (dict(head=lambda: f8_head(n=(1 << 27) - 16, k=128), m=1 << 20), 4),
     (dict(head=lambda: packed_head(b1=80, n=240, k=128), n_vocab=240), 4),
 ]
 
