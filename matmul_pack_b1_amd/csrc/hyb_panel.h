@@ -5,7 +5,7 @@
 // or 64 columns of 16-bit values, in two halves of 1 KiB of four 256-byte
 // units g of 16 bytes for each row r:
 //   8 bits   half h, unit g, row r: columns 64 h + 16 g + 0..15 at 256 g + 16 r
-//   16 bits  columns 32 h + 8 g + 0..7 at 256 g + 16 (r ^ 8 (g & 1))
+//   16 bits  columns 32 h + 8 g + 0..7 at 256 g + 16 r
 // Lane L of a wavefront takes row L%16 and unit L/16, which makes a half the
 // operand of a 16x16x32 matrix instruction (16 bits) and two halves that of a
 // 16x16x128 one (8 bits): a tile goes from memory to LDS as it lies and every
@@ -16,9 +16,11 @@
 // A 16-bit operand may also be read the other way round, its columns as the
 // product's rows and its rows as the summed index, with the transposing LDS
 // read (ds_read_b64_tr_b16: of 16 lanes, lane 4 i + c points at the four
-// columns 4 c.. of row i and lane j receives column j of rows 0..3).  The
-// exchange of rows 0..7 and 8..15 in odd units puts the eight 64-byte pieces
-// of 32 lanes on different banks.  A lane then holds, of the 32 rows of a
+// columns 4 c.. of row i and lane j receives column j of rows 0..3).  On its
+// way into LDS such an operand's rows 0..7 and 8..15 change places in odd
+// units, which puts the eight 64-byte pieces of 32 lanes on different banks.
+// (The straight read wants them in order: exchanged, its 1 KiB took 12 cycles
+// instead of 8.)  A lane then holds, of the 32 rows of a
 // half step, rows 16 (q/2) + 4 (q%2) + {0..3, 8..11}, q = L/16; where the other
 // operand is read straight, its columns are stored in that order.
 //
@@ -155,12 +157,6 @@ __device__ __forceinline__ void panel_block(int32_t g, int32_t na, int32_t nb, i
   ab = first + r % width;
 }
 
-// Byte offset of a lane's 16 bytes within a half.
-template <int KIND>
-__device__ __forceinline__ int panel_lane(int lane) {
-  return is_f8(KIND) ? lane * 16 : (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
-}
-
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
@@ -206,13 +202,14 @@ struct PanelTile {
     __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
       if constexpr (T) {
         constexpr int kChunks = P / 2;  // 32-column halves per panel
+        const int from = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
         const int64_t off = s * 4 * pitch + first * 512;
         const int64_t left = total - off;
         const srd4_t r = panel_srd(data + off, uint32_t(left < 0 ? 0 : left < (int64_t(1) << 31) ? left : (int64_t(1) << 31)));
 #pragma unroll
         for (int t = 0; t < LOADS; ++t) {
           const int c = wave * LOADS + t;
-          panel_dma16(r, dst + c * 1024, int32_t(c / kChunks * pitch) + c % kChunks * 1024 + lane * 16);
+          panel_dma16(r, dst + c * 1024, int32_t(c / kChunks * pitch) + c % kChunks * 1024 + from);
         }
       } else {
 #pragma unroll
@@ -269,7 +266,7 @@ struct PanelTile {
     const Feed<TA, AP, kLoadsA> fa(A, pa);
     const Feed<TB, BP, kLoadsB> fb(B, pb);
     const uint32_t base = panel_lds_addr(smem);
-    const int straight = panel_lane<KIND>(lane);
+    const int straight = lane * 16;
     const int ta0 = turn<AP>(lane, 0), ta1 = turn<AP>(lane, 1);
     const int tb0 = turn<BP>(lane, 0), tb1 = turn<BP>(lane, 1);
 

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void k_xent_pack_x(const uint16_t* __restrict_
   for (int h = 0; h < 2; ++h) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (live) u = *reinterpret_cast<const uint4*>(x + row * ldx + s * 64 + h * 32 + (lane >> 4) * 8);
-    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + panel_lane<HYB_BF16>(lane)) = u;
+    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16) = u;
   }
 }
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t
   const int q = lane >> 4, r = lane & 15;
   char* p = step + (q >> 1) * 1024 + (2 * (q & 1)) * 256;
   *reinterpret_cast<uint4*>(p + r * 16) = make_uint4(e[0], e[1], e[2], e[3]);
-  *reinterpret_cast<uint4*>(p + 256 + (r ^ 8) * 16) = make_uint4(e[4], e[5], e[6], e[7]);
+  *reinterpret_cast<uint4*>(p + 256 + r * 16) = make_uint4(e[4], e[5], e[6], e[7]);
 }
 
 // Rows v0.. of a packed matrix as panels (one wavefront per panel and step):
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ d
     const uint4* src = dense + (int64_t(ti) * b1 * b2 + int64_t(rs) * 16 * b2 + c * 1024) / 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint4*>(dst + h * 1024 + panel_lane<HYB_BF16>(lane)) = row_ok ? src[h * 64 + lane] : zero;
+      *reinterpret_cast<uint4*>(dst + h * 1024 + lane * 16) = row_ok ? src[h * 64 + lane] : zero;
     return;
   }
   uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
         const int q = lane >> 4, u = 2 * ((col >> 4) & 1) + (q & 1);
         if (tok < t.m16 && col < t.g_steps * 64)
           *reinterpret_cast<uint2*>(t.g + (int64_t(tok >> 4) * t.g_steps + (col >> 6)) * kPanelStep +
-                                    ((col & 32) >> 5) * 1024 + u * 256 + ((tok & 15) ^ (8 * (u & 1))) * 16 + (q >> 1) * 8) =
+                                    ((col & 32) >> 5) * 1024 + u * 256 + (tok & 15) * 16 + (q >> 1) * 8) =
               make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
       }
     }
