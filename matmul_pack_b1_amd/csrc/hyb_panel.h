@@ -61,6 +61,11 @@ struct PanelOperand {
   int32_t steps;          // steps per panel
   const uint32_t* scale;  // 8-bit operands only
   int64_t scale_pitch;    // words from four steps' scales to the next four's
+  // The dense stream of a packed matrix without sparse tiles (hyb.h), whose
+  // tiles are panels of their own (b1 / 16 of b2 / 64 steps): logarithms of b1
+  // and b2, and the operand's first row (a multiple of b1).
+  int32_t log_b1, log_b2, tiles_k;
+  int64_t row0;
 };
 
 __device__ __forceinline__ srd4_t panel_srd(const void* base, uint32_t bytes) {
@@ -163,8 +168,8 @@ typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 // LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, STAGES LDS
 // stages of one step each (transfers run STAGES - 1 steps ahead).  TA / TB:
 // that operand is read transposed (its "panels" here are blocks of 16 of its
-// columns).
-template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false>
+// columns).  TILED: A lies in tiles (PanelOperand).
+template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false, bool TILED = false>
 struct PanelTile {
   static_assert(STAGES == 2 || STAGES == 4, "a step's stage is an immediate of the loop unrolled by four");
   static constexpr int kWaves = WA * WB;
@@ -221,6 +226,48 @@ struct PanelTile {
     }
   };
 
+  // The same for A in the tiles of a dense stream: tile (tn, tk) is at
+  // (tn * tiles_k + tk) * b1 * b2 * 2 bytes, its panels of b2 / 64 steps one
+  // after the other.  A wavefront's four transfers are two panels of one step
+  // (straight) or two steps of one panel (transposed).
+  template <bool T, int P, int LOADS>
+  struct TiledFeed {
+    const char* data;
+    int64_t row0;
+    int32_t rows, steps, tiles_k, log_b1, log_b2, unit;
+
+    __device__ TiledFeed(const PanelOperand& o, int32_t p0, int wave) {
+      static_assert(LOADS == 4 && P == 16, "eight wavefronts, 256 rows or columns");
+      data = o.data;
+      rows = o.rows16;
+      steps = o.steps;
+      tiles_k = o.tiles_k;
+      log_b1 = o.log_b1;
+      log_b2 = o.log_b2;
+      row0 = o.row0;
+      unit = T ? p0 / 4 + (wave & 1) * 2 : (p0 + wave * 2) * 16;  // first step, or first row
+    }
+    __device__ __forceinline__ int64_t panel_at(int64_t row) const {
+      return ((((row >> log_b1) * tiles_k) << log_b1 << log_b2) + ((row & ((1 << log_b1) - 1)) << log_b2)) * 2;
+    }
+    __device__ __forceinline__ int64_t step_at(int32_t s) const {
+      const int shift = log_b2 - 6;
+      return (int64_t(s >> shift) << log_b1 << log_b2) * 2 + (s & ((1 << shift) - 1)) * 2048;
+    }
+    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
+      const int32_t row = T ? s * 64 + (wave >> 1) * 16 : unit;
+      const int32_t step = T ? unit : s;
+      const int32_t next = T ? int32_t(step_at(step + 1) - step_at(step)) : 32 << log_b2;
+      // a panel behind the operand, or a step behind the last, reads as zeros
+      const uint32_t bytes = row >= rows || step >= steps ? 0 : T && step + 1 >= steps ? 2048 : next + 2048;
+      const srd4_t r = panel_srd(data + (bytes ? panel_at(row0 + row) + step_at(step) : 0), bytes);
+      const int from = T ? (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16 : lane * 16;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        panel_dma16(r, dst + (wave * 4 + t) * 1024, (t >> 1) * next + (t & 1) * 1024 + from);
+    }
+  };
+
   // The two halves of panel p (of P) of a staged step.
   struct Halves {
     u32x4_t v[2];
@@ -263,7 +310,12 @@ struct PanelTile {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wa = wave % WA, wb = wave / WA;
-    const Feed<TA, AP, kLoadsA> fa(A, pa);
+    const auto fa = [&] {
+      if constexpr (TILED)
+        return TiledFeed<TA, AP, kLoadsA>(A, pa, wave);
+      else
+        return Feed<TA, AP, kLoadsA>(A, pa);
+    }();
     const Feed<TB, BP, kLoadsB> fb(B, pb);
     const uint32_t base = panel_lds_addr(smem);
     const int straight = lane * 16;

@@ -196,9 +196,9 @@ struct XentTile {
 
 // One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
 // leaves the softmax sums, true G.
-template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
+template <int KIND, int DT, bool GRAD, bool TILED, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, XentTile t) {
-  typedef PanelTile<KIND, AP, BP, WA, WB> T;
+  typedef PanelTile<KIND, AP, BP, WA, WB, 2, false, false, TILED> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
   int32_t ab, bb;
@@ -415,10 +415,10 @@ struct XentOut {
 // transposed, B = G), fp32, this workgroup's part of the steps, stored or
 // added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
 // transposed), 16-bit, scaled back by gtop.
-template <int DT, bool DX, int AP, int BP, int WA, int WB>
+template <int DT, bool DX, bool TILED, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (A.steps * 4 + AP - 1) / AP;
   const int32_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
@@ -514,35 +514,43 @@ hipError_t allow_lds(F* fn, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int KIND, int DT, bool GRAD, int AP, int BP, int WA, int WB>
+template <int KIND, int DT, bool GRAD, bool TILED, int AP, int BP, int WA, int WB>
 hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
-  typedef PanelTile<KIND, AP, BP, WA, WB> T;
-  const hipError_t e = allow_lds(&k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>, T::kLds);
+  typedef PanelTile<KIND, AP, BP, WA, WB, 2, false, false, TILED> T;
+  const hipError_t e = allow_lds(&k_xent_tile<KIND, DT, GRAD, TILED, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (W.rows16 + 16 * AP - 1) / (16 * AP), nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
-  hipLaunchKernelGGL((k_xent_tile<KIND, DT, GRAD, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB),
+  hipLaunchKernelGGL((k_xent_tile<KIND, DT, GRAD, TILED, AP, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB),
                      T::kLds, s, W, X, t);
   return hipGetLastError();
 }
 
-template <int DT, bool GRAD>
-hipError_t run_tiles(bool f8, int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
-  if (f8)
-    return bp == 16 ? run_tile<kF8Wide, DT, GRAD, 16, 16, 2, 4>(W, X, t, s)
-                    : run_tile<kF8Wide, DT, GRAD, 16, 4, 4, 2>(W, X, t, s);
-  return bp == 16 ? run_tile<DT, DT, GRAD, 16, 16, 2, 4>(W, X, t, s)
-                  : run_tile<DT, DT, GRAD, 16, 4, 4, 2>(W, X, t, s);
+// The operand form of a head: 8-bit panels, 16-bit panels, or the tiles of a
+// dense stream.
+enum class Form { kF8, kPanels, kTiles };
+
+template <int KIND, int DT, bool GRAD, bool TILED>
+hipError_t run_shape(int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
+  return bp == 16 ? run_tile<KIND, DT, GRAD, TILED, 16, 16, 2, 4>(W, X, t, s)
+                  : run_tile<KIND, DT, GRAD, TILED, 16, 4, 4, 2>(W, X, t, s);
 }
 
-template <int DT, bool DX, int AP, int BP, int WA, int WB>
+template <int DT, bool GRAD>
+hipError_t run_tiles(Form form, int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
+  if (form == Form::kF8) return run_shape<kF8Wide, DT, GRAD, false>(bp, W, X, t, s);
+  if (form == Form::kTiles) return run_shape<DT, DT, GRAD, true>(bp, W, X, t, s);
+  return run_shape<DT, DT, GRAD, false>(bp, W, X, t, s);
+}
+
+template <int DT, bool DX, bool TILED, int AP, int BP, int WA, int WB>
 hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                        hipStream_t s) {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX> T;
-  const hipError_t e = allow_lds(&k_xent_product<DT, DX, AP, BP, WA, WB>, T::kLds);
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED> T;
+  const hipError_t e = allow_lds(&k_xent_product<DT, DX, TILED, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (A.steps * 4 + AP - 1) / AP;
   const int64_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
-  hipLaunchKernelGGL((k_xent_product<DT, DX, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
+  hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
                      dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
   return hipGetLastError();
 }
@@ -581,11 +589,25 @@ hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtyp
   return hipGetLastError();
 }
 
-// The A operand of the logits product for a piece: an 8-bit head's own
-// panels, a packed head's expanded ones.
-PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t v0, int64_t rows, const char* panels) {
+// The form in which a piece of `rows` vocabulary rows is multiplied: a packed
+// head without sparse tiles is read where it lies (no copy: 93 us per
+// 32768 x 4096), unless the piece is the one that pads the vocabulary (its
+// padding has to read as zeros) and `zeros` asks for that.
+Form piece_form(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t v0, int64_t rows, bool zeros) {
+  if (p.f8) return Form::kF8;
+  return head.layout->n_sparse == 0 && !(zeros && v0 + rows > n_vocab) ? Form::kTiles : Form::kPanels;
+}
+
+// The A operand of the logits product for a piece in that form.
+PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, Form form, int64_t v0, int64_t rows,
+                           const char* panels) {
   const int32_t rows16 = int32_t((rows + 15) / 16 * 16);
-  if (!p.f8) return PanelOperand{panels, rows16, int32_t(p.steps), nullptr, 0};
+  if (form == Form::kTiles) {
+    const hyb_layout& L = *head.layout;
+    return PanelOperand{static_cast<const char*>(head.packed->dense), rows16, int32_t(p.steps), nullptr, 0,
+                        __builtin_ctz(L.b1), __builtin_ctz(L.b2), int32_t(L.tiles_k), v0};
+  }
+  if (form == Form::kPanels) return PanelOperand{panels, rows16, int32_t(p.steps), nullptr, 0};
   return PanelOperand{static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep, rows16,
                       int32_t(p.steps), static_cast<const uint32_t*>(head.f8->scales) + v0, f8_rows16(p.n)};
 }
@@ -618,13 +640,15 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
   } else {
     PanelOperand X;
     HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
-    const int64_t step = p.f8 ? n_vocab : p.piece;
+    // nothing is copied: one piece
+    const int64_t step = piece_form(head, p, n_vocab, 0, 0, false) != Form::kPanels ? n_vocab : p.piece;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
       const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
-      if (!p.f8) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, nullptr, ws + p.w, s));
+      const Form form = piece_form(head, p, n_vocab, v0, rows, false);
+      if (form == Form::kPanels) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, nullptr, ws + p.w, s));
       t.v0 = v0;
-      const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
-      HYB_TRY((run_tiles<DT, false>(p.f8, p.bp, W, X, t, s)));
+      const PanelOperand W = piece_operand(head, p, form, v0, rows, ws + p.w);
+      HYB_TRY((run_tiles<DT, false>(form, p.bp, W, X, t, s)));
       chunks = v0 / 256 + (W.rows16 + 255) / 256;
     }
   }
@@ -658,9 +682,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     const int32_t vsteps = int32_t((rows + 63) / 64);
     t.v0 = v0;
     t.g_steps = vsteps;
-    if (!p.f8 || dx) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, top, ws + p.w, s));
-    const PanelOperand W = piece_operand(head, p, v0, rows, ws + p.w);
-    HYB_TRY((run_tiles<DT, true>(p.f8, p.bp, W, X, t, s)));
+    const Form form = piece_form(head, p, n_vocab, v0, rows, true);
+    if (form == Form::kPanels || (p.f8 && dx)) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, top, ws + p.w, s));
+    const PanelOperand W = piece_operand(head, p, form, v0, rows, ws + p.w);
+    HYB_TRY((run_tiles<DT, true>(form, p.bp, W, X, t, s)));
     // G: tokens x entries, vsteps steps; W': entries x columns
     const PanelOperand G{ws + p.g, int32_t(p.m16), vsteps, nullptr, 0};
     if (dx) {
@@ -671,9 +696,14 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.first = v0 == 0;
       o.rows = int32_t(p.m);
       o.cols = krows;
-      const PanelOperand A{ws + p.w, int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), nullptr, 0};
-      HYB_TRY(p.bp == 16 ? (run_product<DT, true, 16, 16, 2, 4>(A, G, vsteps, p.parts, o, s))
-                         : (run_product<DT, true, 16, 4, 4, 2>(A, G, vsteps, p.parts, o, s)));
+      if (form == Form::kTiles) {
+        HYB_TRY(p.bp == 16 ? (run_product<DT, true, true, 16, 16, 2, 4>(W, G, vsteps, p.parts, o, s))
+                           : (run_product<DT, true, true, 16, 4, 4, 2>(W, G, vsteps, p.parts, o, s)));
+      } else {
+        const PanelOperand A{ws + p.w, int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), nullptr, 0};
+        HYB_TRY(p.bp == 16 ? (run_product<DT, true, false, 16, 16, 2, 4>(A, G, vsteps, p.parts, o, s))
+                           : (run_product<DT, true, false, 16, 4, 4, 2>(A, G, vsteps, p.parts, o, s)));
+      }
     }
     if (dw) {
       XentOut o{};
@@ -684,7 +714,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.cols = int32_t(p.k);
       o.live = n_vocab - v0;
       o.vec = reinterpret_cast<uintptr_t>(dw) % 8 == 0 && lddw % 4 == 0;
-      HYB_TRY((run_product<DT, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
+      HYB_TRY((run_product<DT, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
     }
   }
   if (dx) {

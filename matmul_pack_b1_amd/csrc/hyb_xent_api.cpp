@@ -63,7 +63,7 @@ hyb_status check_call(const hyb_head* h, int64_t n_vocab, const void* x, int32_t
   if (h->layout && dt != h->layout->dtype)
     return fail(HYB_ERR_DTYPE, "x_dtype %d differs from the head's type %d", dt, h->layout->dtype);
   if (m < 0 || m > kMaxTokens) return fail(HYB_ERR_SHAPE, "m = %d outside [0, %d]", m, kMaxTokens);
-  if (h->f8 && (n + 255) / 256 * ((int64_t(m) + 63) / 64) >= (int64_t(1) << 23))
+  if ((n + 255) / 256 * ((int64_t(m) + 63) / 64) >= (int64_t(1) << 23))
     return fail(HYB_ERR_UNSUPPORTED, "n x m = %lld x %d is too large for one launch", (long long)n, m);
   if (m == 0) return HYB_OK;
   const uintptr_t align = h->f8 ? 2 : 16;

@@ -33,9 +33,17 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   p.parts = 1;
   if (dx) {
     // The dX product has (k / 256) x (m / 256) tiles; its vocabulary is cut
-    // until the tiles fill the compute units.
+    // into the number of parts that keeps the compute units fullest (rounds of
+    // them per part; 1% a part for the sums it writes).
     const int64_t tiles = up(p.ksteps16 * 64, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp));
-    while (tiles * p.parts * 2 <= cus && p.parts < 32) p.parts *= 2;
+    double least = 1e300;
+    for (int parts = 1; parts <= 32; ++parts) {
+      const double cost = double(up(tiles * parts, cus) / cus) / parts * (1.0 + 0.01 * parts);
+      if (cost < least) {
+        least = cost;
+        p.parts = parts;
+      }
+    }
   }
   size_t at = 0;
   auto take = [&](int64_t bytes) {

@@ -33,7 +33,7 @@ def as64(t):
     return t.detach().cpu().double().numpy()
 
 
-def make(n, k, m, n_vocab, dtype, head="packed", tile=(64, 64), meta="idx2", seed=0, sigma=0.1, scale=1.0):
+def make(n, k, m, n_vocab, dtype, head="packed", tile=(64, 64), meta="idx2", seed=0, sigma=0.1, scale=1.0, sparse=0.5):
     g = torch.Generator().manual_seed(seed)
     w = (torch.randn(n, k, generator=g) * sigma).to(DT[dtype]).cuda()
     x = (torch.randn(m, k, generator=g) * scale).to(DT[dtype]).cuda()
@@ -41,7 +41,7 @@ def make(n, k, m, n_vocab, dtype, head="packed", tile=(64, 64), meta="idx2", see
     target[torch.rand(m, generator=g) < 0.2] = -100
     grad = torch.randn(m, generator=g) / max(m, 1)
     if head == "packed":
-        tmap = (torch.rand(n // tile[0], k // tile[1], generator=g) < 0.5).to(torch.uint8).numpy()
+        tmap = (torch.rand(n // tile[0], k // tile[1], generator=g) < sparse).to(torch.uint8).numpy()
         P = hb.pack(w, tmap, *tile, meta)
     else:
         P = f8.pack(w)
@@ -118,6 +118,21 @@ def test_packed_head(m, n, k, n_vocab):
 @pytest.mark.parametrize("m", [9, 200])
 def test_packed_forms(m, dtype, tile, meta):
     check(*make(768, 512, m, 700, dtype, tile=tile, meta=meta, seed=m), 700)
+
+
+@pytest.mark.parametrize("sparse", [0.0, 1.0])
+@pytest.mark.parametrize("tile", [(64, 64), (64, 256), (128, 128), (256, 64), (256, 256)])
+@pytest.mark.parametrize("m", [7, 70, 300])
+def test_heads_of_one_kind_of_tile(m, tile, sparse):
+    """No sparse tile: the dense stream is multiplied where it lies (but for
+    the piece that holds padding); no dense one."""
+    check(*make(1536, 768, m, 1536, "bf16", tile=tile, sparse=sparse, seed=m), 1536)
+    check(*make(1536, 512, m, 1400, "f16", tile=tile, sparse=sparse, seed=m), 1400)
+
+
+def test_dense_head_of_many_pieces():
+    check(*make(66048, 64, 70, 66000, "bf16", sparse=0.0, seed=1), 66000)
+    check(*make(66048, 320, 40, 66048, "bf16", sparse=0.0, seed=2), 66048)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
