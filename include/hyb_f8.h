@@ -17,10 +17,10 @@
  *
  * Product: Y[i, j] = sum_c X[i, c] W[j, c] over the values that the codes
  * stand for.  The products are exact and are summed in fp32, for an fp32
- * output without further loss.  For a 16-bit output of more than 64 tokens
- * the sums of 128 columns come from the 8-bit matrix instruction, which drops
- * bits of a product that lie far below the largest of the 128: an error of
- * at most 2^-11 of that largest product, ahead of the output's own rounding.
+ * output without further loss.  For a 16-bit output the sums of 128 columns
+ * may come from the 8-bit matrix instruction, which drops bits of a product
+ * that lie far below the largest of the 128: an error of at most 2^-11 of that
+ * largest product, ahead of the output's own rounding.
  *
  * Storage "HYB8", both kinds: rows are rounded up to 16 (a panel), columns to
  * 128 (a step); what is behind the matrix's edge holds code 0.

@@ -10,27 +10,37 @@ namespace {
 
 // ------------------------------------------------------ quantise, read back --
 
+// 16 bytes at any element's address (the hardware takes unaligned global
+// accesses; 77 x 1501 fp16, odd rows: 6.9 us element by element, see below).
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
+};
+
+struct __attribute__((packed, aligned(2))) Bytes8 {
+  uint32_t w[2];
+};
+
 // Eight columns c0.. of one row, as loaded (two elements to a word, or one
-// for fp32); zeros behind the row's end.  `vec`: every row starts 16-byte
-// aligned.
+// for fp32); zeros behind the row's end.
 template <int DT>
 struct Eight {
   uint32_t w[DT == HYB_F32 ? 8 : 4];
 };
 
 template <int DT>
-__device__ __forceinline__ Eight<DT> load8(const void* a, int64_t base, int32_t c0, int32_t k, bool vec) {
+__device__ __forceinline__ Eight<DT> load8(const void* a, int64_t base, int32_t c0, int32_t k) {
   Eight<DT> r;
   constexpr int kWords = DT == HYB_F32 ? 8 : 4;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) r.w[i] = 0;
   if (c0 >= k) return r;
-  if (vec && c0 + 8 <= k) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a) + (base + c0) * (DT == HYB_F32 ? 4 : 2));
+  if (c0 + 8 <= k) {
+    const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const char*>(a) + (base + c0) * (DT == HYB_F32 ? 4 : 2));
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 u = p[i];
-      r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+      const Bytes16 u = p[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = u.w[j];
     }
     return r;
   }
@@ -142,8 +152,7 @@ __device__ __forceinline__ uint2 codes8(const Eight<DT>& r, uint32_t e, bool mar
 // many bytes written (28672 x 8192 bf16: see the measurements).
 template <int DT, bool WEIGHT>
 __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* __restrict__ a, int64_t rows,
-                                                                    int32_t k, int64_t lda, int vec,
-                                                                    char* __restrict__ codes,
+                                                                    int32_t k, int64_t lda, char* __restrict__ codes,
                                                                     char* __restrict__ scales, int32_t panels,
                                                                     int32_t steps) {
   constexpr int kWaves = WEIGHT ? 8 : 4;
@@ -162,7 +171,7 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   uint32_t all = 0;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0, vec);
+    v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0);
   }
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
@@ -216,7 +225,7 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
 template <int DT>
 __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ codes,
                                                        const uint32_t* __restrict__ scales, int64_t rows, int32_t k,
-                                                       int64_t lda, int vec, void* __restrict__ a, int32_t panels,
+                                                       int64_t lda, void* __restrict__ a, int32_t panels,
                                                        int32_t steps) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t panel = int64_t(blockIdx.x) * 4 + wave;
@@ -249,19 +258,25 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ 
       const int32_t c0 = (s0 + s) * 128 + h * 64 + (lane >> 4) * 16;
       if (c0 >= k) continue;
       const int64_t at = row * lda + c0;
-      if (vec && c0 + 16 <= k) {
+      if (c0 + 16 <= k) {
+        Bytes16* p = reinterpret_cast<Bytes16*>(static_cast<char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
         if constexpr (DT == HYB_F32) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(static_cast<float*>(a) + at)[i] =
-                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        } else {
-          uint32_t o[8];
+          for (int i = 0; i < 4; ++i) {
+            Bytes16 o;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = round16<DT>(f[2 * i]) | uint32_t(round16<DT>(f[2 * i + 1])) << 16;
-          uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a) + at);
-          p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            for (int j = 0; j < 4; ++j) o.w[j] = __builtin_bit_cast(uint32_t, f[4 * i + j]);
+            p[i] = o;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            Bytes16 o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o.w[j] = round16<DT>(f[8 * i + 2 * j]) | uint32_t(round16<DT>(f[8 * i + 2 * j + 1])) << 16;
+            p[i] = o;
+          }
         }
       } else {
 #pragma unroll
@@ -277,22 +292,28 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ 
 struct F8Out {
   void* y;
   int64_t ldy;
-  int32_t n, m, ydt, vec;  // vec: four-element stores are aligned
+  int32_t n, m, ydt;
 };
 
 // Four outputs n..n+3 of token m.
 __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, f32x4_t v) {
   if (m >= o.m || n >= o.n) return;
   const int64_t at = m * o.ldy + n;
-  if (o.vec && n + 4 <= o.n) {
+  if (n + 4 <= o.n) {
     if (o.ydt == HYB_F32) {
-      *reinterpret_cast<f32x4_t*>(static_cast<float*>(o.y) + at) = v;
+      Bytes16 u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = v[e];  // (a bit cast of a vector's element reads element 0)
+        u.w[e] = __builtin_bit_cast(uint32_t, f);
+      }
+      *reinterpret_cast<Bytes16*>(static_cast<float*>(o.y) + at) = u;
     } else {
       uint16_t h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e] = o.ydt == HYB_BF16 ? round16<HYB_BF16>(v[e]) : round16<HYB_F16>(v[e]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.y) + at) =
-          make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+      *reinterpret_cast<Bytes8*>(static_cast<uint16_t*>(o.y) + at) =
+          Bytes8{{h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16}};
     }
     return;
   }
@@ -305,9 +326,25 @@ __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, 
 // WAVES wavefronts take four steps (512 columns) in turn, the codes straight
 // from memory to the operand registers.  Bound by the read of w, so the wide
 // kind costs nothing here and serves every output type.
-template <int BP, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOperand X, F8Out out) {
+//
+// XDT other than 0 (BP 1, at most kFusedTokens tokens): X is still in its own
+// type, and every wavefront quantises the columns it multiplies, while its
+// codes of w are on their way.  Per token that costs a wavefront about 60
+// instructions per four steps, a launch of its own 5 us: 14336x4096 at one
+// token 17.7 us in two launches.
+struct PlainRows {
+  const void* x;
+  int64_t ldx;
+  int32_t k;
+};
+constexpr int kFusedTokens = 4;
+
+template <int BP, int WAVES, int XDT = 0>
+__global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOperand X, PlainRows plain, F8Out out) {
   __shared__ f32x4_t part[WAVES][BP][64];
+  // codes of the wavefront's four steps, [step][token][128], and exponent bytes
+  __shared__ __attribute__((aligned(16))) char turn[XDT ? WAVES : 1][4 * kFusedTokens * 128];
+  __shared__ uint32_t exps[XDT ? WAVES : 1][kFusedTokens];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t pw = int32_t(blockIdx.x), px = int32_t(blockIdx.y) * BP, steps = W.steps;
@@ -317,7 +354,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
   __amdgpu_buffer_rsrc_t rx[BP];
 #pragma unroll
   for (int j = 0; j < BP; ++j) {
-    const bool ok = (px + j) * 16 < X.rows16;
+    const bool ok = !XDT && (px + j) * 16 < X.rows16;
     rx[j] = make_rsrc(X.data + (ok ? px + j : 0) * pitch, ok ? int32_t(pitch) : 0);
   }
   f32x4_t acc[BP];
@@ -332,17 +369,46 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
         a[t][h] = __builtin_bit_cast(
             u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, (s + t) * 2048 + h * 1024 + lane * 16, 0, HYB_W_AUX));
     const uint32_t sa = W.scale[int64_t(s >> 2) * W.scale_pitch + pw * 16 + (lane & 15)];
+    if constexpr (XDT != 0) {
+      // one wavefront writes and reads its own LDS: its accesses done suffices
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int r = 0; r < kFusedTokens; ++r) {
+        if (r >= out.m) break;
+        const Eight<XDT> v = load8<XDT>(plain.x, r * plain.ldx, s * 128 + lane * 8, plain.k);
+        uint32_t top = top_of<XDT>(v);
+        const bool mark = __any(top >= kF32Inf);
+        if (mark) top = top_finite<XDT>(v);
+        const uint32_t e = s + (lane >> 4) < steps ? block_exponent(max16(top)) : 127u;
+        *reinterpret_cast<uint2*>(turn[wave] + ((lane >> 4) * kFusedTokens + r) * 128 + (lane & 15) * 8) =
+            codes8<XDT>(v, e, mark);
+        const uint32_t word = __builtin_amdgcn_readlane(e, 0) | __builtin_amdgcn_readlane(e, 16) << 8 |
+                              __builtin_amdgcn_readlane(e, 32) << 16 | __builtin_amdgcn_readlane(e, 48) << 24;
+        if (lane == 0) exps[wave][r] = word;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 #pragma unroll
     for (int j = 0; j < BP; ++j) {
       const int32_t xr = (px + j) * 16 + (lane & 15);
-      const uint32_t sb = X.scale[int64_t(s >> 2) * X.scale_pitch + (xr < X.rows16 ? xr : 0)];
+      uint32_t sb;
+      if constexpr (XDT != 0)
+        sb = xr < out.m ? exps[wave][xr] : 127u;
+      else
+        sb = X.scale[int64_t(s >> 2) * X.scale_pitch + (xr < X.rows16 ? xr : 0)];
       auto step = [&](auto byte) {
         constexpr int t = decltype(byte)::value;
         u32x4_t b[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b[h] = __builtin_bit_cast(
-              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx[j], (s + t) * 2048 + h * 1024 + lane * 16, 0, 0));
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (XDT != 0)
+            b[h] = xr < out.m ? *reinterpret_cast<const u32x4_t*>(turn[wave] + (t * kFusedTokens + xr) * 128 + h * 64 +
+                                                                  (lane >> 4) * 16)
+                              : u32x4_t{0, 0, 0, 0};
+          else
+            b[h] = __builtin_bit_cast(
+                u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx[j], (s + t) * 2048 + h * 1024 + lane * 16, 0, 0));
+        }
         acc[j] = panel_mfma<kF8Wide, t>(panel_regs<kF8Wide, t>(a[t][0], a[t][1], sa),
                                         panel_regs<kF8Wide, t>(b[0], b[1], sb), acc[j], sa, sb);
       };
@@ -460,23 +526,47 @@ hipError_t launch_route(const F8Route& r, const PanelOperand& W, const PanelOper
   return launch_tile<KIND, 8, 8, 2, 4, 4>(W, X, o, r, ws, s);
 }
 
+template <int XDT>
+void launch_fused(const PanelOperand& W, const PlainRows& x, const F8Out& o, hipStream_t s) {
+  hipLaunchKernelGGL((k_f8_rows<1, 8, XDT>), dim3(unsigned(W.rows16 / 16)), dim3(512), 0, s, W, PanelOperand{}, x, o);
+}
+
 }  // namespace
+
+bool f8_fused(int64_t n, int64_t k, int64_t m, int y_dtype) {
+  if (m > kFusedTokens || k == 0) return false;
+  const F8Route r = f8_route(n, k, m, y_dtype == HYB_F32, device_cus());
+  return r.waves == 8 && r.bp == 1;
+}
+
+hipError_t launch_f8_fused(const hyb_f8& w, int64_t n, int64_t k, const void* x, int x_dtype, int64_t m, int64_t ldx,
+                           void* y, int y_dtype, int64_t ldy, hipStream_t s) {
+  const PanelOperand W{static_cast<const char*>(w.codes), int32_t(f8_rows16(n)), int32_t(f8_steps(k)),
+                       static_cast<const uint32_t*>(w.scales), f8_rows16(n)};
+  const F8Out o{y, ldy, int32_t(n), int32_t(m), y_dtype};
+  const PlainRows p{x, ldx, int32_t(k)};
+  if (x_dtype == HYB_F32)
+    launch_fused<HYB_F32>(W, p, o, s);
+  else if (x_dtype == HYB_BF16)
+    launch_fused<HYB_BF16>(W, p, o, s);
+  else
+    launch_fused<HYB_F16>(W, p, o, s);
+  return hipGetLastError();
+}
 
 hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k, int64_t lda, int kind,
                               const hyb_f8& dst, hipStream_t s) {
   const int32_t panels = int32_t(f8_rows16(rows) / 16), steps = int32_t(f8_steps(k));
-  const int esize = dtype == HYB_F32 ? 4 : 2;
-  const int vec = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda * esize % 16 == 0;
   const unsigned quads = unsigned((steps + 3) / 4);
   const dim3 grid = kind == HYB_F8_WEIGHT ? dim3(unsigned((panels + 7) / 8), quads) : dim3(unsigned(panels), (quads + 3) / 4);
   char* codes = static_cast<char*>(dst.codes);
   char* scales = static_cast<char*>(dst.scales);
 #define HYB_F8_QUANT(DT)                                                                                             \
   if (kind == HYB_F8_WEIGHT)                                                                                         \
-    hipLaunchKernelGGL((k_f8_quantize<DT, true>), grid, dim3(512), 0, s, a, rows, int32_t(k), lda, vec, codes,       \
+    hipLaunchKernelGGL((k_f8_quantize<DT, true>), grid, dim3(512), 0, s, a, rows, int32_t(k), lda, codes,            \
                        scales, panels, steps);                                                                       \
   else                                                                                                               \
-    hipLaunchKernelGGL((k_f8_quantize<DT, false>), grid, dim3(256), 0, s, a, rows, int32_t(k), lda, vec, codes,      \
+    hipLaunchKernelGGL((k_f8_quantize<DT, false>), grid, dim3(256), 0, s, a, rows, int32_t(k), lda, codes,           \
                        scales, panels, steps)
   if (dtype == HYB_F32) {
     HYB_F8_QUANT(HYB_F32);
@@ -492,28 +582,24 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
 hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void* a, int dtype, int64_t lda,
                                 hipStream_t s) {
   const int32_t panels = int32_t(f8_rows16(rows) / 16), steps = int32_t(f8_steps(k));
-  const int esize = dtype == HYB_F32 ? 4 : 2;
-  const int vec = reinterpret_cast<uintptr_t>(a) % 16 == 0 && lda * esize % 16 == 0;
   const dim3 grid(unsigned((panels + 3) / 4), unsigned((steps + 3) / 4));
   const char* codes = static_cast<const char*>(src.codes);
   const uint32_t* scales = static_cast<const uint32_t*>(src.scales);
   if (dtype == HYB_F32)
-    hipLaunchKernelGGL((k_f8_dequantize<HYB_F32>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda, vec, a,
+    hipLaunchKernelGGL((k_f8_dequantize<HYB_F32>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda, a,
                        panels, steps);
   else if (dtype == HYB_BF16)
-    hipLaunchKernelGGL((k_f8_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda, vec,
+    hipLaunchKernelGGL((k_f8_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda,
                        a, panels, steps);
   else
-    hipLaunchKernelGGL((k_f8_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda, vec, a,
+    hipLaunchKernelGGL((k_f8_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, rows, int32_t(k), lda, a,
                        panels, steps);
   return hipGetLastError();
 }
 
 hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x, int64_t m, void* y, int y_dtype,
                           int64_t ldy, float* ws, hipStream_t s) {
-  const int esize = y_dtype == HYB_F32 ? 4 : 2;
-  const F8Out o{y,      ldy, int32_t(n), int32_t(m), y_dtype,
-                reinterpret_cast<uintptr_t>(y) % (4 * esize) == 0 && ldy % 4 == 0};
+  const F8Out o{y, ldy, int32_t(n), int32_t(m), y_dtype};
   if (k == 0) {
     const int64_t blocks = (n * m + 255) / 256;
     hipLaunchKernelGGL(k_f8_zero, dim3(unsigned(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, o);
@@ -528,11 +614,11 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
   if (r.waves) {
     const dim3 grid(unsigned(W.rows16 / 16), unsigned((X.rows16 / 16 + r.bp - 1) / r.bp));
     if (r.bp == 1)
-      hipLaunchKernelGGL((k_f8_rows<1, 8>), grid, dim3(512), 0, s, W, X, o);
+      hipLaunchKernelGGL((k_f8_rows<1, 8>), grid, dim3(512), 0, s, W, X, PlainRows{}, o);
     else if (r.bp == 2)
-      hipLaunchKernelGGL((k_f8_rows<2, 8>), grid, dim3(512), 0, s, W, X, o);
+      hipLaunchKernelGGL((k_f8_rows<2, 8>), grid, dim3(512), 0, s, W, X, PlainRows{}, o);
     else
-      hipLaunchKernelGGL((k_f8_rows<4, 8>), grid, dim3(512), 0, s, W, X, o);
+      hipLaunchKernelGGL((k_f8_rows<4, 8>), grid, dim3(512), 0, s, W, X, PlainRows{}, o);
     return hipGetLastError();
   }
   return y_dtype == HYB_F32 ? launch_route<kF8Wide>(r, W, X, o, ws, s) : launch_route<kF8>(r, W, X, o, ws, s);

@@ -164,11 +164,14 @@ hyb_status hyb_f8_linear(const hyb_f8* w, int64_t n, int64_t k, const void* x, i
     return st;
   if (m == 0 || n == 0) return ok();
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (hyb::f8_fused(n, k, m, y_dtype))
+    return hyb::hip_status(hyb::launch_f8_fused(*w, n, k, x, x_dtype, m, ldx, y, y_dtype, ldy, s), "f8 product launch");
   if (k > 0) {
     st = hyb::hip_status(hyb::launch_f8_quantize(x, x_dtype, m, k, ldx, HYB_F8_ROWS, X, s), "f8 quantise launch");
     if (st != HYB_OK) return st;
   }
-  return hyb::hip_status(hyb::launch_f8_gemm(*w, n, k, X, m, y, y_dtype, ldy,
+  const hyb_f8 none{nullptr, nullptr};
+  return hyb::hip_status(hyb::launch_f8_gemm(k > 0 ? *w : none, n, k, X, m, y, y_dtype, ldy,
                                              need > used ? reinterpret_cast<float*>(at + used) : nullptr, s),
                          "f8 gemm launch");
 }

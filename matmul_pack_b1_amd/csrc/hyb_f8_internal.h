@@ -38,6 +38,11 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
                               const hyb_f8& dst, hipStream_t s);
 hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void* a, int dtype, int64_t lda,
                                 hipStream_t s);
+// Whether the product of activations still in their own type quantises them
+// itself (few tokens), and that product.
+bool f8_fused(int64_t n, int64_t k, int64_t m, int y_dtype);
+hipError_t launch_f8_fused(const hyb_f8& w, int64_t n, int64_t k, const void* x, int x_dtype, int64_t m, int64_t ldx,
+                           void* y, int y_dtype, int64_t ldy, hipStream_t s);
 // ws NULL runs the route unsplit.
 hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x, int64_t m, void* y, int y_dtype,
                           int64_t ldy, float* ws, hipStream_t s);
