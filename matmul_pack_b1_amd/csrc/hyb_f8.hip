@@ -170,9 +170,7 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   uint32_t top[16];
   uint32_t all = 0;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0);
-  }
+  for (int r = 0; r < 16; ++r) v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0);
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     top[r] = top_of<DT>(v[r]);
@@ -205,10 +203,15 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   uint32_t mine = 127;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
+    uint2* to = reinterpret_cast<uint2*>(turn + unit * 256 + ((r + unit) & 15) * 16 + (j & 1) * 8);
+    if (r0 + r >= rows) {  // uniform: a short last panel (decode) skips the arithmetic
+      *to = make_uint2(0, 0);
+      continue;
+    }
     if constexpr (!WEIGHT) top[r] = max16(top[r]);
     const uint32_t e = block_exponent(top[r]);
-    if (r == j) mine = r0 + r < rows && s0 + (lane >> 4) < steps ? e : 127u;
-    *reinterpret_cast<uint2*>(turn + unit * 256 + ((r + unit) & 15) * 16 + (j & 1) * 8) = codes8<DT>(v[r], e, mark);
+    if (r == j && s0 + (lane >> 4) < steps) mine = e;
+    *to = codes8<DT>(v[r], e, mark);
   }
   // one wavefront writes and reads `turn`: its own accesses done suffices
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -61,11 +61,15 @@ struct PanelOperand {
   int32_t steps;          // steps per panel
   const uint32_t* scale;  // 8-bit operands only
   int64_t scale_pitch;    // words from four steps' scales to the next four's
-  // The dense stream of a packed matrix without sparse tiles (hyb.h), whose
-  // tiles are panels of their own (b1 / 16 of b2 / 64 steps): logarithms of b1
-  // and b2, and the operand's first row (a multiple of b1).
-  int32_t log_b1, log_b2, tiles_k;
-  int64_t row0;
+  // Rows row0.. (a multiple of b1) of a packed matrix (hyb.h), whose tiles are
+  // panels of their own (b1 / 16 of b2 / 64 steps): `data` is the dense stream,
+  // where tile t lies in slot tidx[t] if that is one of n_dense; the other
+  // tiles, and those of tile rows that reach beyond row `plain`, lie in
+  // `spare` in the order of the tiles from row0 on (NULL: they read as zeros).
+  int32_t log_b1, log_b2, tiles_k, n_dense;
+  int64_t row0, plain;
+  const int32_t* tidx;
+  const char* spare;
 };
 
 __device__ __forceinline__ srd4_t panel_srd(const void* base, uint32_t bytes) {
@@ -226,45 +230,93 @@ struct PanelTile {
     }
   };
 
-  // The same for A in the tiles of a dense stream: tile (tn, tk) is at
-  // (tn * tiles_k + tk) * b1 * b2 * 2 bytes, its panels of b2 / 64 steps one
-  // after the other.  A wavefront's four transfers are two panels of one step
-  // (straight) or two steps of one panel (transposed).
+  // The same for A in tiles (PanelOperand).  A wavefront's four transfers are
+  // two panels of one step in one tile (straight), or two steps of one panel
+  // (transposed), each step in a tile column of its own.  The slots of 64
+  // tiles at a time (of a tile row, or of the two tile columns) are held in
+  // the lanes of a register.
   template <bool T, int P, int LOADS>
   struct TiledFeed {
-    const char* data;
-    int64_t row0;
-    int32_t rows, steps, tiles_k, log_b1, log_b2, unit;
+    const PanelOperand& o;
+    int32_t unit;         // first step (transposed) or first row (straight) of this wavefront
+    int32_t first;        // tile column (straight) or row whose slot lane 0 holds
+    int32_t slot0, slot1;
+    int32_t now;          // tile column or row that the addresses are of
+    const char *at0, *at1;
 
-    __device__ TiledFeed(const PanelOperand& o, int32_t p0, int wave) {
+    __device__ TiledFeed(const PanelOperand& op, int32_t p0, int wave)
+        : o(op), first(-64), slot0(-1), slot1(-1), now(-1), at0(nullptr), at1(nullptr) {
       static_assert(LOADS == 4 && P == 16, "eight wavefronts, 256 rows or columns");
-      data = o.data;
-      rows = o.rows16;
-      steps = o.steps;
-      tiles_k = o.tiles_k;
-      log_b1 = o.log_b1;
-      log_b2 = o.log_b2;
-      row0 = o.row0;
-      unit = T ? p0 / 4 + (wave & 1) * 2 : (p0 + wave * 2) * 16;  // first step, or first row
+      unit = T ? p0 / 4 + (wave & 1) * 2 : (p0 + wave * 2) * 16;
     }
-    __device__ __forceinline__ int64_t panel_at(int64_t row) const {
-      return ((((row >> log_b1) * tiles_k) << log_b1 << log_b2) + ((row & ((1 << log_b1) - 1)) << log_b2)) * 2;
+    // Address of tile (tn, tk) of the operand, or NULL.
+    __device__ __forceinline__ const char* tile_at(int32_t tn, int32_t tk, int32_t slot) const {
+      const bool dense = slot >= 0 && slot < o.n_dense && o.row0 + (int64_t(tn + 1) << o.log_b1) <= o.plain;
+      if (!dense && !o.spare) return nullptr;
+      const int64_t tile = dense ? slot : int64_t(tn) * o.tiles_k + tk;
+      return (dense ? o.data : o.spare) + (tile << (o.log_b1 + o.log_b2 + 1));
     }
-    __device__ __forceinline__ int64_t step_at(int32_t s) const {
-      const int shift = log_b2 - 6;
-      return (int64_t(s >> shift) << log_b1 << log_b2) * 2 + (s & ((1 << shift) - 1)) * 2048;
+    // Straight: on entering a tile column, the address of the first step there
+    // of this wavefront's first panel.
+    __device__ __forceinline__ void enter_column(int32_t tk, int lane) {
+      const int32_t tn = unit >> o.log_b1;
+      const bool live = unit < o.rows16;  // a panel behind the operand reads as zeros
+      if (tk < first || tk >= first + 64) {
+        first = tk;
+        const int64_t t = ((o.row0 >> o.log_b1) + tn) * o.tiles_k;
+        slot0 = live && tk + lane < o.tiles_k ? o.tidx[t + tk + lane] : -1;
+      }
+      const int32_t slot = __builtin_amdgcn_readlane(slot0, tk - first);
+      at0 = live ? tile_at(tn, tk, slot) : nullptr;
+      if (at0) at0 += int64_t(unit & ((1 << o.log_b1) - 1)) << (o.log_b2 + 1);
     }
-    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
-      const int32_t row = T ? s * 64 + (wave >> 1) * 16 : unit;
-      const int32_t step = T ? unit : s;
-      const int32_t next = T ? int32_t(step_at(step + 1) - step_at(step)) : 32 << log_b2;
-      // a panel behind the operand, or a step behind the last, reads as zeros
-      const uint32_t bytes = row >= rows || step >= steps ? 0 : T && step + 1 >= steps ? 2048 : next + 2048;
-      const srd4_t r = panel_srd(data + (bytes ? panel_at(row0 + row) + step_at(step) : 0), bytes);
-      const int from = T ? (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16 : lane * 16;
+    // Transposed: on entering a tile row, the addresses of this wavefront's two
+    // steps of the row's first panel.
+    __device__ __forceinline__ void enter_row(int32_t tn, int lane) {
+      const int shift = o.log_b2 - 6;
+      if (tn < first || tn >= first + 64) {
+        first = tn;
+        const int32_t rows = (o.rows16 + (1 << o.log_b1) - 1) >> o.log_b1;
+        const int64_t t = ((o.row0 >> o.log_b1) + tn + lane) * o.tiles_k;
+        const bool in = tn + lane < rows;
+        slot0 = in && unit < o.steps ? o.tidx[t + (unit >> shift)] : -1;
+        slot1 = in && unit + 1 < o.steps ? o.tidx[t + ((unit + 1) >> shift)] : -1;
+      }
+      const int32_t mask = (1 << shift) - 1;
+      const int32_t s0 = __builtin_amdgcn_readlane(slot0, tn - first), s1 = __builtin_amdgcn_readlane(slot1, tn - first);
+      at0 = unit < o.steps ? tile_at(tn, unit >> shift, s0) : nullptr;
+      at1 = unit + 1 < o.steps ? tile_at(tn, (unit + 1) >> shift, s1) : nullptr;
+      if (at0) at0 += (unit & mask) * 2048;
+      if (at1) at1 += ((unit + 1) & mask) * 2048;
+    }
+    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) {
+      if constexpr (T) {
+        const int32_t row = s * 64 + (wave >> 1) * 16, tn = row >> o.log_b1;
+        if (tn != now) {
+          now = tn;
+          enter_row(tn, lane);
+        }
+        const bool live = row < o.rows16;
+        const int32_t down = (row & ((1 << o.log_b1) - 1)) << (o.log_b2 + 1);
+        const srd4_t r0 = panel_srd(at0 + down, live && at0 ? 2048 : 0);
+        const srd4_t r1 = panel_srd(at1 + down, live && at1 ? 2048 : 0);
+        const int from = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
+        panel_dma16(r0, dst + (wave * 4) * 1024, from);
+        panel_dma16(r0, dst + (wave * 4 + 1) * 1024, 1024 + from);
+        panel_dma16(r1, dst + (wave * 4 + 2) * 1024, from);
+        panel_dma16(r1, dst + (wave * 4 + 3) * 1024, 1024 + from);
+      } else {
+        const int shift = o.log_b2 - 6;
+        if (s >> shift != now) {
+          now = s >> shift;
+          enter_column(now, lane);
+        }
+        const int32_t next = 32 << o.log_b2;  // the tile's next panel
+        const srd4_t r = panel_srd(at0 + (s & ((1 << shift) - 1)) * 2048, at0 ? next + 2048 : 0);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        panel_dma16(r, dst + (wave * 4 + t) * 1024, (t >> 1) * next + (t & 1) * 1024 + from);
+        for (int t = 0; t < 4; ++t)
+          panel_dma16(r, dst + (wave * 4 + t) * 1024, (t >> 1) * next + (t & 1) * 1024 + lane * 16);
+      }
     }
   };
 
@@ -310,7 +362,7 @@ struct PanelTile {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wa = wave % WA, wb = wave / WA;
-    const auto fa = [&] {
+    auto fa = [&] {
       if constexpr (TILED)
         return TiledFeed<TA, AP, kLoadsA>(A, pa, wave);
       else

@@ -59,14 +59,17 @@ __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t
   *reinterpret_cast<uint4*>(p + 256 + r * 16) = make_uint4(e[4], e[5], e[6], e[7]);
 }
 
-// Rows v0.. of a packed matrix as panels (one wavefront per panel and step):
-// a dense tile's chunks already are in panel order, a sparse chunk is
-// expanded from its values and codes.  Rows from n_vocab on are zero.
+// The tiles of rows v0.. of a packed matrix that are not multiplied where they
+// lie, into `out` in tile order (one wavefront per panel and step): sparse ones
+// expanded from their values and codes, those of a tile row that reaches into
+// the padding with its rows from n_vocab on zero, ones without a slot zero.
+// `plain` as in PanelOperand.
 __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ dense, const uint4* __restrict__ val,
                                                      const uint16_t* __restrict__ meta,
                                                      const int32_t* __restrict__ tidx, int b1, int b2, int meta_kind,
                                                      int32_t tiles_k, int32_t n_dense, int32_t n_sparse, int64_t v0,
-                                                     int64_t n_vocab, int32_t steps, char* __restrict__ out) {
+                                                     int64_t n_vocab, int64_t plain, int32_t steps,
+                                                     char* __restrict__ out) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t s = int32_t(blockIdx.y) * 4 + wave;
@@ -76,10 +79,12 @@ __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ d
   const int rs = int(r0 - tn * b1) / 16;              // slab within the tile
   const int spt = b2 / 64, c = s % spt;
   const int32_t ti = tidx[tn * tiles_k + s / spt];
-  char* dst = out + (int64_t(blockIdx.x) * steps + s) * kPanelStep;
+  const bool is_dense = ti >= 0 && ti < n_dense;
+  if (is_dense && (tn + 1) * b1 <= plain) return;
+  char* dst = out + ((tn - v0 / b1) * tiles_k + s / spt) * b1 * b2 * 2 + int64_t(rs) * 32 * b2 + c * kPanelStep;
   const bool row_ok = r0 + (lane & 15) < n_vocab;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (ti >= 0 && ti < n_dense) {
+  if (is_dense) {
     const uint4* src = dense + (int64_t(ti) * b1 * b2 + int64_t(rs) * 16 * b2 + c * 1024) / 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -292,12 +297,12 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
   }
 }
 
-// Softmax sums of rows of fp32 logits (few tokens), one workgroup per chunk of
-// 2048 entries and token.
+// Softmax sums of rows of fp32 logits (few tokens; the piece from t.v0, a
+// multiple of 2048), one workgroup per chunk of 2048 entries and token.
 __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
   __shared__ float2 sums[4];
   const int32_t tok = int32_t(blockIdx.y);
-  const int64_t v0 = int64_t(blockIdx.x) * 2048;
+  const int64_t v0 = t.v0 + int64_t(blockIdx.x) * 2048;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t want = t.target[tok];
   float v[8];
@@ -305,7 +310,7 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t c = v0 + i * 256 + threadIdx.x;
-    v[i] = c < t.n_vocab ? z[tok * ldz + c] : -__builtin_inff();
+    v[i] = c < t.n_vocab && c - t.v0 < ldz ? z[tok * ldz + c - t.v0] : -__builtin_inff();
     if (c == want && c < t.n_vocab) t.zt[tok] = v[i];
     top = v[i] > top || v[i] != v[i] ? v[i] : top;
   }
@@ -328,7 +333,7 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
       const float m = o.x > r.x || o.x != o.x ? o.x : r.x;
       r = make_float2(m, r.y * rescale(r.x, m) + o.y * rescale(o.x, m));
     }
-    t.part[blockIdx.x * int64_t(t.m16) + tok] = r;
+    t.part[v0 / 2048 * t.m16 + tok] = r;
   }
 }
 
@@ -525,10 +530,6 @@ hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, const XentTile
   return hipGetLastError();
 }
 
-// The operand form of a head: 8-bit panels, 16-bit panels, or the tiles of a
-// dense stream.
-enum class Form { kF8, kPanels, kTiles };
-
 template <int KIND, int DT, bool GRAD, bool TILED>
 hipError_t run_shape(int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
   return bp == 16 ? run_tile<KIND, DT, GRAD, TILED, 16, 16, 2, 4>(W, X, t, s)
@@ -536,10 +537,9 @@ hipError_t run_shape(int bp, const PanelOperand& W, const PanelOperand& X, const
 }
 
 template <int DT, bool GRAD>
-hipError_t run_tiles(Form form, int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
-  if (form == Form::kF8) return run_shape<kF8Wide, DT, GRAD, false>(bp, W, X, t, s);
-  if (form == Form::kTiles) return run_shape<DT, DT, GRAD, true>(bp, W, X, t, s);
-  return run_shape<DT, DT, GRAD, false>(bp, W, X, t, s);
+hipError_t run_tiles(const XentPlan& p, const PanelOperand& W, const PanelOperand& X, const XentTile& t,
+                     hipStream_t s) {
+  return p.f8 ? run_shape<kF8Wide, DT, GRAD, false>(p.bp, W, X, t, s) : run_shape<DT, DT, GRAD, true>(p.bp, W, X, t, s);
 }
 
 template <int DT, bool DX, bool TILED, int AP, int BP, int WA, int WB>
@@ -555,23 +555,26 @@ hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t ste
   return hipGetLastError();
 }
 
-// The piece of `rows` vocabulary rows from v0 as 16-bit panels in `out`.
+// What the products of the piece of `rows` vocabulary rows from v0 read beside
+// the head itself, in `out`: an 8-bit head as 16-bit panels (for dX), the
+// tiles of a packed head that PanelOperand calls spare.
 template <int DT>
-hipError_t piece_panels(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t v0, int64_t rows,
-                        const uint32_t* top, char* out, hipStream_t s) {
+hipError_t prepare_piece(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t plain, int64_t v0,
+                         int64_t rows, const uint32_t* top, char* out, hipStream_t s) {
   const unsigned panels = unsigned((rows + 15) / 16);
   if (p.f8) {
     hipLaunchKernelGGL((k_xent_widen<DT>), dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
                        static_cast<const char*>(head.f8->codes), static_cast<const uint32_t*>(head.f8->scales),
                        int32_t(f8_rows16(p.n)), v0, n_vocab, int32_t(p.steps), top, out);
-  } else {
-    const hyb_layout& L = *head.layout;
-    const hyb_packed& P = *head.packed;
-    hipLaunchKernelGGL(k_xent_expand, dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
-                       static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
-                       static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
-                       int32_t(L.n_dense), int32_t(L.n_sparse), v0, n_vocab, int32_t(p.steps), out);
+    return hipGetLastError();
   }
+  const hyb_layout& L = *head.layout;
+  const hyb_packed& P = *head.packed;
+  if (L.n_sparse == 0 && (v0 + rows + L.b1 - 1) / L.b1 * L.b1 <= plain) return hipSuccess;
+  hipLaunchKernelGGL(k_xent_expand, dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
+                     static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
+                     static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
+                     int32_t(L.n_dense), int32_t(L.n_sparse), v0, n_vocab, plain, int32_t(p.steps), out);
   return hipGetLastError();
 }
 
@@ -589,27 +592,29 @@ hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtyp
   return hipGetLastError();
 }
 
-// The form in which a piece of `rows` vocabulary rows is multiplied: a packed
-// head without sparse tiles is read where it lies (no copy: 93 us per
-// 32768 x 4096), unless the piece is the one that pads the vocabulary (its
-// padding has to read as zeros) and `zeros` asks for that.
-Form piece_form(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t v0, int64_t rows, bool zeros) {
-  if (p.f8) return Form::kF8;
-  return head.layout->n_sparse == 0 && !(zeros && v0 + rows > n_vocab) ? Form::kTiles : Form::kPanels;
-}
-
-// The A operand of the logits product for a piece in that form.
-PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, Form form, int64_t v0, int64_t rows,
-                           const char* panels) {
-  const int32_t rows16 = int32_t((rows + 15) / 16 * 16);
-  if (form == Form::kTiles) {
-    const hyb_layout& L = *head.layout;
-    return PanelOperand{static_cast<const char*>(head.packed->dense), rows16, int32_t(p.steps), nullptr, 0,
-                        __builtin_ctz(L.b1), __builtin_ctz(L.b2), int32_t(L.tiles_k), v0};
+// The A operand of the logits product for a piece.
+PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t plain, int64_t v0, int64_t rows,
+                           const char* spare) {
+  PanelOperand o{};
+  o.rows16 = int32_t((rows + 15) / 16 * 16);
+  o.steps = int32_t(p.steps);
+  if (p.f8) {
+    o.data = static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep;
+    o.scale = static_cast<const uint32_t*>(head.f8->scales) + v0;
+    o.scale_pitch = f8_rows16(p.n);
+    return o;
   }
-  if (form == Form::kPanels) return PanelOperand{panels, rows16, int32_t(p.steps), nullptr, 0};
-  return PanelOperand{static_cast<const char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep, rows16,
-                      int32_t(p.steps), static_cast<const uint32_t*>(head.f8->scales) + v0, f8_rows16(p.n)};
+  const hyb_layout& L = *head.layout;
+  o.data = static_cast<const char*>(head.packed->dense);
+  o.log_b1 = __builtin_ctz(L.b1);
+  o.log_b2 = __builtin_ctz(L.b2);
+  o.tiles_k = int32_t(L.tiles_k);
+  o.n_dense = int32_t(L.n_dense);
+  o.row0 = v0;
+  o.plain = plain;
+  o.tidx = head.packed->tidx;
+  o.spare = spare;
+  return o;
 }
 
 #define HYB_TRY(call)                      \
@@ -624,31 +629,46 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
   int64_t chunks = 0;
   if (p.rows) {
     float* z = reinterpret_cast<float*>(ws + p.logits);
-    const int64_t ldz = (p.n + 3) / 4 * 4;
     if (p.f8) {
       PanelOperand X;
       HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
-      HYB_TRY(launch_f8_gemm(*head.f8, p.n, p.k, hyb_f8{ws + p.x, ws + p.xs}, p.m, z, HYB_F32, ldz, nullptr, s));
-    } else if (p.m <= kGemvCrossoverM || (p.m <= kMaxGemvM && gemv_preferred(*head.layout, int(p.m)))) {
-      HYB_TRY(launch_gemv(*head.layout, *head.packed, x, int(p.m), ldx, z, HYB_F32, ldz, s));
-    } else {
-      HYB_TRY(launch_gemm(*head.layout, *head.packed, x, int(p.m), ldx, z, HYB_F32, ldz, s, nullptr, 0));
     }
-    chunks = (n_vocab + 2047) / 2048;
-    hipLaunchKernelGGL(k_xent_rows, dim3(unsigned(chunks), unsigned(p.m)), dim3(256), 0, s, z, ldz, t);
-    HYB_TRY(hipGetLastError());
+    for (int64_t v0 = 0; v0 < n_vocab; v0 += p.rows_piece) {
+      const int64_t rows = p.n - v0 < p.rows_piece ? p.n - v0 : p.rows_piece;
+      const int64_t ldz = (rows + 3) / 4 * 4;
+      if (p.f8) {
+        HYB_TRY(launch_f8_gemm(*head.f8, p.n, p.k, hyb_f8{ws + p.x, ws + p.xs}, p.m, z, HYB_F32, ldz, nullptr, s));
+      } else {
+        // the piece's tile rows: the same streams, a part of the tile index
+        hyb_layout L = *head.layout;
+        hyb_packed P = *head.packed;
+        P.tidx += v0 / L.b1 * L.tiles_k;
+        L.n = rows;
+        L.tiles_n = rows / L.b1;
+        if (p.m <= kGemvCrossoverM || (p.m <= kMaxGemvM && gemv_preferred(L, int(p.m))))
+          HYB_TRY(launch_gemv(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s));
+        else
+          HYB_TRY(launch_gemm(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s, nullptr, 0));
+      }
+      t.v0 = v0;
+      const int64_t live = n_vocab - v0 < rows ? n_vocab - v0 : rows;
+      hipLaunchKernelGGL(k_xent_rows, dim3(unsigned((live + 2047) / 2048), unsigned(p.m)), dim3(256), 0, s, z, ldz, t);
+      HYB_TRY(hipGetLastError());
+      chunks = (v0 + live + 2047) / 2048;
+    }
   } else {
     PanelOperand X;
     HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
-    // nothing is copied: one piece
-    const int64_t step = piece_form(head, p, n_vocab, 0, 0, false) != Form::kPanels ? n_vocab : p.piece;
+    // A head that is multiplied where it lies is one piece.  (Logits of
+    // padding rows are not looked at: no tile row is spare for them.)
+    const bool whole = p.f8 || head.layout->n_sparse == 0;
+    const int64_t step = whole ? n_vocab : p.piece;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
       const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
-      const Form form = piece_form(head, p, n_vocab, v0, rows, false);
-      if (form == Form::kPanels) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, nullptr, ws + p.w, s));
+      if (!whole) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, p.n, v0, rows, nullptr, ws + p.w, s));
       t.v0 = v0;
-      const PanelOperand W = piece_operand(head, p, form, v0, rows, ws + p.w);
-      HYB_TRY((run_tiles<DT, false>(form, p.bp, W, X, t, s)));
+      const PanelOperand W = piece_operand(head, p, p.n, v0, rows, whole ? nullptr : ws + p.w);
+      HYB_TRY((run_tiles<DT, false>(p, W, X, t, s)));
       chunks = v0 / 256 + (W.rows16 + 255) / 256;
     }
   }
@@ -682,10 +702,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     const int32_t vsteps = int32_t((rows + 63) / 64);
     t.v0 = v0;
     t.g_steps = vsteps;
-    const Form form = piece_form(head, p, n_vocab, v0, rows, true);
-    if (form == Form::kPanels || (p.f8 && dx)) HYB_TRY(piece_panels<DT>(head, p, n_vocab, v0, rows, top, ws + p.w, s));
-    const PanelOperand W = piece_operand(head, p, form, v0, rows, ws + p.w);
-    HYB_TRY((run_tiles<DT, true>(form, p.bp, W, X, t, s)));
+    // (an 8-bit head's logits do not need the 16-bit panels)
+    if (!p.f8 || dx) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, n_vocab, v0, rows, top, ws + p.w, s));
+    const PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, ws + p.w);
+    HYB_TRY((run_tiles<DT, true>(p, W, X, t, s)));
     // G: tokens x entries, vsteps steps; W': entries x columns
     const PanelOperand G{ws + p.g, int32_t(p.m16), vsteps, nullptr, 0};
     if (dx) {
@@ -696,7 +716,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.first = v0 == 0;
       o.rows = int32_t(p.m);
       o.cols = krows;
-      if (form == Form::kTiles) {
+      if (!p.f8) {
         HYB_TRY(p.bp == 16 ? (run_product<DT, true, true, 16, 16, 2, 4>(W, G, vsteps, p.parts, o, s))
                            : (run_product<DT, true, true, 16, 4, 4, 2>(W, G, vsteps, p.parts, o, s)));
       } else {

@@ -21,7 +21,16 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   p.steps = p.f8 ? f8_steps(p.k) : p.k / 64;
   p.ksteps16 = p.f8 ? 2 * p.steps : p.steps;
   const bool dx = what & HYB_XENT_DX, dw = what & HYB_XENT_DW;
-  p.rows = !dx && !dw && m <= 64;
+  // The loss alone: for few tokens the logits of a piece go through the
+  // library's product and the workspace (33 MB at 64 tokens x 128256), which
+  // reads the head once as it lies.  A packed head with sparse tiles would have
+  // to be expanded for the tiles below, which costs more than the logits'
+  // round trip up to about 512 tokens (128256 x 4096, 60% of the tiles sparse,
+  // bf16, 100 / 256 / 512 / 1024 tokens: 345 / 386 / 610 / 1127 us through the
+  // product, 669 / 674 / 707 / 1144 through the tiles; 10% sparse, 512 tokens:
+  // 664 and 609).
+  const int64_t few = !p.f8 && head.layout->n_sparse > 0 ? 512 : 64;
+  p.rows = !dx && !dw && m <= few;
   p.bp = m <= 64 ? 4 : 16;
   // A piece's 16-bit dz takes at most 256 MiB.
   p.piece = int64_t(256) << 20;
@@ -29,6 +38,7 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   if (p.piece < 256) p.piece = 256;
   if (p.piece > 32768) p.piece = 32768;
   if (p.piece > up(p.n, 256)) p.piece = up(p.n, 256);
+  p.rows_piece = m <= 64 ? p.n : 32768;
   p.chunks = p.rows ? up(p.n, 2048) / 2048 : up(p.n, 256) / 256;
   p.parts = 1;
   if (dx) {
@@ -64,7 +74,7 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     p.zt = take(p.m16 * 4);
   }
   if (p.rows) {
-    p.logits = take(m * up(p.n, 4) * 4);
+    p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
   } else if (!p.f8 || dx) {
     p.w = take(p.piece * krows * 2);
   }

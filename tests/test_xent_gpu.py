@@ -374,3 +374,31 @@ def test_together_a_frozen_8_bit_layer_under_an_8_bit_head():
     check(W, w, hidden, target, grad, n_vocab)
     ref = fo.values(*fo.quantise(as64(x), 1)) @ fo.values(*fo.quantise(as64(a), 128)).T
     assert np.all(np.abs(as64(hidden) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * np.abs(ref).max())
+
+
+@pytest.mark.parametrize("sparse", [0.0, 0.5])
+@pytest.mark.parametrize("m", [6, 100])
+def test_tile_index_out_of_range_adds_nothing(m, sparse):
+    """Entries of the tile index that name no slot: their tiles count as
+    zeros, as in the library's products."""
+    P, w, x, target, grad = make(512, 256, m, 500, "bf16", tile=(64, 64), sparse=sparse, seed=17)
+    tidx = P.tidx.clone()
+    bad = torch.tensor([0, 5, 9, 30], device="cuda")
+    for value in (P.layout.n_dense, -P.layout.n_sparse - 1, 2 ** 31 - 1, -2 ** 31):
+        P.tidx.copy_(tidx)
+        wv = as64(hb.unpack(P))
+        for t in bad.tolist():
+            r, c = t // 4, t % 4
+            wv[r * 64:(r + 1) * 64, c * 64:(c + 1) * 64] = 0.0
+        P.tidx[bad] = value
+        want, tol = bounds(as64(x), wv, x, target, grad, 500, 256)
+        loss, lse = xent.loss(P, x, target, n_vocab=500)
+        dx, dw = xent.backward(P, x, target, lse, grad, n_vocab=500, need_dw=True)
+        for name, got, ref, lim in zip(("loss", "lse", "dx", "dw"), (loss, lse, dx, dw), want, tol):
+            within(name, got, ref, lim)
+
+
+def test_tile_columns_beyond_one_register():
+    """More than 64 tiles in a row, and more than 64 tile rows in a piece."""
+    check(*make(128, 64 * 130, 70, 128, "bf16", seed=18, sigma=0.02), 128)
+    check(*make(64 * 150, 128, 70, 64 * 150 - 3, "bf16", seed=19), 64 * 150 - 3)
