@@ -20,39 +20,73 @@ struct __attribute__((packed, aligned(2))) Bytes8 {
   uint32_t w[2];
 };
 
-// Eight columns c0.. of one row, as loaded (two elements to a word, or one
-// for fp32); zeros behind the row's end.
+// Eight columns c0.. of one row, as loaded: two elements to a word, or one
+// for fp32 (k = 0: no row, zeros).
 template <int DT>
 struct Eight {
   uint32_t w[DT == HYB_F32 ? 8 : 4];
 };
 
+// A lane at or behind the row's end loads the row's last eight columns, so
+// that a wavefront's loads of many rows need no branches and are all under
+// way at once; trim8 then moves its columns into place and zeros the rest.
 template <int DT>
 __device__ __forceinline__ Eight<DT> load8(const void* a, int64_t base, int32_t c0, int32_t k) {
   Eight<DT> r;
   constexpr int kWords = DT == HYB_F32 ? 8 : 4;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) r.w[i] = 0;
-  if (c0 >= k) return r;
-  if (c0 + 8 <= k) {
-    const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const char*>(a) + (base + c0) * (DT == HYB_F32 ? 4 : 2));
+  if (k == 0) return r;
+  if (k < 8) {
 #pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) {
-      const Bytes16 u = p[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = u.w[j];
-    }
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < k) {
+        if constexpr (DT == HYB_F32)
+          r.w[i] = static_cast<const uint32_t*>(a)[base + c0 + i];
+        else
+          r.w[i / 2] |= uint32_t(static_cast<const uint16_t*>(a)[base + c0 + i]) << (16 * (i & 1));
+      }
     return r;
   }
+  const int64_t at = base + (c0 < k - 8 ? c0 : k - 8);
+  const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c0 + i < k) {
-      if constexpr (DT == HYB_F32)
-        r.w[i] = static_cast<const uint32_t*>(a)[base + c0 + i];
-      else
-        r.w[i / 2] |= uint32_t(static_cast<const uint16_t*>(a)[base + c0 + i]) << (16 * (i & 1));
-    }
+  for (int i = 0; i < kWords / 4; ++i) {
+    const Bytes16 u = p[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[4 * i + j] = u.w[j];
+  }
   return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void trim8(Eight<DT>& r, int32_t c0, int32_t k) {
+  if (k < 8) return;
+  const int32_t by = c0 - (k - 8);  // columns to move down, 8 or more: none left
+  constexpr int kWords = DT == HYB_F32 ? 8 : 4;
+  auto move = [&](bool on, int words) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t u = i + words < kWords ? r.w[i + words < kWords ? i + words : 0] : 0;
+      r.w[i] = on ? u : r.w[i];
+    }
+  };
+  if constexpr (DT == HYB_F32) {
+    move(by > 0 && (by & 4), 4);
+    move(by > 0 && (by & 2), 2);
+    move(by > 0 && (by & 1), 1);
+  } else {
+    move(by > 0 && (by & 4), 2);
+    move(by > 0 && (by & 2), 1);
+    const bool half = by > 0 && (by & 1);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t u = r.w[i] >> 16 | (i + 1 < kWords ? r.w[i + 1 < kWords ? i + 1 : 0] << 16 : 0);
+      r.w[i] = half ? u : r.w[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) r.w[i] = by >= 8 ? 0 : r.w[i];
 }
 
 // Element i as fp32.
@@ -171,6 +205,10 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   uint32_t all = 0;
 #pragma unroll
   for (int r = 0; r < 16; ++r) v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0);
+  if (!__all(c0 + 8 <= k)) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) trim8<DT>(v[r], c0, k);
+  }
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     top[r] = top_of<DT>(v[r]);
@@ -225,31 +263,39 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   scales[((int64_t(s0 / 4) * panels * 16) + r0 + j) * 4 + (lane >> 4)] = char(mine);
 }
 
+// One wavefront per panel and step (a workgroup's four take four steps).
 template <int DT>
 __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ codes,
                                                        const uint32_t* __restrict__ scales, int64_t rows, int32_t k,
                                                        int64_t lda, void* __restrict__ a, int32_t panels,
                                                        int32_t steps) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t panel = int64_t(blockIdx.x) * 4 + wave;
+  const int64_t panel = blockIdx.x;
   const int64_t row = panel * 16 + (lane & 15);
-  if (panel >= panels || row >= rows) return;
-  const int32_t s0 = int32_t(blockIdx.y) * 4;
-  const uint32_t word = scales[int64_t(s0 / 4) * panels * 16 + row];
-  uint4 all[4][2];
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (row >= rows || s >= steps) return;
+  const uint32_t byte = (scales[int64_t(blockIdx.y) * panels * 16 + row] >> (8 * wave)) & 0xFFu;
+  uint4 u[2];
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int h = 0; h < 2; ++h)
+    u[h] = *reinterpret_cast<const uint4*>(codes + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      all[s][h] = s0 + s < steps ? *reinterpret_cast<const uint4*>(codes + (panel * steps + s0 + s) * kPanelStep +
-                                                                   h * 1024 + lane * 16)
-                                 : make_uint4(0, 0, 0, 0);
+  for (int h = 0; h < 2; ++h) {
+    const int32_t c0 = s * 128 + h * 64 + (lane >> 4) * 16;
+    if (c0 >= k) continue;
+    const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+    constexpr int kWords = DT == HYB_F32 ? 16 : 8;
+    uint32_t o[kWords];
+    if constexpr (DT == HYB_BF16) {
+      // reads only the exponent of its scale; exact
+      const float f = __builtin_bit_cast(float, byte << 23);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const float scale = exp2_byte((word >> (8 * s)) & 0xFFu);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w[4] = {all[s][h].x, all[s][h].y, all[s][h].z, all[s][h].w};
+      for (int i = 0; i < 4; ++i) {
+        o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, false));
+        o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, true));
+      }
+    } else {
+      const float scale = exp2_byte(byte);
       float f[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -258,34 +304,28 @@ __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ 
         f[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(int(w[i]), 2) * scale;
         f[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(int(w[i]), 3) * scale;
       }
-      const int32_t c0 = (s0 + s) * 128 + h * 64 + (lane >> 4) * 16;
-      if (c0 >= k) continue;
-      const int64_t at = row * lda + c0;
-      if (c0 + 16 <= k) {
-        Bytes16* p = reinterpret_cast<Bytes16*>(static_cast<char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
-        if constexpr (DT == HYB_F32) {
+      if constexpr (DT == HYB_F32) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            Bytes16 o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o.w[j] = __builtin_bit_cast(uint32_t, f[4 * i + j]);
-            p[i] = o;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            Bytes16 o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o.w[j] = round16<DT>(f[8 * i + 2 * j]) | uint32_t(round16<DT>(f[8 * i + 2 * j + 1])) << 16;
-            p[i] = o;
-          }
-        }
+        for (int i = 0; i < 16; ++i) o[i] = __builtin_bit_cast(uint32_t, f[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c0 + i < k) store_out(a, DT, at + i, f[i]);
+        for (int i = 0; i < 8; ++i) o[i] = round16<DT>(f[2 * i]) | uint32_t(round16<DT>(f[2 * i + 1])) << 16;
       }
+    }
+    const int64_t at = row * lda + c0;
+    if (c0 + 16 <= k) {
+      Bytes16* p = reinterpret_cast<Bytes16*>(static_cast<char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) p[i] = Bytes16{{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]}};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c0 + i < k) {
+          if constexpr (DT == HYB_F32)
+            static_cast<uint32_t*>(a)[at + i] = o[i];
+          else
+            static_cast<uint16_t*>(a)[at + i] = uint16_t(o[i / 2] >> (16 * (i & 1)));
+        }
     }
   }
 }
@@ -378,7 +418,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
 #pragma unroll
       for (int r = 0; r < kFusedTokens; ++r) {
         if (r >= out.m) break;
-        const Eight<XDT> v = load8<XDT>(plain.x, r * plain.ldx, s * 128 + lane * 8, plain.k);
+        Eight<XDT> v = load8<XDT>(plain.x, r * plain.ldx, s * 128 + lane * 8, plain.k);
+        trim8<XDT>(v, s * 128 + lane * 8, plain.k);
         uint32_t top = top_of<XDT>(v);
         const bool mark = __any(top >= kF32Inf);
         if (mark) top = top_finite<XDT>(v);
@@ -585,7 +626,7 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
 hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void* a, int dtype, int64_t lda,
                                 hipStream_t s) {
   const int32_t panels = int32_t(f8_rows16(rows) / 16), steps = int32_t(f8_steps(k));
-  const dim3 grid(unsigned((panels + 3) / 4), unsigned((steps + 3) / 4));
+  const dim3 grid(unsigned(panels), unsigned((steps + 3) / 4));
   const char* codes = static_cast<const char*>(src.codes);
   const uint32_t* scales = static_cast<const uint32_t*>(src.scales);
   if (dtype == HYB_F32)
