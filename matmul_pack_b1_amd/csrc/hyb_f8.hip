@@ -10,16 +10,6 @@ namespace {
 
 // ------------------------------------------------------ quantise, read back --
 
-// 16 bytes at any element's address (the hardware takes unaligned global
-// accesses; 77 x 1501 fp16, odd rows: 6.9 us element by element, see below).
-struct __attribute__((packed, aligned(2))) Bytes16 {
-  uint32_t w[4];
-};
-
-struct __attribute__((packed, aligned(2))) Bytes8 {
-  uint32_t w[2];
-};
-
 // Eight columns c0.. of one row, as loaded: two elements to a word, or one
 // for fp32 (k = 0: no row, zeros).
 template <int DT>
@@ -506,6 +496,35 @@ __global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelO
     for (int j = 0; j < T::kB; ++j)
 #pragma unroll
       for (int i = 0; i < T::kA; ++i) p[(i * T::kB + j) * 64] = acc[i][j];
+    return;
+  }
+  if (out.ydt != HYB_F32) {
+    __syncthreads();  // the tile's LDS stages are free
+    const int64_t m0 = int64_t(bb * BP + wb * T::kB) * 16;
+    const int32_t n0 = (ab * AP + wa * T::kA) * 16;
+    panel_rows16<T::kA, T::kB>(
+        f8_smem + wave * (T::kA * T::kB * 512), lane, lane & 15,
+        [&](int i, int j) {
+          uint16_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = out.ydt == HYB_BF16 ? round16<HYB_BF16>(acc[i][j][e]) : round16<HYB_F16>(acc[i][j][e]);
+          return make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+        },
+        [&](int row, int col, uint4 u) {
+          const int64_t m = m0 + row;
+          const int32_t n = n0 + col;
+          if (m >= out.m || n >= out.n) return;
+          uint16_t* p = static_cast<uint16_t*>(out.y) + m * out.ldy + n;
+          if (n + 8 <= out.n) {
+            *reinterpret_cast<Bytes16*>(p) = Bytes16{{u.x, u.y, u.z, u.w}};
+          } else {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (n + e < out.n) p[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+          }
+        });
     return;
   }
 #pragma unroll

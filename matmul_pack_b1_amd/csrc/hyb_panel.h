@@ -148,6 +148,42 @@ __device__ __forceinline__ f32x4_t panel_mfma(const PanelRegs<KIND>& ar, const P
   }
 }
 
+// 16 and 8 bytes at any 2-byte aligned address (the hardware takes unaligned
+// global accesses).
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
+};
+struct __attribute__((packed, aligned(2))) Bytes8 {
+  uint32_t w[2];
+};
+
+// A wavefront's KA x KB panels of 16-bit results, row by row.  In registers a
+// lane has four columns of a row, so a store would cover 32 bytes of each of
+// 16 rows; through LDS (its own 512 KA KB bytes, 16-byte units rotated by the
+// row against bank conflicts) 16-byte stores cover KA * 32 bytes of a row.
+// quad(i, j) gives the four values of acc[i][j] as two words, row16 the lane's
+// row of 16; put(row, column, values) stores eight columns.
+template <int KA, int KB, typename Quad, typename Put>
+__device__ __forceinline__ void panel_rows16(char* lds, int lane, int row16, Quad quad, Put put) {
+  constexpr int kUnits = KA * 2;  // of a row
+#pragma unroll
+  for (int j = 0; j < KB; ++j)
+#pragma unroll
+    for (int i = 0; i < KA; ++i) {
+      const int row = j * 16 + row16, unit = i * 2 + (lane >> 5);
+      *reinterpret_cast<uint2*>(lds + row * (kUnits * 16) + ((unit ^ (row & (kUnits - 1))) * 16) + ((lane >> 4) & 1) * 8) =
+          quad(i, j);
+    }
+  // one wavefront writes and reads its own part: its accesses done suffices
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  constexpr int kRows = 64 / kUnits;  // per store
+#pragma unroll
+  for (int r = 0; r < KB * 16; r += kRows) {
+    const int row = r + lane / kUnits, unit = lane % kUnits;
+    put(row, unit * 8, *reinterpret_cast<const uint4*>(lds + row * (kUnits * 16) + ((unit ^ (row & (kUnits - 1))) * 16)));
+  }
+}
+
 // Workgroups run round-robin over the 8 XCDs (id L on XCD L % 8), each with
 // its own L2.  XCD x takes a contiguous range of an order in which 4 A blocks
 // are swept across all B blocks before the next 4, so workgroups that run

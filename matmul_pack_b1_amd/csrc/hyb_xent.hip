@@ -413,7 +413,6 @@ struct XentOut {
   const float* gtop;
   int32_t rows, cols;  // rows of B and columns (rows of A) that exist
   int64_t live;        // dW: rows from here on are padding, zero
-  int vec;
 };
 
 // DX: Y[token, column] = sum over the piece's entries of G W' (A = W' read
@@ -437,17 +436,14 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
   T::run(A, B, ab * AP, bb * BP, s0, s1, xent_smem, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wa = wave % WA, wb = wave / WA;
-  const float back = DX ? 1.f : *o.gtop / g_scale<DT>();
+  if constexpr (DX) {
 #pragma unroll
-  for (int j = 0; j < T::kB; ++j) {
-    // dW: G's entries 4..7 and 8..11 of 16 have changed places
-    const int r16 = DX ? lane & 15 : (lane & 3) | (lane & 4) << 1 | (lane & 8) >> 1;
-    const int32_t row = (bb * BP + wb * T::kB + j) * 16 + r16;
-    if (row >= o.rows) continue;
+    for (int j = 0; j < T::kB; ++j) {
+      const int32_t row = (bb * BP + wb * T::kB + j) * 16 + (lane & 15);
+      if (row >= o.rows) continue;
 #pragma unroll
-    for (int i = 0; i < T::kA; ++i) {
-      const int32_t col = (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4;
-      if constexpr (DX) {
+      for (int i = 0; i < T::kA; ++i) {
+        const int32_t col = (ab * AP + wa * T::kA + i) * 16 + (lane >> 4) * 4;
         if (col >= o.ld) continue;
         f32x4_t* p = reinterpret_cast<f32x4_t*>(o.acc + part * o.part + row * o.ld + col);
         f32x4_t v = acc[i][j];
@@ -457,21 +453,28 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
           for (int e = 0; e < 4; ++e) v[e] += u[e];
         }
         *p = v;
-      } else {
-        if (col >= o.cols) continue;
-        uint16_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = row < o.live ? round16<DT>(acc[i][j][e] * back) : uint16_t(0);
-        uint16_t* p = o.y + row * o.ldy + col;
-        if (o.vec && col + 4 <= o.cols) {
-          *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < o.cols) p[e] = h[e];
-        }
       }
     }
+  } else {
+    const float back = *o.gtop / g_scale<DT>();
+    // G's entries 4..7 and 8..11 of 16 have changed places
+    const int row16 = (lane & 3) | (lane & 4) << 1 | (lane & 8) >> 1;
+    const int32_t row0 = (bb * BP + wb * T::kB) * 16, col0 = (ab * AP + wa * T::kA) * 16;
+    __syncthreads();  // the tile's LDS stages are free
+    panel_rows16<T::kA, T::kB>(
+        xent_smem + wave * (T::kA * T::kB * 512), lane, row16,
+        [&](int i, int j) {
+          const bool live = row0 + j * 16 + row16 < o.live;
+          uint16_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = live ? round16<DT>(acc[i][j][e] * back) : uint16_t(0);
+          return make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+        },
+        [&](int r, int c, uint4 u) {
+          const int32_t row = row0 + r, col = col0 + c;  // a packed head's k is a multiple of 64
+          if (row < o.rows && col < o.cols)
+            *reinterpret_cast<Bytes16*>(o.y + row * o.ldy + col) = Bytes16{{u.x, u.y, u.z, u.w}};
+        });
   }
 }
 
@@ -733,7 +736,6 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.rows = int32_t(rows);
       o.cols = int32_t(p.k);
       o.live = n_vocab - v0;
-      o.vec = reinterpret_cast<uintptr_t>(dw) % 8 == 0 && lddw % 4 == 0;
       HYB_TRY((run_product<DT, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
     }
   }
