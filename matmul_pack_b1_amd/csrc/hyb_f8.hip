@@ -661,7 +661,7 @@ hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void
 }
 
 hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x, int64_t m, void* y, int y_dtype,
-                          int64_t ldy, float* ws, hipStream_t s) {
+                          int64_t ldy, float* ws, hipStream_t s, int64_t w_pitch) {
   const F8Out o{y, ldy, int32_t(n), int32_t(m), y_dtype};
   if (k == 0) {
     const int64_t blocks = (n * m + 255) / 256;
@@ -670,7 +670,7 @@ hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x
   }
   const int32_t steps = int32_t(f8_steps(k));
   const PanelOperand W{static_cast<const char*>(w.codes), int32_t(f8_rows16(n)), steps,
-                       static_cast<const uint32_t*>(w.scales), f8_rows16(n)};
+                       static_cast<const uint32_t*>(w.scales), w_pitch ? w_pitch : f8_rows16(n)};
   const PanelOperand X{static_cast<const char*>(x.codes), int32_t(f8_rows16(m)), steps,
                        static_cast<const uint32_t*>(x.scales), f8_rows16(m)};
   const F8Route r = f8_route(n, k, m, y_dtype == HYB_F32, device_cus());

@@ -43,8 +43,10 @@ hipError_t launch_f8_dequantize(const hyb_f8& src, int64_t rows, int64_t k, void
 bool f8_fused(int64_t n, int64_t k, int64_t m, int y_dtype);
 hipError_t launch_f8_fused(const hyb_f8& w, int64_t n, int64_t k, const void* x, int x_dtype, int64_t m, int64_t ldx,
                            void* y, int y_dtype, int64_t ldy, hipStream_t s);
-// ws NULL runs the route unsplit.
+// ws NULL runs the route unsplit.  w_pitch: words between w's scale words of
+// four steps and the next four (0: its own rows; more for a part of the rows
+// of a larger matrix).
 hipError_t launch_f8_gemm(const hyb_f8& w, int64_t n, int64_t k, const hyb_f8& x, int64_t m, void* y, int y_dtype,
-                          int64_t ldy, float* ws, hipStream_t s);
+                          int64_t ldy, float* ws, hipStream_t s, int64_t w_pitch = 0);
 
 }  // namespace hyb

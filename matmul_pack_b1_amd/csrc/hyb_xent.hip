@@ -337,6 +337,41 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
   }
 }
 
+// G of a piece from its logits (few tokens): one wavefront per 16 tokens and 64
+// entries, in the order in which k_xent_tile leaves it.
+template <int DT>
+__global__ __launch_bounds__(256) void k_xent_g_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t s = int32_t(blockIdx.x) * 4 + wave;
+  if (s >= t.g_steps) return;
+  const int32_t tok = int32_t(blockIdx.y) * 16 + (lane & 15);
+  const int64_t want = tok < t.m ? t.target[tok] : t.ignore;
+  const bool seen = tok < t.m && want != t.ignore;
+  const bool valid = want >= 0 && want < t.n_vocab;
+  const float lse = seen ? t.lse[tok] : 0.f;
+  const float f = seen ? t.grad[tok] / *t.gtop * g_scale<DT>() : 0.f;
+  const int u = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint16_t g[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t c = s * 64 + h * 32 + 16 * (u >> 1) + 4 * (u & 1) + 8 * (e >> 2) + (e & 3);
+      const int64_t v = t.v0 + c;
+      const float logit = seen && v < t.n_vocab ? z[tok * ldz + c] : 0.f;
+      float p = (fast_exp(logit - lse) - (v == want ? 1.f : 0.f)) * f;
+      if (!valid) p = __builtin_nanf("");
+      if (!seen || v >= t.n_vocab) p = 0.f;
+      g[e] = round16<DT>(p);
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = g[2 * e] | uint32_t(g[2 * e + 1]) << 16;
+    *reinterpret_cast<uint4*>(t.g + (int64_t(blockIdx.y) * t.g_steps + s) * kPanelStep + h * 1024 + lane * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // Joins a token's partial sums: 16 tokens per workgroup, 64 threads each, in a
 // fixed order.
 __global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ part, int64_t chunks, int32_t m,
@@ -535,8 +570,8 @@ hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, const XentTile
 
 template <int KIND, int DT, bool GRAD, bool TILED>
 hipError_t run_shape(int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
-  return bp == 16 ? run_tile<KIND, DT, GRAD, TILED, 16, 16, 2, 4>(W, X, t, s)
-                  : run_tile<KIND, DT, GRAD, TILED, 16, 4, 4, 2>(W, X, t, s);
+  if (bp == 16) return run_tile<KIND, DT, GRAD, TILED, 16, 16, 2, 4>(W, X, t, s);
+  return run_tile<KIND, DT, GRAD, TILED, 16, 8, 4, 2>(W, X, t, s);
 }
 
 template <int DT, bool GRAD>
@@ -556,6 +591,14 @@ hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t ste
   hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
                      dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
   return hipGetLastError();
+}
+
+template <int DT, bool TILED>
+hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
+                  hipStream_t s) {
+  if (bp == 16) return run_product<DT, true, TILED, 16, 16, 2, 4>(A, B, steps, parts, o, s);
+  if (bp == 8) return run_product<DT, true, TILED, 16, 8, 4, 2>(A, B, steps, parts, o, s);
+  return run_product<DT, true, TILED, 16, 4, 4, 2>(A, B, steps, parts, o, s);
 }
 
 // What the products of the piece of `rows` vocabulary rows from v0 read beside
@@ -626,6 +669,27 @@ PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t plai
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
+// Logits of the vocabulary rows v0 .. v0 + rows - 1 (few tokens) through the
+// library's products, fp32, row stride ldz; an 8-bit head multiplies the
+// quantised x of prepare_x.
+hipError_t piece_logits(const hyb_head& head, const XentPlan& p, const void* x, int64_t ldx, int64_t v0, int64_t rows,
+                        float* z, int64_t ldz, char* ws, hipStream_t s) {
+  if (p.f8) {
+    const hyb_f8 W{static_cast<char*>(head.f8->codes) + v0 / 16 * p.steps * kPanelStep,
+                   static_cast<uint32_t*>(head.f8->scales) + v0};
+    return launch_f8_gemm(W, rows, p.k, hyb_f8{ws + p.x, ws + p.xs}, p.m, z, HYB_F32, ldz, nullptr, s, f8_rows16(p.n));
+  }
+  // the piece's tile rows: the same streams, a part of the tile index
+  hyb_layout L = *head.layout;
+  hyb_packed P = *head.packed;
+  P.tidx += v0 / L.b1 * L.tiles_k;
+  L.n = rows;
+  L.tiles_n = rows / L.b1;
+  if (p.m <= kGemvCrossoverM || (p.m <= kMaxGemvM && gemv_preferred(L, int(p.m))))
+    return launch_gemv(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s);
+  return launch_gemm(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s, nullptr, 0);
+}
+
 template <int DT>
 hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int64_t ldx, XentTile t,
                       float* loss, float* lse, char* ws, hipStream_t s) {
@@ -639,20 +703,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     for (int64_t v0 = 0; v0 < n_vocab; v0 += p.rows_piece) {
       const int64_t rows = p.n - v0 < p.rows_piece ? p.n - v0 : p.rows_piece;
       const int64_t ldz = (rows + 3) / 4 * 4;
-      if (p.f8) {
-        HYB_TRY(launch_f8_gemm(*head.f8, p.n, p.k, hyb_f8{ws + p.x, ws + p.xs}, p.m, z, HYB_F32, ldz, nullptr, s));
-      } else {
-        // the piece's tile rows: the same streams, a part of the tile index
-        hyb_layout L = *head.layout;
-        hyb_packed P = *head.packed;
-        P.tidx += v0 / L.b1 * L.tiles_k;
-        L.n = rows;
-        L.tiles_n = rows / L.b1;
-        if (p.m <= kGemvCrossoverM || (p.m <= kMaxGemvM && gemv_preferred(L, int(p.m))))
-          HYB_TRY(launch_gemv(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s));
-        else
-          HYB_TRY(launch_gemm(L, P, x, int(p.m), ldx, z, HYB_F32, ldz, s, nullptr, 0));
-      }
+      HYB_TRY(piece_logits(head, p, x, ldx, v0, rows, z, ldz, ws, s));
       t.v0 = v0;
       const int64_t live = n_vocab - v0 < rows ? n_vocab - v0 : rows;
       hipLaunchKernelGGL(k_xent_rows, dim3(unsigned((live + 2047) / 2048), unsigned(p.m)), dim3(256), 0, s, z, ldz, t);
@@ -694,8 +745,8 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
                        top);
     HYB_TRY(hipGetLastError());
   }
-  PanelOperand X;
-  HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+  PanelOperand X{};
+  if (p.f8 || !p.rows || dw) HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
   const int32_t krows = int32_t(p.ksteps16 * 64);
   t.g = ws + p.g;
   // dX runs over the vocabulary that counts, dW over every row of the head.
@@ -705,10 +756,20 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     const int32_t vsteps = int32_t((rows + 63) / 64);
     t.v0 = v0;
     t.g_steps = vsteps;
-    // (an 8-bit head's logits do not need the 16-bit panels)
-    if (!p.f8 || dx) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, n_vocab, v0, rows, top, ws + p.w, s));
+    // (logits of few tokens, and an 8-bit head's, do not need them)
+    if ((!p.rows && !p.f8) || dx) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, n_vocab, v0, rows, top, ws + p.w, s));
     const PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, ws + p.w);
-    HYB_TRY((run_tiles<DT, true>(p, W, X, t, s)));
+    if (p.rows) {
+      // all of a packed head's tile rows that the piece reaches into
+      const int64_t b1 = p.f8 ? 1 : head.layout->b1, whole = (rows + b1 - 1) / b1 * b1, ldz = (whole + 3) / 4 * 4;
+      float* z = reinterpret_cast<float*>(ws + p.logits);
+      HYB_TRY(piece_logits(head, p, x, ldx, v0, whole, z, ldz, ws, s));
+      hipLaunchKernelGGL((k_xent_g_rows<DT>), dim3(unsigned((vsteps + 3) / 4), unsigned(p.m16 / 16)), dim3(256), 0, s, z,
+                         ldz, t);
+      HYB_TRY(hipGetLastError());
+    } else {
+      HYB_TRY((run_tiles<DT, true>(p, W, X, t, s)));
+    }
     // G: tokens x entries, vsteps steps; W': entries x columns
     const PanelOperand G{ws + p.g, int32_t(p.m16), vsteps, nullptr, 0};
     if (dx) {
@@ -720,12 +781,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.rows = int32_t(p.m);
       o.cols = krows;
       if (!p.f8) {
-        HYB_TRY(p.bp == 16 ? (run_product<DT, true, true, 16, 16, 2, 4>(W, G, vsteps, p.parts, o, s))
-                           : (run_product<DT, true, true, 16, 4, 4, 2>(W, G, vsteps, p.parts, o, s)));
+        HYB_TRY((run_dx<DT, true>(p.bp, W, G, vsteps, p.parts, o, s)));
       } else {
         const PanelOperand A{ws + p.w, int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), nullptr, 0};
-        HYB_TRY(p.bp == 16 ? (run_product<DT, true, false, 16, 16, 2, 4>(A, G, vsteps, p.parts, o, s))
-                           : (run_product<DT, true, false, 16, 4, 4, 2>(A, G, vsteps, p.parts, o, s)));
+        HYB_TRY((run_dx<DT, false>(p.bp, A, G, vsteps, p.parts, o, s)));
       }
     }
     if (dw) {

@@ -29,16 +29,19 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   // bf16, 100 / 256 / 512 / 1024 tokens: 345 / 386 / 610 / 1127 us through the
   // product, 669 / 674 / 707 / 1144 through the tiles; 10% sparse, 512 tokens:
   // 664 and 609).
-  const int64_t few = !p.f8 && head.layout->n_sparse > 0 ? 512 : 64;
-  p.rows = !dx && !dw && m <= few;
-  p.bp = m <= 64 ? 4 : 16;
+  // Gradients need the expanded tiles anyway; up to 64 tokens their logits go
+  // the same way too (16 tokens, 32768 x 4096 of the head: the tile of 256 x 64
+  // 100 us, the product 40).
+  const int64_t few = !dx && !dw && !p.f8 && head.layout->n_sparse > 0 ? 512 : 64;
+  p.rows = m <= few;
+  p.bp = m <= 64 ? 4 : m <= 128 ? 8 : 16;
   // A piece's 16-bit dz takes at most 256 MiB.
   p.piece = int64_t(256) << 20;
   p.piece = p.piece / (2 * (p.m64 > 0 ? p.m64 : 64)) / 256 * 256;
   if (p.piece < 256) p.piece = 256;
   if (p.piece > 32768) p.piece = 32768;
   if (p.piece > up(p.n, 256)) p.piece = up(p.n, 256);
-  p.rows_piece = m <= 64 ? p.n : 32768;
+  p.rows_piece = dx || dw ? p.piece : m <= 64 ? p.n : 32768;
   p.chunks = p.rows ? up(p.n, 2048) / 2048 : up(p.n, 256) / 256;
   p.parts = 1;
   if (dx) {
@@ -65,7 +68,7 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   if (p.f8) {
     p.x = take(p.m16 * p.steps * 128);
     p.xs = take((p.steps + 3) / 4 * p.m16 * 4);
-  } else if (!p.rows) {
+  } else if (!p.rows || dw) {
     p.x = take(p.m16 * p.k * 2);
   }
   p.misc = take(256);
@@ -73,11 +76,8 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     p.part = take(p.chunks * p.m16 * 8);
     p.zt = take(p.m16 * 4);
   }
-  if (p.rows) {
-    p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
-  } else if (!p.f8 || dx) {
-    p.w = take(p.piece * krows * 2);
-  }
+  if (p.rows) p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
+  if ((!p.rows && !p.f8) || dx) p.w = take(p.piece * krows * 2);
   if (dx || dw) p.g = take(p.m16 * p.piece * 2);
   if (dx) p.dx = take(int64_t(p.parts) * m * krows * 4);
   p.total = at;

@@ -18,7 +18,7 @@ hipError_t launch_f8_fused(const hyb_f8&, int64_t, int64_t, const void*, int, in
   return hipErrorNoDevice;
 }
 hipError_t launch_f8_gemm(const hyb_f8&, int64_t, int64_t, const hyb_f8&, int64_t, void*, int, int64_t, float*,
-                          hipStream_t) {
+                          hipStream_t, int64_t) {
   return hipErrorNoDevice;
 }
 hipError_t launch_xent(const hyb_head&, const XentPlan&, int64_t, const void*, int, int64_t, const int64_t*, int64_t,
