@@ -24,6 +24,12 @@
 // half step, rows 16 (q/2) + 4 (q%2) + {0..3, 8..11}, q = L/16; where the other
 // operand is read straight, its columns are stored in that order.
 //
+// An 8-bit weight may be read the other way round too, as a 16-bit operand: of
+// 16 lanes, lane 2 i + c points at the eight codes 8 c.. of row i and lane j
+// receives column j of rows 0..7 (ds_read_b64_tr_b8); a lane holds rows
+// 16 (q/2) + 8 (q%2) + 0..7 of 32, and the codes are widened with their block's
+// scale (one for the 64 rows of a step, which lie in one block of 128).
+//
 // 8-bit operands carry one exponent byte per row and step (E8M0: 2^(byte -
 // 127)), four steps to a 32-bit word, word (s / 4) * scale_pitch + row; the
 // matrix instruction takes the word of its lane's row as it is and multiplies
@@ -70,6 +76,9 @@ struct PanelOperand {
   int64_t row0, plain;
   const int32_t* tidx;
   const char* spare;
+  // An 8-bit weight read transposed: rows from `plain` on count as zeros; in
+  // fp16 the values are divided by 2^(*top - 133).
+  const uint32_t* top;
 };
 
 __device__ __forceinline__ srd4_t panel_srd(const void* base, uint32_t bytes) {
@@ -204,20 +213,25 @@ __device__ __forceinline__ void panel_block(int32_t g, int32_t na, int32_t nb, i
 
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((ext_vector_type(2))) int i32x2_t;
+typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
 
 // LDS-fed tile: AP x BP panels per workgroup of WA x WB wavefronts, STAGES LDS
 // stages of one step each (transfers run STAGES - 1 steps ahead).  TA / TB:
 // that operand is read transposed (its "panels" here are blocks of 16 of its
-// columns).  TILED: A lies in tiles (PanelOperand).
-template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false, bool TILED = false>
+// columns).  TILED: A lies in tiles (PanelOperand).  CODES: A is an 8-bit weight
+// read transposed by a 16-bit product.
+template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false, bool TILED = false,
+          bool CODES = false>
 struct PanelTile {
   static_assert(STAGES == 2 || STAGES == 4, "a step's stage is an immediate of the loop unrolled by four");
   static constexpr int kWaves = WA * WB;
   static constexpr int kA = AP / WA, kB = BP / WB;  // panels per wavefront
-  static constexpr int kStage = (AP + BP) * 2048;
+  static constexpr int kStageA = CODES ? AP * 1024 : AP * 2048;
+  static constexpr int kStage = kStageA + BP * 2048;
   static constexpr int kScaleStage = is_f8(KIND) ? (AP + BP) * 64 : 0;  // a word per row, four steps
   static constexpr int kLds = STAGES * kStage + 2 * kScaleStage;
-  static constexpr int kLoadsA = AP * 2 / kWaves, kLoadsB = BP * 2 / kWaves;  // 1 KiB transfers per wavefront and step
+  static constexpr int kLoadsA = (CODES ? AP : AP * 2) / kWaves, kLoadsB = BP * 2 / kWaves;  // 1 KiB transfers per wavefront and step
   static_assert(AP % WA == 0 && BP % WB == 0 && AP * 2 % kWaves == 0 && BP * 2 % kWaves == 0, "even split");
   static_assert(!(TA || TB) || !is_f8(KIND), "8-bit operands are read straight");
 
@@ -356,6 +370,25 @@ struct PanelTile {
     }
   };
 
+  // The same for A as codes read transposed: a step is four panels of 16 rows,
+  // the tile's 256 columns two steps of each.  A wavefront transfers one.
+  template <int P, int LOADS>
+  struct CodesFeed {
+    const PanelOperand& o;
+    int32_t column;  // step of the panels
+
+    __device__ CodesFeed(const PanelOperand& op, int32_t p0, int wave) : o(op), column(p0 / 8 + (wave & 1)) {
+      static_assert(LOADS == 2 && P == 16, "eight wavefronts, 256 columns");
+    }
+    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
+      const int32_t panel = s * 4 + (wave >> 1);
+      const bool live = panel * 16 < o.rows16 && column < o.steps;
+      const srd4_t r = panel_srd(o.data + (live ? (int64_t(panel) * o.steps + column) * 2048 : 0), live ? 2048 : 0);
+      panel_dma16(r, dst + wave * 2048, lane * 16);
+      panel_dma16(r, dst + wave * 2048 + 1024, 1024 + lane * 16);
+    }
+  };
+
   // The two halves of panel p (of P) of a staged step.
   struct Halves {
     u32x4_t v[2];
@@ -382,6 +415,38 @@ struct PanelTile {
     return r;
   }
 
+  // A's codes of column block p: the eight rows of each half step in the first
+  // two words of its half.
+  __device__ __forceinline__ static Halves read_codes(const char* src, int p, int off) {
+    Halves r;
+    const char* b = src + (p >> 3) * 2048 + ((p >> 2) & 1) * 1024 + (p & 3) * 256 + off;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint2 u = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t*)(const_cast<char*>(b + h * 8192))));
+      r.v[h] = u32x4_t{u.x, u.y, 0, 0};
+    }
+    return r;
+  }
+  __device__ __forceinline__ static PanelRegs<KIND> widen_codes(const Halves& c, float scale) {
+    PanelRegs<KIND> r;
+    if constexpr (CODES) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (KIND == HYB_BF16) {
+            r.v[h][2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.v[h][i], scale, false));
+            r.v[h][2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.v[h][i], scale, true));
+          } else {
+            r.v[h][2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.v[h][i], scale, false));
+            r.v[h][2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.v[h][i], scale, true));
+          }
+        }
+    }
+    return r;
+  }
+
   // Lane offsets of the two transposing reads of a half: panel q/2 of the
   // half's two, rows 4 (q%2) + i (+ 8), columns 4 c.. of the block's 16.
   template <int P>
@@ -399,7 +464,9 @@ struct PanelTile {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wa = wave % WA, wb = wave / WA;
     auto fa = [&] {
-      if constexpr (TILED)
+      if constexpr (CODES)
+        return CodesFeed<AP, kLoadsA>(A, pa, wave);
+      else if constexpr (TILED)
         return TiledFeed<TA, AP, kLoadsA>(A, pa, wave);
       else
         return Feed<TA, AP, kLoadsA>(A, pa);
@@ -409,11 +476,14 @@ struct PanelTile {
     const int straight = lane * 16;
     const int ta0 = turn<AP>(lane, 0), ta1 = turn<AP>(lane, 1);
     const int tb0 = turn<BP>(lane, 0), tb1 = turn<BP>(lane, 1);
+    [[maybe_unused]] const int codes_off =
+        (lane >> 5) * 4096 + ((lane >> 4) & 1) * 128 + ((lane & 15) >> 1) * 16 + (lane & 1) * 8;
+    [[maybe_unused]] const int codes_top = CODES && KIND == HYB_F16 ? int(*A.top) : 0;
 
     auto issue = [&](int32_t s, int stage) {
       const uint32_t dst = base + stage * kStage;
       fa.issue(s, dst, wave, lane);
-      fb.issue(s, dst + AP * 2048, wave, lane);
+      fb.issue(s, dst + kStageA, wave, lane);
       if constexpr (is_f8(KIND)) {
         // the scale words of steps s .. s+3: AP * 64 + BP * 64 bytes
         if ((s & 3) == 0) {
@@ -453,7 +523,7 @@ struct PanelTile {
     auto compute = [&](int32_t s, int stage, auto byte, bool more) {
       constexpr int kByte = decltype(byte)::value;
       const char* src = smem + stage * kStage;
-      const char* srcb = src + AP * 2048;
+      const char* srcb = src + kStageA;
       if constexpr (is_f8(KIND)) {
         if (kByte == 0) {
           const char* sc = smem + STAGES * kStage + ((s >> 2) & 1) * kScaleStage + (lane & 15) * 4;
@@ -463,7 +533,35 @@ struct PanelTile {
           for (int j = 0; j < kB; ++j) scb[j] = *reinterpret_cast<const uint32_t*>(sc + (AP + wb * kB + j) * 64);
         }
       }
-      Halves a = read<TA, AP>(src, wa * kA, straight, ta0, ta1);
+      auto read_a = [&](int i) {
+        if constexpr (CODES) return read_codes(src, wa * kA + i, codes_off);
+        else return read<TA, AP>(src, wa * kA + i, straight, ta0, ta1);
+      };
+      [[maybe_unused]] float scale = 1.f;
+      if constexpr (CODES) {
+        // this wavefront's columns lie in one step of the panels
+        const int32_t column = pa / 8 + wa * kA / 8, at = column < A.steps ? column : 0;
+        const uint32_t word = A.scale[int64_t(at >> 2) * A.scale_pitch + s * 64];
+        int byte8 = int((word >> (8 * (at & 3))) & 0xFFu);
+        if constexpr (KIND == HYB_F16) {
+          byte8 += 133 - codes_top;
+          byte8 = byte8 < 1 ? 1 : byte8;
+        }
+        scale = __builtin_bit_cast(float, uint32_t(byte8) << 23);
+      }
+      // Rows behind the last that counts: their codes, whatever they are, zero.
+      auto mask_codes = [&](Halves& c) {
+        const int64_t left = A.plain - int64_t(s) * 64;
+        if (left >= 64) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int32_t keep = int32_t(left) - 32 * h - 16 * (lane >> 5) - 8 * ((lane >> 4) & 1);
+          const uint64_t m = keep <= 0 ? 0 : keep >= 8 ? ~uint64_t(0) : (uint64_t(1) << (8 * keep)) - 1;
+          c.v[h][0] &= uint32_t(m);
+          c.v[h][1] &= uint32_t(m >> 32);
+        }
+      };
+      Halves a = read_a(0);
       Halves braw[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) braw[j] = read<TB, BP>(srcb, wb * kB + j, straight, tb0, tb1);
@@ -474,8 +572,15 @@ struct PanelTile {
 #pragma unroll
       for (int i = 0; i < kA; ++i) {
         const Halves was = a;
-        if (i + 1 < kA) a = read<TA, AP>(src, wa * kA + i + 1, straight, ta0, ta1);
-        const PanelRegs<KIND> now = panel_regs<KIND, kByte>(was.v[0], was.v[1], sca[i]);
+        if (i + 1 < kA) a = read_a(i + 1);
+        PanelRegs<KIND> now;
+        if constexpr (CODES) {
+          Halves c = was;
+          mask_codes(c);
+          now = widen_codes(c, scale);
+        } else {
+          now = panel_regs<KIND, kByte>(was.v[0], was.v[1], sca[i]);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(now, b[j], acc[i][j], sca[i], scb[j]);

@@ -116,8 +116,11 @@ __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ d
   store_row16(dst, lane, e);
 }
 
-// Largest exponent byte of an 8-bit head's scales (rows < n_vocab), for the
-// fp16 form of its values; *top starts at 0.
+// Largest exponent byte of an 8-bit head's scales (rows < n_vocab); *top starts
+// at 0.  The fp16 form of its values is divided by 2^(top - 133): at most
+// 448 * 64, and exact for blocks whose scale is within 2^21 of the largest
+// (smaller ones lose bits of values that are below 2^-30 of the head's
+// largest).  bf16 holds every value as it is.
 __global__ __launch_bounds__(256) void k_xent_top_scale(const uint32_t* __restrict__ scales, int64_t rows16,
                                                         int64_t n_vocab, int32_t steps, uint32_t* __restrict__ top) {
   const int64_t row = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -137,48 +140,6 @@ __global__ __launch_bounds__(256) void k_xent_top_scale(const uint32_t* __restri
     t = o > t ? o : t;
   }
   if ((threadIdx.x & 63) == 0 && t > 0) atomicMax(top, t);
-}
-
-// Rows v0.. of an 8-bit head as 16-bit panels.  bf16 holds every value
-// exactly.  fp16 holds it divided by 2^(top - 133), top the head's largest
-// exponent byte: at most 448 * 64, and exact for blocks whose scale is
-// within 2^21 of the largest (smaller ones lose bits of values that are below
-// 2^-30 of the head's largest).
-template <int DT>
-__global__ __launch_bounds__(256) void k_xent_widen(const char* __restrict__ codes, const uint32_t* __restrict__ scales,
-                                                    int32_t rows16, int64_t v0, int64_t n_vocab, int32_t steps,
-                                                    const uint32_t* __restrict__ top, char* __restrict__ out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
-  if (s >= steps) return;
-  const int64_t row = v0 + int64_t(blockIdx.x) * 16 + (lane & 15);
-  const int64_t panel = v0 / 16 + blockIdx.x;
-  const bool row_ok = row < n_vocab;
-  uint32_t byte = row_ok ? (scales[int64_t(s >> 2) * rows16 + row] >> (8 * (s & 3))) & 0xFFu : 127u;
-  if constexpr (DT == HYB_F16) {
-    const int b = int(byte) - int(*top) + 133;
-    byte = uint32_t(b < 1 ? 1 : b);
-  }
-  const float f = __builtin_bit_cast(float, byte << 23);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (row_ok) {
-      const uint4 u = *reinterpret_cast<const uint4*>(codes + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (DT == HYB_BF16) {
-          e[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, false));
-          e[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], f, true));
-        } else {
-          e[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], f, false));
-          e[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], f, true));
-        }
-      }
-    }
-    store_row16(out + (int64_t(blockIdx.x) * 2 * steps + 2 * s + h) * kPanelStep, lane, e);
-  }
 }
 
 // --------------------------------------------------------------- the logits --
@@ -284,13 +245,15 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
         }
         // Row tok % 16 of panel tok / 16.  The four entries 16 i + 4 q + e,
         // q = lane / 16, lie where a lane of the dX product that reads W'
-        // transposed holds the same rows of W': unit 2 (i % 2) + q % 2, half
-        // q / 2 of its 16 bytes.
+        // transposed holds the same rows of W' (hyb_panel.h): unit 2 (i % 2) +
+        // q % 2, half q / 2 of its 16 bytes; of codes, rows in order, unit
+        // 2 (i % 2) + q / 2, half q % 2.
         const int32_t col = (ab * AP + wa * T::kA + i) * 16;
-        const int q = lane >> 4, u = 2 * ((col >> 4) & 1) + (q & 1);
+        const int q = lane >> 4, half = is_f8(KIND) ? q & 1 : q >> 1;
+        const int u = 2 * ((col >> 4) & 1) + (is_f8(KIND) ? q >> 1 : q & 1);
         if (tok < t.m16 && col < t.g_steps * 64)
           *reinterpret_cast<uint2*>(t.g + (int64_t(tok >> 4) * t.g_steps + (col >> 6)) * kPanelStep +
-                                    ((col & 32) >> 5) * 1024 + u * 256 + (tok & 15) * 16 + (q >> 1) * 8) =
+                                    ((col & 32) >> 5) * 1024 + u * 256 + (tok & 15) * 16 + half * 8) =
               make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
       }
     }
@@ -339,7 +302,7 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
 
 // G of a piece from its logits (few tokens): one wavefront per 16 tokens and 64
 // entries, in the order in which k_xent_tile leaves it.
-template <int DT>
+template <int DT, bool F8>
 __global__ __launch_bounds__(256) void k_xent_g_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t s = int32_t(blockIdx.x) * 4 + wave;
@@ -356,7 +319,7 @@ __global__ __launch_bounds__(256) void k_xent_g_rows(const float* __restrict__ z
     uint16_t g[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t c = s * 64 + h * 32 + 16 * (u >> 1) + 4 * (u & 1) + 8 * (e >> 2) + (e & 3);
+      const int64_t c = s * 64 + h * 32 + (F8 ? 8 * u + e : 16 * (u >> 1) + 4 * (u & 1) + 8 * (e >> 2) + (e & 3));
       const int64_t v = t.v0 + c;
       const float logit = seen && v < t.n_vocab ? z[tok * ldz + c] : 0.f;
       float p = (fast_exp(logit - lse) - (v == want ? 1.f : 0.f)) * f;
@@ -454,12 +417,12 @@ struct XentOut {
 // transposed, B = G), fp32, this workgroup's part of the steps, stored or
 // added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
 // transposed), 16-bit, scaled back by gtop.
-template <int DT, bool DX, bool TILED, int AP, int BP, int WA, int WB>
+template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED, CODES> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
-  const int32_t na = (A.steps * 4 + AP - 1) / AP;
+  const int32_t na = (A.steps * (CODES ? 8 : 4) + AP - 1) / AP;
   const int32_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
   int32_t ab, bb;
   const int32_t part = int32_t(blockIdx.y);
@@ -580,40 +543,32 @@ hipError_t run_tiles(const XentPlan& p, const PanelOperand& W, const PanelOperan
   return p.f8 ? run_shape<kF8Wide, DT, GRAD, false>(p.bp, W, X, t, s) : run_shape<DT, DT, GRAD, true>(p.bp, W, X, t, s);
 }
 
-template <int DT, bool DX, bool TILED, int AP, int BP, int WA, int WB>
+template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                        hipStream_t s) {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED> T;
-  const hipError_t e = allow_lds(&k_xent_product<DT, DX, TILED, AP, BP, WA, WB>, T::kLds);
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED, CODES> T;
+  const hipError_t e = allow_lds(&k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
-  const int64_t na = (A.steps * 4 + AP - 1) / AP;
+  const int64_t na = (A.steps * (CODES ? 8 : 4) + AP - 1) / AP;
   const int64_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
-  hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
+  hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
                      dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
   return hipGetLastError();
 }
 
-template <int DT, bool TILED>
+template <int DT, bool F8>
 hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                   hipStream_t s) {
-  if (bp == 16) return run_product<DT, true, TILED, 16, 16, 2, 4>(A, B, steps, parts, o, s);
-  if (bp == 8) return run_product<DT, true, TILED, 16, 8, 4, 2>(A, B, steps, parts, o, s);
-  return run_product<DT, true, TILED, 16, 4, 4, 2>(A, B, steps, parts, o, s);
+  if (bp == 16) return run_product<DT, true, !F8, F8, 16, 16, 2, 4>(A, B, steps, parts, o, s);
+  if (bp == 8) return run_product<DT, true, !F8, F8, 16, 8, 4, 2>(A, B, steps, parts, o, s);
+  return run_product<DT, true, !F8, F8, 16, 4, 4, 2>(A, B, steps, parts, o, s);
 }
 
-// What the products of the piece of `rows` vocabulary rows from v0 read beside
-// the head itself, in `out`: an 8-bit head as 16-bit panels (for dX), the
-// tiles of a packed head that PanelOperand calls spare.
-template <int DT>
+// The tiles of the piece of `rows` vocabulary rows from v0 that PanelOperand
+// calls spare, in `out`.
 hipError_t prepare_piece(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t plain, int64_t v0,
-                         int64_t rows, const uint32_t* top, char* out, hipStream_t s) {
+                         int64_t rows, char* out, hipStream_t s) {
   const unsigned panels = unsigned((rows + 15) / 16);
-  if (p.f8) {
-    hipLaunchKernelGGL((k_xent_widen<DT>), dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
-                       static_cast<const char*>(head.f8->codes), static_cast<const uint32_t*>(head.f8->scales),
-                       int32_t(f8_rows16(p.n)), v0, n_vocab, int32_t(p.steps), top, out);
-    return hipGetLastError();
-  }
   const hyb_layout& L = *head.layout;
   const hyb_packed& P = *head.packed;
   if (L.n_sparse == 0 && (v0 + rows + L.b1 - 1) / L.b1 * L.b1 <= plain) return hipSuccess;
@@ -719,7 +674,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     const int64_t step = whole ? n_vocab : p.piece;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
       const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
-      if (!whole) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, p.n, v0, rows, nullptr, ws + p.w, s));
+      if (!whole) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, s));
       t.v0 = v0;
       const PanelOperand W = piece_operand(head, p, p.n, v0, rows, whole ? nullptr : ws + p.w);
       HYB_TRY((run_tiles<DT, false>(p, W, X, t, s)));
@@ -756,16 +711,23 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     const int32_t vsteps = int32_t((rows + 63) / 64);
     t.v0 = v0;
     t.g_steps = vsteps;
-    // (logits of few tokens, and an 8-bit head's, do not need them)
-    if ((!p.rows && !p.f8) || dx) HYB_TRY(prepare_piece<DT>(head, p, n_vocab, n_vocab, v0, rows, top, ws + p.w, s));
-    const PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, ws + p.w);
+    // (the logits of few tokens do not need them)
+    if (!p.f8 && (!p.rows || dx)) HYB_TRY(prepare_piece(head, p, n_vocab, n_vocab, v0, rows, ws + p.w, s));
+    PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, ws + p.w);
+    if (p.f8) {
+      W.plain = n_vocab - v0;
+      W.top = top;
+    }
     if (p.rows) {
       // all of a packed head's tile rows that the piece reaches into
       const int64_t b1 = p.f8 ? 1 : head.layout->b1, whole = (rows + b1 - 1) / b1 * b1, ldz = (whole + 3) / 4 * 4;
       float* z = reinterpret_cast<float*>(ws + p.logits);
       HYB_TRY(piece_logits(head, p, x, ldx, v0, whole, z, ldz, ws, s));
-      hipLaunchKernelGGL((k_xent_g_rows<DT>), dim3(unsigned((vsteps + 3) / 4), unsigned(p.m16 / 16)), dim3(256), 0, s, z,
-                         ldz, t);
+      const dim3 grid(unsigned((vsteps + 3) / 4), unsigned(p.m16 / 16));
+      if (p.f8)
+        hipLaunchKernelGGL((k_xent_g_rows<DT, true>), grid, dim3(256), 0, s, z, ldz, t);
+      else
+        hipLaunchKernelGGL((k_xent_g_rows<DT, false>), grid, dim3(256), 0, s, z, ldz, t);
       HYB_TRY(hipGetLastError());
     } else {
       HYB_TRY((run_tiles<DT, true>(p, W, X, t, s)));
@@ -780,12 +742,8 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.first = v0 == 0;
       o.rows = int32_t(p.m);
       o.cols = krows;
-      if (!p.f8) {
-        HYB_TRY((run_dx<DT, true>(p.bp, W, G, vsteps, p.parts, o, s)));
-      } else {
-        const PanelOperand A{ws + p.w, int32_t((rows + 15) / 16 * 16), int32_t(p.ksteps16), nullptr, 0};
-        HYB_TRY((run_dx<DT, false>(p.bp, A, G, vsteps, p.parts, o, s)));
-      }
+      HYB_TRY(p.f8 ? (run_dx<DT, true>(p.bp, W, G, vsteps, p.parts, o, s))
+                   : (run_dx<DT, false>(p.bp, W, G, vsteps, p.parts, o, s)));
     }
     if (dw) {
       XentOut o{};
@@ -795,7 +753,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.rows = int32_t(rows);
       o.cols = int32_t(p.k);
       o.live = n_vocab - v0;
-      HYB_TRY((run_product<DT, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
+      HYB_TRY((run_product<DT, false, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
     }
   }
   if (dx) {

@@ -77,7 +77,7 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     p.zt = take(p.m16 * 4);
   }
   if (p.rows) p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
-  if ((!p.rows && !p.f8) || dx) p.w = take(p.piece * krows * 2);
+  if (!p.f8 && (!p.rows || dx)) p.w = take(p.piece * krows * 2);
   if (dx || dw) p.g = take(p.m16 * p.piece * 2);
   if (dx) p.dx = take(int64_t(p.parts) * m * krows * 4);
   p.total = at;
