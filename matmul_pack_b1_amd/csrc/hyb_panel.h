@@ -516,6 +516,27 @@ struct PanelTile {
 #pragma unroll
     for (int j = 0; j < kB; ++j) scb[j] = 0;
 
+    // Scale of the codes of step s: this wavefront's columns lie in one step of
+    // the panels, the step's 64 rows in one block.  Loaded during step s - 1
+    // and turned into a number after its products: a scalar load that is
+    // waited for beside LDS reads waits for all of them.
+    [[maybe_unused]] float codes_scale = 1.f;
+    auto scale_word = [&](int32_t s) -> uint32_t {
+      if constexpr (CODES) {
+        const int32_t column = pa / 8 + wa * kA / 8, at = column < A.steps ? column : 0;
+        return A.scale[int64_t(at >> 2) * A.scale_pitch + s * 64] >> (8 * (at & 3));
+      }
+      return 0;
+    };
+    auto set_scale = [&](uint32_t word) {
+      int byte8 = int(word & 0xFFu);
+      if constexpr (KIND == HYB_F16) {
+        byte8 += 133 - codes_top;
+        byte8 = byte8 < 1 ? 1 : byte8;
+      }
+      codes_scale = __builtin_bit_cast(float, uint32_t(byte8) << 23);
+    };
+
     // Multiplies the staged step s and, once its first reads are under way,
     // starts the transfers of step s + STAGES - 1.  The reads of A panel i + 1 are issued
     // ahead of panel i's products, so that an LDS round trip hides behind
@@ -537,18 +558,6 @@ struct PanelTile {
         if constexpr (CODES) return read_codes(src, wa * kA + i, codes_off);
         else return read<TA, AP>(src, wa * kA + i, straight, ta0, ta1);
       };
-      [[maybe_unused]] float scale = 1.f;
-      if constexpr (CODES) {
-        // this wavefront's columns lie in one step of the panels
-        const int32_t column = pa / 8 + wa * kA / 8, at = column < A.steps ? column : 0;
-        const uint32_t word = A.scale[int64_t(at >> 2) * A.scale_pitch + s * 64];
-        int byte8 = int((word >> (8 * (at & 3))) & 0xFFu);
-        if constexpr (KIND == HYB_F16) {
-          byte8 += 133 - codes_top;
-          byte8 = byte8 < 1 ? 1 : byte8;
-        }
-        scale = __builtin_bit_cast(float, uint32_t(byte8) << 23);
-      }
       // Rows behind the last that counts: their codes, whatever they are, zero.
       auto mask_codes = [&](Halves& c) {
         const int64_t left = A.plain - int64_t(s) * 64;
@@ -566,6 +575,9 @@ struct PanelTile {
 #pragma unroll
       for (int j = 0; j < kB; ++j) braw[j] = read<TB, BP>(srcb, wb * kB + j, straight, tb0, tb1);
       if (more) issue(s + STAGES - 1, (stage + STAGES - 1) % STAGES);
+      [[maybe_unused]] uint32_t next_word = 0;
+      if constexpr (CODES)
+        if (s + 1 < s1) next_word = scale_word(s + 1);
       PanelRegs<KIND> b[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) b[j] = panel_regs<KIND, kByte>(braw[j].v[0], braw[j].v[1], scb[j]);
@@ -577,7 +589,7 @@ struct PanelTile {
         if constexpr (CODES) {
           Halves c = was;
           mask_codes(c);
-          now = widen_codes(c, scale);
+          now = widen_codes(c, codes_scale);
         } else {
           now = panel_regs<KIND, kByte>(was.v[0], was.v[1], sca[i]);
         }
@@ -586,6 +598,7 @@ struct PanelTile {
         for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(now, b[j], acc[i][j], sca[i], scb[j]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (CODES) set_scale(next_word);
     };
 
     // A step waits for its own transfers (those of the STAGES - 2 steps after it
@@ -594,6 +607,7 @@ struct PanelTile {
     // that is filled next are then done too.  Unrolled by four so that stage
     // and scale byte are immediates.
     if (s0 >= s1) return;
+    if constexpr (CODES) set_scale(scale_word(s0));
 #pragma unroll
     for (int t = 0; t < STAGES - 1; ++t)
       if (s0 + t < s1) issue(s0 + t, t);

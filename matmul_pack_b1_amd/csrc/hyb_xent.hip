@@ -559,7 +559,8 @@ hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t ste
 template <int DT, bool F8>
 hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                   hipStream_t s) {
-  if (bp == 16) return run_product<DT, true, !F8, F8, 16, 16, 2, 4>(A, B, steps, parts, o, s);
+  // (codes: four wavefronts along the columns convert each only half as often)
+  if (bp == 16) return run_product<DT, true, !F8, F8, 16, 16, F8 ? 4 : 2, F8 ? 2 : 4>(A, B, steps, parts, o, s);
   if (bp == 8) return run_product<DT, true, !F8, F8, 16, 8, 4, 2>(A, B, steps, parts, o, s);
   return run_product<DT, true, !F8, F8, 16, 4, 4, 2>(A, B, steps, parts, o, s);
 }
