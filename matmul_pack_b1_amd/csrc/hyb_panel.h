@@ -236,6 +236,7 @@ struct PanelTile {
   static_assert(!(TA || TB) || !is_f8(KIND), "8-bit operands are read straight");
 
   // One operand's transfers of step s into its part of a stage.
+  // (prepare() sets up a step, put() issues one of a wavefront's transfers.)
   template <bool T, int P, int LOADS>
   struct Feed {
     srd4_t rsrc;
@@ -258,24 +259,22 @@ struct PanelTile {
         rsrc = panel_srd(data + p0 * pitch, uint32_t(n * pitch));
       }
     }
-    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
+    __device__ __forceinline__ void prepare(int32_t s, int, int) {
+      if constexpr (T) {
+        const int64_t off = s * 4 * pitch + first * 512;
+        const int64_t left = total - off;
+        rsrc = panel_srd(data + off, uint32_t(left < 0 ? 0 : left < (int64_t(1) << 31) ? left : (int64_t(1) << 31)));
+      }
+    }
+    __device__ __forceinline__ void put(int32_t s, uint32_t dst, int wave, int lane, int t) const {
+      const int c = wave * LOADS + t;
       if constexpr (T) {
         constexpr int kChunks = P / 2;  // 32-column halves per panel
         const int from = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
-        const int64_t off = s * 4 * pitch + first * 512;
-        const int64_t left = total - off;
-        const srd4_t r = panel_srd(data + off, uint32_t(left < 0 ? 0 : left < (int64_t(1) << 31) ? left : (int64_t(1) << 31)));
-#pragma unroll
-        for (int t = 0; t < LOADS; ++t) {
-          const int c = wave * LOADS + t;
-          panel_dma16(r, dst + c * 1024, int32_t(c / kChunks * pitch) + c % kChunks * 1024 + from);
-        }
+        panel_dma16(rsrc, dst + c * 1024, int32_t(c / kChunks * pitch) + c % kChunks * 1024 + from);
       } else {
-#pragma unroll
-        for (int t = 0; t < LOADS; ++t) {
-          const int c = wave * LOADS + t;  // panel c / 2, half c % 2
-          panel_dma16(rsrc, dst + c * 1024, int32_t((c >> 1) * pitch) + s * 2048 + (c & 1) * 1024 + lane * 16);
-        }
+        // panel c / 2, half c % 2
+        panel_dma16(rsrc, dst + c * 1024, int32_t((c >> 1) * pitch) + s * 2048 + (c & 1) * 1024 + lane * 16);
       }
     }
   };
@@ -293,6 +292,7 @@ struct PanelTile {
     int32_t slot0, slot1;
     int32_t now;          // tile column or row that the addresses are of
     const char *at0, *at1;
+    srd4_t r0, r1;        // the prepared step's
 
     __device__ TiledFeed(const PanelOperand& op, int32_t p0, int wave)
         : o(op), first(-64), slot0(-1), slot1(-1), now(-1), at0(nullptr), at1(nullptr) {
@@ -339,7 +339,7 @@ struct PanelTile {
       if (at0) at0 += (unit & mask) * 2048;
       if (at1) at1 += ((unit + 1) & mask) * 2048;
     }
-    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) {
+    __device__ __forceinline__ void prepare(int32_t s, int wave, int lane) {
       if constexpr (T) {
         const int32_t row = s * 64 + (wave >> 1) * 16, tn = row >> o.log_b1;
         if (tn != now) {
@@ -348,24 +348,24 @@ struct PanelTile {
         }
         const bool live = row < o.rows16;
         const int32_t down = (row & ((1 << o.log_b1) - 1)) << (o.log_b2 + 1);
-        const srd4_t r0 = panel_srd(at0 + down, live && at0 ? 2048 : 0);
-        const srd4_t r1 = panel_srd(at1 + down, live && at1 ? 2048 : 0);
-        const int from = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
-        panel_dma16(r0, dst + (wave * 4) * 1024, from);
-        panel_dma16(r0, dst + (wave * 4 + 1) * 1024, 1024 + from);
-        panel_dma16(r1, dst + (wave * 4 + 2) * 1024, from);
-        panel_dma16(r1, dst + (wave * 4 + 3) * 1024, 1024 + from);
+        r0 = panel_srd(at0 + down, live && at0 ? 2048 : 0);
+        r1 = panel_srd(at1 + down, live && at1 ? 2048 : 0);
       } else {
         const int shift = o.log_b2 - 6;
         if (s >> shift != now) {
           now = s >> shift;
           enter_column(now, lane);
         }
-        const int32_t next = 32 << o.log_b2;  // the tile's next panel
-        const srd4_t r = panel_srd(at0 + (s & ((1 << shift) - 1)) * 2048, at0 ? next + 2048 : 0);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          panel_dma16(r, dst + (wave * 4 + t) * 1024, (t >> 1) * next + (t & 1) * 1024 + lane * 16);
+        r0 = panel_srd(at0 + (s & ((1 << shift) - 1)) * 2048, at0 ? (32 << o.log_b2) + 2048 : 0);
+      }
+    }
+    __device__ __forceinline__ void put(int32_t, uint32_t dst, int wave, int lane, int t) const {
+      if constexpr (T) {
+        const int from = (lane >> 4) * 256 + ((lane & 15) ^ ((lane >> 4 & 1) * 8)) * 16;
+        panel_dma16(t < 2 ? r0 : r1, dst + (wave * 4 + t) * 1024, (t & 1) * 1024 + from);
+      } else {
+        // the tile's next panel is 32 b2 bytes on
+        panel_dma16(r0, dst + (wave * 4 + t) * 1024, (t >> 1) * (32 << o.log_b2) + (t & 1) * 1024 + lane * 16);
       }
     }
   };
@@ -376,16 +376,18 @@ struct PanelTile {
   struct CodesFeed {
     const PanelOperand& o;
     int32_t column;  // step of the panels
+    srd4_t r;        // the prepared step's
 
     __device__ CodesFeed(const PanelOperand& op, int32_t p0, int wave) : o(op), column(p0 / 8 + (wave & 1)) {
       static_assert(LOADS == 2 && P == 16, "eight wavefronts, 256 columns");
     }
-    __device__ __forceinline__ void issue(int32_t s, uint32_t dst, int wave, int lane) const {
+    __device__ __forceinline__ void prepare(int32_t s, int wave, int) {
       const int32_t panel = s * 4 + (wave >> 1);
       const bool live = panel * 16 < o.rows16 && column < o.steps;
-      const srd4_t r = panel_srd(o.data + (live ? (int64_t(panel) * o.steps + column) * 2048 : 0), live ? 2048 : 0);
-      panel_dma16(r, dst + wave * 2048, lane * 16);
-      panel_dma16(r, dst + wave * 2048 + 1024, 1024 + lane * 16);
+      r = panel_srd(o.data + (live ? (int64_t(panel) * o.steps + column) * 2048 : 0), live ? 2048 : 0);
+    }
+    __device__ __forceinline__ void put(int32_t, uint32_t dst, int wave, int lane, int t) const {
+      panel_dma16(r, dst + wave * 2048 + t * 1024, t * 1024 + lane * 16);
     }
   };
 
@@ -471,7 +473,7 @@ struct PanelTile {
       else
         return Feed<TA, AP, kLoadsA>(A, pa);
     }();
-    const Feed<TB, BP, kLoadsB> fb(B, pb);
+    Feed<TB, BP, kLoadsB> fb(B, pb);
     const uint32_t base = panel_lds_addr(smem);
     const int straight = lane * 16;
     const int ta0 = turn<AP>(lane, 0), ta1 = turn<AP>(lane, 1);
@@ -482,8 +484,12 @@ struct PanelTile {
 
     auto issue = [&](int32_t s, int stage) {
       const uint32_t dst = base + stage * kStage;
-      fa.issue(s, dst, wave, lane);
-      fb.issue(s, dst + kStageA, wave, lane);
+      fa.prepare(s, wave, lane);
+#pragma unroll
+      for (int t = 0; t < kLoadsA; ++t) fa.put(s, dst, wave, lane, t);
+      fb.prepare(s, wave, lane);
+#pragma unroll
+      for (int t = 0; t < kLoadsB; ++t) fb.put(s, dst + kStageA, wave, lane, t);
       if constexpr (is_f8(KIND)) {
         // the scale words of steps s .. s+3: AP * 64 + BP * 64 bytes
         if ((s & 3) == 0) {
@@ -538,9 +544,16 @@ struct PanelTile {
     };
 
     // Multiplies the staged step s and, once its first reads are under way,
-    // starts the transfers of step s + STAGES - 1.  The reads of A panel i + 1 are issued
-    // ahead of panel i's products, so that an LDS round trip hides behind
-    // them (the scheduling barriers keep the compiler from moving them back).
+    // starts the transfers of step s + STAGES - 1: at once, or (kSpread) two
+    // between the products of each A panel, where a transfer waits for the
+    // address unit without holding up the products.  That serves the product
+    // over codes, whose vector unit is busy widening (1000 tokens x 152064 x
+    // 5120 with dX 4145 -> 4045 us); the 16-bit ones lose by it, their
+    // transfers arriving late (dX piece 832 -> 868 us, dW 869 -> 926, logits
+    // even).  The reads of A panel i + 1 are issued ahead of panel i's
+    // products, so that an LDS round trip hides behind them (the scheduling
+    // barriers keep the compiler from moving them back).
+    constexpr bool kSpread = CODES && STAGES == 2 && kB % 2 == 0 && 2 * kA >= kLoadsA + kLoadsB;
     auto compute = [&](int32_t s, int stage, auto byte, bool more) {
       constexpr int kByte = decltype(byte)::value;
       const char* src = smem + stage * kStage;
@@ -574,7 +587,15 @@ struct PanelTile {
       Halves braw[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) braw[j] = read<TB, BP>(srcb, wb * kB + j, straight, tb0, tb1);
-      if (more) issue(s + STAGES - 1, (stage + STAGES - 1) % STAGES);
+      [[maybe_unused]] const uint32_t next_dst = base + ((stage + STAGES - 1) % STAGES) * kStage;
+      if (more) {
+        if constexpr (kSpread) {
+          fa.prepare(s + 1, wave, lane);
+          fb.prepare(s + 1, wave, lane);
+        } else {
+          issue(s + STAGES - 1, (stage + STAGES - 1) % STAGES);
+        }
+      }
       [[maybe_unused]] uint32_t next_word = 0;
       if constexpr (CODES)
         if (s + 1 < s1) next_word = scale_word(s + 1);
@@ -595,7 +616,22 @@ struct PanelTile {
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < kB; ++j) acc[i][j] = panel_mfma<KIND, kByte>(now, b[j], acc[i][j], sca[i], scb[j]);
+        for (int j = 0; j < kB; ++j) {
+          acc[i][j] = panel_mfma<KIND, kByte>(now, b[j], acc[i][j], sca[i], scb[j]);
+          if constexpr (kSpread) {
+            const int t = 2 * i + j / (kB / 2);
+            if (j % (kB / 2) == kB / 2 - 1 && t < kLoadsA + kLoadsB) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (more) {
+                if (t < kLoadsA)
+                  fa.put(s + 1, next_dst, wave, lane, t);
+                else
+                  fb.put(s + 1, next_dst + kStageA, wave, lane, t - kLoadsA);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (CODES) set_scale(next_word);

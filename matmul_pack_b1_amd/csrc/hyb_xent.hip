@@ -754,7 +754,11 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.rows = int32_t(rows);
       o.cols = int32_t(p.k);
       o.live = n_vocab - v0;
-      HYB_TRY((run_product<DT, false, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
+      // few tokens: bound by the writes of dW, and two of the smaller tiles share
+      // a CU (65536 x 4096, 16 / 200 / 400 / 800 tokens, logits included: 340 /
+      // 505 / 601 / 998 us against 386 / 537 / 603 / 956)
+      HYB_TRY(p.m <= 256 ? (run_product<DT, false, false, false, 8, 8, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s))
+                         : (run_product<DT, false, false, false, 16, 16, 2, 4>(X, G, int32_t(p.m64 / 64), 1, o, s)));
     }
   }
   if (dx) {
