@@ -17,6 +17,8 @@ constexpr int64_t kF8MaxK = int64_t(1) << 22;
 // one grid dimension.
 constexpr int64_t kF8MaxRows = (int64_t(1) << 27) - 16;
 constexpr int64_t kF8MaxPanelPairs = int64_t(1) << 29;
+// Largest grid in its second dimension.
+constexpr int64_t kF8MaxGridY = 65535;
 
 inline int64_t f8_steps(int64_t k) { return (k + kF8Step - 1) / kF8Step; }
 inline int64_t f8_rows16(int64_t rows) { return (rows + 15) / 16 * 16; }

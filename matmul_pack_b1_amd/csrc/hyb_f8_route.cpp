@@ -42,6 +42,7 @@ F8Route f8_route(int64_t n, int64_t k, int64_t m, bool wide, int64_t cus) {
     double step, quad;
   };
   for (const Rows& c : {Rows{1, 0.086, 2.0}, Rows{2, 0.125, 3.2}, Rows{4, 0.205, 5.6}}) {
+    if (up(mp, c.bp) > kF8MaxGridY) continue;  // its tokens are the grid's second dimension
     const double full = double(np * up(mp, c.bp)) * double(steps) / double(cus) * c.step;
     offer(F8Route{1, c.bp, 8, 0, 1}, 2.4 + longest(full, double(up(quads, 8)) * c.quad, stream));
   }

@@ -272,3 +272,18 @@ def test_one_call_is_quantise_then_product(m, dtype):
         wide = torch.zeros(m, k + 3, dtype=DT[dtype], device="cuda")
         wide[:, :k] = x
         assert torch.equal(f8.gemm(Q, wide[:, :k], out_dtype=dt), want)
+
+
+def test_more_tokens_than_a_grid_dimension():
+    # 65536 workgroups of 64 tokens and one more panel: the tokens of a narrow
+    # weight do not fit the second dimension of a grid
+    m, n, k = 65536 * 64 + 16, 16, 16
+    W, X = f8.pack(normal(60, n, k, "bf16")), f8.quant(normal(61, m, k, "bf16"))
+    for out in (torch.float32, torch.bfloat16):
+        y = f8.gemm(W, X, out_dtype=out)
+        x8, w8 = as64(f8.unpack(X, out_dtype=torch.float32)), as64(f8.unpack(W, out_dtype=torch.float32))
+        ref, size = x8 @ w8.T, np.abs(x8) @ np.abs(w8.T)
+        bound = k * 2.0 ** -23 * size + HALF[out] * np.abs(ref)
+        if out != torch.float32:
+            bound += 2.0 ** -11 * np.abs(x8).max(1, keepdims=True) * np.abs(w8).max(1)[None]
+        assert (np.abs(as64(y) - ref) <= bound).all()
