@@ -173,7 +173,9 @@ __device__ __forceinline__ uint2 codes8(const Eight<DT>& r, uint32_t e, bool mar
 // the codes go through LDS into panel order and leave as 1 KiB stores.  A
 // weight block is eight panels: a workgroup of eight wavefronts, whose maxima
 // meet in LDS.  Bound by memory: one read of the matrix, half or a quarter as
-// many bytes written (28672 x 8192 bf16: see the measurements).
+// many bytes written.  28672 x 8192 bf16 as a weight 182 us (706 MB, 3.9 TB/s;
+// a copy runs at 4.8), 2048 x 17408 as rows 20 us (5.3 TB/s, from the last-level
+// cache); one token 4 us, a launch and one round trip to memory.
 template <int DT, bool WEIGHT>
 __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* __restrict__ a, int64_t rows,
                                                                     int32_t k, int64_t lda, char* __restrict__ codes,
@@ -253,7 +255,9 @@ __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* 
   scales[((int64_t(s0 / 4) * panels * 16) + r0 + j) * 4 + (lane >> 4)] = char(mine);
 }
 
-// One wavefront per panel and step (a workgroup's four take four steps).
+// One wavefront per panel and step (a workgroup's four take four steps): its
+// 1 KiB loads are the panel's order, its stores 16 columns of 16 rows.  Bound by
+// memory: 28672 x 8192 to bf16 143 us (4.9 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void k_f8_dequantize(const char* __restrict__ codes,
                                                        const uint32_t* __restrict__ scales, int64_t rows, int32_t k,
@@ -358,13 +362,17 @@ __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, 
 // Few tokens: one w panel (16 rows) and BP x panels per workgroup, whose
 // WAVES wavefronts take four steps (512 columns) in turn, the codes straight
 // from memory to the operand registers.  Bound by the read of w, so the wide
-// kind costs nothing here and serves every output type.
+// kind costs nothing here and serves every output type: 14336x4096 12.8 us at 1
+// to 8 quantised tokens, 17408x5120 18.9 (4.7 TB/s).
 //
 // XDT other than 0 (BP 1, at most kFusedTokens tokens): X is still in its own
 // type, and every wavefront quantises the columns it multiplies, while its
-// codes of w are on their way.  Per token that costs a wavefront about 60
-// instructions per four steps, a launch of its own 5 us: 14336x4096 at one
-// token 17.7 us in two launches.
+// codes of w are on their way.  Per token that costs every wavefront about 60
+// instructions per four steps, a launch of its own 4 us once.  In one launch
+// against two, at 1 / 2 / 4 tokens: 14336x4096 12.0 / 13.4 / 16.4 us against
+// 16.4 / 16.6 / 17.0, 5120x5120 8.8 / 9.8 / 11.9 against 12.3 / 12.7 / 12.9,
+// 1024x4096 4.5 / 5.0 / 6.0 against 7.9 / 8.0 / 8.4, 17408x5120 17.5 / 19.5 /
+// 23.7 against 22.4 / 22.6 / 22.8.
 struct PlainRows {
   const void* x;
   int64_t ldx;
@@ -468,7 +476,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
   }
 }
 
-// More tokens: AP x BP panels per workgroup through LDS.  The first `whole`
+// More tokens: AP x BP panels per workgroup through LDS, bound by the matrix
+// instructions and, on a chip that lowers its clock under them, by power:
+// 17408x5120 at 4096 tokens, bf16 to bf16, 333 us with the quantising (2.2
+// PFLOP/s; the library's 8-bit product without block scales takes 330).  The
+// first `whole`
 // tiles (whole rounds of the compute units) run over all of k; each of the
 // rest is cut into `parts`, whose sums are left in `ws` (wavefront by
 // wavefront, as they lie in registers) for k_f8_sum.
@@ -536,7 +548,8 @@ __global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelO
 }
 
 // Adds the parts of a tile in order and stores the outputs: one workgroup per
-// four of a tile's AP x BP panel products.
+// four of a tile's AP x BP panel products.  Bound by memory (17408x5120 at 256
+// tokens 4 us).
 template <int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(256) void k_f8_sum(const f32x4_t* __restrict__ ws, int32_t na, int32_t nb, int32_t whole,
                                                 int parts, F8Out out) {

@@ -33,6 +33,7 @@ constexpr float g_scale() {
 // ------------------------------------------------------------ operand forms --
 
 // x (m x k, row-major) as panels; rows of ignored tokens and behind m zero.
+// Bound by memory (4096 x 4096 17 us, once a call).
 __global__ __launch_bounds__(256) void k_xent_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m,
                                                      int32_t steps, const int64_t* __restrict__ target, int64_t ignore,
                                                      char* __restrict__ out) {
@@ -63,7 +64,8 @@ __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t
 // lie, into `out` in tile order (one wavefront per panel and step): sparse ones
 // expanded from their values and codes, those of a tile row that reaches into
 // the padding with its rows from n_vocab on zero, ones without a slot zero.
-// `plain` as in PanelOperand.
+// `plain` as in PanelOperand.  Bound by the writes: 37 us for a piece of 32768 x
+// 4096 with 30% of its tiles sparse.
 __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ dense, const uint4* __restrict__ val,
                                                      const uint16_t* __restrict__ meta,
                                                      const int32_t* __restrict__ tidx, int b1, int b2, int meta_kind,
@@ -161,7 +163,12 @@ struct XentTile {
 };
 
 // One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
-// leaves the softmax sums, true G.
+// leaves the softmax sums, true G.  Bound by the matrix instructions (and the
+// clock they leave): a piece of 32768 x 4096, bf16, 4096 tokens takes 820 to 855
+// us with the sums (1.3 PFLOP/s), 937 with G, whose exponentials and 256 MB of
+// writes come after the tile's products and hide behind no others, a CU's LDS
+// being full with one tile.  The library's plain product of that size runs at
+// 1.45 PFLOP/s and leaves the logits to read.
 template <int KIND, int DT, bool GRAD, bool TILED, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, XentTile t) {
   typedef PanelTile<KIND, AP, BP, WA, WB, 2, false, false, TILED> T;
@@ -261,7 +268,9 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
 }
 
 // Softmax sums of rows of fp32 logits (few tokens; the piece from t.v0, a
-// multiple of 2048), one workgroup per chunk of 2048 entries and token.
+// multiple of 2048), one workgroup per chunk of 2048 entries and token.  Bound
+// by latency: the logits were just written and lie in the last-level cache (5
+// tokens x 32000 5 us).
 __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
   __shared__ float2 sums[4];
   const int32_t tok = int32_t(blockIdx.y);
@@ -336,7 +345,7 @@ __global__ __launch_bounds__(256) void k_xent_g_rows(const float* __restrict__ z
 }
 
 // Joins a token's partial sums: 16 tokens per workgroup, 64 threads each, in a
-// fixed order.
+// fixed order (4096 tokens x 501 sums 9 us).
 __global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ part, int64_t chunks, int32_t m,
                                                     int32_t m16, const float* __restrict__ zt,
                                                     const int64_t* __restrict__ target, int64_t ignore,
@@ -374,7 +383,7 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ p
 // ------------------------------------------------------------ the gradients --
 
 // Smallest power of two >= the largest finite |grad| of a token that counts
-// (1 if there is none); also clears *top.
+// (2^-100 if there is none); also clears *top.  One workgroup, 5 us.
 __global__ __launch_bounds__(1024) void k_xent_grad_top(const float* __restrict__ grad,
                                                         const int64_t* __restrict__ target, int64_t ignore, int32_t m,
                                                         float* __restrict__ gtop, uint32_t* __restrict__ top) {
@@ -416,7 +425,10 @@ struct XentOut {
 // DX: Y[token, column] = sum over the piece's entries of G W' (A = W' read
 // transposed, B = G), fp32, this workgroup's part of the steps, stored or
 // added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
-// transposed), 16-bit, scaled back by gtop.
+// transposed), 16-bit, scaled back by gtop.  Bound as k_xent_tile is: a piece of
+// 32768 x 4096 with 4096 tokens takes 833 us for dX, 857 for dW (1.3 PFLOP/s);
+// dX over codes, 1000 tokens and 40960 x 5120, 327 us (1.3 PFLOP/s as well, the
+// vector unit widening beside the matrix unit).
 template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
@@ -476,7 +488,8 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
   }
 }
 
-// dX = gtop * sum of the parts (in order), rounded once; ignored tokens 0.
+// dX = gtop * sum of the parts (in order), rounded once; ignored tokens 0.  Bound
+// by memory (4096 x 4096, one part, 22 us).
 template <int DT, bool F8>
 __global__ __launch_bounds__(256) void k_xent_dx(const float* __restrict__ acc, int64_t ld, int64_t part, int parts,
                                                  int32_t m, int32_t k, const int64_t* __restrict__ target,
