@@ -168,91 +168,84 @@ __device__ __forceinline__ uint2 codes8(const Eight<DT>& r, uint32_t e, bool mar
   return make_uint2(w[0], w[1]);
 }
 
-// One wavefront per panel and four steps: a load covers 512 columns of one row
-// (8 per lane, 16 lanes to a step), so a row's maximum is one over 16 lanes;
-// the codes go through LDS into panel order and leave as 1 KiB stores.  A
-// weight block is eight panels: a workgroup of eight wavefronts, whose maxima
+// One wavefront per panel and step: a load covers 128 columns of four rows (8
+// columns per lane, 16 lanes to a row), so a row's maximum is one over 16
+// lanes, and a lane's codes are half of its row's 16 bytes of a unit, which
+// leave as they are, in pieces of 64 bytes.  A workgroup takes four steps of a
+// panel, or (a weight) one step of the eight panels of a block, whose maxima
 // meet in LDS.  Bound by memory: one read of the matrix, half or a quarter as
-// many bytes written.  28672 x 8192 bf16 as a weight 182 us (706 MB, 3.9 TB/s;
-// a copy runs at 4.8), 2048 x 17408 as rows 20 us (5.3 TB/s, from the last-level
-// cache); one token 4 us, a launch and one round trip to memory.
+// many bytes written.  28672 x 8192 bf16 as a weight 162 us (706 MB, 4.4 TB/s; a
+// copy runs at 4.8), 2048 x 17408 as rows 18 us (6 TB/s, from the last-level
+// cache); few rows by latency: one token of 4096 3.3 us, 256 of 5120 4.4.  (Four
+// steps to a wavefront, through LDS into whole 1 KiB stores: 182, 20, 3.8, 9.1.)
 template <int DT, bool WEIGHT>
 __global__ __launch_bounds__(WEIGHT ? 512 : 256) void k_f8_quantize(const void* __restrict__ a, int64_t rows,
                                                                     int32_t k, int64_t lda, char* __restrict__ codes,
                                                                     char* __restrict__ scales, int32_t panels,
-                                                                    int32_t steps) {
-  constexpr int kWaves = WEIGHT ? 8 : 4;
-  __shared__ __attribute__((aligned(16))) char turn_lds[kWaves][8192];
-  __shared__ uint32_t top_lds[8][4];
+                                                                    int32_t steps, int32_t across) {
+  __shared__ uint32_t top_lds[8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // a weight's wavefronts take the panels of a block, a row matrix's the quads
-  const int64_t panel = WEIGHT ? int64_t(blockIdx.x) * 8 + wave : blockIdx.x;
-  const int32_t s0 = (WEIGHT ? int32_t(blockIdx.y) : int32_t(blockIdx.y) * 4 + wave) * 4;
+  const int32_t id = int32_t(blockIdx.x), down = id / across, over = id % across;
+  const int64_t panel = WEIGHT ? int64_t(down) * 8 + wave : down;
+  const int32_t s = WEIGHT ? over : over * 4 + wave;
   const int64_t r0 = panel * 16;
-  const int32_t c0 = s0 * 128 + lane * 8;
-  const bool live = panel < panels && s0 < steps;
-  Eight<DT> v[16];
-  uint32_t top[16];
+  const int g = lane >> 4, j = lane & 15;
+  const int32_t c0 = s * 128 + j * 8;
+  const bool live = panel < panels && s < steps;
+  Eight<DT> v[4];
+  uint32_t top[4];
   uint32_t all = 0;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) v[r] = load8<DT>(a, (r0 + r) * lda, c0, r0 + r < rows && live ? k : 0);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = r0 + i * 4 + g;
+    v[i] = load8<DT>(a, row * lda, c0, row < rows && live ? k : 0);
+  }
   if (!__all(c0 + 8 <= k)) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) trim8<DT>(v[r], c0, k);
+    for (int i = 0; i < 4; ++i) trim8<DT>(v[i], c0, r0 + i * 4 + g < rows && live ? k : 0);
   }
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    top[r] = top_of<DT>(v[r]);
-    all = top[r] > all ? top[r] : all;
+  for (int i = 0; i < 4; ++i) {
+    top[i] = top_of<DT>(v[i]);
+    all = top[i] > all ? top[i] : all;
   }
   const bool mark = __any(all >= kF32Inf);
   if (mark) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) top[r] = top_finite<DT>(v[r]);
+    for (int i = 0; i < 4; ++i) top[i] = top_finite<DT>(v[i]);
   }
   if constexpr (WEIGHT) {
     uint32_t t = 0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) t = top[r] > t ? top[r] : t;
+    for (int i = 0; i < 4; ++i) t = top[i] > t ? top[i] : t;
     t = max16(t);
-    if ((lane & 15) == 0) top_lds[wave][lane >> 4] = t;
+#pragma unroll
+    for (int d = 16; d < 64; d *= 2) {
+      const uint32_t o = __shfl_xor(t, d);
+      t = o > t ? o : t;
+    }
+    if (lane == 0) top_lds[wave] = t;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t = top_lds[w][lane >> 4] > t ? top_lds[w][lane >> 4] : t;
+    for (int w = 0; w < 8; ++w) t = top_lds[w] > t ? top_lds[w] : t;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) top[r] = t;
+    for (int i = 0; i < 4; ++i) top[i] = t;
   }
-  if (!live) return;
-  // Columns 8 j.. (j = lane % 16) of a step: half j / 8, unit (j % 8) / 2, one
-  // half of its row's 16 bytes.  Rows are rotated within a unit so that the
-  // units, all multiples of 256 bytes, are written through different banks.
-  char* turn = turn_lds[wave];
-  const int j = lane & 15;
-  const int unit = (lane >> 4) * 8 + (j >> 1);  // 256-byte unit of the 8 KiB
-  uint32_t mine = 127;
+  if (panel >= panels) return;
+  // Columns 8 j.. of a step: half j / 8, unit (j % 8) / 2, one half of the
+  // row's 16 bytes.
+  char* out = codes + (panel * steps + s) * kPanelStep + (j >> 1) * 256 + (j & 1) * 8;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    uint2* to = reinterpret_cast<uint2*>(turn + unit * 256 + ((r + unit) & 15) * 16 + (j & 1) * 8);
-    if (r0 + r >= rows) {  // uniform: a short last panel (decode) skips the arithmetic
-      *to = make_uint2(0, 0);
-      continue;
-    }
-    if constexpr (!WEIGHT) top[r] = max16(top[r]);
-    const uint32_t e = block_exponent(top[r]);
-    if (r == j && s0 + (lane >> 4) < steps) mine = e;
-    *to = codes8<DT>(v[r], e, mark);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 4 + g;
+    if constexpr (!WEIGHT) top[i] = max16(top[i]);
+    const bool in = live && r0 + r < rows;
+    const uint32_t e = in ? block_exponent(top[i]) : 127u;
+    const uint2 u = codes8<DT>(v[i], e, mark);
+    if (live) *reinterpret_cast<uint2*>(out + r * 16) = u;
+    if (j == 0) scales[((int64_t(s >> 2) * panels * 16) + r0 + r) * 4 + (s & 3)] = char(e);
   }
-  // one wavefront writes and reads `turn`: its own accesses done suffices
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    if (s0 + p / 2 >= steps) break;
-    const int u = p * 4 + (lane >> 4);
-    *reinterpret_cast<uint4*>(codes + (panel * steps + s0) * kPanelStep + p * 1024 + lane * 16) =
-        *reinterpret_cast<const uint4*>(turn + u * 256 + ((j + u) & 15) * 16);
-  }
-  scales[((int64_t(s0 / 4) * panels * 16) + r0 + j) * 4 + (lane >> 4)] = char(mine);
 }
 
 // One wavefront per panel and step (a workgroup's four take four steps): its
@@ -368,17 +361,17 @@ __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, 
 // XDT other than 0 (BP 1, at most kFusedTokens tokens): X is still in its own
 // type, and every wavefront quantises the columns it multiplies, while its
 // codes of w are on their way.  Per token that costs every wavefront about 60
-// instructions per four steps, a launch of its own 4 us once.  In one launch
-// against two, at 1 / 2 / 4 tokens: 14336x4096 12.0 / 13.4 / 16.4 us against
-// 16.4 / 16.6 / 17.0, 5120x5120 8.8 / 9.8 / 11.9 against 12.3 / 12.7 / 12.9,
-// 1024x4096 4.5 / 5.0 / 6.0 against 7.9 / 8.0 / 8.4, 17408x5120 17.5 / 19.5 /
-// 23.7 against 22.4 / 22.6 / 22.8.
+// instructions per four steps, a launch of its own 3 us once.  In one launch
+// against two, at 1 / 2 / 4 tokens: 14336x4096 12.0 / 13.3 / 16.4 us against
+// 15.5 / 15.7 / 15.7, 5120x5120 8.8 / 9.7 / 11.9 against 11.6 / 11.8 / 11.6,
+// 4096x14336 12.7 / 15.1 / 18.5 against 16.0 / 16.4 / 16.3, 17408x5120 17.5 /
+// 19.5 / 23.8 against 21.8 / 21.5 / 21.7.
 struct PlainRows {
   const void* x;
   int64_t ldx;
   int32_t k;
 };
-constexpr int kFusedTokens = 4;
+constexpr int kFusedTokens = 3;
 
 template <int BP, int WAVES, int XDT = 0>
 __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOperand X, PlainRows plain, F8Out out) {
@@ -634,16 +627,20 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
                               const hyb_f8& dst, hipStream_t s) {
   const int32_t panels = int32_t(f8_rows16(rows) / 16), steps = int32_t(f8_steps(k));
   const unsigned quads = unsigned((steps + 3) / 4);
-  const dim3 grid = kind == HYB_F8_WEIGHT ? dim3(unsigned((panels + 7) / 8), quads) : dim3(unsigned(panels), (quads + 3) / 4);
+  // workgroups along a panel's steps (its bytes of scales beyond the last step
+  // are written too), and in all
+  const int32_t across = int32_t(kind == HYB_F8_WEIGHT ? quads * 4 : quads);
+  const int64_t grid = int64_t(kind == HYB_F8_WEIGHT ? (panels + 7) / 8 : panels) * across;
+  if (grid * 512 >= int64_t(1) << 32) return hipErrorInvalidValue;  // more elements than a card holds
   char* codes = static_cast<char*>(dst.codes);
   char* scales = static_cast<char*>(dst.scales);
 #define HYB_F8_QUANT(DT)                                                                                             \
   if (kind == HYB_F8_WEIGHT)                                                                                         \
-    hipLaunchKernelGGL((k_f8_quantize<DT, true>), grid, dim3(512), 0, s, a, rows, int32_t(k), lda, codes,            \
-                       scales, panels, steps);                                                                       \
+    hipLaunchKernelGGL((k_f8_quantize<DT, true>), dim3(unsigned(grid)), dim3(512), 0, s, a, rows, int32_t(k), lda, codes,            \
+                       scales, panels, steps, across);                                                               \
   else                                                                                                               \
-    hipLaunchKernelGGL((k_f8_quantize<DT, false>), grid, dim3(256), 0, s, a, rows, int32_t(k), lda, codes,           \
-                       scales, panels, steps)
+    hipLaunchKernelGGL((k_f8_quantize<DT, false>), dim3(unsigned(grid)), dim3(256), 0, s, a, rows, int32_t(k), lda, codes,           \
+                       scales, panels, steps, across)
   if (dtype == HYB_F32) {
     HYB_F8_QUANT(HYB_F32);
   } else if (dtype == HYB_BF16) {

@@ -427,8 +427,8 @@ struct XentOut {
 // added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
 // transposed), 16-bit, scaled back by gtop.  Bound as k_xent_tile is: a piece of
 // 32768 x 4096 with 4096 tokens takes 833 us for dX, 857 for dW (1.3 PFLOP/s);
-// dX over codes, 1000 tokens and 40960 x 5120, 327 us (1.3 PFLOP/s as well, the
-// vector unit widening beside the matrix unit).
+// dX over codes, 1000 tokens and 32768 x 5120, 327 us (1.05 PFLOP/s: 240
+// workgroups, the vector unit widening beside the matrix unit).
 template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {

@@ -258,7 +258,7 @@ def test_two_streams():
         assert all(torch.equal(g, w_) for g in got[i]), i
 
 
-@pytest.mark.parametrize("m", [1, 16, 70, 300, 2100])
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 16, 70, 300, 2100])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_one_call_is_quantise_then_product(m, dtype):
     n, k = 1100, 3000
