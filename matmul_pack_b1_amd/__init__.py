@@ -3,7 +3,8 @@
 The compute lives in libhyb.so (HIP kernels behind the C ABI of
 include/hyb.h); this package is its ctypes binding plus the seeded synthetic
 workloads.  Importing the package does not load the library; the first call
-that needs it does, and raises if it has not been built.
+that needs it does, and raises if it has not been built.  The modules f8 and
+xent hold the 8-bit block-scaled product and the cross entropy.
 """
 from .binding import (  # noqa: F401
     HybError, HybLayout, HybPacked, PackedWeight, allocate, bits_to_tensor, gemm,
