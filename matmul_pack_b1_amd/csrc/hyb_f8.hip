@@ -339,11 +339,9 @@ __device__ __forceinline__ void f8_store4(const F8Out& o, int64_t m, int32_t n, 
       }
       *reinterpret_cast<Bytes16*>(static_cast<float*>(o.y) + at) = u;
     } else {
-      uint16_t h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = o.ydt == HYB_BF16 ? round16<HYB_BF16>(v[e]) : round16<HYB_F16>(v[e]);
-      *reinterpret_cast<Bytes8*>(static_cast<uint16_t*>(o.y) + at) =
-          Bytes8{{h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16}};
+      const uint2 h = o.ydt == HYB_BF16 ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3])
+                                        : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<Bytes8*>(static_cast<uint16_t*>(o.y) + at) = Bytes8{{h.x, h.y}};
     }
     return;
   }
@@ -471,7 +469,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_f8_rows(PanelOperand W, PanelOpe
 
 // More tokens: AP x BP panels per workgroup through LDS, bound by the matrix
 // instructions and, on a chip that lowers its clock under them, by power:
-// 17408x5120 at 4096 tokens, bf16 to bf16, 333 us with the quantising (2.2
+// 17408x5120 at 4096 tokens, bf16 to bf16, 322 us with the quantising (2.3
 // PFLOP/s; the library's 8-bit product without block scales takes 330).  The
 // first `whole`
 // tiles (whole rounds of the compute units) run over all of k; each of the
@@ -510,11 +508,9 @@ __global__ __launch_bounds__(64 * WA * WB) void k_f8_tile(PanelOperand W, PanelO
     panel_rows16<T::kA, T::kB>(
         f8_smem + wave * (T::kA * T::kB * 512), lane, lane & 15,
         [&](int i, int j) {
-          uint16_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = out.ydt == HYB_BF16 ? round16<HYB_BF16>(acc[i][j][e]) : round16<HYB_F16>(acc[i][j][e]);
-          return make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+          const f32x4_t v = acc[i][j];
+          return out.ydt == HYB_BF16 ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3])
+                                     : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
         },
         [&](int row, int col, uint4 u) {
           const int64_t m = m0 + row;

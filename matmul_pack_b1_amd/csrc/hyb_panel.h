@@ -166,6 +166,25 @@ struct __attribute__((packed, aligned(2))) Bytes8 {
   uint32_t w[2];
 };
 
+// Two or four fp32 values to 16 bits, to nearest even: one instruction for two
+// (rounding in integers takes six for each).
+template <int DT>
+__device__ __forceinline__ uint32_t round16x2(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+  const f32x2_t v = {a, b};
+  if constexpr (DT == HYB_BF16) {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+  } else {
+    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint2 round16x4(float a, float b, float c, float d) {
+  return make_uint2(round16x2<DT>(a, b), round16x2<DT>(c, d));
+}
+
 // A wavefront's KA x KB panels of 16-bit results, row by row.  In registers a
 // lane has four columns of a row, so a store would cover 32 bytes of each of
 // 16 rows; through LDS (its own 512 KA KB bytes, 16-byte units rotated by the

@@ -21,6 +21,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// exp(z - x) as exp2(fma(z, log2 e, -hi)) * fix, two instructions an element:
+// hi is x log2 e rounded, fix takes its rounding back.
+struct ExpBase {
+  float hi, fix;
+  __device__ __forceinline__ explicit ExpBase(float x) {
+    hi = x * kLog2e;
+    fix = __builtin_fabsf(hi) < __builtin_inff() ? __builtin_amdgcn_exp2f(-__builtin_fmaf(x, kLog2e, -hi)) : 1.f;
+  }
+  __device__ __forceinline__ float raw(float z) const {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -hi));
+  }
+};
+
 // exp(a - b) for a <= b where both may be -inf (an empty sum): 0.
 __device__ __forceinline__ float rescale(float a, float b) { return a == b ? 1.f : fast_exp(a - b); }
 
@@ -164,11 +177,12 @@ struct XentTile {
 
 // One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
 // leaves the softmax sums, true G.  Bound by the matrix instructions (and the
-// clock they leave): a piece of 32768 x 4096, bf16, 4096 tokens takes 820 to 855
-// us with the sums (1.3 PFLOP/s), 937 with G, whose exponentials and 256 MB of
-// writes come after the tile's products and hide behind no others, a CU's LDS
-// being full with one tile.  The library's plain product of that size runs at
-// 1.45 PFLOP/s and leaves the logits to read.
+// clock they leave): a piece of 32768 x 4096, bf16, 4096 tokens takes 800 us with
+// the sums (1.37 PFLOP/s), 844 with G.  What comes after a tile's products
+// hides behind no others, a CU's LDS being full with one tile: with comparisons
+// for masks and targets at every element and rounding in integers (17
+// instructions an element) it was 829 and 939.  The library's plain product of
+// that size runs at 1.45 PFLOP/s and leaves the logits to read.
 template <int KIND, int DT, bool GRAD, bool TILED, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, PanelOperand X, XentTile t) {
   typedef PanelTile<KIND, AP, BP, WA, WB, 2, false, false, TILED> T;
@@ -184,34 +198,53 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
   // entry of acc[i][.][e]: vbase + 16 i + e; token of acc[.][j]: tbase + 16 j
   const int64_t vbase = t.v0 + int64_t(ab * AP + wa * T::kA) * 16 + (lane >> 4) * 4;
   const int32_t tbase = (bb * BP + wb * T::kB) * 16 + (lane & 15);
+  // entries of this lane's 16 kA that are in the vocabulary, and which of them a
+  // target is (-1: none)
+  constexpr int kSpan = 16 * T::kA;
+  const int32_t live = t.n_vocab - vbase < kSpan ? int32_t(t.n_vocab - vbase) : kSpan;
+  const bool edge = __any(live < kSpan);
+  auto place = [&](int64_t want) {
+    const uint64_t at = uint64_t(want) - uint64_t(vbase);
+    return at < uint64_t(kSpan) ? int32_t(at) : -1;
+  };
   if constexpr (!GRAD) {
     __syncthreads();  // the tile's LDS stages are free
     float2* sums = reinterpret_cast<float2*>(xent_smem);  // [WA][16 BP]
 #pragma unroll
     for (int j = 0; j < T::kB; ++j) {
       const int32_t tok = tbase + 16 * j;
-      const int64_t want = tok < t.m ? t.target[tok] : -1;
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * i + e >= live) acc[i][j][e] = -__builtin_inff();
+      }
+      // the target's logit, in the few wavefronts that hold one
+      const int32_t at = tok < t.m ? place(t.target[tok]) : -1;
+      if (__any(at >= 0)) {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (at == 16 * i + e) t.zt[tok] = acc[i][j][e];
+      }
+      // (a maximum passes NaN over; the sum does not)
       float top = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < T::kA; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t v = vbase + 16 * i + e;
-          if (v >= t.n_vocab) acc[i][j][e] = -__builtin_inff();
-          if (v == want && v < t.n_vocab && tok < t.m) t.zt[tok] = acc[i][j][e];
-          // a NaN logit makes the maximum NaN, and with it the loss
-          top = acc[i][j][e] > top || acc[i][j][e] != acc[i][j][e] ? acc[i][j][e] : top;
-        }
+        for (int e = 0; e < 4; ++e) top = __builtin_fmaxf(top, acc[i][j][e]);
 #pragma unroll
-      for (int d = 16; d < 64; d *= 2) {
-        const float o = __shfl_xor(top, d);
-        top = o > top || o != o ? o : top;
-      }
+      for (int d = 16; d < 64; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+      // an infinite maximum (no entry above -inf, or one of +inf) would give NaN
+      const ExpBase base(__builtin_fabsf(top) < __builtin_inff() ? top : 0.f);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < T::kA; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += rescale(acc[i][j][e], top) * (acc[i][j][e] == -__builtin_inff() ? 0.f : 1.f);
+        for (int e = 0; e < 4; ++e) sum += base.raw(acc[i][j][e]);
+      sum *= base.fix;
 #pragma unroll
       for (int d = 16; d < 64; d *= 2) sum += __shfl_xor(sum, d);
       if (lane < 16) sums[wa * (BP * 16) + (wb * T::kB + j) * 16 + lane] = make_float2(top, sum);
@@ -237,19 +270,33 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
       const int64_t want = tok < t.m ? t.target[tok] : t.ignore;
       const bool seen = tok < t.m && want != t.ignore;
       const bool valid = want >= 0 && want < t.n_vocab;
-      const float lse = seen ? t.lse[tok] : 0.f;
-      const float f = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
+      const ExpBase base(seen ? t.lse[tok] : 0.f);
+      const float g = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
+      const float f = g * base.fix;
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = base.raw(acc[i][j][e]) * f;
+      // the few wavefronts that hold a target, a token that does not count or
+      // has no valid target, or rows behind the vocabulary
+      const int32_t at = place(want);
+      if (__any(at >= 0)) {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] -= at == 16 * i + e ? g : 0.f;
+      }
+      if (edge || __any(!seen || !valid)) {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!valid) acc[i][j][e] = __builtin_nanf("");
+            if (!seen || 16 * i + e >= live) acc[i][j][e] = 0.f;
+          }
+      }
 #pragma unroll
       for (int i = 0; i < T::kA; ++i) {
-        uint16_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t v = vbase + 16 * i + e;
-          float p = (fast_exp(acc[i][j][e] - lse) - (v == want ? 1.f : 0.f)) * f;
-          if (!valid) p = __builtin_nanf("");
-          if (!seen || v >= t.n_vocab) p = 0.f;
-          h[e] = round16<DT>(p);
-        }
         // Row tok % 16 of panel tok / 16.  The four entries 16 i + 4 q + e,
         // q = lane / 16, lie where a lane of the dX product that reads W'
         // transposed holds the same rows of W' (hyb_panel.h): unit 2 (i % 2) +
@@ -261,7 +308,7 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
         if (tok < t.m16 && col < t.g_steps * 64)
           *reinterpret_cast<uint2*>(t.g + (int64_t(tok >> 4) * t.g_steps + (col >> 6)) * kPanelStep +
                                     ((col & 32) >> 5) * 1024 + u * 256 + (tok & 15) * 16 + half * 8) =
-              make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+              round16x4<DT>(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
       }
     }
   }
@@ -475,10 +522,9 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, P
         xent_smem + wave * (T::kA * T::kB * 512), lane, row16,
         [&](int i, int j) {
           const bool live = row0 + j * 16 + row16 < o.live;
-          uint16_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = live ? round16<DT>(acc[i][j][e] * back) : uint16_t(0);
-          return make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+          const f32x4_t v = acc[i][j];
+          const uint2 h = round16x4<DT>(v[0] * back, v[1] * back, v[2] * back, v[3] * back);
+          return live ? h : make_uint2(0, 0);
         },
         [&](int r, int c, uint4 u) {
           const int32_t row = row0 + r, col = col0 + c;  // a packed head's k is a multiple of 64

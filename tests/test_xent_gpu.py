@@ -402,3 +402,38 @@ def test_tile_columns_beyond_one_register():
     """More than 64 tiles in a row, and more than 64 tile rows in a piece."""
     check(*make(128, 64 * 130, 70, 128, "bf16", seed=18, sigma=0.02), 128)
     check(*make(64 * 150, 128, 70, 64 * 150 - 3, "bf16", seed=19), 64 * 150 - 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [5, 100, 300])
+def test_logits_that_are_not_finite(m, dtype):
+    """An entry at -inf has no share in the sum; one at +inf makes it +inf; a NaN
+    makes it NaN; no entry above -inf gives -inf."""
+    n, k = 600, 64
+    _, w, x, target, _ = make(1024, k, m, n, dtype, sparse=0.0, seed=m)
+    x[:, 0] = x[:, 0].abs() + 0.5
+    target[:] = torch.arange(m).cuda() % n
+    w[3, 0] = w[599, 0] = float("-inf")
+    z = as64(x) @ np.nan_to_num(as64(w)[:n], neginf=0.0).T
+    z[:, [3, 599]] = -np.inf
+    top = z.max(1)
+    want = top + np.log(np.exp(z - top[:, None]).sum(1))
+    tol = 2 * k * 2.0 ** -23 * (np.abs(as64(x)) @ np.nan_to_num(np.abs(as64(w)[:n]), posinf=0.0).T).max(1) \
+        + 2.0 ** -17 + 2.0 ** -22 * np.abs(want)
+    none = np.zeros((1024 // 64, k // 64), np.uint8)
+
+    def run(w):
+        loss, lse = xent.loss(hb.pack(w, none, 64, 64), x, target, n_vocab=n)
+        return as64(loss), as64(lse)
+    loss, lse = run(w)
+    within("lse", torch.from_numpy(lse), want, tol)
+    assert loss[3] == np.inf and np.isfinite(np.delete(loss, [3])).all()
+    w[400, 0] = float("inf")
+    loss, lse = run(w)
+    assert (lse == np.inf).all() and (np.delete(loss, [3]) == np.inf).all()
+    w[400, 0] = float("nan")
+    loss, lse = run(w)
+    assert np.isnan(lse).all() and np.isnan(loss).all()
+    w[:, 0] = float("-inf")
+    loss, lse = run(w)
+    assert (lse == -np.inf).all() and np.isnan(loss).all()
