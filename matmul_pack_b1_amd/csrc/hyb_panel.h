@@ -542,14 +542,21 @@ struct PanelTile {
     for (int j = 0; j < kB; ++j) scb[j] = 0;
 
     // Scale of the codes of step s: this wavefront's columns lie in one step of
-    // the panels, the step's 64 rows in one block.  Loaded during step s - 1
-    // and turned into a number after its products: a scalar load that is
-    // waited for beside LDS reads waits for all of them.
+    // the panels, the step's 64 rows in one block.  The lanes hold the words of
+    // 64 steps (a load for each step, waited for beside the LDS reads, cost a
+    // trip to memory a step).
     [[maybe_unused]] float codes_scale = 1.f;
+    [[maybe_unused]] uint32_t scale_words = 0;
+    [[maybe_unused]] int32_t scale_first = s0 - 64;  // step of lane 0's word
     auto scale_word = [&](int32_t s) -> uint32_t {
       if constexpr (CODES) {
         const int32_t column = pa / 8 + wa * kA / 8, at = column < A.steps ? column : 0;
-        return A.scale[int64_t(at >> 2) * A.scale_pitch + s * 64] >> (8 * (at & 3));
+        if (s >= scale_first + 64) {
+          scale_first = s;
+          const int64_t row = int64_t(s + lane) * 64;
+          scale_words = row < A.rows16 ? A.scale[int64_t(at >> 2) * A.scale_pitch + row] : 0;
+        }
+        return uint32_t(__builtin_amdgcn_readlane(int(scale_words), s - scale_first)) >> (8 * (at & 3));
       }
       return 0;
     };

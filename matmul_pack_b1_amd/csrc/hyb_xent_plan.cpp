@@ -34,13 +34,29 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   // 100 us, the product 40).
   const int64_t few = !dx && !dw && !p.f8 && head.layout->n_sparse > 0 ? 512 : 64;
   p.rows = m <= few;
-  p.bp = m <= 64 ? 4 : m <= 128 ? 8 : 16;
-  // A piece's 16-bit dz takes at most 256 MiB.
-  p.piece = int64_t(256) << 20;
-  p.piece = p.piece / (2 * (p.m64 > 0 ? p.m64 : 64)) / 256 * 256;
-  if (p.piece < 256) p.piece = 256;
-  if (p.piece > 32768) p.piece = 32768;
+  // Pieces of 32768 entries (at 4096 tokens 2048 tiles of 256 x 256, eight rounds
+  // of 256 compute units), fewer where their 16-bit dz would pass 256 MiB.  Few
+  // tokens take more, up to 64 MiB of dz, which fills the units and saves
+  // launches (loss and dX, dense 128256 x 4096, 16 / 64 / 100 tokens: pieces of
+  // 32768 606 / 725 / 883 us, whole 577 / 666 / 676); over sparse tiles as far as
+  // the expanded copy of a piece stays within 512 MiB.
+  const int64_t dz = 2 * (p.m64 > 0 ? p.m64 : 64);
+  p.piece = (int64_t(256) << 20) / dz;
+  if (p.piece > 32768) {
+    int64_t most = (int64_t(64) << 20) / dz;
+    if (!p.f8 && head.layout->n_sparse > 0) {
+      const int64_t copy = (int64_t(512) << 20) / (2 * p.k);
+      most = most < copy ? most : copy;
+    }
+    if (most > 32768) most = up(p.n, up(p.n, most) / most) / (up(p.n, most) / most);  // even pieces
+    p.piece = most > 32768 ? up(most, 256) : 32768;
+  }
+  p.piece = p.piece < 256 ? 256 : p.piece / 256 * 256;
   if (p.piece > up(p.n, 256)) p.piece = up(p.n, 256);
+  // Token panels per tile: fewer where 256 tokens a tile would leave more than
+  // half of the compute units without one.
+  const int64_t wide = up(p.piece, 256) / 256 * (up(m, 256) / 256);
+  p.bp = m <= 64 ? 4 : m <= 128 || 2 * wide <= cus ? 8 : 16;
   p.rows_piece = dx || dw ? p.piece : m <= 64 ? p.n : 32768;
   p.chunks = p.rows ? up(p.n, 2048) / 2048 : up(p.n, 256) / 256;
   p.parts = 1;
@@ -50,7 +66,8 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     // them per part; 1% a part for the sums it writes).
     const int64_t tiles = up(p.ksteps16 * 64, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp));
     double least = 1e300;
-    for (int parts = 1; parts <= 32; ++parts) {
+    const int64_t quads = up(p.piece, 256) / 256;  // of four 64-entry steps, a part at least one
+    for (int parts = 1; parts <= 32 && parts <= quads; ++parts) {
       const double cost = double(up(tiles * parts, cus) / cus) / parts * (1.0 + 0.01 * parts);
       if (cost < least) {
         least = cost;
