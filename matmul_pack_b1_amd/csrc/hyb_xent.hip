@@ -476,10 +476,10 @@ struct XentOut {
 // 32768 x 4096 with 4096 tokens takes 833 us for dX, 857 for dW (1.3 PFLOP/s);
 // dX over codes, 1000 tokens and 32768 x 5120, 327 us (1.05 PFLOP/s: 240
 // workgroups, the vector unit widening beside the matrix unit).
-template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB, int STAGES = 2>
+template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
                                                                int parts, XentOut o) {
-  typedef PanelTile<DT, AP, BP, WA, WB, STAGES, true, !DX, TILED, CODES> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED, CODES> T;
   extern __shared__ __attribute__((aligned(1024))) char xent_smem[];
   const int32_t na = (A.steps * (CODES ? 8 : 4) + AP - 1) / AP;
   const int32_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
@@ -603,15 +603,15 @@ hipError_t run_tiles(const XentPlan& p, const PanelOperand& W, const PanelOperan
   return p.f8 ? run_shape<kF8Wide, DT, GRAD, false>(p.bp, W, X, t, s) : run_shape<DT, DT, GRAD, true>(p.bp, W, X, t, s);
 }
 
-template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB, int STAGES = 2>
+template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                        hipStream_t s) {
-  typedef PanelTile<DT, AP, BP, WA, WB, STAGES, true, !DX, TILED, CODES> T;
-  const hipError_t e = allow_lds(&k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB, STAGES>, T::kLds);
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, !DX, TILED, CODES> T;
+  const hipError_t e = allow_lds(&k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB>, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (A.steps * (CODES ? 8 : 4) + AP - 1) / AP;
   const int64_t nb = DX ? (B.rows16 / 16 + BP - 1) / BP : (B.steps * 4 + BP - 1) / BP;
-  hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB, STAGES>), dim3(unsigned(na * nb), unsigned(parts)),
+  hipLaunchKernelGGL((k_xent_product<DT, DX, TILED, CODES, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)),
                      dim3(64 * WA * WB), T::kLds, s, A, B, steps, parts, o);
   return hipGetLastError();
 }
@@ -619,10 +619,12 @@ hipError_t run_product(const PanelOperand& A, const PanelOperand& B, int32_t ste
 template <int DT, bool F8>
 hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t steps, int parts, const XentOut& o,
                   hipStream_t s) {
-  // (codes: four wavefronts along the columns convert each only half as often)
+  // (codes: the more wavefronts along the columns, the fewer convert the same
+  // one; at eight of them the 128-token tile needs 150 registers, which leaves one
+  // workgroup a compute unit: 100 tokens, 128256 x 4096 215 us against 128)
   if (bp == 16) return run_product<DT, true, !F8, F8, 16, 16, F8 ? 4 : 2, F8 ? 2 : 4>(A, B, steps, parts, o, s);
   if (bp == 8) return run_product<DT, true, !F8, F8, 16, 8, 4, 2>(A, B, steps, parts, o, s);
-  return run_product<DT, true, !F8, F8, 16, 4, 4, 2, F8 ? 4 : 2>(A, B, steps, parts, o, s);
+  return run_product<DT, true, !F8, F8, 16, 4, F8 ? 8 : 4, F8 ? 1 : 2>(A, B, steps, parts, o, s);
 }
 
 // The tiles of the piece of `rows` vocabulary rows from v0 that PanelOperand

@@ -63,12 +63,16 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   if (dx) {
     // The dX product has (k / 256) x (m / 256) tiles; its vocabulary is cut
     // into the number of parts that keeps the compute units fullest (rounds of
-    // them per part; 1% a part for the sums it writes).
+    // them per part; 1% a part for the sums it writes).  Where two workgroups'
+    // LDS fits a unit, one's reads hide behind the other's waits: 16 tokens over
+    // an 8-bit 152064 x 5120 head 225 us with one a unit, 149 with two; a packed
+    // 64128 x 4096 piece 101 and 89.
     const int64_t tiles = up(p.ksteps16 * 64, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp));
+    const int64_t slots = p.bp == 4 || (p.bp == 8 && p.f8) ? 2 * cus : cus;
     double least = 1e300;
     const int64_t quads = up(p.piece, 256) / 256;  // of four 64-entry steps, a part at least one
     for (int parts = 1; parts <= 32 && parts <= quads; ++parts) {
-      const double cost = double(up(tiles * parts, cus) / cus) / parts * (1.0 + 0.01 * parts);
+      const double cost = double(up(tiles * parts, slots) / slots) / parts * (1.0 + 0.01 * parts);
       if (cost < least) {
         least = cost;
         p.parts = parts;
