@@ -797,7 +797,10 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     }
     // G: tokens x entries, vsteps steps; W': entries x columns
     const PanelOperand G{ws + p.g, int32_t(p.m16), vsteps, nullptr, 0};
-    if (dx) {
+    if (dx && v0 < n_vocab) {
+      // (the steps of the vocabulary, so that dX does not depend on whether dW
+      // is asked for)
+      const int32_t dx_steps = int32_t(((n_vocab - v0 < rows ? n_vocab - v0 : rows) + 63) / 64);
       XentOut o{};
       o.acc = reinterpret_cast<float*>(ws + p.dx);
       o.ld = krows;
@@ -805,8 +808,8 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       o.first = v0 == 0;
       o.rows = int32_t(p.m);
       o.cols = krows;
-      HYB_TRY(p.f8 ? (run_dx<DT, true>(p.bp, W, G, vsteps, p.parts, o, s))
-                   : (run_dx<DT, false>(p.bp, W, G, vsteps, p.parts, o, s)));
+      HYB_TRY(p.f8 ? (run_dx<DT, true>(p.bp, W, G, dx_steps, p.parts, o, s))
+                   : (run_dx<DT, false>(p.bp, W, G, dx_steps, p.parts, o, s)));
     }
     if (dw) {
       XentOut o{};

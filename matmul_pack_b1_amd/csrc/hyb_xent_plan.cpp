@@ -29,11 +29,16 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   // bf16, 100 / 256 / 512 / 1024 tokens: 345 / 386 / 610 / 1127 us through the
   // product, 669 / 674 / 707 / 1144 through the tiles; 10% sparse, 512 tokens:
   // 664 and 609).
+  // So do products of up to an eighth as many tiles of 256 x 256 as there are
+  // compute units, which the library's products cut finer (loss, dense, k = 4096,
+  // entries x tokens: 1024 x 100 27 us, the tiles 61; 4096 x 300, 32 tiles, 37 and
+  // 68; 4096 x 1000, 64 tiles, 123 and 70; 8-bit 28 / 59, 47 / 60, 54 / 63; loss and
+  // dX of 4096 x 300 104 and 164).
   // Gradients need the expanded tiles anyway; up to 64 tokens their logits go
   // the same way too (16 tokens, 32768 x 4096 of the head: the tile of 256 x 64
   // 100 us, the product 40).
   const int64_t few = !dx && !dw && !p.f8 && head.layout->n_sparse > 0 ? 512 : 64;
-  p.rows = m <= few;
+  p.rows = m <= few || up(p.n, 256) / 256 * (up(m, 256) / 256) * 8 <= cus;
   // Pieces of 32768 entries (at 4096 tokens 2048 tiles of 256 x 256, eight rounds
   // of 256 compute units), fewer where their 16-bit dz would pass 256 MiB.  Few
   // tokens take more, up to 64 MiB of dz, which fills the units and saves

@@ -157,22 +157,22 @@ def test_many_tokens():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("head", ["packed", "f8"])
-@pytest.mark.parametrize("m", [10, 150])
-def test_confident_and_flat_rows(m, head, dtype):
+@pytest.mark.parametrize("m,n", [(10, 512), (150, 512), (150, 8448)])
+def test_confident_and_flat_rows(m, n, head, dtype):
     """Logits of +-hundreds (softmax one-hot, probabilities far below the
     smallest 16-bit number) and all equal (x = 0)."""
-    P, w, x, target, grad = make(512, 256, m, 500, dtype, head=head, seed=4, scale=40.0)
+    P, w, x, target, grad = make(n, 256, m, n - 12, dtype, head=head, seed=4, scale=40.0)
     x[0] = 0.0
     target[0] = 7
-    check(P, w, x, target, grad, 500)
+    check(P, w, x, target, grad, n - 12)
 
 
 @pytest.mark.parametrize("head", ["packed", "f8"])
-@pytest.mark.parametrize("m", [6, 100])
-def test_masked_places_are_not_looked_at(m, head):
+@pytest.mark.parametrize("m,n", [(6, 512), (100, 512), (100, 8576)])
+def test_masked_places_are_not_looked_at(m, n, head):
     """NaN and infinities in ignored tokens' x and grad and in the head's
     padding rows change nothing."""
-    n, k, n_vocab = 512, 256, 384        # padding from a block of 128 on
+    k, n_vocab = 256, n - 128       # padding from a block of 128 on
     P, w, x, target, grad = make(n, k, m, n_vocab, "bf16", head=head, seed=5)
     target[1], target[3] = -100, -100
     want = check(P, w, x, target, grad, n_vocab)
@@ -195,44 +195,44 @@ def test_masked_places_are_not_looked_at(m, head):
     assert float(loss[1]) == 0 and float(lse[3]) == 0 and bool((dx[1] == 0).all())
 
 
-@pytest.mark.parametrize("m", [6, 100])
-def test_all_tokens_ignored(m):
-    P, w, x, target, grad = make(512, 128, m, 500, "bf16", seed=6)
+@pytest.mark.parametrize("m,n", [(6, 512), (100, 512), (100, 8448)])
+def test_all_tokens_ignored(m, n):
+    P, w, x, target, grad = make(n, 128, m, n - 12, "bf16", seed=6)
     target.fill_(-100)
     x.fill_(float("nan"))
-    loss, lse = xent.loss(P, x, target, n_vocab=500)
-    dx, dw = xent.backward(P, x, target, lse, grad * float("nan"), n_vocab=500, need_dw=True)
+    loss, lse = xent.loss(P, x, target, n_vocab=n - 12)
+    dx, dw = xent.backward(P, x, target, lse, grad * float("nan"), n_vocab=n - 12, need_dw=True)
     for t in (loss, lse, dx, dw):
         assert bool((t == 0).all())
 
 
 @pytest.mark.parametrize("head", ["packed", "f8"])
-@pytest.mark.parametrize("m", [6, 100])
-def test_bad_targets_are_nan(m, head):
-    P, w, x, target, grad = make(512, 128, m, 500, "bf16", head=head, seed=7)
-    ok = check(P, w, x, target, grad, 500)
-    target[0], target[2], target[4] = 500, -1, 2 ** 40
-    loss, lse = xent.loss(P, x, target, n_vocab=500)
-    dx, dw = xent.backward(P, x, target, lse, grad, n_vocab=500, need_dw=head == "packed")
+@pytest.mark.parametrize("m,n", [(6, 512), (100, 512), (100, 8448)])
+def test_bad_targets_are_nan(m, n, head):
+    P, w, x, target, grad = make(n, 128, m, n - 12, "bf16", head=head, seed=7)
+    ok = check(P, w, x, target, grad, n - 12)
+    target[0], target[2], target[4] = n - 12, -1, 2 ** 40
+    loss, lse = xent.loss(P, x, target, n_vocab=n - 12)
+    dx, dw = xent.backward(P, x, target, lse, grad, n_vocab=n - 12, need_dw=head == "packed")
     bad = torch.zeros(m, dtype=torch.bool, device="cuda")
     bad[[0, 2, 4]] = True
     assert bool(loss[bad].isnan().all()) and bool(dx[bad].isnan().all())
     assert torch.equal(loss[~bad], ok[0][~bad]) and torch.equal(dx[~bad], ok[2][~bad])
     if dw is not None:
-        assert bool(dw[:500].isnan().all())
-    other = torch.where(target == 500, torch.full_like(target, 99), target)
-    assert bool((xent.loss(P, x, other, n_vocab=500, ignore_index=2 ** 40)[0][[2]]).isnan().all())
+        assert bool(dw[:n - 12].isnan().all())
+    other = torch.where(target == n - 12, torch.full_like(target, 99), target)
+    assert bool((xent.loss(P, x, other, n_vocab=n - 12, ignore_index=2 ** 40)[0][[2]]).isnan().all())
 
 
-@pytest.mark.parametrize("m", [6, 100])
-def test_nan_in_a_token_stays_there(m):
-    P, w, x, target, grad = make(512, 128, m, 500, "bf16", seed=8)
+@pytest.mark.parametrize("m,n", [(6, 512), (100, 512), (100, 8448)])
+def test_nan_in_a_token_stays_there(m, n):
+    P, w, x, target, grad = make(n, 128, m, n - 12, "bf16", seed=8)
     target[:] = torch.arange(m) % 500
-    loss, lse = xent.loss(P, x, target, n_vocab=500)
-    dx, _ = xent.backward(P, x, target, lse, grad, n_vocab=500)
+    loss, lse = xent.loss(P, x, target, n_vocab=n - 12)
+    dx, _ = xent.backward(P, x, target, lse, grad, n_vocab=n - 12)
     x[2, 5] = float("nan")
-    loss2, lse2 = xent.loss(P, x, target, n_vocab=500)
-    dx2, _ = xent.backward(P, x, target, lse2, grad, n_vocab=500)
+    loss2, lse2 = xent.loss(P, x, target, n_vocab=n - 12)
+    dx2, _ = xent.backward(P, x, target, lse2, grad, n_vocab=n - 12)
     rest = torch.arange(m, device="cuda") != 2
     assert bool(loss2[2].isnan()) and bool(dx2[2].isnan().all())
     assert torch.equal(loss2[rest], loss[rest]) and torch.equal(dx2[rest], dx[rest])
@@ -277,19 +277,21 @@ def test_empty_batch():
 
 @pytest.mark.parametrize("scale", [2.0 ** -60, 1.0, 2.0 ** 40])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_gradients_of_any_size(dtype, scale):
+@pytest.mark.parametrize("n", [256, 8448])
+def test_gradients_of_any_size(dtype, scale, n):
     """dW's 16-bit operand carries grad: scaled by its largest magnitude."""
-    P, w, x, target, grad = make(256, 128, 90, 250, "bf16", seed=12)
+    P, w, x, target, grad = make(n, 128, 90, n - 6, "bf16", seed=12)
     if dtype == "f16":
-        P, w, x, target, grad = make(256, 128, 90, 250, "f16", seed=12)
+        P, w, x, target, grad = make(n, 128, 90, n - 6, "f16", seed=12)
         scale = min(max(scale, 2.0 ** -6), 2.0 ** 6)     # what an fp16 gradient can hold
-    check(P, w, x, target, grad * scale, 250)
+    check(P, w, x, target, grad * scale, n - 6)
 
 
-def test_gradient_against_differences():
+@pytest.mark.parametrize("n", [512, 8448])
+def test_gradient_against_differences(n):
     """Loss differences along single coordinates of x against dX: both sides'
     bounds and the cubic term of a central difference."""
-    n, k, m, n_vocab, step = 512, 128, 96, 500, 2.0 ** -3
+    k, m, n_vocab, step = 128, 96, n - 12, 2.0 ** -3
     P, w, x, target, grad = make(n, k, m, n_vocab, "bf16", seed=13, sigma=0.25)
     x = (x * 16).round() / 16                     # x +- step stay exact
     x = x.clamp(-7, 7)
@@ -309,9 +311,9 @@ def test_gradient_against_differences():
 
 
 @pytest.mark.parametrize("head", ["packed", "f8"])
-@pytest.mark.parametrize("m", [5, 130])
-def test_graph_replays(m, head):
-    n, k, n_vocab = 1024, 256, 1000
+@pytest.mark.parametrize("m,n", [(5, 1024), (130, 1024), (130, 8448)])
+def test_graph_replays(m, n, head):
+    k, n_vocab = 256, n - 24
     P, w, x, target, grad = make(n, k, m, n_vocab, "bf16", head=head, seed=14)
     packed = head == "packed"
 
@@ -377,11 +379,11 @@ def test_together_a_frozen_8_bit_layer_under_an_8_bit_head():
 
 
 @pytest.mark.parametrize("sparse", [0.0, 0.5])
-@pytest.mark.parametrize("m", [6, 100])
-def test_tile_index_out_of_range_adds_nothing(m, sparse):
+@pytest.mark.parametrize("m,n", [(6, 512), (100, 512), (100, 8448)])
+def test_tile_index_out_of_range_adds_nothing(m, n, sparse):
     """Entries of the tile index that name no slot: their tiles count as
     zeros, as in the library's products."""
-    P, w, x, target, grad = make(512, 256, m, 500, "bf16", tile=(64, 64), sparse=sparse, seed=17)
+    P, w, x, target, grad = make(n, 256, m, n - 12, "bf16", tile=(64, 64), sparse=sparse, seed=17)
     tidx = P.tidx.clone()
     bad = torch.tensor([0, 5, 9, 30], device="cuda")
     for value in (P.layout.n_dense, -P.layout.n_sparse - 1, 2 ** 31 - 1, -2 ** 31):
@@ -391,9 +393,9 @@ def test_tile_index_out_of_range_adds_nothing(m, sparse):
             r, c = t // 4, t % 4
             wv[r * 64:(r + 1) * 64, c * 64:(c + 1) * 64] = 0.0
         P.tidx[bad] = value
-        want, tol = bounds(as64(x), wv, x, target, grad, 500, 256)
-        loss, lse = xent.loss(P, x, target, n_vocab=500)
-        dx, dw = xent.backward(P, x, target, lse, grad, n_vocab=500, need_dw=True)
+        want, tol = bounds(as64(x), wv, x, target, grad, n - 12, 256)
+        loss, lse = xent.loss(P, x, target, n_vocab=n - 12)
+        dx, dw = xent.backward(P, x, target, lse, grad, n_vocab=n - 12, need_dw=True)
         for name, got, ref, lim in zip(("loss", "lse", "dx", "dw"), (loss, lse, dx, dw), want, tol):
             within(name, got, ref, lim)
 
@@ -405,22 +407,22 @@ def test_tile_columns_beyond_one_register():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("m", [5, 100, 300])
-def test_logits_that_are_not_finite(m, dtype):
+@pytest.mark.parametrize("m,h", [(5, 1024), (100, 1024), (300, 1024), (300, 8448)])
+def test_logits_that_are_not_finite(m, h, dtype):
     """An entry at -inf has no share in the sum; one at +inf makes it +inf; a NaN
     makes it NaN; no entry above -inf gives -inf."""
-    n, k = 600, 64
-    _, w, x, target, _ = make(1024, k, m, n, dtype, sparse=0.0, seed=m)
+    n, k = h - 424, 64
+    _, w, x, target, _ = make(h, k, m, n, dtype, sparse=0.0, seed=m)
     x[:, 0] = x[:, 0].abs() + 0.5
     target[:] = torch.arange(m).cuda() % n
-    w[3, 0] = w[599, 0] = float("-inf")
+    w[3, 0] = w[n - 1, 0] = float("-inf")
     z = as64(x) @ np.nan_to_num(as64(w)[:n], neginf=0.0).T
-    z[:, [3, 599]] = -np.inf
+    z[:, [3, n - 1]] = -np.inf
     top = z.max(1)
     want = top + np.log(np.exp(z - top[:, None]).sum(1))
     tol = 2 * k * 2.0 ** -23 * (np.abs(as64(x)) @ np.nan_to_num(np.abs(as64(w)[:n]), posinf=0.0).T).max(1) \
         + 2.0 ** -17 + 2.0 ** -22 * np.abs(want)
-    none = np.zeros((1024 // 64, k // 64), np.uint8)
+    none = np.zeros((h // 64, k // 64), np.uint8)
 
     def run(w):
         loss, lse = xent.loss(hb.pack(w, none, 64, 64), x, target, n_vocab=n)
@@ -437,3 +439,25 @@ def test_logits_that_are_not_finite(m, dtype):
     w[:, 0] = float("-inf")
     loss, lse = run(w)
     assert (lse == -np.inf).all() and np.isnan(loss).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sparse", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("tile,meta", [((64, 64), "idx2"), ((128, 128), "mask8"), ((256, 256), "mask4"), ((64, 256), "idx2"),
+                                       ((256, 64), "mask4")])
+@pytest.mark.parametrize("m", [65, 129, 300, 600])
+def test_packed_heads_of_many_tiles(m, tile, meta, sparse, dtype):
+    """As many tiles as the logits need to be multiplied tile by tile."""
+    check(*make(8448, 256, m, 8400, dtype, tile=tile, meta=meta, sparse=sparse, seed=m), 8400)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [65, 128, 200, 300])
+@pytest.mark.parametrize("n,k,n_vocab", [(8449, 1, 8449), (8450, 333, 8321), (9000, 512, 8990)])
+def test_8_bit_heads_of_many_tiles(m, n, k, n_vocab, dtype):
+    check(*make(n, k, m, n_vocab, dtype, head="f8", seed=m + n), n_vocab)
+
+
+def test_tile_columns_beyond_one_register_in_many_tiles():
+    check(*make(8448, 64 * 70, 70, 8448, "bf16", seed=18, sigma=0.02), 8448)
+    check(*make(64 * 150, 128, 70, 64 * 150 - 3, "bf16", seed=19), 64 * 150 - 3)
