@@ -177,8 +177,8 @@ struct XentTile {
 
 // One tile of Z = W' X^T: AP x BP panels (entries x tokens).  GRAD false
 // leaves the softmax sums, true G.  Bound by the matrix instructions (and the
-// clock they leave): a piece of 32768 x 4096, bf16, 4096 tokens takes 800 us with
-// the sums (1.37 PFLOP/s), 844 with G.  What comes after a tile's products
+// clock they leave): a piece of 32768 x 4096, bf16, 4096 tokens takes 795 us with
+// the sums (1.38 PFLOP/s), 834 with G.  What comes after a tile's products
 // hides behind no others, a CU's LDS being full with one tile: with comparisons
 // for masks and targets at every element and rounding in integers (17
 // instructions an element) it was 829 and 939.  The library's plain product of
@@ -473,8 +473,8 @@ struct XentOut {
 // transposed, B = G), fp32, this workgroup's part of the steps, stored or
 // added.  Else dW: Y[entry, column] = sum over tokens of G^T X (both read
 // transposed), 16-bit, scaled back by gtop.  Bound as k_xent_tile is: a piece of
-// 32768 x 4096 with 4096 tokens takes 833 us for dX, 857 for dW (1.3 PFLOP/s);
-// dX over codes, 1000 tokens and 32768 x 5120, 327 us (1.05 PFLOP/s: 240
+// 32768 x 4096 with 4096 tokens takes 835 us for dX, 819 for dW (1.3 PFLOP/s);
+// dX over codes, 1000 tokens and 32768 x 5120, 291 us (1.15 PFLOP/s: 240
 // workgroups, the vector unit widening beside the matrix unit).
 template <int DT, bool DX, bool TILED, bool CODES, int AP, int BP, int WA, int WB>
 __global__ __launch_bounds__(64 * WA * WB) void k_xent_product(PanelOperand A, PanelOperand B, int32_t steps,
