@@ -627,7 +627,8 @@ hipError_t launch_f8_quantize(const void* a, int dtype, int64_t rows, int64_t k,
   // are written too), and in all
   const int32_t across = int32_t(kind == HYB_F8_WEIGHT ? quads * 4 : quads);
   const int64_t grid = int64_t(kind == HYB_F8_WEIGHT ? (panels + 7) / 8 : panels) * across;
-  if (grid * 512 >= int64_t(1) << 32) return hipErrorInvalidValue;  // more elements than a card holds
+  // (2^37 elements: more than a card holds)
+  if (grid * (kind == HYB_F8_WEIGHT ? 512 : 256) >= int64_t(1) << 32) return hipErrorInvalidValue;
   char* codes = static_cast<char*>(dst.codes);
   char* scales = static_cast<char*>(dst.scales);
 #define HYB_F8_QUANT(DT)                                                                                             \

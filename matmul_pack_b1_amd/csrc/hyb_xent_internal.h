@@ -19,7 +19,7 @@ struct XentPlan {
   int64_t piece;       // vocabulary rows per piece (multiple of 256, or all)
   int64_t m16, m64;    // tokens rounded up
   int bp;              // token panels per tile of the logits product
-  bool rows;           // few tokens: logits through the library's product ...
+  bool rows;           // few tokens or tiles: logits through the library's product ...
   int64_t rows_piece;  // ... of this many vocabulary rows at a time
   int64_t chunks;      // partial softmax sums per token
   int parts;           // cuts of the vocabulary in the dX product
