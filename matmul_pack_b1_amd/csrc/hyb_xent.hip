@@ -314,23 +314,40 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
   }
 }
 
-// Softmax sums of rows of fp32 logits (few tokens; the piece from t.v0, a
-// multiple of 2048), one workgroup per chunk of 2048 entries and token.  Bound
-// by latency: the logits were just written and lie in the last-level cache (5
-// tokens x 32000 5 us).
-__global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, int64_t ldz, XentTile t) {
+// Loss and lse of a token from its softmax sums and its target's logit.
+__device__ __forceinline__ void store_loss(float2 sums, float z_target, int64_t want, int64_t ignore, int64_t n_vocab,
+                                           float* loss, float* lse) {
+  const float total = sums.x + logf(sums.y);
+  if (want == ignore) {
+    *loss = 0.f;
+    *lse = 0.f;
+  } else {
+    *loss = want >= 0 && want < n_vocab ? total - z_target : __builtin_nanf("");
+    *lse = total;
+  }
+}
+
+// Softmax sums of rows of fp32 logits (the piece from t.v0, a multiple of a
+// chunk), one workgroup per chunk of 256 EACH entries and token.  LAST: the one
+// chunk is all of the vocabulary, and the loss follows at once (1024 x 512, 200
+// tokens 4 us; two launches 3.7 + 3.4).  Bound by latency: the logits were just
+// written and lie in the last-level cache (5 tokens x 32000 5 us).
+template <int EACH, bool LAST>
+__global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, int64_t ldz, XentTile t,
+                                                   float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ float2 sums[4];
+  __shared__ float z_target;
   const int32_t tok = int32_t(blockIdx.y);
-  const int64_t v0 = t.v0 + int64_t(blockIdx.x) * 2048;
+  const int64_t v0 = t.v0 + int64_t(blockIdx.x) * (256 * EACH);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t want = t.target[tok];
-  float v[8];
+  float v[EACH];
   float top = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < EACH; ++i) {
     const int64_t c = v0 + i * 256 + threadIdx.x;
     v[i] = c < t.n_vocab && c - t.v0 < ldz ? z[tok * ldz + c - t.v0] : -__builtin_inff();
-    if (c == want && c < t.n_vocab) t.zt[tok] = v[i];
+    if (c == want && c < t.n_vocab) (LAST ? z_target : t.zt[tok]) = v[i];
     top = v[i] > top || v[i] != v[i] ? v[i] : top;
   }
 #pragma unroll
@@ -340,7 +357,7 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
   }
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum += rescale(v[i], top) * (v[i] == -__builtin_inff() ? 0.f : 1.f);
+  for (int i = 0; i < EACH; ++i) sum += rescale(v[i], top) * (v[i] == -__builtin_inff() ? 0.f : 1.f);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
   if (lane == 0) sums[wave] = make_float2(top, sum);
@@ -352,7 +369,10 @@ __global__ __launch_bounds__(256) void k_xent_rows(const float* __restrict__ z, 
       const float m = o.x > r.x || o.x != o.x ? o.x : r.x;
       r = make_float2(m, r.y * rescale(r.x, m) + o.y * rescale(o.x, m));
     }
-    t.part[v0 / 2048 * t.m16 + tok] = r;
+    if constexpr (LAST)
+      store_loss(r, z_target, want, t.ignore, t.n_vocab, loss + tok, lse + tok);
+    else
+      t.part[v0 / (256 * EACH) * t.m16 + tok] = r;
   }
 }
 
@@ -414,16 +434,7 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2* __restrict__ p
     if (g < d) sums[g][l] = join(sums[g][l], sums[g + d][l]);
   }
   if (g == 0 && tok < m) {
-    const float2 f = sums[0][l];
-    const float total = f.x + logf(f.y);
-    const int64_t want = target[tok];
-    if (want == ignore) {
-      loss[tok] = 0.f;
-      lse[tok] = 0.f;
-    } else {
-      loss[tok] = want >= 0 && want < n_vocab ? total - zt[tok] : __builtin_nanf("");
-      lse[tok] = total;
-    }
+    store_loss(sums[0][l], zt[tok], target[tok], ignore, n_vocab, loss + tok, lse + tok);
   }
 }
 
@@ -724,7 +735,16 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
       HYB_TRY(piece_logits(head, p, x, ldx, v0, rows, z, ldz, ws, s));
       t.v0 = v0;
       const int64_t live = n_vocab - v0 < rows ? n_vocab - v0 : rows;
-      hipLaunchKernelGGL(k_xent_rows, dim3(unsigned((live + 2047) / 2048), unsigned(p.m)), dim3(256), 0, s, z, ldz, t);
+      if (n_vocab <= 8192) {  // (one piece)
+        const dim3 grid(1, unsigned(p.m));
+        if (n_vocab <= 2048)
+          hipLaunchKernelGGL((k_xent_rows<8, true>), grid, dim3(256), 0, s, z, ldz, t, loss, lse);
+        else
+          hipLaunchKernelGGL((k_xent_rows<32, true>), grid, dim3(256), 0, s, z, ldz, t, loss, lse);
+        return hipGetLastError();
+      }
+      hipLaunchKernelGGL((k_xent_rows<8, false>), dim3(unsigned((live + 2047) / 2048), unsigned(p.m)), dim3(256), 0, s, z,
+                         ldz, t, loss, lse);
       HYB_TRY(hipGetLastError());
       chunks = (v0 + live + 2047) / 2048;
     }
