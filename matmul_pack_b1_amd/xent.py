@@ -87,16 +87,20 @@ def _check(P, x, target, n_vocab):
 def workspace_bytes(P, m: int, dx: bool = False, dw: bool = False) -> int:
     """Workspace bytes of loss() (neither flag) or backward() on the current
     device."""
+    return _need(_head(P)[0], int(m), dx, dw)
+
+
+def _need(head, m, dx, dw):
     nbytes = ctypes.c_size_t(0)
-    hb.check(lib().hyb_xent_workspace_size(ctypes.byref(_head(P)[0]), int(m), (DX if dx else 0) | (DW if dw else 0),
+    hb.check(lib().hyb_xent_workspace_size(ctypes.byref(head), m, (DX if dx else 0) | (DW if dw else 0),
                                            ctypes.byref(nbytes)), "hyb_xent_workspace_size")
     return int(nbytes.value)
 
 
-def _workspace(P, m, dx, dw, workspace, device):
+def _workspace(head, m, dx, dw, workspace, device):
     torch = hb._torch()
     if workspace is None:
-        need = workspace_bytes(P, m, dx, dw)
+        need = _need(head, m, dx, dw)
         return torch.empty(need, dtype=torch.uint8, device=device), need
     hb._check_gpu(workspace, "workspace", device)
     if not workspace.is_contiguous():
@@ -115,7 +119,7 @@ def loss(P, x, target, n_vocab=None, ignore_index=-100, workspace=None):
     out = torch.empty(m, dtype=torch.float32, device=x.device)
     lse = torch.empty(m, dtype=torch.float32, device=x.device)
     with f8._on(x.device):
-        ws, nbytes = _workspace(P, m, False, False, workspace, x.device)
+        ws, nbytes = _workspace(head, m, False, False, workspace, x.device)
         hb.check(lib().hyb_xent(ctypes.byref(head), n_vocab, hb._ptr(x), f8._code(x.dtype), m, f8._pitch(x, k),
                                 hb._ptr(target), int(ignore_index), hb._ptr(out), hb._ptr(lse), hb._ptr(ws), nbytes,
                                 f8._stream(x.device)), "hyb_xent")
@@ -144,7 +148,7 @@ def backward(P, x, target, lse, grad, n_vocab=None, ignore_index=-100, need_dx=T
             hb._check_out(t, shape, x.dtype, name)
             hb._check_gpu(t, name, x.device)
     with f8._on(x.device):
-        ws, nbytes = _workspace(P, m, need_dx, need_dw, workspace, x.device)
+        ws, nbytes = _workspace(head, m, need_dx, need_dw, workspace, x.device)
         hb.check(lib().hyb_xent_backward(
             ctypes.byref(head), n_vocab, hb._ptr(x), f8._code(x.dtype), m, f8._pitch(x, k), hb._ptr(target),
             int(ignore_index), hb._ptr(lse), hb._ptr(grad), hb._ptr(dx), f8._pitch(dx, k) if need_dx else 0,
