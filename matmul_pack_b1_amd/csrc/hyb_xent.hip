@@ -22,16 +22,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // exp(z - x) as exp2(fma(z, log2 e, -hi)) * fix, two instructions an element:
-// hi is x log2 e rounded, fix takes its rounding back.
+// hi is x log2 e rounded, fix takes its rounding back.  That rounding is half an
+// ulp of hi, a sixteenth at |x| = 2^20 but 2^7 from about 2^31 on, where one factor
+// is 0 and the other infinite: an x beyond kNear is `far`, and raw_any takes the
+// difference first (three instructions, fix 1).  Where a wavefront has no far x,
+// raw serves it; a near x has the same bits either way.
 struct ExpBase {
-  float hi, fix;
-  __device__ __forceinline__ explicit ExpBase(float x) {
+  static constexpr float kNear = 1048576.f;
+  float x, hi, fix;
+  bool far;
+  __device__ __forceinline__ explicit ExpBase(float at) : x(at) {
     hi = x * kLog2e;
-    fix = __builtin_fabsf(hi) < __builtin_inff() ? __builtin_amdgcn_exp2f(-__builtin_fmaf(x, kLog2e, -hi)) : 1.f;
+    far = __builtin_fabsf(x) > kNear;
+    fix = far ? 1.f : __builtin_amdgcn_exp2f(-__builtin_fmaf(x, kLog2e, -hi));
   }
   __device__ __forceinline__ float raw(float z) const {
     return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -hi));
   }
+  __device__ __forceinline__ float raw_any(float z) const { return far ? fast_exp(z - x) : raw(z); }
 };
 
 // exp(a - b) for a <= b where both may be -inf (an empty sum): 0.
@@ -240,10 +248,17 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
       // an infinite maximum (no entry above -inf, or one of +inf) would give NaN
       const ExpBase base(__builtin_fabsf(top) < __builtin_inff() ? top : 0.f);
       float sum = 0.f;
+      if (__any(base.far)) {
 #pragma unroll
-      for (int i = 0; i < T::kA; ++i)
+        for (int i = 0; i < T::kA; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += base.raw(acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) sum += base.raw_any(acc[i][j][e]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += base.raw(acc[i][j][e]);
+      }
       sum *= base.fix;
 #pragma unroll
       for (int d = 16; d < 64; d *= 2) sum += __shfl_xor(sum, d);
@@ -273,10 +288,17 @@ __global__ __launch_bounds__(64 * WA * WB) void k_xent_tile(PanelOperand W, Pane
       const ExpBase base(seen ? t.lse[tok] : 0.f);
       const float g = seen ? t.grad[tok] / gtop * g_scale<DT>() : 0.f;
       const float f = g * base.fix;
+      if (__any(base.far)) {
 #pragma unroll
-      for (int i = 0; i < T::kA; ++i)
+        for (int i = 0; i < T::kA; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = base.raw(acc[i][j][e]) * f;
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = base.raw_any(acc[i][j][e]) * f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = base.raw(acc[i][j][e]) * f;
+      }
       // the few wavefronts that hold a target, a token that does not count or
       // has no valid target, or rows behind the vocabulary
       const int32_t at = place(want);
