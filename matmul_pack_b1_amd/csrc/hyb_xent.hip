@@ -661,13 +661,16 @@ hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t 
 }
 
 // The tiles of the piece of `rows` vocabulary rows from v0 that PanelOperand
-// calls spare, in `out`.
+// calls spare, in `out`; *spare is `out`, or NULL where the piece needs none (a
+// tile without a slot then reads as zeros).
 hipError_t prepare_piece(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t plain, int64_t v0,
-                         int64_t rows, char* out, hipStream_t s) {
+                         int64_t rows, char* out, const char** spare, hipStream_t s) {
   const unsigned panels = unsigned((rows + 15) / 16);
   const hyb_layout& L = *head.layout;
   const hyb_packed& P = *head.packed;
+  *spare = nullptr;
   if (L.n_sparse == 0 && (v0 + rows + L.b1 - 1) / L.b1 * L.b1 <= plain) return hipSuccess;
+  *spare = out;
   hipLaunchKernelGGL(k_xent_expand, dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
                      static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
                      static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
@@ -779,9 +782,10 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     const int64_t step = whole ? n_vocab : p.piece;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
       const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
-      if (!whole) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, s));
+      const char* spare = nullptr;
+      if (!whole) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, &spare, s));
       t.v0 = v0;
-      const PanelOperand W = piece_operand(head, p, p.n, v0, rows, whole ? nullptr : ws + p.w);
+      const PanelOperand W = piece_operand(head, p, p.n, v0, rows, spare);
       HYB_TRY((run_tiles<DT, false>(p, W, X, t, s)));
       chunks = v0 / 256 + (W.rows16 + 255) / 256;
     }
@@ -817,8 +821,9 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     t.v0 = v0;
     t.g_steps = vsteps;
     // (the logits of few tokens do not need them)
-    if (!p.f8 && (!p.rows || dx)) HYB_TRY(prepare_piece(head, p, n_vocab, n_vocab, v0, rows, ws + p.w, s));
-    PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, ws + p.w);
+    const char* spare = nullptr;
+    if (!p.f8 && (!p.rows || dx)) HYB_TRY(prepare_piece(head, p, n_vocab, n_vocab, v0, rows, ws + p.w, &spare, s));
+    PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, spare);
     if (p.f8) {
       W.plain = n_vocab - v0;
       W.top = top;
