@@ -829,10 +829,13 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
       W.top = top;
     }
     if (p.rows) {
-      // all of a packed head's tile rows that the piece reaches into
-      const int64_t b1 = p.f8 ? 1 : head.layout->b1, whole = (rows + b1 - 1) / b1 * b1, ldz = (whole + 3) / 4 * 4;
+      // all of a packed head's tile rows that the piece's vocabulary reaches into
+      // (not its padding: a product of other rows may take another route, and dX
+      // would differ in its last bits with and without dW)
+      const int64_t live = n_vocab - v0 < rows ? n_vocab - v0 : rows;
+      const int64_t b1 = p.f8 ? 1 : head.layout->b1, whole = (live + b1 - 1) / b1 * b1, ldz = (whole + 3) / 4 * 4;
       float* z = reinterpret_cast<float*>(ws + p.logits);
-      HYB_TRY(piece_logits(head, p, x, ldx, v0, whole, z, ldz, ws, s));
+      if (live > 0) HYB_TRY(piece_logits(head, p, x, ldx, v0, whole, z, ldz, ws, s));
       const dim3 grid(unsigned((vsteps + 3) / 4), unsigned(p.m16 / 16));
       if (p.f8)
         hipLaunchKernelGGL((k_xent_g_rows<DT, true>), grid, dim3(256), 0, s, z, ldz, t);
