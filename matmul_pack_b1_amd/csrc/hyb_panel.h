@@ -71,11 +71,13 @@ struct PanelOperand {
   // panels of their own (b1 / 16 of b2 / 64 steps): `data` is the dense stream,
   // where tile t lies in slot tidx[t] if that is one of n_dense; the other
   // tiles, and those of tile rows that reach beyond row `plain`, lie in
-  // `spare` in the order of the tiles from row0 on (NULL: they read as zeros).
+  // `spare`, tile rows spare0 .. spare1 - 1 (from row0) in the order of the
+  // tiles; where it does not hold their row they read as zeros.
   int32_t log_b1, log_b2, tiles_k, n_dense;
   int64_t row0, plain;
   const int32_t* tidx;
   const char* spare;
+  int32_t spare0, spare1;
   // An 8-bit weight read transposed: rows from `plain` on count as zeros; in
   // fp16 the values are divided by 2^(*top - 133).
   const uint32_t* top;
@@ -321,8 +323,8 @@ struct PanelTile {
     // Address of tile (tn, tk) of the operand, or NULL.
     __device__ __forceinline__ const char* tile_at(int32_t tn, int32_t tk, int32_t slot) const {
       const bool dense = slot >= 0 && slot < o.n_dense && o.row0 + (int64_t(tn + 1) << o.log_b1) <= o.plain;
-      if (!dense && !o.spare) return nullptr;
-      const int64_t tile = dense ? slot : int64_t(tn) * o.tiles_k + tk;
+      if (!dense && (tn < o.spare0 || tn >= o.spare1)) return nullptr;
+      const int64_t tile = dense ? slot : int64_t(tn - o.spare0) * o.tiles_k + tk;
       return (dense ? o.data : o.spare) + (tile << (o.log_b1 + o.log_b2 + 1));
     }
     // Straight: on entering a tile column, the address of the first step there

@@ -81,8 +81,8 @@ __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t
   *reinterpret_cast<uint4*>(p + 256 + r * 16) = make_uint4(e[4], e[5], e[6], e[7]);
 }
 
-// The tiles of rows v0.. of a packed matrix that are not multiplied where they
-// lie, into `out` in tile order (one wavefront per panel and step): sparse ones
+// The tiles of rows v0.. (a multiple of b1) of a packed matrix that are not
+// multiplied where they lie, into `out` in tile order (one wavefront per panel and step): sparse ones
 // expanded from their values and codes, those of a tile row that reaches into
 // the padding with its rows from n_vocab on zero, ones without a slot zero.
 // `plain` as in PanelOperand.  Bound by the writes: 37 us for a piece of 32768 x
@@ -660,21 +660,32 @@ hipError_t run_dx(int bp, const PanelOperand& A, const PanelOperand& B, int32_t 
   return run_product<DT, true, !F8, F8, 16, 4, F8 ? 8 : 4, F8 ? 1 : 2>(A, B, steps, parts, o, s);
 }
 
+// The tile rows of a piece that were expanded (PanelOperand): none by default.
+struct Spare {
+  const char* at = nullptr;
+  int32_t first = 0, end = 0;
+};
+
 // The tiles of the piece of `rows` vocabulary rows from v0 that PanelOperand
-// calls spare, in `out`; *spare is `out`, or NULL where the piece needs none (a
-// tile without a slot then reads as zeros).
+// calls spare, in `out`: over sparse tiles those of every tile row, else the one
+// tile row that the vocabulary ends within (tiles behind it, and ones without a
+// slot, read as zeros).
 hipError_t prepare_piece(const hyb_head& head, const XentPlan& p, int64_t n_vocab, int64_t plain, int64_t v0,
-                         int64_t rows, char* out, const char** spare, hipStream_t s) {
-  const unsigned panels = unsigned((rows + 15) / 16);
+                         int64_t rows, char* out, Spare* spare, hipStream_t s) {
   const hyb_layout& L = *head.layout;
   const hyb_packed& P = *head.packed;
-  *spare = nullptr;
-  if (L.n_sparse == 0 && (v0 + rows + L.b1 - 1) / L.b1 * L.b1 <= plain) return hipSuccess;
-  *spare = out;
+  int64_t from = v0, end = v0 + rows;
+  if (L.n_sparse == 0) {
+    from = n_vocab / L.b1 * L.b1;
+    if (from == n_vocab || from < v0 || from >= end) return hipSuccess;
+    if (end > from + L.b1) end = from + L.b1;
+  }
+  *spare = Spare{out, int32_t((from - v0) / L.b1), int32_t((end - v0 + L.b1 - 1) / L.b1)};
+  const unsigned panels = unsigned((end - from + 15) / 16);
   hipLaunchKernelGGL(k_xent_expand, dim3(panels, unsigned((p.steps + 3) / 4)), dim3(256), 0, s,
                      static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
                      static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
-                     int32_t(L.n_dense), int32_t(L.n_sparse), v0, n_vocab, plain, int32_t(p.steps), out);
+                     int32_t(L.n_dense), int32_t(L.n_sparse), from, n_vocab, plain, int32_t(p.steps), out);
   return hipGetLastError();
 }
 
@@ -694,7 +705,7 @@ hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtyp
 
 // The A operand of the logits product for a piece.
 PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t plain, int64_t v0, int64_t rows,
-                           const char* spare) {
+                           const Spare& spare) {
   PanelOperand o{};
   o.rows16 = int32_t((rows + 15) / 16 * 16);
   o.steps = int32_t(p.steps);
@@ -713,7 +724,9 @@ PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t plai
   o.row0 = v0;
   o.plain = plain;
   o.tidx = head.packed->tidx;
-  o.spare = spare;
+  o.spare = spare.at;
+  o.spare0 = spare.first;
+  o.spare1 = spare.end;
   return o;
 }
 
@@ -782,7 +795,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     const int64_t step = whole ? n_vocab : p.piece;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
       const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
-      const char* spare = nullptr;
+      Spare spare;
       if (!whole) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, &spare, s));
       t.v0 = v0;
       const PanelOperand W = piece_operand(head, p, p.n, v0, rows, spare);
@@ -821,7 +834,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     t.v0 = v0;
     t.g_steps = vsteps;
     // (the logits of few tokens do not need them)
-    const char* spare = nullptr;
+    Spare spare;
     if (!p.f8 && (!p.rows || dx)) HYB_TRY(prepare_piece(head, p, n_vocab, n_vocab, v0, rows, ws + p.w, &spare, s));
     PanelOperand W = piece_operand(head, p, n_vocab, v0, rows, spare);
     if (p.f8) {

@@ -103,7 +103,16 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     p.zt = take(p.m16 * 4);
   }
   if (p.rows) p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
-  if (!p.f8 && (!p.rows || dx)) p.w = take(p.piece * krows * 2);
+  // Expanded tiles: a piece of them over sparse tiles; without any the loss
+  // needs none and the gradients one tile row, where the vocabulary may end (loss
+  // of 100 tokens over a dense 128256 x 4096 head: 1.4 MB in all, 1052 with a
+  // piece).
+  if (!p.f8 && (!p.rows || dx)) {
+    if (head.layout->n_sparse > 0)
+      p.w = take(p.piece * krows * 2);
+    else if (dx || dw)
+      p.w = take(int64_t(head.layout->b1) * krows * 2);
+  }
   if (dx || dw) p.g = take(p.m16 * p.piece * 2);
   if (dx) p.dx = take(int64_t(p.parts) * m * krows * 4);
   p.total = at;
