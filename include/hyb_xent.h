@@ -61,6 +61,11 @@ enum { HYB_XENT_LOSS = 0, HYB_XENT_DX = 1, HYB_XENT_DW = 2 };
  * Host only. */
 hyb_status hyb_xent_workspace_size(const hyb_head* head, int32_t m, int32_t what, size_t* bytes);
 
+/* Vocabulary rows that the call of hyb_xent_workspace_size's arguments works
+ * through at a time on the current device (n: all at once; the last piece may
+ * be shorter).  Host only. */
+hyb_status hyb_xent_piece_rows(const hyb_head* head, int32_t m, int32_t what, int64_t* rows);
+
 /* loss (m fp32) and lse (m fp32).
  *   x       device m x k of x_dtype (HYB_BF16 or HYB_F16; a packed head's own
  *           type), row stride ldx >= k; 16-byte aligned with ldx % 8 == 0

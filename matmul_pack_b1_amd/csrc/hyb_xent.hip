@@ -767,8 +767,8 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
       PanelOperand X;
       HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
     }
-    for (int64_t v0 = 0; v0 < n_vocab; v0 += p.rows_piece) {
-      const int64_t rows = p.n - v0 < p.rows_piece ? p.n - v0 : p.rows_piece;
+    for (int64_t v0 = 0; v0 < n_vocab; v0 += p.at_once) {
+      const int64_t rows = p.n - v0 < p.at_once ? p.n - v0 : p.at_once;
       const int64_t ldz = (rows + 3) / 4 * 4;
       HYB_TRY(piece_logits(head, p, x, ldx, v0, rows, z, ldz, ws, s));
       t.v0 = v0;
@@ -789,14 +789,12 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
   } else {
     PanelOperand X;
     HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
-    // A head that is multiplied where it lies is one piece.  (Logits of
-    // padding rows are not looked at: no tile row is spare for them.)
-    const bool whole = p.f8 || head.layout->n_sparse == 0;
-    const int64_t step = whole ? n_vocab : p.piece;
-    for (int64_t v0 = 0; v0 < n_vocab; v0 += step) {
-      const int64_t rows = n_vocab - v0 < step ? n_vocab - v0 : step;
+    // (Logits of padding rows are not looked at: no tile row is spare for them.)
+    const bool expand = !p.f8 && head.layout->n_sparse > 0;
+    for (int64_t v0 = 0; v0 < n_vocab; v0 += p.at_once) {
+      const int64_t rows = n_vocab - v0 < p.at_once ? n_vocab - v0 : p.at_once;
       Spare spare;
-      if (!whole) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, &spare, s));
+      if (expand) HYB_TRY(prepare_piece(head, p, n_vocab, p.n, v0, rows, ws + p.w, &spare, s));
       t.v0 = v0;
       const PanelOperand W = piece_operand(head, p, p.n, v0, rows, spare);
       HYB_TRY((run_tiles<DT, false>(p, W, X, t, s)));
@@ -828,8 +826,8 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
   t.g = ws + p.g;
   // dX runs over the vocabulary that counts, dW over every row of the head.
   const int64_t end = dw ? p.n : n_vocab;
-  for (int64_t v0 = 0; v0 < end; v0 += p.piece) {
-    const int64_t rows = end - v0 < p.piece ? end - v0 : p.piece;
+  for (int64_t v0 = 0; v0 < end; v0 += p.at_once) {
+    const int64_t rows = end - v0 < p.at_once ? end - v0 : p.at_once;
     const int32_t vsteps = int32_t((rows + 63) / 64);
     t.v0 = v0;
     t.g_steps = vsteps;

@@ -99,6 +99,17 @@ hyb_status hyb_xent_workspace_size(const hyb_head* head, int32_t m, int32_t what
   return ok();
 }
 
+hyb_status hyb_xent_piece_rows(const hyb_head* head, int32_t m, int32_t what, int64_t* rows) {
+  hyb_status st = check_head(head, false);
+  if (st != HYB_OK) return st;
+  if (m < 1 || m > kMaxTokens) return fail(HYB_ERR_SHAPE, "m = %d outside [1, %d]", m, kMaxTokens);
+  if (what < 0 || what > 3) return fail(HYB_ERR_INVALID_ARG, "what = %d", what);
+  if ((what & HYB_XENT_DW) && head->f8) return fail(HYB_ERR_UNSUPPORTED, "an 8-bit head has no weight gradient");
+  if (!rows) return fail(HYB_ERR_INVALID_ARG, "rows is NULL");
+  *rows = hyb::xent_plan(*head, m, what, hyb::device_cus()).at_once;
+  return ok();
+}
+
 hyb_status hyb_xent(const hyb_head* head, int64_t n_vocab, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
                     const int64_t* target, int64_t ignore_index, float* loss, float* lse, void* workspace,
                     size_t workspace_bytes, void* stream) {

@@ -16,11 +16,11 @@ struct XentPlan {
   int64_t m;           // tokens
   int64_t steps;       // steps of k in the logits product
   int64_t ksteps16;    // 64-column steps of k in 16-bit panels
-  int64_t piece;       // vocabulary rows per piece (multiple of 256, or all)
+  int64_t piece;       // vocabulary rows per piece of dz or of expanded tiles (multiple of 256)
   int64_t m16, m64;    // tokens rounded up
   int bp;              // token panels per tile of the logits product
-  bool rows;           // few tokens or tiles: logits through the library's product ...
-  int64_t rows_piece;  // ... of this many vocabulary rows at a time
+  bool rows;           // few tokens or tiles: logits through the library's product
+  int64_t at_once;     // vocabulary rows the call works through at a time
   int64_t chunks;      // partial softmax sums per token
   int parts;           // cuts of the vocabulary in the dX product
   size_t x, xs, part, zt, logits, w, g, dx, misc, total;

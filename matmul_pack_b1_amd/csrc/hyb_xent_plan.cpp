@@ -62,7 +62,13 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   // half of the compute units without one.
   const int64_t wide = up(p.piece, 256) / 256 * (up(m, 256) / 256);
   p.bp = m <= 64 ? 4 : m <= 128 || 2 * wide <= cus ? 8 : 16;
-  p.rows_piece = dx || dw ? p.piece : m <= 64 ? p.n : 32768;
+  if (dx || dw)
+    p.at_once = p.piece;
+  else if (p.rows)
+    p.at_once = m <= 64 ? p.n : 32768;
+  else  // a head that is multiplied where it lies is one piece
+    p.at_once = p.f8 || head.layout->n_sparse == 0 ? p.n : p.piece;
+  if (p.at_once > p.n) p.at_once = p.n;
   p.chunks = p.rows ? up(p.n, 2048) / 2048 : up(p.n, 256) / 256;
   p.parts = 1;
   if (dx) {
@@ -102,7 +108,7 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
     p.part = take(p.chunks * p.m16 * 8);
     p.zt = take(p.m16 * 4);
   }
-  if (p.rows) p.logits = take(m * up(p.rows_piece < p.n ? p.rows_piece : p.n, 4) * 4);
+  if (p.rows) p.logits = take(m * up(p.at_once, 4) * 4);
   // Expanded tiles: a piece of them over sparse tiles; without any the loss
   // needs none and the gradients one tile row, where the vocabulary may end (loss
   // of 100 tokens over a dense 128256 x 4096 head: 1.4 MB in all, 1052 with a

@@ -17,7 +17,7 @@ from . import binding as hb
 from . import f8
 
 DX, DW = 1, 2   # HYB_XENT_DX, HYB_XENT_DW
-EXPORTED = ("hyb_xent_workspace_size", "hyb_xent", "hyb_xent_backward")
+EXPORTED = ("hyb_xent_workspace_size", "hyb_xent_piece_rows", "hyb_xent", "hyb_xent_backward")
 
 
 class HybHead(ctypes.Structure):
@@ -35,6 +35,7 @@ def lib() -> ctypes.CDLL:
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         H = ctypes.POINTER(HybHead)
         L.hyb_xent_workspace_size.argtypes = [H, I32, I32, ctypes.POINTER(SZ)]
+        L.hyb_xent_piece_rows.argtypes = [H, I32, I32, ctypes.POINTER(I64)]
         L.hyb_xent.argtypes = [H, I64, P, I32, I32, I64, P, I64, P, P, P, SZ, P]
         L.hyb_xent_backward.argtypes = [H, I64, P, I32, I32, I64, P, I64, P, P, P, I64, P, I64, P, SZ, P]
         for name in EXPORTED:
@@ -88,6 +89,15 @@ def workspace_bytes(P, m: int, dx: bool = False, dw: bool = False) -> int:
     """Workspace bytes of loss() (neither flag) or backward() on the current
     device."""
     return _need(_head(P)[0], int(m), dx, dw)
+
+
+def piece_rows(P, m: int, dx: bool = False, dw: bool = False) -> int:
+    """Rows of the head that loss() (neither flag) or backward() works through
+    at a time for m tokens on the current device."""
+    rows = ctypes.c_int64(0)
+    hb.check(lib().hyb_xent_piece_rows(ctypes.byref(_head(P)[0]), int(m), (DX if dx else 0) | (DW if dw else 0),
+                                       ctypes.byref(rows)), "hyb_xent_piece_rows")
+    return int(rows.value)
 
 
 def _need(head, m, dx, dw):
