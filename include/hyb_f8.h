@@ -20,7 +20,9 @@
  * output without further loss.  For a 16-bit output the sums of 128 columns
  * may come from the 8-bit matrix instruction, which drops bits of a product
  * that lie far below the largest of the 128: an error of at most 2^-11 of that
- * largest product, ahead of the output's own rounding.
+ * largest product, ahead of the output's own rounding.  Values, products and
+ * sums below 2^-126, the smallest normal number of fp32 and bf16, may count as
+ * zero: a weight of 1e-38 may add nothing, however large its activation.
  *
  * Storage "HYB8", both kinds: rows are rounded up to 16 (a panel), columns to
  * 128 (a step); what is behind the matrix's edge holds code 0.
@@ -67,8 +69,9 @@ hyb_status hyb_f8_quantize(const void* a, int32_t dtype, int64_t rows, int64_t k
                            const hyb_f8* dst, void* stream);
 
 /* The values that the codes stand for, rows x k of `dtype` (any of the three;
- * exact for the type that was quantised and for HYB_F32 and HYB_BF16,
- * rounded to nearest otherwise), row stride lda >= k. */
+ * exact for the type that was quantised, for HYB_F32 and, from 2^-130 on, for
+ * HYB_BF16, rounded to nearest, halves to even, otherwise), row stride
+ * lda >= k. */
 hyb_status hyb_f8_dequantize(const hyb_f8* src, int64_t rows, int64_t k, void* a, int32_t dtype, int64_t lda,
                              void* stream);
 
