@@ -130,9 +130,15 @@ def _check_matrix(Q, kind, name):
         raise TypeError(f"{name} must be an F8Matrix")
     if Q.kind != kind:
         raise TypeError(f"{name} is quantised as {KIND_NAMES[Q.kind]}, expected {KIND_NAMES[kind]}")
-    need = _sizes(*Q.shape)
-    if (Q.codes.numel(), Q.scales.numel()) != need:
-        raise ValueError(f"{name}: buffers of {(Q.codes.numel(), Q.scales.numel())} bytes, its shape needs {need}")
+    codes, scales, need = Q.codes, Q.scales, _sizes(*Q.shape)
+    if (codes.numel(), scales.numel()) != need:
+        raise ValueError(f"{name}: buffers of {(codes.numel(), scales.numel())} bytes, its shape needs {need}")
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"{name}: buffers of {codes.dtype} and {scales.dtype}, expected uint8")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: buffers must be contiguous")
+    if scales.device != codes.device:
+        raise ValueError(f"{name}: its scales are on {scales.device}, its codes on {codes.device}")
 
 
 def _quantize(a, kind, out, name):
