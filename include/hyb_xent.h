@@ -26,7 +26,10 @@
  * backward pass dz is rounded once to the 16-bit type of the products (bf16;
  * or fp16, scaled by 2^14 over the largest |grad| rounded up to a power of two,
  * so that a dz of 4e-9 of that grad keeps 11 bits) and both gradients are
- * summed in fp32 and rounded once.
+ * summed in fp32 and rounded once.  An fp16 dX over an 8-bit head takes W'
+ * scaled into fp16's range: exact for blocks whose scale is within 2^21 of the
+ * head's largest, off by at most 2^-31 of that largest scale for others (2^-38
+ * of the largest magnitude); in bf16 all of W' is exact from 2^-126 on.
  * The vocabulary is worked through in pieces; the logits of a piece live in
  * registers (or, for few tokens, in the workspace).
  *
@@ -68,8 +71,8 @@ hyb_status hyb_xent_piece_rows(const hyb_head* head, int32_t m, int32_t what, in
 
 /* loss (m fp32) and lse (m fp32).
  *   x       device m x k of x_dtype (HYB_BF16 or HYB_F16; a packed head's own
- *           type), row stride ldx >= k; 16-byte aligned with ldx % 8 == 0
- *           for a packed head, element-aligned for an 8-bit one
+ *           type), row stride ldx, k <= ldx < 2^22; 16-byte aligned with
+ *           ldx % 8 == 0 for a packed head, element-aligned for an 8-bit one
  *   target  device int64[m]
  * 0 <= m <= 2^22 tokens; a head has 1 <= n <= 2^27 - 16 and
  * 1 <= k <= 2^21. */
