@@ -626,6 +626,7 @@ hipError_t run_tile(const PanelOperand& W, const PanelOperand& X, const XentTile
 
 template <int KIND, int DT, bool GRAD, bool TILED>
 hipError_t run_shape(int bp, const PanelOperand& W, const PanelOperand& X, const XentTile& t, hipStream_t s) {
+  // (4 goes with up to 64 tokens, whose logits come from the library's product)
   if (bp == 16) return run_tile<KIND, DT, GRAD, TILED, 16, 16, 2, 4>(W, X, t, s);
   return run_tile<KIND, DT, GRAD, TILED, 16, 8, 4, 2>(W, X, t, s);
 }
@@ -690,8 +691,8 @@ hipError_t prepare_piece(const hyb_head& head, const XentPlan& p, int64_t n_voca
 }
 
 // x as the B operand of the logits product.
-hipError_t prepare_x(const hyb_head&, const XentPlan& p, const void* x, int dtype, int64_t ldx, const int64_t* target,
-                     int64_t ignore, char* ws, hipStream_t s, PanelOperand* out) {
+hipError_t prepare_x(const XentPlan& p, const void* x, int dtype, int64_t ldx, const int64_t* target, int64_t ignore,
+                     char* ws, hipStream_t s, PanelOperand* out) {
   if (p.f8) {
     const hyb_f8 X{ws + p.x, ws + p.xs};
     *out = PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.steps), reinterpret_cast<const uint32_t*>(ws + p.xs), p.m16};
@@ -738,7 +739,8 @@ PanelOperand piece_operand(const hyb_head& head, const XentPlan& p, int64_t plai
 
 // Logits of the vocabulary rows v0 .. v0 + rows - 1 (few tokens) through the
 // library's products, fp32, row stride ldz; an 8-bit head multiplies the
-// quantised x of prepare_x.
+// quantised x of prepare_x.  The products get no workspace: where their route
+// would cut k, its tile runs over all of k.
 hipError_t piece_logits(const hyb_head& head, const XentPlan& p, const void* x, int64_t ldx, int64_t v0, int64_t rows,
                         float* z, int64_t ldz, char* ws, hipStream_t s) {
   if (p.f8) {
@@ -765,7 +767,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     float* z = reinterpret_cast<float*>(ws + p.logits);
     if (p.f8) {
       PanelOperand X;
-      HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+      HYB_TRY(prepare_x(p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
     }
     for (int64_t v0 = 0; v0 < n_vocab; v0 += p.at_once) {
       const int64_t rows = p.n - v0 < p.at_once ? p.n - v0 : p.at_once;
@@ -788,7 +790,7 @@ hipError_t loss_typed(const hyb_head& head, const XentPlan& p, int64_t n_vocab, 
     }
   } else {
     PanelOperand X;
-    HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+    HYB_TRY(prepare_x(p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
     // (Logits of padding rows are not looked at: no tile row is spare for them.)
     const bool expand = !p.f8 && head.layout->n_sparse > 0;
     for (int64_t v0 = 0; v0 < n_vocab; v0 += p.at_once) {
@@ -821,7 +823,7 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
     HYB_TRY(hipGetLastError());
   }
   PanelOperand X{};
-  if (p.f8 || !p.rows || dw) HYB_TRY(prepare_x(head, p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
+  if (p.f8 || !p.rows || dw) HYB_TRY(prepare_x(p, x, DT, ldx, t.target, t.ignore, ws, s, &X));
   const int32_t krows = int32_t(p.ksteps16 * 64);
   t.g = ws + p.g;
   // dX runs over the vocabulary that counts, dW over every row of the head.

@@ -30,7 +30,8 @@ XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus) {
   // product, 669 / 674 / 707 / 1144 through the tiles; 10% sparse, 512 tokens:
   // 664 and 609).
   // So do products of up to an eighth as many tiles of 256 x 256 as there are
-  // compute units, which the library's products cut finer (loss, dense, k = 4096,
+  // compute units, for which the library's products have smaller tiles (k is not
+  // cut here, even where their route would; loss, dense, k = 4096,
   // entries x tokens: 1024 x 100 27 us, the tiles 61; 4096 x 300, 32 tiles, 37 and
   // 68; 4096 x 1000, 64 tiles, 123 and 70; 8-bit 28 / 59, 47 / 60, 54 / 63; loss and
   // dX of 4096 x 300 104 and 164).
