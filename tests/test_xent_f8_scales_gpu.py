@@ -51,3 +51,30 @@ def test_blocks_of_far_apart_scales(m, n, dtype, drops):
     cols = slice(128 * small, min(k, 128 * (small + 1)))
     if drops[small] <= 26 or dtype == "bf16":
         assert tol_dx[:, cols].max() < 0.1 * np.abs(dx[:, cols]).max()
+
+
+@pytest.mark.parametrize("pad", [0, 1, 63, 100, 300, 8000])
+@pytest.mark.parametrize("m,dtype", [(9, "f16"), (100, "bf16"), (300, "f16")])
+def test_vocabulary_ends_anywhere(m, dtype, pad):
+    """Padding rows of NaN (a block's scale leaves them out), workspaces of NaN
+    bytes."""
+    n, k = 8450, 333
+    n_vocab = n - pad
+    g = torch.Generator().manual_seed(m + pad)
+    w = (torch.randn(n, k, generator=g) * 0.1).to(DT[dtype])
+    w[n_vocab:] = float("nan")
+    x = torch.randn(m, k, generator=g).to(DT[dtype]).cuda()
+    target = torch.randint(0, n_vocab, (m,), generator=g)
+    target[::5] = -100
+    target, grad = target.cuda(), (torch.randn(m, generator=g) / m).cuda()
+    P = f8.pack(w.cuda())
+    xv = fo.values(*fo.quantise(as64(x), 1))
+    wv = np.nan_to_num(fo.values(*fo.quantise(as64(w), 128)))
+    want, tol = bounds(xv, wv, x, target, grad, n_vocab, k)
+
+    def workspace(**what):
+        return torch.full((xent.workspace_bytes(P, m, **what),), 0xFF, dtype=torch.uint8, device="cuda")
+    loss, lse = xent.loss(P, x, target, n_vocab=n_vocab, workspace=workspace())
+    dx, _ = xent.backward(P, x, target, lse, grad, n_vocab=n_vocab, workspace=workspace(dx=True))
+    for name, got, ref, lim in zip(("loss", "lse", "dx"), (loss, lse, dx), want, tol):
+        within(name, got, ref, lim)
