@@ -23,10 +23,10 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 
 // exp(z - x) as exp2(fma(z, log2 e, -hi)) * fix, two instructions an element:
 // hi is x log2 e rounded, fix takes its rounding back.  That rounding is half an
-// ulp of hi, a sixteenth at |x| = 2^20 but 2^7 from about 2^31 on, where one factor
-// is 0 and the other infinite: an x beyond kNear is `far`, and raw_any takes the
-// difference first (three instructions, fix 1).  Where a wavefront has no far x,
-// raw serves it; a near x has the same bits either way.
+// ulp of hi: a sixteenth at |x| = 2^20, but 2^7 from 1.5e9 on and 2^8 from 3e9,
+// where one factor can be 0 and the other infinite.  An x beyond kNear is `far`,
+// and raw_any takes the difference first (three instructions, fix 1).  Where a
+// wavefront has no far x, raw serves it; a near x has the same bits either way.
 struct ExpBase {
   static constexpr float kNear = 1048576.f;
   float x, hi, fix;
@@ -82,11 +82,11 @@ __device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t
 }
 
 // The tiles of rows v0.. (a multiple of b1) of a packed matrix that are not
-// multiplied where they lie, into `out` in tile order (one wavefront per panel and step): sparse ones
-// expanded from their values and codes, those of a tile row that reaches into
-// the padding with its rows from n_vocab on zero, ones without a slot zero.
-// `plain` as in PanelOperand.  Bound by the writes: 37 us for a piece of 32768 x
-// 4096 with 30% of its tiles sparse.
+// multiplied where they lie, into `out` in tile order (one wavefront per panel
+// and step): sparse ones expanded from their values and codes, those of a tile
+// row that reaches into the padding with its rows from n_vocab on zero, ones
+// without a slot zero.  `plain` as in PanelOperand.  Bound by the writes: 37 us
+// for a piece of 32768 x 4096 with 30% of its tiles sparse.
 __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ dense, const uint4* __restrict__ val,
                                                      const uint16_t* __restrict__ meta,
                                                      const int32_t* __restrict__ tidx, int b1, int b2, int meta_kind,
