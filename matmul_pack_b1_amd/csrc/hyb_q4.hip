@@ -1,0 +1,836 @@
+// Kernels of the 4-bit weights (include/hyb_q4.h): quantise, read back, the
+// product, and the gated product of two weights (include/hyb_gated.h).
+#include <type_traits>
+
+#include "hyb_act.h"
+#include "hyb_panel.h"
+#include "hyb_q4_internal.h"
+
+namespace hyb {
+namespace {
+
+// ------------------------------------------------------ quantise, read back --
+
+// Eight columns c0.. of one row as fp32; columns from k on are zero.
+template <int DT>
+__device__ __forceinline__ void load8_f32(const void* a, int64_t base, int32_t c0, int32_t k, float (&v)[8]) {
+  if (c0 + 8 <= k) {
+    if constexpr (DT == HYB_F32) {
+      const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const float*>(a) + base + c0);
+      const Bytes16 lo = p[0], hi = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __builtin_bit_cast(float, lo.w[i]);
+        v[4 + i] = __builtin_bit_cast(float, hi.w[i]);
+      }
+    } else {
+      const Bytes16 u = *reinterpret_cast<const Bytes16*>(static_cast<const uint16_t*>(a) + base + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = widen16<DT>(u.w[i] & 0xFFFFu);
+        v[2 * i + 1] = widen16<DT>(u.w[i] >> 16);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0.f;
+    if (c0 + i < k) {
+      if constexpr (DT == HYB_F32)
+        v[i] = static_cast<const float*>(a)[base + c0 + i];
+      else
+        v[i] = widen16<DT>(static_cast<const uint16_t*>(a)[base + c0 + i]);
+    }
+  }
+}
+
+// Scale byte of a group from its largest magnitude's bits: e + 127 with the
+// smallest e in [-125, 125] for which the magnitude is at most 7 * 2^e (7 is
+// 1.75 * 2^2); 127 for zero, 255 for infinities and NaN.
+__device__ __forceinline__ uint32_t group_byte(uint32_t top) {
+  if (top == 0) return 127u;
+  if (top >= 0x7F800000u) return 255u;
+  const int e = int((top + 0x1FFFFFu) >> 23) - 2;  // the next binade from above 1.75 on
+  return uint32_t(e < 2 ? 2 : e > 252 ? 252 : e);
+}
+
+// One workgroup per panel, a wavefront per four steps at a time: a load covers
+// 128 columns of four rows (8 columns per lane, 16 lanes to a row, four to a
+// group), codes and scales are put into the stream's order in LDS.
+template <int DT>
+__global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a, int64_t n, int32_t k, int64_t lda,
+                                                     int32_t steps, int64_t rows16, char* __restrict__ codes,
+                                                     char* __restrict__ scales) {
+  __shared__ __attribute__((aligned(16))) char stage[4][4096 + 256];
+  __shared__ uint32_t tops[4][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t panel = blockIdx.x;
+  const int32_t quads = (steps + 3) / 4;
+  const int j = lane & 15, rr = lane >> 4;
+  uint32_t best[4] = {0, 0, 0, 0};  // of rows 4 i + rr
+  char* mine = stage[wave];
+  for (int32_t q = wave; q < quads; q += 4) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + rr;
+        const int64_t row = panel * 16 + r;
+        const int32_t c0 = (q * 4 + s) * 128 + j * 8;
+        float v[8];
+        if (row < n) {
+          load8_f32<DT>(a, row * lda, c0, k, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu;
+          top = b > top ? b : top;
+        }
+        uint32_t o = __shfl_xor(top, 1);
+        top = o > top ? o : top;
+        o = __shfl_xor(top, 2);
+        top = o > top ? o : top;
+        const uint32_t byte = group_byte(top);
+        const float scale = __builtin_bit_cast(float, byte << 23);
+        uint32_t code = 0;
+        if (byte != 255u) {
+          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[0], v[1], scale, 0);
+          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[2], v[3], scale, 1);
+          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[4], v[5], scale, 2);
+          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[6], v[7], scale, 3);
+        }
+        *reinterpret_cast<uint32_t*>(mine + s * 1024 + (j & 3) * 256 + r * 16 + (j >> 2) * 4) = code;
+        if ((j & 3) == 0) mine[4096 + r * 16 + s * 4 + (j >> 2)] = char(byte);
+        if (byte != 255u && top != 0 && byte > best[i]) best[i] = byte;
+      }
+    }
+    // one wavefront writes and reads its own part: its accesses done suffices
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (q * 4 + s < steps)
+        *reinterpret_cast<uint4*>(codes + (panel * steps + q * 4 + s) * kQ4StepBytes + lane * 16) =
+            *reinterpret_cast<const uint4*>(mine + s * 1024 + lane * 16);
+    *reinterpret_cast<uint32_t*>(scales + (q * rows16 + panel * 16) * 16 + lane * 4) =
+        *reinterpret_cast<const uint32_t*>(mine + 4096 + lane * 4);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b = best[i];
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+      const uint32_t o = __shfl_xor(b, d);
+      b = o > b ? o : b;
+    }
+    if (j == 0) tops[wave][4 * i + rr] = b;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    uint32_t b = 0;
+    for (int w = 0; w < 4; ++w) b = tops[w][threadIdx.x] > b ? tops[w][threadIdx.x] : b;
+    scales[quads * rows16 * 16 + panel * 16 + threadIdx.x] = char(b == 0 ? 127u : b);
+  }
+}
+
+// One wavefront per panel and step: codes through LDS into rows, 8 columns per
+// lane.
+template <int DT>
+__global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ codes,
+                                                       const char* __restrict__ scales, int64_t n, int32_t k,
+                                                       int64_t lda, int32_t steps, int64_t rows16,
+                                                       void* __restrict__ a) {
+  __shared__ __attribute__((aligned(16))) char stage[4][1024];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t panel = blockIdx.x;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps) return;
+  char* mine = stage[wave];
+  *reinterpret_cast<uint4*>(mine + lane * 16) =
+      *reinterpret_cast<const uint4*>(codes + (panel * steps + s) * kQ4StepBytes + lane * 16);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const int j = lane & 15, rr = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + rr;
+    const int64_t row = panel * 16 + r;
+    const int32_t c0 = s * 128 + j * 8;
+    if (row >= n || c0 >= k) continue;
+    const uint32_t code = *reinterpret_cast<const uint32_t*>(mine + (j & 3) * 256 + r * 16 + (j >> 2) * 4);
+    const uint32_t byte = uint8_t(scales[((s >> 2) * rows16 + row) * 16 + (s & 3) * 4 + (j >> 2)]);
+    const float scale = __builtin_bit_cast(float, byte << 23);
+    float v[8];
+    auto two = [&](auto sel) {
+      constexpr int b = decltype(sel)::value;
+      const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, scale, b);
+      v[2 * b] = p[0];
+      v[2 * b + 1] = p[1];
+    };
+    two(std::integral_constant<int, 0>());
+    two(std::integral_constant<int, 1>());
+    two(std::integral_constant<int, 2>());
+    two(std::integral_constant<int, 3>());
+    if constexpr (DT == HYB_F32) {
+      float* p = static_cast<float*>(a) + row * lda + c0;
+      if (c0 + 8 <= k) {
+        Bytes16 u[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e >> 2].w[e & 3] = __builtin_bit_cast(uint32_t, v[e]);
+        reinterpret_cast<Bytes16*>(p)[0] = u[0];
+        reinterpret_cast<Bytes16*>(p)[1] = u[1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c0 + e < k) p[e] = v[e];
+      }
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(a) + row * lda + c0;
+      if (c0 + 8 <= k) {
+        Bytes16 u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u.w[e] = round16x2<DT>(v[2 * e], v[2 * e + 1]);
+        *reinterpret_cast<Bytes16*>(p) = u;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c0 + e < k) p[e] = round16<DT>(v[e]);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- products --
+
+struct Q4Weight {
+  const char* codes;
+  const char* scales;
+  const uint8_t* tops;
+};
+
+struct Q4Args {
+  Q4Weight w[2];  // the second for the gated product
+  int64_t rows16;
+  int32_t steps, n, k;
+  const uint16_t* x;
+  int64_t ldx, m;
+  void* y;
+  int64_t ldy;
+  int ydt, act;
+  // tiles: activations as they are (pitch: bytes from a row to the next, `step`:
+  // to a row's next 64 columns, `half`: to its next 32), or as panels
+  const char* xt;
+  int64_t x_panel, x_row, x_unit;
+  int32_t x_step, x_half, packed, steps64;
+  f32x4_t* ws;
+  int32_t parts;
+};
+
+// fp16 operands carry a row's values divided by 2^(top - 139): at most 6 * 2^12,
+// normal numbers for scales down to 2^-25 of the row's largest.
+constexpr int kTopLift = 139;
+
+// The scale of group h of a word's four: its byte as the exponent of a float.
+// (The conversion reads only the exponent: bits of the bytes around it may lie
+// in the sign and the mantissa.)  For fp16 `lift` is kTopLift - top.
+template <int DT>
+__device__ __forceinline__ float group_scale(uint32_t word, int h, int lift) {
+  if constexpr (DT == HYB_BF16) {
+    return __builtin_bit_cast(float, h < 3 ? word << (23 - 8 * h) : word >> 1);
+  } else {
+    const int b = (word >> (8 * h)) & 0xFFu;
+    const int e = b + lift < 0 ? 0 : b + lift;
+    return __builtin_bit_cast(float, uint32_t(b == 255 ? 255 : e) << 23);
+  }
+}
+
+// Eight codes as an operand of the 16-bit matrix instruction.
+template <int DT>
+__device__ __forceinline__ uint4 widen_codes4(uint32_t c, float scale) {
+  uint4 r;
+  if constexpr (DT == HYB_BF16) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+  } else {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 0));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3));
+  }
+  return r;
+}
+
+// Eight columns c0.. of a row of 16-bit elements; columns from k on are zero.
+__device__ __forceinline__ uint4 load8_16(const uint16_t* row, int32_t c0, int32_t k) {
+  if (c0 + 8 <= k) {
+    const Bytes16 u = *reinterpret_cast<const Bytes16*>(row + c0);
+    return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i < k) w[i >> 1] |= uint32_t(row[c0 + i]) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Few tokens: one workgroup per panel (of each weight, gated), its wavefronts
+// cut k.  A lane loads 16 bytes of codes a step (32 codes of its row, eight for
+// each of four matrix instructions), 16 bytes of scales per four steps, and the
+// wavefront MT tokens' 512 columns, which it keeps in LDS.
+template <int DT, int MT, bool GATED, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
+  constexpr int P = GATED ? 2 : 1;
+  constexpr int kRow = 1024 + 16;  // a token's 512 columns, rows 4 banks apart
+  constexpr int kOwn = MT * kRow > P * MT * 64 ? MT * kRow : P * MT * 64;
+  __shared__ __attribute__((aligned(16))) char smem[WAVES * kOwn];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* xs = smem + wave * kOwn;
+  const int64_t panel = blockIdx.x, tok0 = int64_t(blockIdx.y) * MT;
+  const int32_t quads = (a.steps + 3) / 4;
+  const int32_t q0 = quads * wave / WAVES, q1 = quads * (wave + 1) / WAVES;
+  const int64_t row = panel * 16 + (lane & 15);
+
+  __amdgpu_buffer_rsrc_t code_rsrc[P];
+  const char* scale_at[P];
+  int lift[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    code_rsrc[p] = make_rsrc(a.w[p].codes + panel * a.steps * kQ4StepBytes, a.steps * int32_t(kQ4StepBytes));
+    scale_at[p] = a.w[p].scales + row * 16;
+    lift[p] = DT == HYB_F16 ? kTopLift - int(a.w[p].tops[row]) : 0;
+  }
+  uint4 code[2][P][4], scale[2][P], xr[MT];
+  f32x4_t acc[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto load_x = [&](int32_t q) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      xr[t] = tok0 + t < a.m ? load8_16(a.x + (tok0 + t) * a.ldx, q * 512 + lane * 8, a.k) : make_uint4(0, 0, 0, 0);
+  };
+  auto load_w = [&](int32_t q, uint4 (&c)[P][4], uint4 (&sc)[P]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)  // (steps behind the last lie behind the resource: zeros)
+        c[p][s] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], (q * 4 + s) * 1024 + lane * 16, 0, HYB_W_AUX));
+    }
+  };
+  const int t16 = lane & 15;
+  const char* xb = xs + (t16 < MT ? t16 : MT - 1) * kRow + (lane >> 4) * 16;
+  auto step = [&](int32_t q, auto buf) {
+    constexpr int B = decltype(buf)::value;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) *reinterpret_cast<uint4*>(xs + t * kRow + lane * 16) = xr[t];
+    __builtin_amdgcn_wave_barrier();
+    if (q + 1 < q1) {
+      load_x(q + 1);
+      load_w(q + 1, code[1 - B], scale[1 - B]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint4 b[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) b[h] = *reinterpret_cast<const uint4*>(xb + s * 256 + h * 64);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const uint4 cw = code[B][p][s];
+        const uint32_t c[4] = {cw.x, cw.y, cw.z, cw.w};
+        const uint32_t sw = s == 0 ? scale[B][p].x : s == 1 ? scale[B][p].y : s == 2 ? scale[B][p].z : scale[B][p].w;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          acc[p] = mfma16x16x32<DT>(widen_codes4<DT>(c[h], group_scale<DT>(sw, h, lift[p])), b[h], acc[p]);
+      }
+    }
+  };
+  if (q0 < q1) {
+    load_x(q0);
+    load_w(q0, code[0], scale[0]);
+  }
+  for (int32_t q = q0; q < q1; q += 2) {
+    step(q, std::integral_constant<int, 0>());
+    if (q + 1 < q1) step(q + 1, std::integral_constant<int, 1>());
+  }
+  // sums of the wavefronts, in order: [wave][weight][token][row]
+  __builtin_amdgcn_wave_barrier();
+  float* red = reinterpret_cast<float*>(xs);
+  if (t16 < MT) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      *reinterpret_cast<f32x4_t*>(red + (p * MT + t16) * 16 + (lane >> 4) * 4) = acc[p];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * 16; i += 64 * WAVES) {
+    const int t = i >> 4, r = i & 15;
+    if (tok0 + t >= a.m || panel * 16 + r >= a.n) continue;
+    float v[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      v[p] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) v[p] += reinterpret_cast<const float*>(smem + w * kOwn)[(p * MT + t) * 16 + r];
+      if constexpr (DT == HYB_F16) v[p] = __builtin_ldexpf(v[p], int(a.w[p].tops[panel * 16 + r]) - kTopLift);
+    }
+    const float out = GATED ? act_value(a.act, v[0]) * v[P - 1] : v[0];
+    store_out(a.y, a.ydt, (tok0 + t) * a.ldy + panel * 16 + r, out);
+  }
+}
+
+// Activations as panels (hyb_panel.h; rows behind m and columns behind k zero),
+// for tiles whose x is not in 16-byte pieces of whole 64-column steps.
+__global__ __launch_bounds__(256) void k_q4_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m, int32_t k,
+                                                   int32_t steps64, char* __restrict__ out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t panel = blockIdx.x;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps64) return;
+  const int64_t row = panel * 16 + (lane & 15);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 u = row < m ? load8_16(x + row * ldx, s * 64 + h * 32 + (lane >> 4) * 8, k) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(out + (panel * steps64 + s) * 2048 + h * 1024 + lane * 16) = u;
+  }
+}
+
+// Four outputs j0.. of token `tok`: sums v (and u of the second weight).
+__device__ __forceinline__ void q4_store4(const Q4Args& a, int64_t tok, int64_t j0, f32x4_t v) {
+  if (tok >= a.m || j0 >= a.n) return;
+  const int64_t at = tok * a.ldy + j0;
+  if (j0 + 4 <= a.n) {
+    if (a.ydt == HYB_F32) {
+      const u32x4_t u = __builtin_bit_cast(u32x4_t, v);
+      *reinterpret_cast<Bytes16*>(static_cast<float*>(a.y) + at) = Bytes16{{u[0], u[1], u[2], u[3]}};
+    } else {
+      const uint2 h = a.ydt == HYB_BF16 ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3])
+                                        : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<Bytes8*>(static_cast<uint16_t*>(a.y) + at) = Bytes8{{h.x, h.y}};
+    }
+    return;
+  }
+  for (int e = 0; e < 4; ++e)
+    if (j0 + e < a.n) store_out(a.y, a.ydt, at + e, v[e]);
+}
+
+// Sums of rows j0.. of weight p in their own scale.
+template <int DT>
+__device__ __forceinline__ f32x4_t q4_lift(const Q4Args& a, int p, int64_t j0, f32x4_t v) {
+  if constexpr (DT == HYB_F16) {
+    if (j0 >= a.rows16) return v;
+    const uint32_t t = *reinterpret_cast<const uint32_t*>(a.w[p].tops + j0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], int((t >> (8 * e)) & 0xFFu) - kTopLift);
+  }
+  return v;
+}
+
+template <int DT, bool GATED>
+__device__ __forceinline__ f32x4_t q4_finish(const Q4Args& a, int64_t j0, f32x4_t v, f32x4_t u) {
+  v = q4_lift<DT>(a, 0, j0, v);
+  if constexpr (GATED) {
+    u = q4_lift<DT>(a, 1, j0, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = act_value(a.act, v[e]) * u[e];
+  }
+  return v;
+}
+
+// More tokens: AP panels of codes x BP panels of tokens through LDS, WA x WB
+// wavefronts.  Codes stay 4-bit up to the registers, where two instructions'
+// worth of eight are widened, scale included, for every BP / WB x 2 matrix
+// instructions they feed.  A step is 64 columns of x; codes come 128 columns at
+// a time (half the panels in each of two steps), scales 512.
+template <int DT, bool GATED, int AP, int BP, int WA, int WB>
+struct Q4Tile {
+  static constexpr int kWaves = WA * WB;
+  static constexpr int kA = AP / WA, kB = BP / WB;
+  static constexpr int kCodes = AP * 1024, kScales = AP * 256, kX = BP * 2048;
+  static constexpr int kStages = 2 * (kCodes + kScales + kX);
+  static constexpr int kOutA = GATED ? kA / 2 : kA;
+  static constexpr int kOutBytes = kWaves * kOutA * kB * 512;
+  static constexpr int kLds = kStages > kOutBytes ? kStages : kOutBytes;
+  static constexpr int kPanels = GATED ? AP / 2 : AP;  // of each weight
+  static constexpr int kLoadsX = BP * 2 / kWaves;
+  static_assert(AP / 2 == kWaves && BP * 2 % kWaves == 0 && AP % WA == 0 && BP % WB == 0, "even split");
+
+  __device__ static void run(const Q4Args& a, int32_t ab, int32_t bb, int32_t s0, int32_t s1, char* smem,
+                             f32x4_t (&acc)[kA][kB]) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wa = wave % WA, wb = wave / WA;
+    const uint32_t base = __builtin_amdgcn_readfirstlane(panel_lds_addr(smem));
+    constexpr int kAtScales = 2 * kCodes, kAtX = kAtScales + 2 * kScales;
+    const int64_t panels = a.rows16 / 16, first = int64_t(ab) * kPanels;
+    const int64_t exist = panels - first < kPanels ? panels - first : kPanels;
+
+    // codes: chunk c is panel c of the tile (gated: the second weight's from
+    // AP / 2 on); this wavefront's are `wave` and `wave + AP / 2`
+    const int c0 = wave, c1 = wave + AP / 2;
+    auto code_rsrc = [&](int c) {
+      const char* from = GATED && c >= AP / 2 ? a.w[1].codes : a.w[0].codes;
+      return panel_srd(from + first * a.steps * kQ4StepBytes, uint32_t(exist * a.steps * kQ4StepBytes));
+    };
+    const srd4_t cr0 = code_rsrc(c0), cr1 = code_rsrc(c1);
+    const int32_t pitch = a.steps * int32_t(kQ4StepBytes);
+    const int32_t co0 = c0 * pitch + lane * 16, co1 = (GATED ? c1 - AP / 2 : c1) * pitch + lane * 16;
+    auto issue_codes = [&](int32_t d, int half) {
+      const uint32_t dst = base + (d & 1) * kCodes;
+      if (half == 0)
+        panel_dma16(cr0, __builtin_amdgcn_readfirstlane(dst + c0 * 1024), co0 + d * 1024);
+      else
+        panel_dma16(cr1, __builtin_amdgcn_readfirstlane(dst + c1 * 1024), co1 + d * 1024);
+    };
+    // scales: 1 KiB is four panels
+    auto issue_scales = [&](int32_t q) {
+      if (wave >= AP / 4) return;
+      const int c = wave;
+      const bool second = GATED && c >= AP / 8;
+      const char* from = second ? a.w[1].scales : a.w[0].scales;
+      const srd4_t r = panel_srd(from + (int64_t(q) * a.rows16 + first * 16) * 16, uint32_t(exist * 256));
+      panel_dma16(r, __builtin_amdgcn_readfirstlane(base + kAtScales + (q & 1) * kScales + c * 1024), (second ? c - AP / 8 : c) * 1024 + lane * 16);
+    };
+    // x: chunk c is half c % 2 of panel c / 2
+    const int64_t tok0 = int64_t(bb) * BP * 16, left = a.m - tok0;
+    const int64_t rows = left < BP * 16 ? left : BP * 16;
+    const srd4_t xr = panel_srd(a.xt + int64_t(bb) * BP * a.x_panel,
+                                uint32_t(a.packed ? (rows + 15) / 16 * a.x_panel : (rows - 1) * a.x_row + int64_t(a.k) * 2));
+    int32_t xo[kLoadsX];
+#pragma unroll
+    for (int t = 0; t < kLoadsX; ++t) {
+      const int c = wave * kLoadsX + t;
+      xo[t] = int32_t((c >> 1) * a.x_panel + (lane & 15) * a.x_row + (lane >> 4) * a.x_unit) + (c & 1) * a.x_half;
+    }
+    auto issue_x = [&](int32_t s) {
+      const uint32_t dst = base + kAtX + (s & 1) * kX;
+#pragma unroll
+      for (int t = 0; t < kLoadsX; ++t) panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + (wave * kLoadsX + t) * 1024), xo[t] + s * a.x_step);
+    };
+    // panel i of this wavefront in the tile's order
+    auto panel_of = [&](int i) {
+      if constexpr (GATED) return i < kA / 2 ? wa * (kA / 2) + i : AP / 2 + wa * (kA / 2) + i - kA / 2;
+      return wa * kA + i;
+    };
+    int lift[kA];
+#pragma unroll
+    for (int i = 0; i < kA; ++i) {
+      lift[i] = 0;
+      if constexpr (DT == HYB_F16) {
+        const int p = panel_of(i);
+        const bool second = GATED && p >= AP / 2;
+        const int64_t row = (first + (second ? p - AP / 2 : p)) * 16 + (lane & 15);
+        if (row < a.rows16) lift[i] = kTopLift - int(a.w[second ? 1 : 0].tops[row]);
+      }
+#pragma unroll
+      for (int j = 0; j < kB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    if (s0 >= s1) return;
+    issue_x(s0);
+    issue_codes(s0 >> 1, 0);
+    issue_codes(s0 >> 1, 1);
+    issue_scales(s0 >> 3);
+
+    uint32_t sw[kA];
+#pragma unroll
+    for (int i = 0; i < kA; ++i) sw[i] = 0;
+    auto compute = [&](int32_t s, auto phase) {
+      constexpr int kPhase = decltype(phase)::value;  // s % 4
+      constexpr int half = kPhase & 1;
+      const char* codes = smem + ((kPhase >> 1) & 1) * kCodes + lane * 16 + half * 8;
+      const char* xs = smem + kAtX + half * kX + lane * 16;
+      if constexpr (half == 0) {
+        const char* sc = smem + kAtScales + ((s >> 3) & 1) * kScales + (lane & 15) * 16 + ((s >> 1) & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < kA; ++i) sw[i] = *reinterpret_cast<const uint32_t*>(sc + panel_of(i) * 256);
+      }
+      uint2 c = *reinterpret_cast<const uint2*>(codes + panel_of(0) * 1024);
+      uint4 b[kB][2];
+#pragma unroll
+      for (int j = 0; j < kB; ++j) {
+        b[j][0] = *reinterpret_cast<const uint4*>(xs + (wb * kB + j) * 2048);
+        b[j][1] = *reinterpret_cast<const uint4*>(xs + (wb * kB + j) * 2048 + 1024);
+      }
+      if (s + 1 < s1) issue_x(s + 1);
+      const int32_t d = (s >> 1) + 1;
+      if (2 * d < s1) issue_codes(d, half);
+      if (kPhase == 0 && (s & 7) == 0 && s + 8 < s1) issue_scales((s >> 3) + 1);
+#pragma unroll
+      for (int i = 0; i < kA; ++i) {
+        const uint2 was = c;
+        if (i + 1 < kA) c = *reinterpret_cast<const uint2*>(codes + panel_of(i + 1) * 1024);
+        const uint4 a0 = widen_codes4<DT>(was.x, group_scale<DT>(sw[i], 2 * half, lift[i]));
+        const uint4 a1 = widen_codes4<DT>(was.y, group_scale<DT>(sw[i], 2 * half + 1, lift[i]));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kB; ++j) acc[i][j] = mfma16x16x32<DT>(a0, b[j][0], acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < kB; ++j) acc[i][j] = mfma16x16x32<DT>(a1, b[j][1], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int32_t q = s0; q < s1; q += 4) {
+      auto one = [&](auto phase) {
+        const int32_t s = q + decltype(phase)::value;
+        if (s >= s1) return;
+        panel_wait<0>();
+        __syncthreads();
+        compute(s, phase);
+      };
+      one(std::integral_constant<int, 0>());
+      one(std::integral_constant<int, 1>());
+      one(std::integral_constant<int, 2>());
+      one(std::integral_constant<int, 3>());
+    }
+  }
+};
+
+// Column steps of a part: whole multiples of eight (the scales' 512 columns).
+__device__ __forceinline__ int32_t q4_part_step(int32_t steps64, int32_t part, int32_t parts) {
+  const int32_t octs = (steps64 + 7) / 8;
+  const int32_t s = int32_t(int64_t(octs) * part / parts) * 8;
+  return s < steps64 ? s : steps64;
+}
+
+template <int DT, bool GATED, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_q4_tile(Q4Args a) {
+  typedef Q4Tile<DT, GATED, AP, BP, WA, WB> T;
+  extern __shared__ __attribute__((aligned(1024))) char q4_smem[];
+  const int32_t na = int32_t((a.rows16 / 16 + T::kPanels - 1) / T::kPanels);
+  const int32_t nb = int32_t((a.m + BP * 16 - 1) / (BP * 16));
+  int32_t ab, bb;
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  const int32_t part = int32_t(blockIdx.y);
+  f32x4_t acc[T::kA][T::kB];
+  T::run(a, ab, bb, q4_part_step(a.steps64, part, a.parts), q4_part_step(a.steps64, part + 1, a.parts), q4_smem, acc);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wa = wave % WA, wb = wave / WA;
+  if (a.parts > 1) {
+    f32x4_t* out = a.ws + ((int64_t(blockIdx.x) * a.parts + part) * T::kWaves + wave) * (T::kA * T::kB * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kB; ++j) out[(i * T::kB + j) * 64] = acc[i][j];
+    return;
+  }
+  const int64_t col0 = (int64_t(ab) * T::kPanels + wa * T::kOutA) * 16;
+  const int64_t row0 = (int64_t(bb) * BP + wb * T::kB) * 16;
+  if (a.ydt == HYB_F32) {
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j)
+#pragma unroll
+      for (int i = 0; i < T::kOutA; ++i) {
+        const int64_t j0 = col0 + i * 16 + (lane >> 4) * 4;
+        q4_store4(a, row0 + j * 16 + (lane & 15), j0,
+                  q4_finish<DT, GATED>(a, j0, acc[i][j], acc[GATED ? i + T::kA / 2 : i][j]));
+      }
+    return;
+  }
+  __syncthreads();  // the tile's LDS stages are free
+  const bool bf = a.ydt == HYB_BF16;
+  panel_rows16<T::kOutA, T::kB>(
+      q4_smem + wave * (T::kOutA * T::kB * 512), lane, lane & 15,
+      [&](int i, int j) {
+        const f32x4_t v = q4_finish<DT, GATED>(a, col0 + i * 16 + (lane >> 4) * 4, acc[i][j],
+                                               acc[GATED ? i + T::kA / 2 : i][j]);
+        return bf ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3]) : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
+      },
+      [&](int r, int c, uint4 u) {
+        const int64_t tok = row0 + r, col = col0 + c;
+        if (tok >= a.m || col >= a.n) return;
+        uint16_t* p = static_cast<uint16_t*>(a.y) + tok * a.ldy + col;
+        if (col + 8 <= a.n) {
+          *reinterpret_cast<Bytes16*>(p) = Bytes16{{u.x, u.y, u.z, u.w}};
+        } else {
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          for (int e = 0; e < 8; ++e)
+            if (col + e < a.n) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+        }
+      });
+}
+
+// Adds the parts of a tile in order and stores the outputs: one thread per four
+// outputs, in the order of the tile's registers.
+template <int DT, bool GATED, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(256) void k_q4_sum(Q4Args a) {
+  typedef Q4Tile<DT, GATED, AP, BP, WA, WB> T;
+  constexpr int kEach = T::kWaves * T::kOutA * T::kB;  // of 64 lanes, a tile
+  const int32_t na = int32_t((a.rows16 / 16 + T::kPanels - 1) / T::kPanels);
+  const int32_t nb = int32_t((a.m + BP * 16 - 1) / (BP * 16));
+  int32_t ab, bb;
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  const int lane = threadIdx.x & 63;
+  const int c = int(blockIdx.y) * 4 + (threadIdx.x >> 6);
+  if (c >= kEach) return;
+  const int wave = c / (T::kOutA * T::kB), i = c / T::kB % T::kOutA, j = c % T::kB;
+  const int64_t j0 = (int64_t(ab) * T::kPanels + wave % WA * T::kOutA + i) * 16 + (lane >> 4) * 4;
+  const int64_t tok = (int64_t(bb) * BP + wave / WA * T::kB + j) * 16 + (lane & 15);
+  if (tok >= a.m || j0 >= a.n) return;
+  f32x4_t v[2];
+#pragma unroll
+  for (int p = 0; p < (GATED ? 2 : 1); ++p) {
+    const f32x4_t* at = a.ws + (int64_t(blockIdx.x) * a.parts * T::kWaves + wave) * (T::kA * T::kB * 64) +
+                        ((i + p * (T::kA / 2)) * T::kB + j) * 64 + lane;
+    f32x4_t sum = at[0];
+#pragma unroll 4
+    for (int t = 1; t < a.parts; ++t) {
+      const f32x4_t o = at[int64_t(t) * T::kWaves * (T::kA * T::kB * 64)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += o[e];
+    }
+    v[p] = sum;
+  }
+  q4_store4(a, tok, j0, q4_finish<DT, GATED>(a, j0, v[0], v[GATED ? 1 : 0]));
+}
+
+// Zeros (k = 0).
+__global__ __launch_bounds__(256) void k_q4_zero(Q4Args a) {
+  const int64_t j = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (j >= a.n) return;
+  for (int64_t t = blockIdx.y; t < a.m; t += gridDim.y) store_out(a.y, a.ydt, t * a.ldy + j, 0.f);
+}
+
+// ----------------------------------------------------------------- launches --
+
+template <int DT, int MT, bool GATED>
+hipError_t run_rows(const Q4Args& a, hipStream_t s) {
+  const dim3 grid(unsigned(a.rows16 / 16), unsigned((a.m + MT - 1) / MT));
+  if (a.steps > 16)
+    hipLaunchKernelGGL((k_q4_rows<DT, MT, GATED, 8>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_q4_rows<DT, MT, GATED, 4>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool GATED, int AP, int BP, int WA, int WB>
+hipError_t run_tile(const Q4Args& a, hipStream_t s) {
+  typedef Q4Tile<DT, GATED, AP, BP, WA, WB> T;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_q4_tile<DT, GATED, AP, BP, WA, WB>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+  if (e != hipSuccess) return e;
+  const int64_t na = (a.rows16 / 16 + T::kPanels - 1) / T::kPanels, nb = (a.m + BP * 16 - 1) / (BP * 16);
+  hipLaunchKernelGGL((k_q4_tile<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(a.parts)),
+                     dim3(64 * T::kWaves), T::kLds, s, a);
+  if ((e = hipGetLastError()) != hipSuccess || a.parts <= 1) return e;
+  constexpr int kEach = T::kWaves * T::kOutA * T::kB;
+  hipLaunchKernelGGL((k_q4_sum<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned((kEach + 3) / 4)), dim3(256),
+                     0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool GATED>
+hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
+  if (r.ap == 0) {
+    if (a.m == 1) return run_rows<DT, 1, GATED>(a, s);
+    if (a.m == 2) return run_rows<DT, 2, GATED>(a, s);
+    if (a.m <= 4) return run_rows<DT, 4, GATED>(a, s);
+    if (a.m <= 8) return run_rows<DT, 8, GATED>(a, s);
+    return run_rows<DT, 16, GATED>(a, s);
+  }
+  // x where it lies if its rows are 16-byte pieces of whole steps
+  a.packed = a.k % 64 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
+  if (a.packed) {
+    hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((a.m + 15) / 16), unsigned((a.steps64 + 3) / 4)), dim3(256), 0, s, a.x,
+                       a.ldx, a.m, a.k, a.steps64, ws);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.xt = ws;
+    a.x_panel = int64_t(a.steps64) * 2048;
+    a.x_row = 16;
+    a.x_unit = 256;
+    a.x_step = 2048;
+    a.x_half = 1024;
+  } else {
+    a.xt = reinterpret_cast<const char*>(a.x);
+    a.x_row = a.ldx * 2;
+    a.x_panel = 16 * a.x_row;
+    a.x_unit = 16;
+    a.x_step = 128;
+    a.x_half = 64;
+  }
+  a.parts = r.parts;
+  a.ws = reinterpret_cast<f32x4_t*>(ws + q4_pack_bytes(r, a.k, a.m));
+  if (r.ap == 8 && r.bp == 2) return run_tile<DT, GATED, 8, 2, 4, 1>(a, s);
+  if (r.ap == 8) return run_tile<DT, GATED, 8, 4, 4, 1>(a, s);
+  if (r.bp == 8) return run_tile<DT, GATED, 16, 8, 4, 2>(a, s);
+  return run_tile<DT, GATED, 16, 16, 2, 4>(a, s);
+}
+
+Q4Weight weight_of(const hyb_q4& w, int64_t n, int64_t k) {
+  const char* scales = static_cast<const char*>(w.scales);
+  return Q4Weight{static_cast<const char*>(w.codes), scales,
+                  reinterpret_cast<const uint8_t*>(scales) + q4_quads(k) * q4_rows16(n) * 16};
+}
+
+}  // namespace
+
+hipError_t launch_q4_quantize(const void* a, int dtype, int64_t n, int64_t k, int64_t lda, const hyb_q4& dst,
+                              hipStream_t s) {
+  const int64_t rows16 = q4_rows16(n);
+  const int32_t steps = int32_t(q4_steps(k));
+  const dim3 grid(unsigned(rows16 / 16));
+  char* codes = static_cast<char*>(dst.codes);
+  char* scales = static_cast<char*>(dst.scales);
+  if (dtype == HYB_F32)
+    hipLaunchKernelGGL((k_q4_quantize<HYB_F32>), grid, dim3(256), 0, s, a, n, int32_t(k), lda, steps, rows16, codes, scales);
+  else if (dtype == HYB_BF16)
+    hipLaunchKernelGGL((k_q4_quantize<HYB_BF16>), grid, dim3(256), 0, s, a, n, int32_t(k), lda, steps, rows16, codes, scales);
+  else
+    hipLaunchKernelGGL((k_q4_quantize<HYB_F16>), grid, dim3(256), 0, s, a, n, int32_t(k), lda, steps, rows16, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a, int dtype, int64_t lda,
+                                hipStream_t s) {
+  const int64_t rows16 = q4_rows16(n);
+  const int32_t steps = int32_t(q4_steps(k));
+  const dim3 grid(unsigned(rows16 / 16), unsigned((steps + 3) / 4));
+  const char* codes = static_cast<const char*>(src.codes);
+  const char* scales = static_cast<const char*>(src.scales);
+  if (dtype == HYB_F32)
+    hipLaunchKernelGGL((k_q4_dequantize<HYB_F32>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+  else if (dtype == HYB_BF16)
+    hipLaunchKernelGGL((k_q4_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+  else
+    hipLaunchKernelGGL((k_q4_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_product(const hyb_q4& w, const hyb_q4* up, int act, int64_t n, int64_t k, const void* x,
+                             int x_dtype, int64_t m, int64_t ldx, void* y, int y_dtype, int64_t ldy, char* ws,
+                             hipStream_t s) {
+  Q4Args a{};
+  a.rows16 = q4_rows16(n);
+  a.steps = int32_t(q4_steps(k));
+  a.steps64 = int32_t((k + 63) / 64);
+  a.n = int32_t(n);
+  a.k = int32_t(k);
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.m = m;
+  a.y = y;
+  a.ldy = ldy;
+  a.ydt = y_dtype;
+  a.act = act;
+  if (k == 0) {
+    hipLaunchKernelGGL(k_q4_zero, dim3(unsigned((n + 255) / 256), unsigned(m < 65535 ? m : 65535)), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  a.w[0] = weight_of(w, n, k);
+  if (up) a.w[1] = weight_of(*up, n, k);
+  const Q4Route r = q4_route(n, k, m, up ? 2 : 1, device_cus());
+  if (x_dtype == HYB_BF16)
+    return up ? run_product<HYB_BF16, true>(a, r, ws, s) : run_product<HYB_BF16, false>(a, r, ws, s);
+  return up ? run_product<HYB_F16, true>(a, r, ws, s) : run_product<HYB_F16, false>(a, r, ws, s);
+}
+
+}  // namespace hyb

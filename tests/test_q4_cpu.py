@@ -1,0 +1,152 @@
+"""4-bit weights without a GPU: the oracle's own pins, the C ABI's sizes and
+refusals (include/hyb_q4.h), and the binding's checks.  Every call below fails
+validation or does host work only."""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from matmul_pack_b1_amd import binding as hb
+from matmul_pack_b1_amd import q4
+from oracle import q4_oracle as qo
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_oracle_rounds_to_the_nearest_code():
+    rng = np.random.default_rng(0)
+    v = np.clip(rng.standard_normal(5000) * 3, -7, 7)
+    c = qo.encode(v)
+    got = qo.GRID[c & 7] * np.where(c & 8, -1, 1)
+    best = np.abs(qo.GRID[None] - np.abs(v)[:, None]).min(axis=1)
+    assert np.array_equal(np.abs(np.abs(got) - np.abs(v)), best)
+    halves = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -5.0, 0.0, -0.0])
+    assert qo.encode(halves).tolist() == [0, 2, 2, 4, 4, 6, 6, 8, 14, 0, 8]
+
+
+@pytest.mark.parametrize("top,byte", [(0.0, 127), (7.0, 127), (7.0001, 128), (3.5, 126), (3.6, 127), (6.0, 127),
+                                      (np.inf, 255), (np.nan, 255), (2.0 ** -149, 2), (3.4e38, 252)])
+def test_oracle_scale(top, byte):
+    codes, scale = qo.quantise(np.array([[0.0, top]]))
+    assert scale[0, 0] == byte
+    if np.isfinite(top):
+        v = qo.values(codes, scale)[0, 1]
+        # half the spacing of the codes' top binade, or of the smallest code
+        assert abs(v - top) <= 2.0 ** (byte - 127) or byte == 252
+
+
+def test_exports_match_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "hyb_q4.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(hyb_[a-z0-9_]+)\s*\(", text))
+    assert names == set(q4.EXPORTED)
+    out = subprocess.run(["nm", "-D", "--defined-only", hb.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (hyb_\w+)", out))
+
+
+@pytest.mark.parametrize("n,k", [(0, 0), (0, 5), (5, 0), (1, 1), (16, 128), (17, 129), (300, 513), (2 ** 20, 8192)])
+def test_sizes(n, k):
+    rows16, steps = -(-n // 16) * 16, -(-k // 128)
+    want = (rows16 * steps * 64, rows16 * (-(-steps // 4) * 16 + 1)) if n and k else (0, 0)
+    assert q4.sizes(n, k) == want
+    if 0 < n <= 300 and k:
+        cb, sb = qo.buffers(np.zeros((n, k)))
+        assert (cb.size, sb.size) == want
+
+
+def _status(call):
+    with pytest.raises(hb.HybError) as e:
+        hb.check(call, "call")
+    return e.value.status
+
+
+P16 = 1 << 20  # any 16-byte aligned non-null address: never followed
+
+
+def _m(codes=P16, scales=P16):
+    return ctypes.byref(q4.HybQ4(codes, scales))
+
+
+def test_size_refusals():
+    n = ctypes.c_size_t(0)
+    L = q4.lib()
+    assert _status(L.hyb_q4_size(-1, 8, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_size(8, -1, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_size(8, (1 << 22) + 1, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_size(1 << 27, 8, ctypes.byref(n), ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_size(8, 8, None, ctypes.byref(n))) == 1
+    assert _status(L.hyb_q4_gemm_workspace_size(8, 8, -1, ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_gemm_workspace_size(8, 8, (1 << 22) + 1, ctypes.byref(n))) == 2
+    assert _status(L.hyb_q4_gemm_workspace_size(8, 8, 1, None)) == 1
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(dtype=7), 3), (dict(n=-1), 2), (dict(k=-3), 2), (dict(a=None), 1), (dict(a=P16 + 1), 1), (dict(lda=7), 1),
+    (dict(lda=-8), 1), (dict(lda=(1 << 31) + 1), 4), (dict(codes=None), 1), (dict(scales=None), 1),
+    (dict(codes=P16 + 8), 1), (dict(scales=P16 + 4), 1),
+])
+def test_quantise_refusals(args, status):
+    d = dict(a=P16, dtype=hb.HYB_BF16, n=4, k=8, lda=8, codes=P16, scales=P16)
+    d.update(args)
+    L = q4.lib()
+    dst = _m(d["codes"], d["scales"])
+    assert _status(L.hyb_q4_quantize(d["a"], d["dtype"], d["n"], d["k"], d["lda"], dst, None)) == status
+    assert _status(L.hyb_q4_dequantize(dst, d["n"], d["k"], d["a"], d["dtype"], d["lda"], None)) == status
+    assert hb.last_error()
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(dt=hb.HYB_F32), 3), (dict(dt=0), 3), (dict(y_dtype=0), 3), (dict(n=-1), 2), (dict(k=(1 << 22) + 1), 2),
+    (dict(m=-1), 2), (dict(m=(1 << 22) + 1), 2), (dict(x=None), 1), (dict(x=P16 + 1), 1), (dict(ldx=255), 1),
+    (dict(y=None), 1), (dict(y=P16 + 2), 1), (dict(ldy=7), 1), (dict(w=(None, P16)), 1), (dict(w=(P16, None)), 1),
+    (dict(w=(P16 + 1, P16)), 1), (dict(m=40, ws=None), 1), (dict(m=40, ws=P16 + 8), 1), (dict(m=40, nbytes=100), 1),
+    (dict(n=2 ** 27 - 16, m=2 ** 22, ldy=2 ** 31, nbytes=1 << 62), 4),
+])
+def test_gemm_refusals(args, status):
+    d = dict(w=(P16, P16), n=8, k=256, x=P16, dt=hb.HYB_BF16, m=2, ldx=256, y=P16, y_dtype=hb.HYB_F32, ldy=8, ws=P16,
+             nbytes=1 << 30)
+    d.update(args)
+    st = q4.lib().hyb_q4_gemm(_m(*d["w"]), d["n"], d["k"], d["x"], d["dt"], d["m"], d["ldx"], d["y"], d["y_dtype"],
+                              d["ldy"], d["ws"], d["nbytes"], None)
+    assert _status(st) == status
+
+
+def test_empty_calls_do_nothing():
+    L = q4.lib()
+    assert L.hyb_q4_gemm(None, 8, 8, None, hb.HYB_BF16, 0, 8, None, hb.HYB_F32, 8, None, 0, None) == 0
+    assert L.hyb_q4_gemm(None, 0, 8, None, hb.HYB_BF16, 4, 8, None, hb.HYB_F32, 0, None, 0, None) == 0
+    assert L.hyb_q4_quantize(None, hb.HYB_F32, 0, 8, 8, None, None) == 0
+    assert L.hyb_q4_quantize(None, hb.HYB_F32, 8, 0, 0, None, None) == 0
+    assert L.hyb_q4_dequantize(None, 8, 0, None, hb.HYB_F32, 0, None) == 0
+
+
+def _fake(n, k, dtype=torch.bfloat16):
+    nc, ns = q4.sizes(n, k)
+    return q4.Q4Matrix((n, k), dtype, torch.empty(nc, dtype=torch.uint8), torch.empty(ns, dtype=torch.uint8))
+
+
+def test_binding_refusals():
+    w = torch.zeros(8, 256, dtype=torch.bfloat16)
+    for call, err in [
+        (lambda: q4.pack(w.double()), TypeError), (lambda: q4.pack(w[0]), ValueError),
+        (lambda: q4.pack(w.t()), ValueError), (lambda: q4.pack(w), ValueError),              # not on a GPU
+        (lambda: q4.pack(w, out=_fake(8, 128)), ValueError), (lambda: q4.pack(w, out=w), TypeError),
+        (lambda: q4.unpack(w), TypeError), (lambda: q4.unpack(_fake(2, 3), out_dtype=torch.int8), TypeError),
+        (lambda: q4.gemm(w, w), TypeError), (lambda: q4.gemm(_fake(8, 128), w), ValueError),
+        (lambda: q4.gemm(_fake(8, 256), w.float()), TypeError),
+        (lambda: q4.gemm(_fake(8, 256), w, out=torch.zeros(8, 9)), ValueError),
+        (lambda: q4.gemm(_fake(8, 256), w, out_dtype=torch.int32), TypeError),
+    ]:
+        with pytest.raises(err):
+            call()
+    short = _fake(8, 256)
+    short.codes = short.codes[:-1]
+    with pytest.raises(ValueError, match="buffers"):
+        q4.gemm(short, w)
+    signed = _fake(8, 256)
+    signed.scales = signed.scales.view(torch.int8)
+    with pytest.raises(TypeError, match="uint8"):
+        q4.gemm(signed, w)
