@@ -1,0 +1,531 @@
+// Kernels of the gated projection over packed weights (include/hyb_gated.h).
+//
+// Forward: a tile holds the same rows of the gate and the up projection, so
+// that a wavefront ends with G and U of the same outputs in its registers and H
+// leaves without a round trip.  Few tokens take the decode or matrix-core
+// products of hyb.h into the workspace.  Backward: dG and dU as 16-bit panels
+// from one pass over G, U and dH, then dX = dG W_g' + dU W_u' in one product
+// over both (W' transposed on its way out of LDS) and dW = dG^T X, dU^T X.
+#include <type_traits>
+
+#include "hyb_act.h"
+#include "hyb_gated_internal.h"
+#include "hyb_panel.h"
+#include "hyb_xent_internal.h"
+
+namespace hyb {
+namespace {
+
+#define HYB_TRY(call)                      \
+  do {                                     \
+    const hipError_t e_ = (call);          \
+    if (e_ != hipSuccess) return e_;       \
+  } while (0)
+
+// x (m x k, row-major) as panels; rows behind m zero.
+__global__ __launch_bounds__(256) void k_gated_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m,
+                                                      int32_t steps, char* __restrict__ out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t panel = blockIdx.x;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= steps) return;
+  const int64_t row = panel * 16 + (lane & 15);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (row < m) u = *reinterpret_cast<const uint4*>(x + row * ldx + s * 64 + h * 32 + (lane >> 4) * 8);
+    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16) = u;
+  }
+}
+
+struct GatedOut {
+  uint16_t *h, *g, *u;
+  int64_t ldh, ldg, ldu;
+  int32_t m, n;
+  int act;
+};
+
+// H (and G, U) from fp32 G and U in the workspace: four outputs a thread (a
+// packed weight's n is a multiple of 64).
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_act(const float* __restrict__ gu, GatedOut o) {
+  const int64_t tok = blockIdx.y;
+  const int32_t j = (int32_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (j >= o.n) return;
+  const f32x4_t g = *reinterpret_cast<const f32x4_t*>(gu + tok * o.n + j);
+  const f32x4_t u = *reinterpret_cast<const f32x4_t*>(gu + (o.m + tok) * o.n + j);
+  f32x4_t h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = act_value(o.act, g[e]) * u[e];
+  auto put = [&](uint16_t* p, f32x4_t v) {
+    const uint2 r = round16x4<DT>(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<Bytes8*>(p) = Bytes8{{r.x, r.y}};
+  };
+  put(o.h + tok * o.ldh + j, h);
+  if (o.g) {
+    put(o.g + tok * o.ldg + j, g);
+    put(o.u + tok * o.ldu + j, u);
+  }
+}
+
+// AP / 2 panels of each weight x BP panels of tokens.
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, PanelOperand U, PanelOperand X, GatedOut o) {
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, false, false, true, false, true> T;
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  constexpr int kRows = 16 * AP / 2, kOut = T::kA / 2;
+  const int32_t na = (G.rows16 + kRows - 1) / kRows, nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  int32_t ab, bb;
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  f32x4_t acc[T::kA][T::kB];
+  T::run(G, X, ab * (AP / 2), bb * BP, 0, G.steps, gated_smem, acc, false, &U);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wa = wave % WA, wb = wave / WA;
+  const int32_t col0 = (ab * (AP / 2) + wa * kOut) * 16, row0 = (bb * BP + wb * T::kB) * 16;
+  char* lds = gated_smem + wave * (kOut * T::kB * 512);
+  __syncthreads();  // the tile's LDS stages are free
+  auto rows = [&](uint16_t* y, int64_t ld, auto value) {
+    panel_rows16<kOut, T::kB>(
+        lds, lane, lane & 15,
+        [&](int i, int j) {
+          const f32x4_t v = value(i, j);
+          return round16x4<DT>(v[0], v[1], v[2], v[3]);
+        },
+        [&](int r, int c, uint4 v) {
+          const int32_t row = row0 + r, col = col0 + c;
+          if (row < o.m && col < o.n) *reinterpret_cast<Bytes16*>(y + row * ld + col) = Bytes16{{v.x, v.y, v.z, v.w}};
+        });
+  };
+  if (o.g) {
+    rows(o.g, o.ldg, [&](int i, int j) { return acc[i][j]; });
+    rows(o.u, o.ldu, [&](int i, int j) { return acc[i + kOut][j]; });
+  }
+  rows(o.h, o.ldh, [&](int i, int j) {
+    f32x4_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = act_value(o.act, acc[i][j][e]) * acc[i + kOut][j][e];
+    return v;
+  });
+}
+
+// ------------------------------------------------------------ the gradients --
+
+struct GatedGrad {
+  const uint16_t *g, *u, *dh;
+  int64_t ldg, ldu, lddh;
+  int32_t m, n, steps;
+  int act;
+  char* out[2];   // dG, dU panels: tokens x outputs
+  uint32_t* top;  // fp16: bits of the largest finite |dG|, |dU|
+};
+
+// Eight outputs' dG and dU from 16-bit g, u and dh.
+template <int DT>
+__device__ __forceinline__ void gated_grad8(int act, const uint32_t (&g)[4], const uint32_t (&u)[4],
+                                            const uint32_t (&d)[4], float (&dg)[8], float (&du)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int s = 16 * (e & 1);
+    const float dh = widen16<DT>((d[e >> 1] >> s) & 0xFFFFu);
+    float a;
+    const float slope = act_slope(act, widen16<DT>((g[e >> 1] >> s) & 0xFFFFu), &a);
+    dg[e] = dh * widen16<DT>((u[e >> 1] >> s) & 0xFFFFu) * slope;
+    du[e] = dh * a;
+  }
+}
+
+// The power of two that brings a magnitude of these bits to [2^13, 2^14) (1 for
+// zero), and its reciprocal.
+__device__ __forceinline__ float gated_lift(uint32_t top, float* back) {
+  int e = top == 0 ? 0 : 13 + 127 - int(top >> 23);
+  e = e > 100 ? 100 : e < -100 ? -100 : e;
+  *back = __builtin_bit_cast(float, uint32_t(127 - e) << 23);
+  return __builtin_bit_cast(float, uint32_t(127 + e) << 23);
+}
+
+__global__ void k_gated_clear(uint32_t* top) { *top = 0; }
+
+// Largest finite |dG|, |dU| (fp16).
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
+  __shared__ uint32_t tops[4];
+  uint32_t best = 0;
+  const int32_t per = o.n / 8;  // a packed weight's n is a multiple of 64
+  for (int64_t t = blockIdx.y; t < o.m; t += gridDim.y) {
+    const int32_t c = int32_t(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= per) break;
+    const Bytes16 g = *reinterpret_cast<const Bytes16*>(o.g + t * o.ldg + c * 8);
+    const Bytes16 u = *reinterpret_cast<const Bytes16*>(o.u + t * o.ldu + c * 8);
+    const Bytes16 d = *reinterpret_cast<const Bytes16*>(o.dh + t * o.lddh + c * 8);
+    float dg[8], du[8];
+    gated_grad8<DT>(o.act, g.w, u.w, d.w, dg, du);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t a = __builtin_bit_cast(uint32_t, dg[e]) & 0x7FFFFFFFu;
+      const uint32_t b = __builtin_bit_cast(uint32_t, du[e]) & 0x7FFFFFFFu;
+      if (a < 0x7F800000u && a > best) best = a;
+      if (b < 0x7F800000u && b > best) best = b;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t v = __shfl_xor(best, d);
+    best = v > best ? v : best;
+  }
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = best;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 4; ++i) best = tops[i] > best ? tops[i] : best;
+    if (best > 0) atomicMax(o.top, best);  // (the largest, whatever the order)
+  }
+}
+
+// dG and dU as panels, in the column order in which a lane of the dX product
+// holds the rows of a W' that is read transposed (hyb_panel.h): unit u of a half
+// has columns 16 (u / 2) + 4 (u % 2) + {0..3, 8..11}.  Rows behind m are zero.
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  if (s >= o.steps) return;
+  const int64_t panel = blockIdx.x, tok = panel * 16 + (lane & 15);
+  float back;
+  const float lift = DT == HYB_F16 ? gated_lift(*o.top, &back) : 1.f;
+  const int u4 = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+    if (tok < o.m) {
+      const int32_t c = s * 64 + h * 32 + 16 * (u4 >> 1) + 4 * (u4 & 1);
+      uint32_t w[3][4];
+      auto load = [&](const uint16_t* p, uint32_t (&v)[4]) {
+        const Bytes8 lo = *reinterpret_cast<const Bytes8*>(p + c), hi = *reinterpret_cast<const Bytes8*>(p + c + 8);
+        v[0] = lo.w[0];
+        v[1] = lo.w[1];
+        v[2] = hi.w[0];
+        v[3] = hi.w[1];
+      };
+      load(o.g + tok * o.ldg, w[0]);
+      load(o.u + tok * o.ldu, w[1]);
+      load(o.dh + tok * o.lddh, w[2]);
+      float dg[8], du[8];
+      gated_grad8<DT>(o.act, w[0], w[1], w[2], dg, du);
+      a = make_uint4(round16x2<DT>(dg[0] * lift, dg[1] * lift), round16x2<DT>(dg[2] * lift, dg[3] * lift),
+                     round16x2<DT>(dg[4] * lift, dg[5] * lift), round16x2<DT>(dg[6] * lift, dg[7] * lift));
+      b = make_uint4(round16x2<DT>(du[0] * lift, du[1] * lift), round16x2<DT>(du[2] * lift, du[3] * lift),
+                     round16x2<DT>(du[4] * lift, du[5] * lift), round16x2<DT>(du[6] * lift, du[7] * lift));
+    }
+    const int64_t at = (panel * o.steps + s) * kPanelStep + h * 1024 + lane * 16;
+    *reinterpret_cast<uint4*>(o.out[0] + at) = a;
+    *reinterpret_cast<uint4*>(o.out[1] + at) = b;
+  }
+}
+
+struct GatedDx {
+  float* acc;  // parts: [part][row][k] fp32
+  uint16_t* dx;
+  int64_t lddx;
+  int32_t m, k;
+  const uint32_t* top;
+};
+
+// dX[token, column] = sum over the outputs of dG W_g' + dU W_u' (A = W' read
+// transposed, B = the panels).  A part takes the same steps of both.
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_dx(PanelOperand G, PanelOperand U, PanelOperand DG,
+                                                           PanelOperand DU, int32_t steps, int parts, GatedDx o) {
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, false, true> T;
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  const int32_t na = (G.steps * 4 + AP - 1) / AP, nb = (DG.rows16 / 16 + BP - 1) / BP;
+  int32_t ab, bb;
+  const int32_t part = int32_t(blockIdx.y);
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  const int32_t quads = (steps + 3) / 4;  // a part is a whole number of four steps
+  const int32_t s0 = int32_t(int64_t(quads) * part / parts) * 4;
+  const int32_t s1 = part + 1 == parts ? steps : int32_t(int64_t(quads) * (part + 1) / parts) * 4;
+  f32x4_t acc[T::kA][T::kB];
+  T::run(G, DG, ab * AP, bb * BP, s0, s1, gated_smem, acc);
+  __syncthreads();  // the first product's last stages are free
+  T::run(U, DU, ab * AP, bb * BP, s0, s1, gated_smem, acc, true);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wa = wave % WA, wb = wave / WA;
+  const int32_t row0 = (bb * BP + wb * T::kB) * 16, col0 = (ab * AP + wa * T::kA) * 16;
+  if (parts > 1) {
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j) {
+      const int32_t row = row0 + j * 16 + (lane & 15);
+      if (row >= o.m) continue;
+#pragma unroll
+      for (int i = 0; i < T::kA; ++i) {
+        const int32_t col = col0 + i * 16 + (lane >> 4) * 4;
+        if (col < o.k) *reinterpret_cast<f32x4_t*>(o.acc + (int64_t(part) * o.m + row) * o.k + col) = acc[i][j];
+      }
+    }
+    return;
+  }
+  float back = 1.f;
+  if constexpr (DT == HYB_F16) gated_lift(*o.top, &back);
+  __syncthreads();  // the tile's LDS stages are free
+  panel_rows16<T::kA, T::kB>(
+      gated_smem + wave * (T::kA * T::kB * 512), lane, lane & 15,
+      [&](int i, int j) {
+        const f32x4_t v = acc[i][j];
+        return round16x4<DT>(v[0] * back, v[1] * back, v[2] * back, v[3] * back);
+      },
+      [&](int r, int c, uint4 u) {
+        const int32_t row = row0 + r, col = col0 + c;  // a packed weight's k is a multiple of 64
+        if (row < o.m && col < o.k)
+          *reinterpret_cast<Bytes16*>(o.dx + row * o.lddx + col) = Bytes16{{u.x, u.y, u.z, u.w}};
+      });
+}
+
+// dX = the sum of the parts, in order, rounded once.
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_dx_sum(int parts, GatedDx o) {
+  const int64_t tok = blockIdx.x;
+  const int32_t col = (int32_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  if (col >= o.k) return;
+  float back = 1.f;
+  if constexpr (DT == HYB_F16) gated_lift(*o.top, &back);
+  f32x4_t v = *reinterpret_cast<const f32x4_t*>(o.acc + tok * o.k + col);
+#pragma unroll 8
+  for (int p = 1; p < parts; ++p) {
+    const f32x4_t u = *reinterpret_cast<const f32x4_t*>(o.acc + (int64_t(p) * o.m + tok) * o.k + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += u[e];
+  }
+  const uint2 r = round16x4<DT>(v[0] * back, v[1] * back, v[2] * back, v[3] * back);
+  *reinterpret_cast<Bytes8*>(o.dx + tok * o.lddx + col) = Bytes8{{r.x, r.y}};
+}
+
+struct GatedDw {
+  uint16_t* dw[2];
+  int64_t ld[2];
+  int32_t n, k;
+  const uint32_t* top;
+};
+
+// dW[output, column] = sum over the tokens of dG^T X (both read transposed); the
+// grid's second dimension is the weight.
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_dw(PanelOperand X, PanelOperand DG, PanelOperand DU,
+                                                           int32_t steps, GatedDw o) {
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, true> T;
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  const int32_t na = (X.steps * 4 + AP - 1) / AP, nb = (DG.steps * 4 + BP - 1) / BP;
+  int32_t ab, bb;
+  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  const bool second = blockIdx.y != 0;
+  PanelOperand D = DG;
+  if (second) D.data = DU.data;
+  f32x4_t acc[T::kA][T::kB];
+  T::run(X, D, ab * AP, bb * BP, 0, steps, gated_smem, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wa = wave % WA, wb = wave / WA;
+  float back = 1.f;
+  if constexpr (DT == HYB_F16) gated_lift(*o.top, &back);
+  // the panels' columns 4..7 and 8..11 of 16 have changed places
+  const int row16 = (lane & 3) | (lane & 4) << 1 | (lane & 8) >> 1;
+  const int32_t row0 = (bb * BP + wb * T::kB) * 16, col0 = (ab * AP + wa * T::kA) * 16;
+  uint16_t* y = second ? o.dw[1] : o.dw[0];
+  const int64_t ld = second ? o.ld[1] : o.ld[0];
+  __syncthreads();  // the tile's LDS stages are free
+  panel_rows16<T::kA, T::kB>(
+      gated_smem + wave * (T::kA * T::kB * 512), lane, row16,
+      [&](int i, int j) {
+        const f32x4_t v = acc[i][j];
+        return round16x4<DT>(v[0] * back, v[1] * back, v[2] * back, v[3] * back);
+      },
+      [&](int r, int c, uint4 u) {
+        const int32_t row = row0 + r, col = col0 + c;
+        if (row < o.n && col < o.k) *reinterpret_cast<Bytes16*>(y + row * ld + col) = Bytes16{{u.x, u.y, u.z, u.w}};
+      });
+}
+
+// dW of an empty batch.
+__global__ __launch_bounds__(256) void k_gated_zero(uint16_t* __restrict__ dw, int64_t n, int64_t ld, int32_t k) {
+  const int32_t c = int32_t(blockIdx.y) * 256 + threadIdx.x;
+  for (int64_t r = blockIdx.x; r < n; r += gridDim.x)
+    if (c < k) dw[r * ld + c] = 0;
+}
+
+// ----------------------------------------------------------------- launches --
+
+template <typename F>
+hipError_t allow_lds(F* fn, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// A packed weight as a tile operand; its sparse tiles lie expanded at `spare`.
+PanelOperand weight_operand(const hyb_layout& L, const hyb_packed& P, const char* spare) {
+  PanelOperand o{};
+  o.rows16 = int32_t(L.n);
+  o.steps = int32_t(L.k / 64);
+  o.data = static_cast<const char*>(P.dense);
+  o.log_b1 = __builtin_ctz(L.b1);
+  o.log_b2 = __builtin_ctz(L.b2);
+  o.tiles_k = int32_t(L.tiles_k);
+  o.n_dense = int32_t(L.n_dense);
+  o.plain = L.n;
+  o.tidx = P.tidx;
+  if (L.n_sparse > 0) {
+    o.spare = spare;
+    o.spare1 = int32_t(L.tiles_n);
+  }
+  return o;
+}
+
+hipError_t expand_pair(const hyb_gated_pair& w, const GatedPlan& p, char* ws, hipStream_t s, PanelOperand (&out)[2]) {
+  const hyb_layout* L[2] = {w.gate_layout, w.up_layout};
+  const hyb_packed* P[2] = {w.gate, w.up};
+  for (int i = 0; i < 2; ++i) {
+    if (L[i]->n_sparse > 0) HYB_TRY(launch_expand_tiles(*L[i], *P[i], ws + p.w[i], s));
+    out[i] = weight_operand(*L[i], *P[i], ws + p.w[i]);
+  }
+  return hipSuccess;
+}
+
+hipError_t pack_x(const GatedPlan& p, const void* x, int64_t ldx, char* ws, hipStream_t s, PanelOperand* out) {
+  const int32_t steps = int32_t(p.k / 64);
+  *out = PanelOperand{ws + p.x, int32_t(p.m16), steps, nullptr, 0};
+  hipLaunchKernelGGL(k_gated_pack_x, dim3(unsigned(p.m16 / 16), unsigned((steps + 3) / 4)), dim3(256), 0, s,
+                     static_cast<const uint16_t*>(x), ldx, p.m, steps, ws + p.x);
+  return hipGetLastError();
+}
+
+template <int DT, int BP, int WA, int WB>
+hipError_t run_forward_tile(const PanelOperand (&W)[2], const PanelOperand& X, const GatedOut& o, hipStream_t s) {
+  typedef PanelTile<DT, 16, BP, WA, WB, 2, false, false, true, false, true> T;
+  HYB_TRY(allow_lds(&k_gated_tile<DT, 16, BP, WA, WB>, T::kLds));
+  const int64_t na = (W[0].rows16 + 127) / 128, nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  hipLaunchKernelGGL((k_gated_tile<DT, 16, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB), T::kLds, s, W[0],
+                     W[1], X, o);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int64_t ldx,
+                         const GatedForward& f, char* ws, hipStream_t s) {
+  const GatedOut o{static_cast<uint16_t*>(f.h), static_cast<uint16_t*>(f.g), static_cast<uint16_t*>(f.u), f.ldh, f.ldg,
+                   f.ldu, int32_t(p.m), int32_t(p.n), act};
+  if (p.rows) {
+    float* gu = reinterpret_cast<float*>(ws + p.gu);
+    const hyb_layout L[2] = {*w.gate_layout, *w.up_layout};
+    const hyb_packed P[2] = {*w.gate, *w.up};
+    void* const y[2] = {gu, gu + p.m * p.n};
+    const int64_t ldy[2] = {p.n, p.n};
+    if (p.decode) {
+      HYB_TRY(launch_gemv_grouped(2, L, P, x, int(p.m), ldx, y, HYB_F32, ldy, s));
+    } else {
+      for (int i = 0; i < 2; ++i)
+        HYB_TRY(launch_gemm(L[i], P[i], x, int(p.m), ldx, y[i], HYB_F32, p.n, s, ws + p.split, p.split_bytes));
+    }
+    hipLaunchKernelGGL((k_gated_act<DT>), dim3(unsigned((p.n + 1023) / 1024), unsigned(p.m)), dim3(256), 0, s, gu, o);
+    return hipGetLastError();
+  }
+  PanelOperand W[2], X;
+  HYB_TRY(expand_pair(w, p, ws, s, W));
+  HYB_TRY(pack_x(p, x, ldx, ws, s, &X));
+  if (p.bp == 16) return run_forward_tile<DT, 16, 2, 4>(W, X, o, s);
+  return run_forward_tile<DT, 8, 4, 2>(W, X, o, s);
+}
+
+template <int DT, int BP, int WA, int WB>
+hipError_t run_dx(const PanelOperand (&W)[2], const PanelOperand (&D)[2], int parts, const GatedDx& o, hipStream_t s) {
+  typedef PanelTile<DT, 16, BP, WA, WB, 2, true, false, true> T;
+  HYB_TRY(allow_lds(&k_gated_dx<DT, 16, BP, WA, WB>, T::kLds));
+  const int64_t na = (W[0].steps * 4 + 15) / 16, nb = (D[0].rows16 / 16 + BP - 1) / BP;
+  hipLaunchKernelGGL((k_gated_dx<DT, 16, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)), dim3(64 * WA * WB),
+                     T::kLds, s, W[0], W[1], D[0], D[1], D[0].steps, parts, o);
+  return hipGetLastError();
+}
+
+template <int DT, int AP, int BP, int WA, int WB>
+hipError_t run_dw(const PanelOperand& X, const PanelOperand (&D)[2], int32_t steps, const GatedDw& o, hipStream_t s) {
+  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, true> T;
+  HYB_TRY(allow_lds(&k_gated_dw<DT, AP, BP, WA, WB>, T::kLds));
+  const int64_t na = (X.steps * 4 + AP - 1) / AP, nb = (D[0].steps * 4 + BP - 1) / BP;
+  hipLaunchKernelGGL((k_gated_dw<DT, AP, BP, WA, WB>), dim3(unsigned(na * nb), 2), dim3(64 * WA * WB), T::kLds, s, X, D[0],
+                     D[1], steps, o);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int64_t ldx,
+                          const GatedBackward& b, char* ws, hipStream_t s) {
+  uint32_t* top = reinterpret_cast<uint32_t*>(ws + p.misc);
+  GatedGrad g{};
+  g.g = static_cast<const uint16_t*>(b.g);
+  g.u = static_cast<const uint16_t*>(b.u);
+  g.dh = static_cast<const uint16_t*>(b.dh);
+  g.ldg = b.ldg;
+  g.ldu = b.ldu;
+  g.lddh = b.lddh;
+  g.m = int32_t(p.m);
+  g.n = int32_t(p.n);
+  g.steps = int32_t(p.n / 64);
+  g.act = act;
+  g.out[0] = ws + p.g[0];
+  g.out[1] = ws + p.g[1];
+  g.top = top;
+  if (DT == HYB_F16) {
+    hipLaunchKernelGGL(k_gated_clear, dim3(1), dim3(1), 0, s, top);
+    HYB_TRY(hipGetLastError());
+    const unsigned across = unsigned((p.n / 8 + 255) / 256);
+    const int64_t down = 2048 / across + 1;
+    hipLaunchKernelGGL((k_gated_top<DT>), dim3(across, unsigned(p.m < down ? p.m : down)), dim3(256), 0, s, g);
+    HYB_TRY(hipGetLastError());
+  }
+  hipLaunchKernelGGL((k_gated_grad<DT>), dim3(unsigned(p.m16 / 16), unsigned((g.steps + 3) / 4)), dim3(256), 0, s, g);
+  HYB_TRY(hipGetLastError());
+  const PanelOperand D[2] = {PanelOperand{ws + p.g[0], int32_t(p.m16), g.steps, nullptr, 0},
+                             PanelOperand{ws + p.g[1], int32_t(p.m16), g.steps, nullptr, 0}};
+  if (b.dx) {
+    PanelOperand W[2];
+    HYB_TRY(expand_pair(w, p, ws, s, W));
+    const GatedDx o{reinterpret_cast<float*>(ws + p.dx), static_cast<uint16_t*>(b.dx), b.lddx, int32_t(p.m),
+                    int32_t(p.k), top};
+    HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4>(W, D, p.parts, o, s))
+            : p.bp == 8 ? (run_dx<DT, 8, 4, 2>(W, D, p.parts, o, s))
+                        : (run_dx<DT, 4, 4, 2>(W, D, p.parts, o, s)));
+    if (p.parts > 1) {
+      hipLaunchKernelGGL((k_gated_dx_sum<DT>), dim3(unsigned(p.m), unsigned((p.k + 1023) / 1024)), dim3(256), 0, s,
+                         p.parts, o);
+      HYB_TRY(hipGetLastError());
+    }
+  }
+  if (b.dw[0]) {
+    PanelOperand X;
+    HYB_TRY(pack_x(p, x, ldx, ws, s, &X));
+    const GatedDw o{{static_cast<uint16_t*>(b.dw[0]), static_cast<uint16_t*>(b.dw[1])}, {b.lddw[0], b.lddw[1]},
+                    int32_t(p.n), int32_t(p.k), top};
+    const int32_t steps = int32_t(p.m64 / 64);
+    HYB_TRY(p.m <= 256 ? (run_dw<DT, 8, 8, 2, 4>(X, D, steps, o, s)) : (run_dw<DT, 16, 16, 2, 4>(X, D, steps, o, s)));
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_gated(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int dtype, int64_t ldx,
+                        const GatedForward& out, char* ws, hipStream_t s) {
+  return dtype == HYB_BF16 ? forward_typed<HYB_BF16>(w, p, act, x, ldx, out, ws, s)
+                           : forward_typed<HYB_F16>(w, p, act, x, ldx, out, ws, s);
+}
+
+hipError_t launch_gated_backward(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int dtype,
+                                 int64_t ldx, const GatedBackward& b, char* ws, hipStream_t s) {
+  if (p.m == 0) {
+    for (int i = 0; i < 2; ++i) {
+      hipLaunchKernelGGL(k_gated_zero, dim3(unsigned(p.n < 4096 ? p.n : 4096), unsigned((p.k + 255) / 256)), dim3(256), 0,
+                         s, static_cast<uint16_t*>(b.dw[i]), p.n, b.lddw[i], int32_t(p.k));
+      HYB_TRY(hipGetLastError());
+    }
+    return hipSuccess;
+  }
+  return dtype == HYB_BF16 ? backward_typed<HYB_BF16>(w, p, act, x, ldx, b, ws, s)
+                           : backward_typed<HYB_F16>(w, p, act, x, ldx, b, ws, s);
+}
+
+}  // namespace hyb

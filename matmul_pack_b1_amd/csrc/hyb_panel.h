@@ -241,9 +241,11 @@ typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
 // stages of one step each (transfers run STAGES - 1 steps ahead).  TA / TB:
 // that operand is read transposed (its "panels" here are blocks of 16 of its
 // columns).  TILED: A lies in tiles (PanelOperand).  CODES: A is an 8-bit weight
-// read transposed by a 16-bit product.
+// read transposed by a 16-bit product.  PAIR: two operands in tiles, of one
+// shape; the tile's A panels are AP / 2 of each, and a wavefront's first kA / 2
+// are the first operand's, its others the same rows of the second.
 template <int KIND, int AP, int BP, int WA, int WB, int STAGES = 2, bool TA = false, bool TB = false, bool TILED = false,
-          bool CODES = false>
+          bool CODES = false, bool PAIR = false>
 struct PanelTile {
   static_assert(STAGES == 2 || STAGES == 4, "a step's stage is an immediate of the loop unrolled by four");
   static constexpr int kWaves = WA * WB;
@@ -255,6 +257,12 @@ struct PanelTile {
   static constexpr int kLoadsA = (CODES ? AP : AP * 2) / kWaves, kLoadsB = BP * 2 / kWaves;  // 1 KiB transfers per wavefront and step
   static_assert(AP % WA == 0 && BP % WB == 0 && AP * 2 % kWaves == 0 && BP * 2 % kWaves == 0, "even split");
   static_assert(!(TA || TB) || !is_f8(KIND), "8-bit operands are read straight");
+  static_assert(!PAIR || (TILED && !TA && !CODES && kA % 2 == 0), "pairs are read straight");
+  // Panel i of wavefront column wa in the tile's order.
+  __device__ __forceinline__ static int panel_of(int wa, int i) {
+    if constexpr (PAIR) return i < kA / 2 ? wa * (kA / 2) + i : AP / 2 + wa * (kA / 2) + i - kA / 2;
+    return wa * kA + i;
+  }
 
   // One operand's transfers of step s into its part of a stage.
   // (prepare() sets up a step, put() issues one of a wavefront's transfers.)
@@ -318,7 +326,7 @@ struct PanelTile {
     __device__ TiledFeed(const PanelOperand& op, int32_t p0, int wave)
         : o(op), first(-64), slot0(-1), slot1(-1), now(-1), at0(nullptr), at1(nullptr) {
       static_assert(LOADS == 4 && P == 16, "eight wavefronts, 256 rows or columns");
-      unit = T ? p0 / 4 + (wave & 1) * 2 : (p0 + wave * 2) * 16;
+      unit = T ? p0 / 4 + (wave & 1) * 2 : (p0 + (PAIR ? wave % (kWaves / 2) : wave) * 2) * 16;
     }
     // Address of tile (tn, tk) of the operand, or NULL.
     __device__ __forceinline__ const char* tile_at(int32_t tn, int32_t tk, int32_t slot) const {
@@ -481,10 +489,13 @@ struct PanelTile {
   // Sums of steps [s0, s1), s0 a multiple of four, of A panels pa.. and B
   // panels pb..; wavefront (wa, wb) ends with acc[i][j] of its panels
   // pa + wa kA + i, pb + wb kB + j (lane L: A rows 4 (L/16) + 0..3, B row L%16).
-  __device__ static void run(const PanelOperand& A, const PanelOperand& B, int32_t pa, int32_t pb, int32_t s0,
-                             int32_t s1, char* smem, f32x4_t (&acc)[kA][kB]) {
+  // With `add` they add to what acc holds.  A pair's second operand is *A2.
+  __device__ static void run(const PanelOperand& A1, const PanelOperand& B, int32_t pa, int32_t pb, int32_t s0,
+                             int32_t s1, char* smem, f32x4_t (&acc)[kA][kB], bool add = false,
+                             const PanelOperand* A2 = nullptr) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const PanelOperand A = PAIR && wave >= kWaves / 2 ? *A2 : A1;
     const int wa = wave % WA, wb = wave / WA;
     auto fa = [&] {
       if constexpr (CODES)
@@ -532,10 +543,12 @@ struct PanelTile {
       }
     };
 
+    if (!add) {
 #pragma unroll
-    for (int i = 0; i < kA; ++i)
+      for (int i = 0; i < kA; ++i)
 #pragma unroll
-      for (int j = 0; j < kB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < kB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
 
     uint32_t sca[kA], scb[kB];
 #pragma unroll
@@ -597,7 +610,7 @@ struct PanelTile {
       }
       auto read_a = [&](int i) {
         if constexpr (CODES) return read_codes(src, wa * kA + i, codes_off);
-        else return read<TA, AP>(src, wa * kA + i, straight, ta0, ta1);
+        else return read<TA, AP>(src, panel_of(wa, i), straight, ta0, ta1);
       };
       // Rows behind the last that counts: their codes, whatever they are, zero.
       auto mask_codes = [&](Halves& c) {

@@ -905,6 +905,15 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
 
 }  // namespace
 
+hipError_t launch_expand_tiles(const hyb_layout& L, const hyb_packed& P, char* out, hipStream_t s) {
+  const int32_t steps = int32_t(L.k / 64);
+  hipLaunchKernelGGL(k_xent_expand, dim3(unsigned(L.n / 16), unsigned((steps + 3) / 4)), dim3(256), 0, s,
+                     static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
+                     static_cast<const uint16_t*>(P.meta), P.tidx, L.b1, L.b2, L.meta, int32_t(L.tiles_k),
+                     int32_t(L.n_dense), int32_t(L.n_sparse), int64_t(0), L.n, L.n, steps, out);
+  return hipGetLastError();
+}
+
 hipError_t launch_xent(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype, int64_t ldx,
                        const int64_t* target, int64_t ignore, float* loss, float* lse, char* ws, hipStream_t s) {
   XentTile t{};
