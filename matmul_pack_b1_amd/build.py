@@ -22,7 +22,8 @@ SOURCES = ["hyb_api.cpp", "hyb_route.cpp", "hyb_pack.hip", "hyb_gemv.hip", "hyb_
            "hyb_f8_api.cpp", "hyb_f8_route.cpp", "hyb_f8.hip",
            "hyb_xent_api.cpp", "hyb_xent_plan.cpp", "hyb_xent.hip",
            "hyb_q4_api.cpp", "hyb_q4_route.cpp", "hyb_q4.hip",
-           "hyb_gated_api.cpp", "hyb_gated_plan.cpp", "hyb_gated.hip"]
+           "hyb_gated_api.cpp", "hyb_gated_plan.cpp", "hyb_gated.hip",
+           "hyb_clip_api.cpp", "hyb_clip.hip"]
 ARCH = os.environ.get("HYB_ARCH", "gfx950")
 
 

@@ -1,0 +1,107 @@
+"""The norm and the clipping without a GPU: the C ABI's refusals
+(include/hyb_clip.h) and workspace sizes, and the binding's checks.  Every call
+below fails validation or does host work only."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from matmul_pack_b1_amd import binding as hb
+from matmul_pack_b1_amd import clip
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P16 = 1 << 20  # any aligned non-null address: never followed
+
+
+def test_exports_match_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "hyb_clip.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(hyb_[a-z0-9_]+)\s*\(", text))
+    assert names == set(clip.EXPORTED)
+    out = subprocess.run(["nm", "-D", "--defined-only", hb.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (hyb_\w+)", out))
+
+
+def _status(call):
+    with pytest.raises(hb.HybError) as e:
+        hb.check(call, "call")
+    return e.value.status
+
+
+def tensor(data=P16, out=2 * P16, rows=4, cols=8, lda=8, ldo=8, dtype=hb.HYB_F32):
+    return clip.HybTensor(data, out, rows, cols, lda, ldo, dtype)
+
+
+def array(*ts):
+    return (clip.HybTensor * max(len(ts), 1))(*ts)
+
+
+def call_clip(ts, max_norm=1.0, norm=64, ws=P16 // 2, nbytes=1 << 20, count=None):
+    return clip.lib().hyb_clip(len(ts) if count is None else count, array(*ts), max_norm, norm, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(dtype=0), 3), (dict(dtype=4), 3), (dict(rows=-1), 2), (dict(cols=-1), 2), (dict(rows=1 << 21, cols=1 << 20), 2),
+    (dict(cols=(1 << 40) + 1), 2), (dict(lda=7), 1), (dict(ldo=7), 1), (dict(ldo=-9), 1), (dict(lda=(1 << 40) + 1), 1),
+    (dict(data=None), 1), (dict(out=None), 1), (dict(data=P16 + 2), 1), (dict(out=P16 + 1), 1),
+    (dict(out=P16 + 16), 1), (dict(out=P16 - 16), 1), (dict(out=P16, ldo=9), 1), (dict(data=32), 1), (dict(out=60), 1),
+])
+def test_refused_tensors(args, status):
+    assert _status(call_clip([tensor(data=16 * P16, out=17 * P16), tensor(**args)])) == status
+    assert hb.last_error()
+
+
+def test_refused_calls():
+    t = tensor()
+    assert _status(call_clip([t], count=-1)) == 2
+    assert _status(clip.lib().hyb_clip(1, None, 1.0, 64, P16, 1 << 20, None)) == 1
+    for max_norm in (-1.0, float("nan")):
+        assert _status(call_clip([t], max_norm=max_norm)) == 1
+    for norm in (None, 66):
+        assert _status(call_clip([t], norm=norm)) == 1
+        assert _status(clip.lib().hyb_norm(1, array(t), norm, P16, 1 << 20, None)) == 1
+    for more in (dict(ws=None), dict(ws=P16 + 8), dict(nbytes=7)):
+        assert _status(call_clip([t], **more)) == 1
+    assert _status(clip.lib().hyb_norm(1, array(t), P16 + 4, P16, 1 << 20, None)) == 1      # norm inside the data
+    n = ctypes.c_size_t(0)
+    assert _status(clip.lib().hyb_clip_workspace_size(1, array(t), None)) == 1
+    assert _status(clip.lib().hyb_clip_workspace_size(-1, None, ctypes.byref(n))) == 2
+
+
+def test_overlaps():
+    a, b, c = (i * P16 for i in (4, 5, 6))
+    # the same output twice, an output in another's data, the same data in place twice
+    for ts in ([tensor(a, c), tensor(b, c)], [tensor(a, b), tensor(b, c)], [tensor(a, a), tensor(a, a)],
+               [tensor(a, a), tensor(a, c)], [tensor(a, c), tensor(b, c + 64)],
+               [tensor(a, c, rows=3, lda=100, ldo=100), tensor(b, c + 420, rows=1, cols=2)]):
+        assert _status(call_clip(ts)) == 1
+        assert "overlap" in hb.last_error()
+
+
+def test_workspace_sizes():
+    n = ctypes.c_size_t(0)
+
+    def need(*ts):
+        assert clip.lib().hyb_clip_workspace_size(len(ts), array(*ts), ctypes.byref(n)) == 0
+        return n.value
+    assert need() == 0 and need(tensor(rows=0), tensor(cols=0)) == 0
+    assert need(tensor()) == 8
+    assert need(tensor(rows=1, cols=16385)) == 16
+    assert need(tensor(rows=3, cols=8, lda=9, ldo=9)) == 24         # a chunk for each row apart
+    assert need(tensor(rows=1, cols=1 << 30)) == 2048 * 8
+    assert need(*[tensor()] * 65) == 65 * 8
+
+
+def test_binding_refusals():
+    t = torch.zeros(4, 8)
+    for call, err in [
+        (lambda: clip.norm([t.double()]), TypeError), (lambda: clip.norm([t.t()]), ValueError),
+        (lambda: clip.norm([1.0]), TypeError), (lambda: clip.norm([t]), ValueError),            # not on a GPU
+        (lambda: clip.norm([t.view(2, 2, 8)[:, :1]]), ValueError), (lambda: clip.clip([t], 1.0, outs=[]), ValueError),
+        (lambda: clip.clip([t], 1.0, outs=[t.half()]), TypeError), (lambda: clip.clip([t], 1.0, outs=[t[:2]]), ValueError),
+        (lambda: clip.clip([t], 1.0, outs=[t.t().contiguous().t()]), ValueError),
+    ]:
+        with pytest.raises(err):
+            call()
