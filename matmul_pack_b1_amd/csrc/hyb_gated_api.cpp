@@ -165,7 +165,7 @@ hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == 0) {
-    if (k > 0 && hyb::q4_tiles(hyb::q4_route(n, k, m, 2, hyb::device_cus()), n, m, 2) >= hyb::kQ4MaxTiles)
+    if (k > 0 && hyb::q4_groups(hyb::q4_route(n, k, m, 2, hyb::device_cus()), n, m, 2) >= hyb::kQ4MaxTiles)
       return fail(HYB_ERR_UNSUPPORTED, "n x m = %lld x %d is too large for one launch", (long long)n, m);
     return hyb::hip_status(
         hyb::launch_q4_product(*w->gate4, w->up4, act, n, k, x, x_dtype, m, ldx, h, x_dtype, ldh, ws, s),

@@ -221,13 +221,16 @@ struct Q4Args {
   void* y;
   int64_t ldy;
   int ydt, act;
-  // tiles: activations as they are (pitch: bytes from a row to the next, `step`:
-  // to a row's next 64 columns, `half`: to its next 32), or as panels
+  // more than a few tokens: the activations as they lie, or as panels: bytes from
+  // a panel of 16 to the next, from a row to the next, from a row's 8 columns to
+  // the next, 64 columns and 32 columns on
   const char* xt;
   int64_t x_panel, x_row, x_unit;
   int32_t x_step, x_half, packed, steps64;
+  // tiles that run over all of k, and the parts each of the others is cut into,
+  // whose sums are left in `ws`
   f32x4_t* ws;
-  int32_t parts;
+  int32_t whole, parts;
 };
 
 // fp16 operands carry a row's values divided by 2^(top - 139): at most 6 * 2^12,
@@ -388,7 +391,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
 }
 
 // Activations as panels (hyb_panel.h; rows behind m and columns behind k zero),
-// for tiles whose x is not in 16-byte pieces of whole 64-column steps.
+// for an x whose rows are not whole 16-byte pieces.
 __global__ __launch_bounds__(256) void k_q4_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m, int32_t k,
                                                    int32_t steps64, char* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -443,6 +446,144 @@ __device__ __forceinline__ f32x4_t q4_finish(const Q4Args& a, int64_t j0, f32x4_
     for (int e = 0; e < 4; ++e) v[e] = act_value(a.act, v[e]) * u[e];
   }
   return v;
+}
+
+// Up to 64 tokens: eight panels (of each weight) per workgroup, one per
+// wavefront, whose codes go from memory to its registers; the 16 BP tokens'
+// activations, 512 columns at a time, come through LDS for all eight.  The k of a
+// workgroup's panels may be cut into parts, a workgroup each.
+template <int DT, bool GATED, int BP>
+__global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
+  constexpr int P = GATED ? 2 : 1;
+  constexpr int kX = BP * 16384;       // 512 columns
+  constexpr int kLoads = BP * 16 / 8;  // 1 KiB transfers per wavefront
+  extern __shared__ __attribute__((aligned(1024))) char q4_smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t part = int32_t(blockIdx.y);
+  const int32_t quads = (a.steps + 3) / 4;
+  const int32_t q0 = int32_t(int64_t(quads) * part / a.parts), q1 = int32_t(int64_t(quads) * (part + 1) / a.parts);
+  const int64_t panels = a.rows16 / 16, mine = int64_t(blockIdx.x) * 8 + wave;
+  // (a wavefront behind the last panel multiplies the last one again)
+  const int64_t panel = mine < panels ? mine : panels - 1;
+  const int64_t row = panel * 16 + (lane & 15);
+
+  __amdgpu_buffer_rsrc_t code_rsrc[P];
+  const char* scale_at[P];
+  int lift[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    code_rsrc[p] = make_rsrc(a.w[p].codes + panel * a.steps * kQ4StepBytes, a.steps * int32_t(kQ4StepBytes));
+    scale_at[p] = a.w[p].scales + row * 16;
+    lift[p] = DT == HYB_F16 ? kTopLift - int(a.w[p].tops[row]) : 0;
+  }
+  // x: chunk c of a quad is half c % 2 of 64-column step c / 2 % 8 of token
+  // panel c / 16
+  const uint32_t base = __builtin_amdgcn_readfirstlane(panel_lds_addr(q4_smem));
+  const int64_t tok_panels = (a.m + 15) / 16;
+  const srd4_t xr = panel_srd(a.xt, uint32_t(a.packed ? tok_panels * a.x_panel : (a.m - 1) * a.x_row + int64_t(a.k) * 2));
+  auto issue_x = [&](int32_t q) {
+    const uint32_t dst = base + (q & 1) * kX;
+#pragma unroll
+    for (int t = 0; t < kLoads; ++t) {
+      const int c = wave * kLoads + t;
+      const int32_t s = q * 8 + (c >> 1) % 8;
+      int32_t off = int32_t((c >> 4) * a.x_panel + (lane & 15) * a.x_row + (lane >> 4) * a.x_unit) + s * a.x_step +
+                    (c & 1) * a.x_half;
+      // columns from k on read as zeros
+      if (a.packed ? s >= a.steps64 : s * 64 + (c & 1) * 32 + (lane >> 4) * 8 >= a.k) off = 0x7FFFFFF0;
+      panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + c * 1024), off);
+    }
+  };
+  uint4 code[2][P][4], scale[2][P];
+  auto load_w = [&](int32_t q, uint4 (&c)[P][4], uint4 (&sc)[P]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)  // (steps behind the last lie behind the resource: zeros)
+        c[p][s] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], (q * 4 + s) * 1024 + lane * 16, 0, HYB_W_AUX));
+    }
+  };
+  f32x4_t acc[P][BP];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int j = 0; j < BP; ++j) acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](int32_t q, auto buf) {
+    constexpr int B = decltype(buf)::value;
+    panel_wait<0>();
+    __syncthreads();
+    if (q + 1 < q1) {
+      issue_x(q + 1);
+      load_w(q + 1, code[1 - B], scale[1 - B]);
+    }
+    const char* xs = q4_smem + (q & 1) * kX + lane * 16;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint4 b[BP];
+#pragma unroll
+        for (int j = 0; j < BP; ++j) b[j] = *reinterpret_cast<const uint4*>(xs + j * 16384 + s * 4096 + h * 1024);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint4 cw = code[B][p][s];
+          const uint32_t c = h == 0 ? cw.x : h == 1 ? cw.y : h == 2 ? cw.z : cw.w;
+          const uint32_t sw = s == 0 ? scale[B][p].x : s == 1 ? scale[B][p].y : s == 2 ? scale[B][p].z : scale[B][p].w;
+          const uint4 w = widen_codes4<DT>(c, group_scale<DT>(sw, h, lift[p]));
+#pragma unroll
+          for (int j = 0; j < BP; ++j) acc[p][j] = mfma16x16x32<DT>(w, b[j], acc[p][j]);
+        }
+      }
+    }
+  };
+  if (q0 < q1) {
+    issue_x(q0);
+    load_w(q0, code[0], scale[0]);
+  }
+  for (int32_t q = q0; q < q1; q += 2) {
+    step(q, std::integral_constant<int, 0>());
+    if (q + 1 < q1) step(q + 1, std::integral_constant<int, 1>());
+  }
+  if (a.parts > 1) {
+    f32x4_t* out = a.ws + ((int64_t(blockIdx.x) * a.parts + part) * 8 + wave) * (P * BP * 64) + lane;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int j = 0; j < BP; ++j) out[(p * BP + j) * 64] = acc[p][j];
+    return;
+  }
+  if (mine >= panels) return;
+  const int64_t j0 = panel * 16 + (lane >> 4) * 4;
+#pragma unroll
+  for (int j = 0; j < BP; ++j)
+    q4_store4(a, j * 16 + (lane & 15), j0, q4_finish<DT, GATED>(a, j0, acc[0][j], acc[P - 1][j]));
+}
+
+// Adds the parts of k_q4_shared in order: one thread per four outputs.
+template <int DT, bool GATED, int BP>
+__global__ __launch_bounds__(256) void k_q4_shared_sum(Q4Args a) {
+  constexpr int P = GATED ? 2 : 1;
+  const int lane = threadIdx.x & 63;
+  const int c = int(blockIdx.y) * 4 + (threadIdx.x >> 6), wave = c / BP, j = c % BP;
+  const int64_t j0 = (int64_t(blockIdx.x) * 8 + wave) * 16 + (lane >> 4) * 4, tok = j * 16 + (lane & 15);
+  if (tok >= a.m || j0 >= a.n) return;
+  f32x4_t v[2];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const f32x4_t* at = a.ws + (int64_t(blockIdx.x) * a.parts * 8 + wave) * (P * BP * 64) + (p * BP + j) * 64 + lane;
+    f32x4_t sum = at[0];
+#pragma unroll 4
+    for (int t = 1; t < a.parts; ++t) {
+      const f32x4_t o = at[int64_t(t) * 8 * (P * BP * 64)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += o[e];
+    }
+    v[p] = sum;
+  }
+  q4_store4(a, tok, j0, q4_finish<DT, GATED>(a, j0, v[0], v[P - 1]));
 }
 
 // More tokens: AP panels of codes x BP panels of tokens through LDS, WA x WB
@@ -513,7 +654,13 @@ struct Q4Tile {
     auto issue_x = [&](int32_t s) {
       const uint32_t dst = base + kAtX + (s & 1) * kX;
 #pragma unroll
-      for (int t = 0; t < kLoadsX; ++t) panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + (wave * kLoadsX + t) * 1024), xo[t] + s * a.x_step);
+      for (int t = 0; t < kLoadsX; ++t) {
+        const int c = wave * kLoadsX + t;
+        int32_t off = xo[t] + s * a.x_step;
+        // columns from k on read as zeros
+        if (!a.packed && s * 64 + 64 > a.k && s * 64 + (c & 1) * 32 + (lane >> 4) * 8 >= a.k) off = 0x7FFFFFF0;
+        panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + c * 1024), off);
+      }
     };
     // panel i of this wavefront in the tile's order
     auto panel_of = [&](int i) {
@@ -606,16 +753,19 @@ __global__ __launch_bounds__(64 * WA * WB) void k_q4_tile(Q4Args a) {
   extern __shared__ __attribute__((aligned(1024))) char q4_smem[];
   const int32_t na = int32_t((a.rows16 / 16 + T::kPanels - 1) / T::kPanels);
   const int32_t nb = int32_t((a.m + BP * 16 - 1) / (BP * 16));
+  const int32_t id = int32_t(blockIdx.x), rest = id - a.whole;
+  const bool cut = rest >= 0;
+  const int32_t part = cut ? rest % a.parts : 0;
   int32_t ab, bb;
-  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
-  const int32_t part = int32_t(blockIdx.y);
+  panel_block(cut ? a.whole + rest / a.parts : panel_order(id, a.whole), na, nb, ab, bb);
   f32x4_t acc[T::kA][T::kB];
-  T::run(a, ab, bb, q4_part_step(a.steps64, part, a.parts), q4_part_step(a.steps64, part + 1, a.parts), q4_smem, acc);
+  T::run(a, ab, bb, cut ? q4_part_step(a.steps64, part, a.parts) : 0,
+         cut ? q4_part_step(a.steps64, part + 1, a.parts) : a.steps64, q4_smem, acc);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave % WA, wb = wave / WA;
-  if (a.parts > 1) {
-    f32x4_t* out = a.ws + ((int64_t(blockIdx.x) * a.parts + part) * T::kWaves + wave) * (T::kA * T::kB * 64) + lane;
+  if (cut) {
+    f32x4_t* out = a.ws + (int64_t(rest) * T::kWaves + wave) * (T::kA * T::kB * 64) + lane;
 #pragma unroll
     for (int i = 0; i < T::kA; ++i)
 #pragma unroll
@@ -667,7 +817,7 @@ __global__ __launch_bounds__(256) void k_q4_sum(Q4Args a) {
   const int32_t na = int32_t((a.rows16 / 16 + T::kPanels - 1) / T::kPanels);
   const int32_t nb = int32_t((a.m + BP * 16 - 1) / (BP * 16));
   int32_t ab, bb;
-  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  panel_block(a.whole + int32_t(blockIdx.x), na, nb, ab, bb);
   const int lane = threadIdx.x & 63;
   const int c = int(blockIdx.y) * 4 + (threadIdx.x >> 6);
   if (c >= kEach) return;
@@ -718,12 +868,26 @@ hipError_t run_tile(const Q4Args& a, hipStream_t s) {
                                      hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (e != hipSuccess) return e;
   const int64_t na = (a.rows16 / 16 + T::kPanels - 1) / T::kPanels, nb = (a.m + BP * 16 - 1) / (BP * 16);
-  hipLaunchKernelGGL((k_q4_tile<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(a.parts)),
+  const int64_t rest = na * nb - a.whole;
+  hipLaunchKernelGGL((k_q4_tile<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(a.whole + rest * a.parts)),
                      dim3(64 * T::kWaves), T::kLds, s, a);
-  if ((e = hipGetLastError()) != hipSuccess || a.parts <= 1) return e;
+  if ((e = hipGetLastError()) != hipSuccess || rest == 0) return e;
   constexpr int kEach = T::kWaves * T::kOutA * T::kB;
-  hipLaunchKernelGGL((k_q4_sum<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(na * nb), unsigned((kEach + 3) / 4)), dim3(256),
-                     0, s, a);
+  hipLaunchKernelGGL((k_q4_sum<DT, GATED, AP, BP, WA, WB>), dim3(unsigned(rest), unsigned((kEach + 3) / 4)), dim3(256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+
+template <int DT, bool GATED, int BP>
+hipError_t run_shared(const Q4Args& a, hipStream_t s) {
+  constexpr int kLds = 2 * BP * 16384;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_q4_shared<DT, GATED, BP>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  const unsigned blocks = unsigned((a.rows16 / 16 + 7) / 8);
+  hipLaunchKernelGGL((k_q4_shared<DT, GATED, BP>), dim3(blocks, unsigned(a.parts)), dim3(512), kLds, s, a);
+  if ((e = hipGetLastError()) != hipSuccess || a.parts <= 1) return e;
+  hipLaunchKernelGGL((k_q4_shared_sum<DT, GATED, BP>), dim3(blocks, 2 * BP), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -732,12 +896,10 @@ hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
   if (r.ap == 0) {
     if (a.m == 1) return run_rows<DT, 1, GATED>(a, s);
     if (a.m == 2) return run_rows<DT, 2, GATED>(a, s);
-    if (a.m <= 4) return run_rows<DT, 4, GATED>(a, s);
-    if (a.m <= 8) return run_rows<DT, 8, GATED>(a, s);
-    return run_rows<DT, 16, GATED>(a, s);
+    return run_rows<DT, 4, GATED>(a, s);
   }
-  // x where it lies if its rows are 16-byte pieces of whole steps
-  a.packed = a.k % 64 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
+  // x where it lies if its rows are whole 16-byte pieces
+  a.packed = a.k % 8 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
   if (a.packed) {
     hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((a.m + 15) / 16), unsigned((a.steps64 + 3) / 4)), dim3(256), 0, s, a.x,
                        a.ldx, a.m, a.k, a.steps64, ws);
@@ -758,9 +920,11 @@ hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
     a.x_half = 64;
   }
   a.parts = r.parts;
+  a.whole = int32_t(r.whole);
   a.ws = reinterpret_cast<f32x4_t*>(ws + q4_pack_bytes(r, a.k, a.m));
-  if (r.ap == 8 && r.bp == 2) return run_tile<DT, GATED, 8, 2, 4, 1>(a, s);
-  if (r.ap == 8) return run_tile<DT, GATED, 8, 4, 4, 1>(a, s);
+  if (r.bp == 1) return run_shared<DT, GATED, 1>(a, s);
+  if (r.bp == 2) return run_shared<DT, GATED, 2>(a, s);
+  if (r.bp == 4) return run_shared<DT, GATED, 4>(a, s);
   if (r.bp == 8) return run_tile<DT, GATED, 16, 8, 4, 2>(a, s);
   return run_tile<DT, GATED, 16, 16, 2, 4>(a, s);
 }

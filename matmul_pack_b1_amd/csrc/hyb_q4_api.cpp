@@ -103,7 +103,7 @@ hyb_status hyb_q4_gemm(const hyb_q4* w, int64_t n, int64_t k, const void* x, int
     if ((st = check_q4(w, "w")) != HYB_OK) return st;
     if ((st = check_plain(x, x_dtype, k, ldx, "x")) != HYB_OK) return st;
     const hyb::Q4Route r = hyb::q4_route(n, k, m, 1, hyb::device_cus());
-    if (hyb::q4_tiles(r, n, m, 1) >= hyb::kQ4MaxTiles)
+    if (hyb::q4_groups(r, n, m, 1) >= hyb::kQ4MaxTiles)
       return fail(HYB_ERR_UNSUPPORTED, "n x m = %lld x %d is too large for one launch", (long long)n, m);
   }
   const hyb_q4 none{nullptr, nullptr};

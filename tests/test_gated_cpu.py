@@ -185,7 +185,7 @@ def test_workspace_sizes():
     assert need(200, gated.DX) >= dz and need(200, gated.DW) >= dz
     assert need(200, gated.DX | gated.DW) >= max(need(200, gated.DX), need(200, gated.DW))
     four = ctypes.byref(_q4_pair())
-    assert need(1, 0, four) == need(16, 0, four) == 0 and need(40, 0, four) >= 48 * 256 * 2
+    assert need(1, 0, four) == need(4, 0, four) == 0 and need(40, 0, four) >= 48 * 256 * 2
 
 
 def test_empty_calls_do_nothing():
