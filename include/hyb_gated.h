@@ -16,10 +16,11 @@
  * distribution function; HYB_ACT_GELU_TANH its usual approximation
  * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2.
  *
- * Products are exact and summed in fp32, act is taken of the fp32 sums, and H,
- * G and U are each rounded once to the 16-bit type of X.  The backward pass
- * takes the rounded G and U; dG and dU are rounded once to the 16-bit type of
- * its products (bf16; or fp16, scaled by the power of two that brings the
+ * Products are exact and summed in fp32, act is taken of the fp32 sums, and H is
+ * rounded once to the 16-bit type of X.  The backward pass takes G and U in fp32
+ * (rounded to 16 bits they would add as much to the gradients' errors as the
+ * roundings below do); dG and dU are rounded once to the 16-bit type of its
+ * products (bf16; or fp16, scaled by the power of two that brings the
  * largest finite one to [2^13, 2^14), so that they neither overflow nor, down
  * to 2^-28 of the largest, lose bits) and the gradients are summed in fp32 and
  * rounded once.
@@ -65,13 +66,13 @@ hyb_status hyb_gated_workspace_size(const hyb_gated_pair* w, int32_t m, int32_t 
  *         type), row stride ldx >= k; for packed weights 16-byte aligned with
  *         ldx % 8 == 0 and ldx < 2^22, else element-aligned
  *   h     device m x n of x_dtype, row stride ldh >= n, element-aligned
- *   g, u  device m x n of x_dtype, row strides ldg, ldu >= n, element-aligned:
+ *   g, u  device m x n fp32, row strides ldg, ldu >= n, element-aligned:
  *         receive G and U for hyb_gated_backward; both or neither (NULL), and
  *         neither with 4-bit weights (HYB_ERR_UNSUPPORTED)
  * 0 <= m <= 2^22; 1 <= n <= 2^27 - 16 and 1 <= k <= 2^21 for packed weights,
  * 0 <= n and 0 <= k <= 2^22 for 4-bit ones (k = 0 gives zeros). */
 hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
-                     void* h, int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* workspace,
+                     void* h, int64_t ldh, float* g, int64_t ldg, float* u, int64_t ldu, void* workspace,
                      size_t workspace_bytes, void* stream);
 
 /* Gradients (packed weights; 4-bit ones are HYB_ERR_UNSUPPORTED); g and u are
@@ -83,7 +84,7 @@ hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_
  *           element-aligned; both or neither (NULL).  Dense: the gradient of
  *           every entry, dropped ones included. */
 hyb_status hyb_gated_backward(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m,
-                              int64_t ldx, const void* g, int64_t ldg, const void* u, int64_t ldu, const void* dh,
+                              int64_t ldx, const float* g, int64_t ldg, const float* u, int64_t ldu, const void* dh,
                               int64_t lddh, void* dx, int64_t lddx, void* dw_gate, int64_t lddw_gate, void* dw_up,
                               int64_t lddw_up, void* workspace, size_t workspace_bytes, void* stream);
 

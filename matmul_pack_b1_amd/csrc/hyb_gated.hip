@@ -11,6 +11,7 @@
 #include "hyb_act.h"
 #include "hyb_gated_internal.h"
 #include "hyb_panel.h"
+#include "hyb_q4_internal.h"
 #include "hyb_xent_internal.h"
 
 namespace hyb {
@@ -22,97 +23,151 @@ namespace {
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
-// x (m x k, row-major) as panels; rows behind m zero.
-__global__ __launch_bounds__(256) void k_gated_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m,
-                                                      int32_t steps, char* __restrict__ out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t panel = blockIdx.x;
-  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
-  if (s >= steps) return;
-  const int64_t row = panel * 16 + (lane & 15);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (row < m) u = *reinterpret_cast<const uint4*>(x + row * ldx + s * 64 + h * 32 + (lane >> 4) * 8);
-    *reinterpret_cast<uint4*>(out + (panel * steps + s) * kPanelStep + h * 1024 + lane * 16) = u;
-  }
-}
-
 struct GatedOut {
-  uint16_t *h, *g, *u;
+  uint16_t* h;
+  float *g, *u;  // NULL: not kept
   int64_t ldh, ldg, ldu;
   int32_t m, n;
   int act;
+  // tiles that run over all of k, and the parts each of the others is cut into,
+  // whose sums are left in `ws`
+  f32x4_t* ws;
+  int32_t whole, parts;
 };
 
-// H (and G, U) from fp32 G and U in the workspace: four outputs a thread (a
-// packed weight's n is a multiple of 64).
+// Four outputs j.. of a token; fp32 rows may be at any 4-byte aligned address.
 template <int DT>
-__global__ __launch_bounds__(256) void k_gated_act(const float* __restrict__ gu, GatedOut o) {
-  const int64_t tok = blockIdx.y;
-  const int32_t j = (int32_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (j >= o.n) return;
-  const f32x4_t g = *reinterpret_cast<const f32x4_t*>(gu + tok * o.n + j);
-  const f32x4_t u = *reinterpret_cast<const f32x4_t*>(gu + (o.m + tok) * o.n + j);
+__device__ __forceinline__ void gated_put(const GatedOut& o, int64_t tok, int32_t j, f32x4_t g, f32x4_t u) {
   f32x4_t h;
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = act_value(o.act, g[e]) * u[e];
-  auto put = [&](uint16_t* p, f32x4_t v) {
-    const uint2 r = round16x4<DT>(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<Bytes8*>(p) = Bytes8{{r.x, r.y}};
+  const uint2 r = round16x4<DT>(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<Bytes8*>(o.h + tok * o.ldh + j) = Bytes8{{r.x, r.y}};
+}
+__device__ __forceinline__ void gated_keep(float* p, f32x4_t v) {
+  const u32x4_t b = __builtin_bit_cast(u32x4_t, v);
+  *reinterpret_cast<Bytes16*>(p) = Bytes16{{b[0], b[1], b[2], b[3]}};
+}
+
+// H from fp32 G and U, which the products left in memory: four outputs a thread
+// (a packed weight's n is a multiple of 64).
+template <int DT>
+__global__ __launch_bounds__(256) void k_gated_act(GatedOut o) {
+  const int64_t tok = blockIdx.y;
+  const int32_t j = (int32_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (j >= o.n) return;
+  auto load = [&](const float* p) {
+    const Bytes16 b = *reinterpret_cast<const Bytes16*>(p);
+    return __builtin_bit_cast(f32x4_t, u32x4_t{b.w[0], b.w[1], b.w[2], b.w[3]});
   };
-  put(o.h + tok * o.ldh + j, h);
-  if (o.g) {
-    put(o.g + tok * o.ldg + j, g);
-    put(o.u + tok * o.ldu + j, u);
-  }
+  gated_put<DT>(o, tok, j, load(o.g + tok * o.ldg + j), load(o.u + tok * o.ldu + j));
 }
 
 // AP / 2 panels of each weight x BP panels of tokens.
 template <int DT, int AP, int BP, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, PanelOperand U, PanelOperand X, GatedOut o) {
+struct GatedTile {
   typedef PanelTile<DT, AP, BP, WA, WB, 2, false, false, true, false, true> T;
+  static constexpr int kRows = 16 * AP / 2, kOut = T::kA / 2;
+};
+
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, PanelOperand U, PanelOperand X, GatedOut o) {
+  typedef GatedTile<DT, AP, BP, WA, WB> D;
+  typedef typename D::T T;
+  constexpr int kOut = D::kOut;
   extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
-  constexpr int kRows = 16 * AP / 2, kOut = T::kA / 2;
-  const int32_t na = (G.rows16 + kRows - 1) / kRows, nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  const int32_t na = (G.rows16 + D::kRows - 1) / D::kRows, nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
+  const int32_t id = int32_t(blockIdx.x), rest = id - o.whole;
+  const bool cut = rest >= 0;
   int32_t ab, bb;
-  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  panel_block(cut ? o.whole + rest / o.parts : panel_order(id, o.whole), na, nb, ab, bb);
+  int32_t s0 = 0, s1 = G.steps;
+  if (cut) {
+    const int32_t quads = (G.steps + 3) / 4, part = rest % o.parts;  // a part is a whole number of four steps
+    s0 = int32_t(int64_t(quads) * part / o.parts) * 4;
+    if (part + 1 < o.parts) s1 = int32_t(int64_t(quads) * (part + 1) / o.parts) * 4;
+  }
   f32x4_t acc[T::kA][T::kB];
-  T::run(G, X, ab * (AP / 2), bb * BP, 0, G.steps, gated_smem, acc, false, &U);
+  T::run(G, X, ab * (AP / 2), bb * BP, s0, s1, gated_smem, acc, false, &U);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wa = wave % WA, wb = wave / WA;
-  const int32_t col0 = (ab * (AP / 2) + wa * kOut) * 16, row0 = (bb * BP + wb * T::kB) * 16;
-  char* lds = gated_smem + wave * (kOut * T::kB * 512);
-  __syncthreads();  // the tile's LDS stages are free
-  auto rows = [&](uint16_t* y, int64_t ld, auto value) {
-    panel_rows16<kOut, T::kB>(
-        lds, lane, lane & 15,
-        [&](int i, int j) {
-          const f32x4_t v = value(i, j);
-          return round16x4<DT>(v[0], v[1], v[2], v[3]);
-        },
-        [&](int r, int c, uint4 v) {
-          const int32_t row = row0 + r, col = col0 + c;
-          if (row < o.m && col < o.n) *reinterpret_cast<Bytes16*>(y + row * ld + col) = Bytes16{{v.x, v.y, v.z, v.w}};
-        });
-  };
-  if (o.g) {
-    rows(o.g, o.ldg, [&](int i, int j) { return acc[i][j]; });
-    rows(o.u, o.ldu, [&](int i, int j) { return acc[i + kOut][j]; });
-  }
-  rows(o.h, o.ldh, [&](int i, int j) {
-    f32x4_t v;
+  if (cut) {
+    f32x4_t* out = o.ws + (int64_t(rest) * T::kWaves + wave) * (T::kA * T::kB * 64) + lane;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = act_value(o.act, acc[i][j][e]) * acc[i + kOut][j][e];
-    return v;
-  });
+    for (int i = 0; i < T::kA; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kB; ++j) out[(i * T::kB + j) * 64] = acc[i][j];
+    return;
+  }
+  const int32_t col0 = (ab * (AP / 2) + wa * kOut) * 16, row0 = (bb * BP + wb * T::kB) * 16;
+  if (o.g) {
+#pragma unroll
+    for (int j = 0; j < T::kB; ++j) {
+      const int32_t row = row0 + j * 16 + (lane & 15);
+      if (row >= o.m) continue;
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) {
+        const int32_t col = col0 + i * 16 + (lane >> 4) * 4;
+        if (col >= o.n) continue;
+        gated_keep(o.g + row * o.ldg + col, acc[i][j]);
+        gated_keep(o.u + row * o.ldu + col, acc[i + kOut][j]);
+      }
+    }
+  }
+  __syncthreads();  // the tile's LDS stages are free
+  panel_rows16<kOut, T::kB>(
+      gated_smem + wave * (kOut * T::kB * 512), lane, lane & 15,
+      [&](int i, int j) {
+        f32x4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_value(o.act, acc[i][j][e]) * acc[i + kOut][j][e];
+        return round16x4<DT>(v[0], v[1], v[2], v[3]);
+      },
+      [&](int r, int c, uint4 v) {
+        const int32_t row = row0 + r, col = col0 + c;
+        if (row < o.m && col < o.n) *reinterpret_cast<Bytes16*>(o.h + row * o.ldh + col) = Bytes16{{v.x, v.y, v.z, v.w}};
+      });
+}
+
+// Adds the parts of the tiles that were cut, in order: one thread per four
+// outputs, in the order of the tile's registers.
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(256) void k_gated_sum(int32_t na, int32_t nb, GatedOut o) {
+  typedef GatedTile<DT, AP, BP, WA, WB> D;
+  typedef typename D::T T;
+  int32_t ab, bb;
+  panel_block(o.whole + int32_t(blockIdx.x), na, nb, ab, bb);
+  const int lane = threadIdx.x & 63, c = int(blockIdx.y) * 4 + (threadIdx.x >> 6);
+  const int wave = c / (D::kOut * T::kB), i = c / T::kB % D::kOut, j = c % T::kB;
+  const int32_t col = (ab * (AP / 2) + wave % WA * D::kOut + i) * 16 + (lane >> 4) * 4;
+  const int32_t row = (bb * BP + wave / WA * T::kB + j) * 16 + (lane & 15);
+  if (row >= o.m || col >= o.n) return;
+  f32x4_t v[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const f32x4_t* at = o.ws + (int64_t(blockIdx.x) * o.parts * T::kWaves + wave) * (T::kA * T::kB * 64) +
+                        ((i + p * D::kOut) * T::kB + j) * 64 + lane;
+    v[p] = at[0];
+#pragma unroll 4
+    for (int t = 1; t < o.parts; ++t) {
+      const f32x4_t u = at[int64_t(t) * T::kWaves * (T::kA * T::kB * 64)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[p][e] += u[e];
+    }
+  }
+  if (o.g) {
+    gated_keep(o.g + row * o.ldg + col, v[0]);
+    gated_keep(o.u + row * o.ldu + col, v[1]);
+  }
+  gated_put<DT>(o, row, col, v[0], v[1]);
 }
 
 // ------------------------------------------------------------ the gradients --
 
 struct GatedGrad {
-  const uint16_t *g, *u, *dh;
+  const float *g, *u;
+  const uint16_t* dh;
   int64_t ldg, ldu, lddh;
   int32_t m, n, steps;
   int act;
@@ -120,19 +175,24 @@ struct GatedGrad {
   uint32_t* top;  // fp16: bits of the largest finite |dG|, |dU|
 };
 
-// Eight outputs' dG and dU from 16-bit g, u and dh.
+// dG and dU of one output.
+__device__ __forceinline__ void gated_grad1(int act, float g, float u, float dh, float* dg, float* du) {
+  float a;
+  const float slope = act_slope(act, g, &a);
+  *dg = dh * u * slope;
+  *du = dh * a;
+}
+
+// Four outputs' dG and dU, from column c on of the rows' starts.
 template <int DT>
-__device__ __forceinline__ void gated_grad8(int act, const uint32_t (&g)[4], const uint32_t (&u)[4],
-                                            const uint32_t (&d)[4], float (&dg)[8], float (&du)[8]) {
+__device__ __forceinline__ void gated_grad4(int act, const float* g, const float* u, const uint16_t* dh, int64_t c,
+                                            float* dg, float* du) {
+  const Bytes16 gb = *reinterpret_cast<const Bytes16*>(g + c), ub = *reinterpret_cast<const Bytes16*>(u + c);
+  const Bytes8 db = *reinterpret_cast<const Bytes8*>(dh + c);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int s = 16 * (e & 1);
-    const float dh = widen16<DT>((d[e >> 1] >> s) & 0xFFFFu);
-    float a;
-    const float slope = act_slope(act, widen16<DT>((g[e >> 1] >> s) & 0xFFFFu), &a);
-    dg[e] = dh * widen16<DT>((u[e >> 1] >> s) & 0xFFFFu) * slope;
-    du[e] = dh * a;
-  }
+  for (int e = 0; e < 4; ++e)
+    gated_grad1(act, __builtin_bit_cast(float, gb.w[e]), __builtin_bit_cast(float, ub.w[e]),
+                widen16<DT>((db.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu), dg + e, du + e);
 }
 
 // The power of two that brings a magnitude of these bits to [2^13, 2^14) (1 for
@@ -151,17 +211,14 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
   __shared__ uint32_t tops[4];
   uint32_t best = 0;
-  const int32_t per = o.n / 8;  // a packed weight's n is a multiple of 64
+  const int32_t per = o.n / 4;  // a packed weight's n is a multiple of 64
   for (int64_t t = blockIdx.y; t < o.m; t += gridDim.y) {
     const int32_t c = int32_t(blockIdx.x) * 256 + threadIdx.x;
     if (c >= per) break;
-    const Bytes16 g = *reinterpret_cast<const Bytes16*>(o.g + t * o.ldg + c * 8);
-    const Bytes16 u = *reinterpret_cast<const Bytes16*>(o.u + t * o.ldu + c * 8);
-    const Bytes16 d = *reinterpret_cast<const Bytes16*>(o.dh + t * o.lddh + c * 8);
-    float dg[8], du[8];
-    gated_grad8<DT>(o.act, g.w, u.w, d.w, dg, du);
+    float dg[4], du[4];
+    gated_grad4<DT>(o.act, o.g + t * o.ldg, o.u + t * o.ldu, o.dh + t * o.lddh, int64_t(c) * 4, dg, du);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
       const uint32_t a = __builtin_bit_cast(uint32_t, dg[e]) & 0x7FFFFFFFu;
       const uint32_t b = __builtin_bit_cast(uint32_t, du[e]) & 0x7FFFFFFFu;
       if (a < 0x7F800000u && a > best) best = a;
@@ -198,19 +255,11 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
     uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
     if (tok < o.m) {
       const int32_t c = s * 64 + h * 32 + 16 * (u4 >> 1) + 4 * (u4 & 1);
-      uint32_t w[3][4];
-      auto load = [&](const uint16_t* p, uint32_t (&v)[4]) {
-        const Bytes8 lo = *reinterpret_cast<const Bytes8*>(p + c), hi = *reinterpret_cast<const Bytes8*>(p + c + 8);
-        v[0] = lo.w[0];
-        v[1] = lo.w[1];
-        v[2] = hi.w[0];
-        v[3] = hi.w[1];
-      };
-      load(o.g + tok * o.ldg, w[0]);
-      load(o.u + tok * o.ldu, w[1]);
-      load(o.dh + tok * o.lddh, w[2]);
       float dg[8], du[8];
-      gated_grad8<DT>(o.act, w[0], w[1], w[2], dg, du);
+      const float *g = o.g + tok * o.ldg, *u = o.u + tok * o.ldu;
+      const uint16_t* dh = o.dh + tok * o.lddh;
+      gated_grad4<DT>(o.act, g, u, dh, c, dg, du);
+      gated_grad4<DT>(o.act, g, u, dh, c + 8, dg + 4, du + 4);
       a = make_uint4(round16x2<DT>(dg[0] * lift, dg[1] * lift), round16x2<DT>(dg[2] * lift, dg[3] * lift),
                      round16x2<DT>(dg[4] * lift, dg[5] * lift), round16x2<DT>(dg[6] * lift, dg[7] * lift));
       b = make_uint4(round16x2<DT>(du[0] * lift, du[1] * lift), round16x2<DT>(du[2] * lift, du[3] * lift),
@@ -386,47 +435,67 @@ hipError_t expand_pair(const hyb_gated_pair& w, const GatedPlan& p, char* ws, hi
   return hipSuccess;
 }
 
+// x as panels.
 hipError_t pack_x(const GatedPlan& p, const void* x, int64_t ldx, char* ws, hipStream_t s, PanelOperand* out) {
-  const int32_t steps = int32_t(p.k / 64);
-  *out = PanelOperand{ws + p.x, int32_t(p.m16), steps, nullptr, 0};
-  hipLaunchKernelGGL(k_gated_pack_x, dim3(unsigned(p.m16 / 16), unsigned((steps + 3) / 4)), dim3(256), 0, s,
-                     static_cast<const uint16_t*>(x), ldx, p.m, steps, ws + p.x);
-  return hipGetLastError();
+  *out = PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.k / 64), nullptr, 0};
+  return launch_pack_x(static_cast<const uint16_t*>(x), ldx, p.m, p.k, ws + p.x, s);
 }
 
 template <int DT, int BP, int WA, int WB>
 hipError_t run_forward_tile(const PanelOperand (&W)[2], const PanelOperand& X, const GatedOut& o, hipStream_t s) {
-  typedef PanelTile<DT, 16, BP, WA, WB, 2, false, false, true, false, true> T;
+  typedef GatedTile<DT, 16, BP, WA, WB> D;
+  typedef typename D::T T;
   HYB_TRY(allow_lds(&k_gated_tile<DT, 16, BP, WA, WB>, T::kLds));
-  const int64_t na = (W[0].rows16 + 127) / 128, nb = (X.rows16 + 16 * BP - 1) / (16 * BP);
-  hipLaunchKernelGGL((k_gated_tile<DT, 16, BP, WA, WB>), dim3(unsigned(na * nb)), dim3(64 * WA * WB), T::kLds, s, W[0],
-                     W[1], X, o);
+  const int64_t na = (W[0].rows16 + 127) / 128, nb = (X.rows16 + 16 * BP - 1) / (16 * BP), rest = na * nb - o.whole;
+  hipLaunchKernelGGL((k_gated_tile<DT, 16, BP, WA, WB>), dim3(unsigned(o.whole + rest * o.parts)), dim3(64 * WA * WB),
+                     T::kLds, s, W[0], W[1], X, o);
+  HYB_TRY(hipGetLastError());
+  if (rest == 0) return hipSuccess;
+  constexpr int kEach = T::kWaves * D::kOut * T::kB;  // of 64 lanes, a tile
+  static_assert(kEach % 4 == 0, "whole workgroups");
+  hipLaunchKernelGGL((k_gated_sum<DT, 16, BP, WA, WB>), dim3(unsigned(rest), kEach / 4), dim3(256), 0, s, int32_t(na),
+                     int32_t(nb), o);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int64_t ldx,
                          const GatedForward& f, char* ws, hipStream_t s) {
-  const GatedOut o{static_cast<uint16_t*>(f.h), static_cast<uint16_t*>(f.g), static_cast<uint16_t*>(f.u), f.ldh, f.ldg,
-                   f.ldu, int32_t(p.m), int32_t(p.n), act};
+  GatedOut o{};
+  o.h = static_cast<uint16_t*>(f.h);
+  o.g = f.g;
+  o.u = f.u;
+  o.ldh = f.ldh;
+  o.ldg = f.ldg;
+  o.ldu = f.ldu;
+  o.m = int32_t(p.m);
+  o.n = int32_t(p.n);
+  o.act = act;
   if (p.rows) {
-    float* gu = reinterpret_cast<float*>(ws + p.gu);
+    if (!o.g) {  // not kept: in the workspace
+      o.g = reinterpret_cast<float*>(ws + p.gu);
+      o.u = o.g + p.m * p.n;
+      o.ldg = o.ldu = p.n;
+    }
     const hyb_layout L[2] = {*w.gate_layout, *w.up_layout};
     const hyb_packed P[2] = {*w.gate, *w.up};
-    void* const y[2] = {gu, gu + p.m * p.n};
-    const int64_t ldy[2] = {p.n, p.n};
+    void* const y[2] = {o.g, o.u};
+    const int64_t ldy[2] = {o.ldg, o.ldu};
     if (p.decode) {
       HYB_TRY(launch_gemv_grouped(2, L, P, x, int(p.m), ldx, y, HYB_F32, ldy, s));
     } else {
       for (int i = 0; i < 2; ++i)
-        HYB_TRY(launch_gemm(L[i], P[i], x, int(p.m), ldx, y[i], HYB_F32, p.n, s, ws + p.split, p.split_bytes));
+        HYB_TRY(launch_gemm(L[i], P[i], x, int(p.m), ldx, y[i], HYB_F32, ldy[i], s, ws + p.split, p.split_bytes));
     }
-    hipLaunchKernelGGL((k_gated_act<DT>), dim3(unsigned((p.n + 1023) / 1024), unsigned(p.m)), dim3(256), 0, s, gu, o);
+    hipLaunchKernelGGL((k_gated_act<DT>), dim3(unsigned((p.n + 1023) / 1024), unsigned(p.m)), dim3(256), 0, s, o);
     return hipGetLastError();
   }
   PanelOperand W[2], X;
   HYB_TRY(expand_pair(w, p, ws, s, W));
   HYB_TRY(pack_x(p, x, ldx, ws, s, &X));
+  o.ws = reinterpret_cast<f32x4_t*>(ws + p.gu);
+  o.whole = int32_t(p.whole);
+  o.parts = p.parts;
   if (p.bp == 16) return run_forward_tile<DT, 16, 2, 4>(W, X, o, s);
   return run_forward_tile<DT, 8, 4, 2>(W, X, o, s);
 }
@@ -456,8 +525,8 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
                           const GatedBackward& b, char* ws, hipStream_t s) {
   uint32_t* top = reinterpret_cast<uint32_t*>(ws + p.misc);
   GatedGrad g{};
-  g.g = static_cast<const uint16_t*>(b.g);
-  g.u = static_cast<const uint16_t*>(b.u);
+  g.g = b.g;
+  g.u = b.u;
   g.dh = static_cast<const uint16_t*>(b.dh);
   g.ldg = b.ldg;
   g.ldu = b.ldu;
@@ -472,7 +541,7 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
   if (DT == HYB_F16) {
     hipLaunchKernelGGL(k_gated_clear, dim3(1), dim3(1), 0, s, top);
     HYB_TRY(hipGetLastError());
-    const unsigned across = unsigned((p.n / 8 + 255) / 256);
+    const unsigned across = unsigned((p.n / 4 + 255) / 256);
     const int64_t down = 2048 / across + 1;
     hipLaunchKernelGGL((k_gated_top<DT>), dim3(across, unsigned(p.m < down ? p.m : down)), dim3(256), 0, s, g);
     HYB_TRY(hipGetLastError());

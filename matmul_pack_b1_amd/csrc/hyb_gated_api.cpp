@@ -91,9 +91,9 @@ hyb_status check_x(const void* x, int64_t k, int64_t ldx, bool packed) {
   return HYB_OK;
 }
 
-// A 16-bit matrix of rows of `cols`.
-hyb_status check_rows(const void* p, int64_t cols, int64_t ld, const char* name) {
-  if (!p || !aligned(p, 2)) return fail(HYB_ERR_INVALID_ARG, "%s is NULL or not 2-byte aligned", name);
+// A matrix of rows of `cols` elements of `size` bytes.
+hyb_status check_rows(const void* p, int64_t cols, int64_t ld, const char* name, int size = 2) {
+  if (!p || !aligned(p, size)) return fail(HYB_ERR_INVALID_ARG, "%s is NULL or not %d-byte aligned", name, size);
   if (ld < cols) return fail(HYB_ERR_INVALID_ARG, "%s row stride %lld < %lld", name, (long long)ld, (long long)cols);
   if (ld > (int64_t(1) << 31))
     return fail(HYB_ERR_UNSUPPORTED, "%s row stride %lld is above 2^31", name, (long long)ld);
@@ -142,7 +142,7 @@ hyb_status hyb_gated_workspace_size(const hyb_gated_pair* w, int32_t m, int32_t 
 }
 
 hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
-                     void* h, int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* workspace,
+                     void* h, int64_t ldh, float* g, int64_t ldg, float* u, int64_t ldu, void* workspace,
                      size_t workspace_bytes, void* stream) {
   int64_t n, k;
   int32_t dtype;
@@ -157,8 +157,8 @@ hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_
   if (m == 0 || n == 0) return ok();
   if ((st = check_rows(h, n, ldh, "h")) != HYB_OK) return st;
   if (g) {
-    if ((st = check_rows(g, n, ldg, "g")) != HYB_OK) return st;
-    if ((st = check_rows(u, n, ldu, "u")) != HYB_OK) return st;
+    if ((st = check_rows(g, n, ldg, "g", 4)) != HYB_OK) return st;
+    if ((st = check_rows(u, n, ldu, "u", 4)) != HYB_OK) return st;
   }
   if (k > 0 && (st = check_x(x, k, ldx, dtype != 0)) != HYB_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, need)) != HYB_OK) return st;
@@ -178,7 +178,7 @@ hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_
 }
 
 hyb_status hyb_gated_backward(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m,
-                              int64_t ldx, const void* g, int64_t ldg, const void* u, int64_t ldu, const void* dh,
+                              int64_t ldx, const float* g, int64_t ldg, const float* u, int64_t ldu, const void* dh,
                               int64_t lddh, void* dx, int64_t lddx, void* dw_gate, int64_t lddw_gate, void* dw_up,
                               int64_t lddw_up, void* workspace, size_t workspace_bytes, void* stream) {
   int64_t n, k;
@@ -199,8 +199,8 @@ hyb_status hyb_gated_backward(const hyb_gated_pair* w, int32_t act, const void* 
   if ((st = hyb_gated_workspace_size(w, m, what, &need)) != HYB_OK) return st;
   if (m > 0) {
     if ((st = check_x(x, k, ldx, true)) != HYB_OK) return st;
-    if ((st = check_rows(g, n, ldg, "g")) != HYB_OK) return st;
-    if ((st = check_rows(u, n, ldu, "u")) != HYB_OK) return st;
+    if ((st = check_rows(g, n, ldg, "g", 4)) != HYB_OK) return st;
+    if ((st = check_rows(u, n, ldu, "u", 4)) != HYB_OK) return st;
     if ((st = check_rows(dh, n, lddh, "dh")) != HYB_OK) return st;
     if (dx && (st = check_rows(dx, k, lddx, "dx")) != HYB_OK) return st;
     if ((st = check_ws(workspace, workspace_bytes, need)) != HYB_OK) return st;

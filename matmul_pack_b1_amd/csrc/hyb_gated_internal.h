@@ -17,25 +17,26 @@ constexpr int32_t kGatedMaxTokens = 1 << 22;
 struct GatedPlan {
   int64_t n, k, m, m16, m64;
   bool decode;  // forward: both products in the decode kernel ...
-  bool rows;    // ... or (also) G and U as fp32 in the workspace, then act
+  bool rows;    // ... or (also) G and U as fp32 in memory, then act
   int bp;       // token panels per tile
-  int parts;    // cuts of n in the dX product
+  int64_t whole;  // forward tiles that run over all of k; the others are cut
+  int parts;      // parts of those, or cuts of n in the dX product
   size_t x, w[2], g[2], gu, split, split_bytes, dx, misc, total;
 };
 GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus);
 
 struct GatedForward {
   void* h;
-  void* g;
-  void* u;
+  float* g;
+  float* u;
   int64_t ldh, ldg, ldu;
 };
 hipError_t launch_gated(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int dtype, int64_t ldx,
                         const GatedForward& out, char* ws, hipStream_t s);
 
 struct GatedBackward {
-  const void* g;
-  const void* u;
+  const float* g;
+  const float* u;
   const void* dh;
   int64_t ldg, ldu, lddh;
   void* dx;

@@ -30,7 +30,6 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
   if (!dx && !dw) {
     p.decode = m <= kGemvCrossoverM || (m <= kMaxGemvM && gemv_preferred(L, int(m)));
     p.rows = p.decode || m <= 64;
-    p.bp = up(p.n, 128) / 128 * (up(m, 256) / 256) * 2 <= cus || m <= 128 ? 8 : 16;
     if (p.rows) {
       p.gu = take(2 * m * p.n * 4);
       if (!p.decode) {
@@ -43,15 +42,41 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
       p.total = at;
       return p;
     }
-  }
-  if (!dx && !dw) {
-    p.x = take(p.m16 * p.k * 2);
+    // Whole rounds of the compute units run over all of k; the tiles beyond them
+    // are cut into parts.
+    const int64_t quads = (p.k / 64 + 3) / 4;
+    double least = 1e300;
+    struct Tile {
+      int bp;
+      double step;
+    };
+    for (const Tile& c : {Tile{8, 0.55}, Tile{16, 1.0}}) {
+      const int64_t tiles = up(p.n, 128) / 128 * (up(m, 16 * c.bp) / (16 * c.bp));
+      const int64_t whole = tiles / cus * cus, rest = tiles - whole;
+      auto offer = [&](int64_t first, int64_t parts, double cost) {
+        if (cost < least) {
+          least = cost;
+          p.bp = c.bp;
+          p.whole = first;
+          p.parts = int(parts);
+        }
+      };
+      offer(tiles, 1, double(up(tiles, cus) / cus * quads) * c.step);
+      for (int64_t parts = 2; rest > 0 && parts <= quads && parts <= 32 && rest * parts <= 2 * cus; ++parts)
+        offer(whole, parts,
+              double(whole / cus * quads + up(rest * parts, cus) / cus * (up(quads, parts) / parts)) * c.step + 2.0 +
+                  0.004 * double(rest * parts) * c.bp / 16);
+    }
+    if (p.parts > 1) {
+      const int64_t tiles = up(p.n, 128) / 128 * (up(m, 16 * p.bp) / (16 * p.bp));
+      p.gu = take((tiles - p.whole) * p.parts * 16 * p.bp * 1024);
+    }
   } else {
-    if (dw) p.x = take(p.m16 * p.k * 2);
     p.misc = take(256);
     for (int i = 0; i < 2; ++i) p.g[i] = take(p.m16 * p.n * 2);
     p.bp = m <= 64 ? 4 : m <= 128 ? 8 : 16;
   }
+  if (!dx || dw) p.x = take(p.m16 * p.k * 2);
   if (!dw || dx)
     for (int i = 0; i < 2; ++i)
       if (both[i]->n_sparse > 0) p.w[i] = take(p.n * p.k * 2);

@@ -390,20 +390,23 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
   }
 }
 
-// Activations as panels (hyb_panel.h; rows behind m and columns behind k zero),
-// for an x whose rows are not whole 16-byte pieces.
+// Activations as panels (hyb_panel.h), rows behind m and columns behind k zero:
+// a wavefront per panel and four steps, whose eight loads are under way at once.
 __global__ __launch_bounds__(256) void k_q4_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m, int32_t k,
                                                    int32_t steps64, char* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t panel = blockIdx.x;
-  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  const int32_t s = (int32_t(blockIdx.y) * 4 + wave) * 4;
   if (s >= steps64) return;
   const int64_t row = panel * 16 + (lane & 15);
+  const int32_t c0 = s * 64 + (lane >> 4) * 8;
+  uint4 u[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 u = row < m ? load8_16(x + row * ldx, s * 64 + h * 32 + (lane >> 4) * 8, k) : make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(out + (panel * steps64 + s) * 2048 + h * 1024 + lane * 16) = u;
-  }
+  for (int h = 0; h < 8; ++h) u[h] = row < m ? load8_16(x + row * ldx, c0 + h * 32, k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int h = 0; h < 8; ++h)
+    if (s + h / 2 < steps64)
+      *reinterpret_cast<uint4*>(out + (panel * steps64 + s) * 2048 + h * 1024 + lane * 16) = u[h];
 }
 
 // Four outputs j0.. of token `tok`: sums v (and u of the second weight).
@@ -643,23 +646,14 @@ struct Q4Tile {
     // x: chunk c is half c % 2 of panel c / 2
     const int64_t tok0 = int64_t(bb) * BP * 16, left = a.m - tok0;
     const int64_t rows = left < BP * 16 ? left : BP * 16;
-    const srd4_t xr = panel_srd(a.xt + int64_t(bb) * BP * a.x_panel,
-                                uint32_t(a.packed ? (rows + 15) / 16 * a.x_panel : (rows - 1) * a.x_row + int64_t(a.k) * 2));
-    int32_t xo[kLoadsX];
-#pragma unroll
-    for (int t = 0; t < kLoadsX; ++t) {
-      const int c = wave * kLoadsX + t;
-      xo[t] = int32_t((c >> 1) * a.x_panel + (lane & 15) * a.x_row + (lane >> 4) * a.x_unit) + (c & 1) * a.x_half;
-    }
+    const srd4_t xr = panel_srd(a.xt + int64_t(bb) * BP * a.x_panel, uint32_t((rows + 15) / 16 * a.x_panel));
     auto issue_x = [&](int32_t s) {
       const uint32_t dst = base + kAtX + (s & 1) * kX;
 #pragma unroll
       for (int t = 0; t < kLoadsX; ++t) {
         const int c = wave * kLoadsX + t;
-        int32_t off = xo[t] + s * a.x_step;
-        // columns from k on read as zeros
-        if (!a.packed && s * 64 + 64 > a.k && s * 64 + (c & 1) * 32 + (lane >> 4) * 8 >= a.k) off = 0x7FFFFFF0;
-        panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + c * 1024), off);
+        panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + c * 1024),
+                    int32_t((c >> 1) * a.x_panel) + s * 2048 + (c & 1) * 1024 + lane * 16);
       }
     };
     // panel i of this wavefront in the tile's order
@@ -898,12 +892,11 @@ hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
     if (a.m == 2) return run_rows<DT, 2, GATED>(a, s);
     return run_rows<DT, 4, GATED>(a, s);
   }
-  // x where it lies if its rows are whole 16-byte pieces
-  a.packed = a.k % 8 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
+  // the few tokens of k_q4_shared where they lie if their rows are whole 16-byte
+  // pieces (a tile's, read 64 bytes of a row at a time, cost it a fifth of its time)
+  a.packed = r.bp > 4 || a.k % 8 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
   if (a.packed) {
-    hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((a.m + 15) / 16), unsigned((a.steps64 + 3) / 4)), dim3(256), 0, s, a.x,
-                       a.ldx, a.m, a.k, a.steps64, ws);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_pack_x(a.x, a.ldx, a.m, a.k, ws, s);
     if (e != hipSuccess) return e;
     a.xt = ws;
     a.x_panel = int64_t(a.steps64) * 2048;
@@ -966,6 +959,13 @@ hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a
     hipLaunchKernelGGL((k_q4_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
   else
     hipLaunchKernelGGL((k_q4_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack_x(const uint16_t* x, int64_t ldx, int64_t m, int64_t k, char* out, hipStream_t s) {
+  const int32_t steps64 = int32_t((k + 63) / 64);
+  hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((m + 15) / 16), unsigned((steps64 + 15) / 16)), dim3(256), 0, s, x, ldx, m,
+                     int32_t(k), steps64, out);
   return hipGetLastError();
 }
 

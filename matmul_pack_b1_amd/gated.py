@@ -108,8 +108,8 @@ def workspace_bytes(G, U, m: int, dx: bool = False, dw: bool = False) -> int:
 def forward(G, U, x, act="silu", save=False, out=None, workspace=None):
     """H = act(x G^T) * (x U^T) for any number of tokens, of x's dtype (packed
     weights: their own; 4-bit ones: float16 or bfloat16).  act: "silu", "gelu" or
-    "gelu_tanh".  With `save` (packed weights) the result is (H, x G^T, x U^T),
-    each rounded to x's dtype, for backward().  `out` may give H.  The workspace
+    "gelu_tanh".  With `save` (packed weights) the result is (H, x G^T, x U^T), the
+    last two in float32, for backward().  `out` may give H.  The workspace
     comes from torch's allocator unless `workspace` (a contiguous device tensor
     of at least workspace_bytes(G, U, m) bytes) is given."""
     pair, n, k, m = _check(G, U, x, act)
@@ -120,7 +120,7 @@ def forward(G, U, x, act="silu", save=False, out=None, workspace=None):
     _check_devices(G, U, x)
     h = torch.empty((m, n), dtype=x.dtype, device=x.device) if out is None else out
     hb._check_gpu(h, "out", x.device)
-    g, u = (torch.empty((m, n), dtype=x.dtype, device=x.device) for _ in range(2)) if save else (None, None)
+    g, u = (torch.empty((m, n), dtype=torch.float32, device=x.device) for _ in range(2)) if save else (None, None)
     with _on(x.device):
         ws, nbytes = q4._workspace(workspace, _need(pair, m, 0) if workspace is None else 0, x.device)
         hb.check(lib().hyb_gated(ctypes.byref(pair), ACTS[act], hb._ptr(x), _code(x.dtype), m, _pitch(x, k), hb._ptr(h),
@@ -139,8 +139,8 @@ def backward(G, U, x, g, u, dh, act="silu", need_dx=True, need_dw=False, dx=None
     pair, n, k, m = _check(G, U, x, act)
     if not isinstance(G, hb.PackedWeight):
         raise TypeError("4-bit weights have no gradients")
-    for t, name in ((g, "g"), (u, "u"), (dh, "dh")):
-        hb._check_out(t, (m, n), x.dtype, name)
+    for t, dtype, name in ((g, torch.float32, "g"), (u, torch.float32, "u"), (dh, x.dtype, "dh")):
+        hb._check_out(t, (m, n), dtype, name)
     if (dw_gate is None) != (dw_up is None):
         raise ValueError("give both dw_gate and dw_up, or neither")
     need_dx, need_dw = need_dx or dx is not None, need_dw or dw_gate is not None

@@ -119,7 +119,7 @@ FORWARD = [
     (dict(act=0), 1), (dict(act=4), 1), (dict(dt=hb.HYB_F32), 3), (dict(dt=hb.HYB_F16), 3), (dict(m=-1), 2),
     (dict(m=(1 << 22) + 1), 2), (dict(x=None), 1), (dict(x=P16 + 8), 1), (dict(ldx=255), 1), (dict(ldx=260), 1),
     (dict(ldx=1 << 22), 4), (dict(h=None), 1), (dict(h=P16 + 1), 1), (dict(ldh=127), 1), (dict(ldh=2 ** 31 + 1), 4),
-    (dict(g=None), 1), (dict(u=None), 1), (dict(g=P16 + 1), 1), (dict(ldu=100), 1), (dict(ws=None), 1),
+    (dict(g=None), 1), (dict(u=None), 1), (dict(g=P16 + 2), 1), (dict(ldu=100), 1), (dict(ws=None), 1),
     (dict(ws=P16 + 8), 1), (dict(nbytes=64), 1),
 ]
 
@@ -212,7 +212,7 @@ def _fake4(n, k):
 def test_binding_refusals():
     x = torch.zeros(3, 128, dtype=torch.bfloat16)
     P, Q = _fake(64, 128), _fake4(64, 128)
-    y = torch.zeros(3, 64, dtype=torch.bfloat16)
+    y, f = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(3, 64)
     for call, err in [
         (lambda: gated.forward(P, Q, x), TypeError), (lambda: gated.forward(x, x, x), TypeError),
         (lambda: gated.forward(P, _fake(128, 128), x), ValueError), (lambda: gated.forward(Q, _fake4(32, 128), x), ValueError),
@@ -221,11 +221,11 @@ def test_binding_refusals():
         (lambda: gated.forward(P, P, x[:, :64]), ValueError), (lambda: gated.forward(Q, Q, x.float()), TypeError),
         (lambda: gated.forward(Q, Q, x, save=True), TypeError), (lambda: gated.forward(P, P, x, out=x), ValueError),
         (lambda: gated.forward(P, P, x, out=y.float()), TypeError), (lambda: gated.forward(P, P, x), ValueError),
-        (lambda: gated.backward(Q, Q, x, y, y, y), TypeError), (lambda: gated.backward(P, P, x, y, y, x), ValueError),
-        (lambda: gated.backward(P, P, x, y, y.half(), y), TypeError),
-        (lambda: gated.backward(P, P, x, y, y, y, dw_gate=torch.zeros(64, 128, dtype=torch.bfloat16)), ValueError),
-        (lambda: gated.backward(P, P, x, y, y, y, dx=y), ValueError),
-        (lambda: gated.backward(P, P, x, y, y, y), ValueError),              # not on a GPU
+        (lambda: gated.backward(Q, Q, x, f, f, y), TypeError), (lambda: gated.backward(P, P, x, f, f, x), ValueError),
+        (lambda: gated.backward(P, P, x, f, y, y), TypeError),
+        (lambda: gated.backward(P, P, x, f, f, y, dw_gate=torch.zeros(64, 128, dtype=torch.bfloat16)), ValueError),
+        (lambda: gated.backward(P, P, x, f, f, y, dx=y), ValueError),
+        (lambda: gated.backward(P, P, x, f, f, y), ValueError),              # not on a GPU
     ]:
         with pytest.raises(err):
             call()
