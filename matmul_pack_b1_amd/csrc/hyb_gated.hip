@@ -471,6 +471,9 @@ hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, c
   o.m = int32_t(p.m);
   o.n = int32_t(p.n);
   o.act = act;
+  if (p.decode)
+    return launch_gemv_gated(*w.gate_layout, *w.gate, *w.up_layout, *w.up, act, x, int(p.m), ldx, f.h, f.ldh, f.g, f.ldg,
+                             f.u, f.ldu, s);
   if (p.rows) {
     if (!o.g) {  // not kept: in the workspace
       o.g = reinterpret_cast<float*>(ws + p.gu);
@@ -481,12 +484,11 @@ hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, c
     const hyb_packed P[2] = {*w.gate, *w.up};
     void* const y[2] = {o.g, o.u};
     const int64_t ldy[2] = {o.ldg, o.ldu};
-    if (p.decode) {
+    if (p.grouped)
       HYB_TRY(launch_gemv_grouped(2, L, P, x, int(p.m), ldx, y, HYB_F32, ldy, s));
-    } else {
+    else
       for (int i = 0; i < 2; ++i)
         HYB_TRY(launch_gemm(L[i], P[i], x, int(p.m), ldx, y[i], HYB_F32, ldy[i], s, ws + p.split, p.split_bytes));
-    }
     hipLaunchKernelGGL((k_gated_act<DT>), dim3(unsigned((p.n + 1023) / 1024), unsigned(p.m)), dim3(256), 0, s, o);
     return hipGetLastError();
   }

@@ -16,8 +16,9 @@ constexpr int32_t kGatedMaxTokens = 1 << 22;
 // workspace (byte offsets).
 struct GatedPlan {
   int64_t n, k, m, m16, m64;
-  bool decode;  // forward: both products in the decode kernel ...
-  bool rows;    // ... or (also) G and U as fp32 in memory, then act
+  bool decode;   // forward: the gated decode kernel ...
+  bool rows;     // ... or G and U as fp32 in memory, then act ...
+  bool grouped;  // ... from the grouped decode kernel, or the matrix-core ones
   int bp;       // token panels per tile
   int64_t whole;  // forward tiles that run over all of k; the others are cut
   int parts;      // parts of those, or cuts of n in the dX product

@@ -28,11 +28,13 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
   const bool dx = what & HYB_GATED_DX, dw = what & HYB_GATED_DW;
   const hyb_layout* both[2] = {w.gate_layout, w.up_layout};
   if (!dx && !dw) {
-    p.decode = m <= kGemvCrossoverM || (m <= kMaxGemvM && gemv_preferred(L, int(m)));
-    p.rows = p.decode || m <= 64;
+    p.decode = m <= kGemvCrossoverM;
+    if (p.decode) return p;
+    p.rows = m <= 64;
+    p.grouped = m <= kMaxGemvM && gemv_preferred(L, int(m));
     if (p.rows) {
       p.gu = take(2 * m * p.n * 4);
-      if (!p.decode) {
+      if (!p.grouped) {
         for (const hyb_layout* l : both) {
           const size_t need = split_workspace_bytes(gemm_route_device(*l, int(m)));
           if (need > p.split_bytes) p.split_bytes = need;

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "hyb_act.h"
 #include "hyb_device.h"
 
 namespace hyb {
@@ -194,12 +195,22 @@ __host__ __device__ constexpr bool gemv_has_halves(int mt, int waves) { return w
 // The LDS of one decode workgroup.  The kernel declares it and hands it to
 // gemv_slab, so that two instantiations of gemv_slab in one kernel (the two
 // ring depths of the mixed launch) share one allocation.
-template <int MT, int B2, int META, int WAVES, bool XR>
+template <int MT, int B2, int META, int WAVES, bool XR, bool PAIR = false>
 struct GemvSmem {
   static constexpr int XS = XR ? kXrTiles<B2> * B2 : B2;  // x row stride
+  static constexpr int kAll = PAIR ? 2 * WAVES : WAVES;
   uint4 lut8[META == HYB_META_MASK8 ? 256 : 1];
-  __attribute__((aligned(16))) uint16_t xs[WAVES][MT * XS];
-  float red[WAVES][MT][16];
+  __attribute__((aligned(16))) uint16_t xs[kAll][MT * XS];
+  float red[kAll][MT][16];
+};
+
+// Outputs of the gated decode product: H in the type of x, and G and U (fp32)
+// where they are kept.
+struct GemvGated {
+  uint16_t* h;
+  float *g, *u;
+  int64_t ldh, ldg, ldu;
+  int32_t act;
 };
 
 // The product of one 16-row slab (the whole work of one workgroup).  With
@@ -217,12 +228,16 @@ struct GemvSmem {
 // nothing, and their rows are not stored.  The rows taken see the same
 // loads in the same order as with half < 0, so their results are bitwise
 // equal.  x comes through the real lane in either case.
-template <int MT, int B2, int DT, int META, int WAVES, int STAGES, bool LR = false, bool XR = false>
+// With PAIR the workgroup has 2 WAVES wavefronts, of which the second half is
+// called with the other weight's streams; they meet at the end, where the two
+// sums become one output (o).
+template <int MT, int B2, int DT, int META, int WAVES, int STAGES, bool LR = false, bool XR = false, bool PAIR = false>
 __device__ __forceinline__ void gemv_slab(const uint4* __restrict__ dense, const uint4* __restrict__ val,
                                           const uint16_t* __restrict__ meta, const int32_t* __restrict__ tidx,
                                           const uint16_t* __restrict__ x, void* __restrict__ y,
                                           const GemvDims& d, int64_t slab,
-                                          GemvSmem<MT, B2, META, WAVES, XR>& sm, int half = -1) {
+                                          GemvSmem<MT, B2, META, WAVES, XR, PAIR>& sm, int half = -1,
+                                          const GemvGated* o = nullptr) {
   constexpr int XS = GemvSmem<MT, B2, META, WAVES, XR>::XS;
   uint4* lut8 = sm.lut8;
   if constexpr (META == HYB_META_MASK8) {
@@ -231,14 +246,15 @@ __device__ __forceinline__ void gemv_slab(const uint4* __restrict__ dense, const
   }
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = PAIR ? all % WAVES : all;
   const int slabs_per_tile = d.b1 / 16;
   const int64_t tn = slab / slabs_per_tile;
   const int rs = int(slab - tn * slabs_per_tile);
   const int32_t tk0 = (wave * d.tiles_k) / WAVES;
   const int32_t cnt = ((wave + 1) * d.tiles_k) / WAVES - tk0;
   const int32_t* __restrict__ trow = tidx + tn * d.tiles_k + tk0;
-  uint16_t* xs = sm.xs[wave];
+  uint16_t* xs = sm.xs[all];
   const int ln = (half < 0 || ((lane & 15) >> 3) == half) ? lane : (1 << 22);
 
   float acc[MT];
@@ -341,9 +357,28 @@ __device__ __forceinline__ void gemv_slab(const uint4* __restrict__ dense, const
   }
   if (lane < 16) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sm.red[wave][m][lane] = acc[m];
+    for (int m = 0; m < MT; ++m) sm.red[all][m][lane] = acc[m];
   }
   __syncthreads();
+  if constexpr (PAIR) {
+    for (int i = threadIdx.x; i < MT * 16; i += blockDim.x) {
+      const int m = i >> 4, r = i & 15;
+      if (m >= d.m) continue;
+      float g = sm.red[0][m][r], u = sm.red[WAVES][m][r];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) {
+        g += sm.red[w][m][r];
+        u += sm.red[WAVES + w][m][r];
+      }
+      const int64_t row = slab * 16 + r;
+      if (o->g) {
+        o->g[m * o->ldg + row] = g;
+        o->u[m * o->ldu + row] = u;
+      }
+      o->h[m * o->ldh + row] = round16<DT>(act_value(o->act, g) * u);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < MT * 16; i += blockDim.x) {
     const int m = i >> 4, r = i & 15;
     if (m < d.m && (half < 0 || (r >> 3) == half)) {
@@ -420,6 +455,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemv_grouped(const uint16_t* __r
   __shared__ GemvSmem<MT, B2, META, WAVES, XR> sm;
   gemv_slab<MT, B2, DT, META, WAVES, STAGES, false, XR>(g.dense[gi], g.val[gi], g.meta[gi], g.tidx[gi], x, g.y[gi], d,
                                                         b - g.slab_start[gi], sm);
+}
+
+// Gated decode product of a few tokens: one workgroup per 16 rows, wavefronts 0 ..
+// W - 1 on the gate's slab, the others on the up projection's, each as in
+// k_gemv.  Bound by memory: 14336x4096, 70% of 128x128 tiles 2:4, one token
+// KERNELFIGURE.
+template <int MT, int B2, int DT, int META, int WAVES, int STAGES, bool XR>
+__global__ __launch_bounds__(128 * WAVES) void k_gemv_gated(GemvPtrs g, GemvPtrs u, GemvDims d, int32_t u_dense,
+                                                            int32_t u_sparse, GemvGated o) {
+  __shared__ GemvSmem<MT, B2, META, WAVES, XR, true> sm;
+  const bool second = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= WAVES;
+  d.n_dense = second ? u_dense : d.n_dense;
+  d.n_sparse = second ? u_sparse : d.n_sparse;
+  gemv_slab<MT, B2, DT, META, WAVES, STAGES, false, XR, true>(
+      second ? u.dense : g.dense, second ? u.val : g.val, second ? u.meta : g.meta, second ? u.tidx : g.tidx, g.x, nullptr,
+      d, blockIdx.x, sm, -1, &o);
 }
 
 }  // namespace
@@ -664,6 +715,72 @@ hipError_t launch_gemv_grouped(int count, const hyb_layout* L, const hyb_packed*
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+namespace {
+
+template <int MT, int DT, int META, bool XR>
+void gemv_gated_b2(int b2, dim3 grid, hipStream_t s, const GemvPtrs& g, const GemvPtrs& u, const GemvDims& d, int32_t ud,
+                   int32_t us, const GemvGated& o) {
+  const dim3 block(128 * kGemvWaves);
+  switch (b2) {
+    case 64:
+      hipLaunchKernelGGL((k_gemv_gated<MT, 64, DT, META, kGemvWaves, kGemvStages, XR>), grid, block, 0, s, g, u, d, ud, us, o);
+      break;
+    case 128:
+      hipLaunchKernelGGL((k_gemv_gated<MT, 128, DT, META, kGemvWaves, kGemvStages, XR>), grid, block, 0, s, g, u, d, ud, us, o);
+      break;
+    default:
+      hipLaunchKernelGGL((k_gemv_gated<MT, 256, DT, META, kGemvWaves, kGemvStages, XR>), grid, block, 0, s, g, u, d, ud, us, o);
+      break;
+  }
+}
+
+template <int DT, int META>
+void gemv_gated_mt(int m, bool xr, int b2, dim3 grid, hipStream_t s, const GemvPtrs& g, const GemvPtrs& u,
+                   const GemvDims& d, int32_t ud, int32_t us, const GemvGated& o) {
+  if (m <= 1) {
+    if (xr) return gemv_gated_b2<1, DT, META, true>(b2, grid, s, g, u, d, ud, us, o);
+    return gemv_gated_b2<1, DT, META, false>(b2, grid, s, g, u, d, ud, us, o);
+  }
+  if (m <= 2) {
+    if (xr) return gemv_gated_b2<2, DT, META, true>(b2, grid, s, g, u, d, ud, us, o);
+    return gemv_gated_b2<2, DT, META, false>(b2, grid, s, g, u, d, ud, us, o);
+  }
+  gemv_gated_b2<4, DT, META, false>(b2, grid, s, g, u, d, ud, us, o);
+}
+
+}  // namespace
+
+hipError_t launch_gemv_gated(const hyb_layout& G, const hyb_packed& PG, const hyb_layout& U, const hyb_packed& PU,
+                             int act, const void* x, int m, int64_t ldx, void* h, int64_t ldh, float* g, int64_t ldg,
+                             float* u, int64_t ldu, hipStream_t s) {
+  auto ptrs = [&](const hyb_packed& P) {
+    return GemvPtrs{static_cast<const uint4*>(P.dense), static_cast<const uint4*>(P.val),
+                    static_cast<const uint16_t*>(P.meta), P.tidx, static_cast<const uint16_t*>(x), nullptr};
+  };
+  const GemvPtrs pg = ptrs(PG), pu = ptrs(PU);
+  GemvDims d{};
+  d.ldx = ldx;
+  d.tiles_k = int32_t(G.tiles_k);
+  d.n_dense = int32_t(G.n_dense);
+  d.n_sparse = int32_t(G.n_sparse);
+  d.b1 = G.b1;
+  d.m = m;
+  const int32_t ud = int32_t(U.n_dense), us = int32_t(U.n_sparse);
+  const GemvGated o{static_cast<uint16_t*>(h), g, u, ldh, ldg, ldu, act};
+  const bool xr = gemv_xr(G.tiles_k, G.b2, kGemvWaves, m);
+  const dim3 grid(unsigned(G.n / 16));
+  if (G.dtype == HYB_BF16) {
+    if (G.meta == HYB_META_IDX2) gemv_gated_mt<HYB_BF16, HYB_META_IDX2>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+    else if (G.meta == HYB_META_MASK4) gemv_gated_mt<HYB_BF16, HYB_META_MASK4>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+    else gemv_gated_mt<HYB_BF16, HYB_META_MASK8>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+  } else {
+    if (G.meta == HYB_META_IDX2) gemv_gated_mt<HYB_F16, HYB_META_IDX2>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+    else if (G.meta == HYB_META_MASK4) gemv_gated_mt<HYB_F16, HYB_META_MASK4>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+    else gemv_gated_mt<HYB_F16, HYB_META_MASK8>(m, xr, G.b2, grid, s, pg, pu, d, ud, us, o);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace hyb

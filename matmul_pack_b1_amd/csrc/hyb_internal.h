@@ -52,6 +52,11 @@ constexpr int kMaxRank = HYB_MAX_RANK;
 // All matrices share k, b2, dtype and metadata kind (checked by the caller).
 hipError_t launch_gemv_grouped(int count, const hyb_layout* L, const hyb_packed* P, const void* x, int m,
                                int64_t ldx, void* const* y, int y_dtype, const int64_t* ldy, hipStream_t s);
+// act(x G'^T) * (x U'^T) for up to kGemvCrossoverM tokens, in the weights' type;
+// g and u (both or neither) receive the two products.
+hipError_t launch_gemv_gated(const hyb_layout& G, const hyb_packed& PG, const hyb_layout& U, const hyb_packed& PU,
+                             int act, const void* x, int m, int64_t ldx, void* h, int64_t ldh, float* g, int64_t ldg,
+                             float* u, int64_t ldu, hipStream_t s);
 hipError_t launch_stream_read(const void* p, int64_t bytes, uint32_t* sink, int grid, hipStream_t s);
 // Compute units of the current device (256 when no device is visible);
 // cached per device.

@@ -221,12 +221,9 @@ struct Q4Args {
   void* y;
   int64_t ldy;
   int ydt, act;
-  // more than a few tokens: the activations as they lie, or as panels: bytes from
-  // a panel of 16 to the next, from a row to the next, from a row's 8 columns to
-  // the next, 64 columns and 32 columns on
-  const char* xt;
-  int64_t x_panel, x_row, x_unit;
-  int32_t x_step, x_half, packed, steps64;
+  const char* xt;  // tiles: the activations as panels, of x_panel bytes
+  int64_t x_panel;
+  int32_t steps64;
   // tiles that run over all of k, and the parts each of the others is cut into,
   // whose sums are left in `ws`
   f32x4_t* ws;
@@ -390,8 +387,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
   }
 }
 
-// Activations as panels (hyb_panel.h), rows behind m and columns behind k zero:
-// a wavefront per panel and four steps, whose eight loads are under way at once.
+// Activations as panels (hyb_panel.h), rows behind m and columns behind k zero
+// (read where they lie, 64 bytes of a row at a time, they cost a tile a fifth of its
+// time): a wavefront per panel and four steps, whose eight loads are under way at once.
 __global__ __launch_bounds__(256) void k_q4_pack_x(const uint16_t* __restrict__ x, int64_t ldx, int64_t m, int32_t k,
                                                    int32_t steps64, char* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -451,15 +449,16 @@ __device__ __forceinline__ f32x4_t q4_finish(const Q4Args& a, int64_t j0, f32x4_
   return v;
 }
 
-// Up to 64 tokens: eight panels (of each weight) per workgroup, one per
-// wavefront, whose codes go from memory to its registers; the 16 BP tokens'
-// activations, 512 columns at a time, come through LDS for all eight.  The k of a
-// workgroup's panels may be cut into parts, a workgroup each.
+// Up to a few hundred tokens on short matrices: eight panels (of each weight) per
+// workgroup, one per wavefront, whose codes go from memory to its registers; 16
+// BP tokens' activations, 512 columns at a time, come through LDS for all eight
+// (from registers, in which a row at any alignment and the end of k cost nothing
+// more).  The k of a workgroup's panels may be cut into parts, a workgroup each.
 template <int DT, bool GATED, int BP>
 __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
   constexpr int P = GATED ? 2 : 1;
   constexpr int kX = BP * 16384;       // 512 columns
-  constexpr int kLoads = BP * 16 / 8;  // 1 KiB transfers per wavefront
+  constexpr int kLoads = BP * 16 / 8;  // 1 KiB of them per wavefront
   extern __shared__ __attribute__((aligned(1024))) char q4_smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -467,6 +466,7 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
   const int32_t quads = (a.steps + 3) / 4;
   const int32_t q0 = int32_t(int64_t(quads) * part / a.parts), q1 = int32_t(int64_t(quads) * (part + 1) / a.parts);
   const int64_t panels = a.rows16 / 16, mine = int64_t(blockIdx.x) * 8 + wave;
+  const int64_t tok0 = int64_t(blockIdx.z) * (BP * 16);
   // (a wavefront behind the last panel multiplies the last one again)
   const int64_t panel = mine < panels ? mine : panels - 1;
   const int64_t row = panel * 16 + (lane & 15);
@@ -480,23 +480,22 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
     scale_at[p] = a.w[p].scales + row * 16;
     lift[p] = DT == HYB_F16 ? kTopLift - int(a.w[p].tops[row]) : 0;
   }
-  // x: chunk c of a quad is half c % 2 of 64-column step c / 2 % 8 of token
-  // panel c / 16
-  const uint32_t base = __builtin_amdgcn_readfirstlane(panel_lds_addr(q4_smem));
-  const int64_t tok_panels = (a.m + 15) / 16;
-  const srd4_t xr = panel_srd(a.xt, uint32_t(a.packed ? tok_panels * a.x_panel : (a.m - 1) * a.x_row + int64_t(a.k) * 2));
-  auto issue_x = [&](int32_t q) {
-    const uint32_t dst = base + (q & 1) * kX;
+  // x: KiB c of a quad is half c % 2 of 64-column step c / 2 % 8 of token panel
+  // c / 16; this wavefront's are wave * kLoads ..
+  uint4 xr[kLoads];
+  auto load_x = [&](int32_t q) {
 #pragma unroll
     for (int t = 0; t < kLoads; ++t) {
       const int c = wave * kLoads + t;
-      const int32_t s = q * 8 + (c >> 1) % 8;
-      int32_t off = int32_t((c >> 4) * a.x_panel + (lane & 15) * a.x_row + (lane >> 4) * a.x_unit) + s * a.x_step +
-                    (c & 1) * a.x_half;
-      // columns from k on read as zeros
-      if (a.packed ? s >= a.steps64 : s * 64 + (c & 1) * 32 + (lane >> 4) * 8 >= a.k) off = 0x7FFFFFF0;
-      panel_dma16(xr, __builtin_amdgcn_readfirstlane(dst + c * 1024), off);
+      const int64_t tok = tok0 + (c >> 4) * 16 + (lane & 15);
+      const int32_t col = q * 512 + (c & 15) * 32 + (lane >> 4) * 8;
+      xr[t] = tok < a.m ? load8_16(a.x + tok * a.ldx, col, a.k) : make_uint4(0, 0, 0, 0);
     }
+  };
+  auto store_x = [&](int32_t q) {
+#pragma unroll
+    for (int t = 0; t < kLoads; ++t)
+      *reinterpret_cast<uint4*>(q4_smem + (q & 1) * kX + (wave * kLoads + t) * 1024 + lane * 16) = xr[t];
   };
   uint4 code[2][P][4], scale[2][P];
   auto load_w = [&](int32_t q, uint4 (&c)[P][4], uint4 (&sc)[P]) {
@@ -516,12 +515,13 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
     for (int j = 0; j < BP; ++j) acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto step = [&](int32_t q, auto buf) {
     constexpr int B = decltype(buf)::value;
-    panel_wait<0>();
-    __syncthreads();
+    // the other half of the LDS was read ahead of the last barrier
+    store_x(q);
     if (q + 1 < q1) {
-      issue_x(q + 1);
+      load_x(q + 1);
       load_w(q + 1, code[1 - B], scale[1 - B]);
     }
+    __syncthreads();
     const char* xs = q4_smem + (q & 1) * kX + lane * 16;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -543,15 +543,16 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
     }
   };
   if (q0 < q1) {
-    issue_x(q0);
+    load_x(q0);
     load_w(q0, code[0], scale[0]);
   }
   for (int32_t q = q0; q < q1; q += 2) {
     step(q, std::integral_constant<int, 0>());
     if (q + 1 < q1) step(q + 1, std::integral_constant<int, 1>());
   }
+  const int64_t block = int64_t(blockIdx.z) * gridDim.x + blockIdx.x;
   if (a.parts > 1) {
-    f32x4_t* out = a.ws + ((int64_t(blockIdx.x) * a.parts + part) * 8 + wave) * (P * BP * 64) + lane;
+    f32x4_t* out = a.ws + ((block * a.parts + part) * 8 + wave) * (P * BP * 64) + lane;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -562,7 +563,7 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
   const int64_t j0 = panel * 16 + (lane >> 4) * 4;
 #pragma unroll
   for (int j = 0; j < BP; ++j)
-    q4_store4(a, j * 16 + (lane & 15), j0, q4_finish<DT, GATED>(a, j0, acc[0][j], acc[P - 1][j]));
+    q4_store4(a, tok0 + j * 16 + (lane & 15), j0, q4_finish<DT, GATED>(a, j0, acc[0][j], acc[P - 1][j]));
 }
 
 // Adds the parts of k_q4_shared in order: one thread per four outputs.
@@ -571,12 +572,13 @@ __global__ __launch_bounds__(256) void k_q4_shared_sum(Q4Args a) {
   constexpr int P = GATED ? 2 : 1;
   const int lane = threadIdx.x & 63;
   const int c = int(blockIdx.y) * 4 + (threadIdx.x >> 6), wave = c / BP, j = c % BP;
-  const int64_t j0 = (int64_t(blockIdx.x) * 8 + wave) * 16 + (lane >> 4) * 4, tok = j * 16 + (lane & 15);
+  const int64_t j0 = (int64_t(blockIdx.x) * 8 + wave) * 16 + (lane >> 4) * 4;
+  const int64_t block = int64_t(blockIdx.z) * gridDim.x + blockIdx.x, tok = (int64_t(blockIdx.z) * BP + j) * 16 + (lane & 15);
   if (tok >= a.m || j0 >= a.n) return;
   f32x4_t v[2];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const f32x4_t* at = a.ws + (int64_t(blockIdx.x) * a.parts * 8 + wave) * (P * BP * 64) + (p * BP + j) * 64 + lane;
+    const f32x4_t* at = a.ws + (block * a.parts * 8 + wave) * (P * BP * 64) + (p * BP + j) * 64 + lane;
     f32x4_t sum = at[0];
 #pragma unroll 4
     for (int t = 1; t < a.parts; ++t) {
@@ -878,10 +880,10 @@ hipError_t run_shared(const Q4Args& a, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_q4_shared<DT, GATED, BP>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
-  const unsigned blocks = unsigned((a.rows16 / 16 + 7) / 8);
-  hipLaunchKernelGGL((k_q4_shared<DT, GATED, BP>), dim3(blocks, unsigned(a.parts)), dim3(512), kLds, s, a);
+  const unsigned blocks = unsigned((a.rows16 / 16 + 7) / 8), tokens = unsigned((a.m + BP * 16 - 1) / (BP * 16));
+  hipLaunchKernelGGL((k_q4_shared<DT, GATED, BP>), dim3(blocks, unsigned(a.parts), tokens), dim3(512), kLds, s, a);
   if ((e = hipGetLastError()) != hipSuccess || a.parts <= 1) return e;
-  hipLaunchKernelGGL((k_q4_shared_sum<DT, GATED, BP>), dim3(blocks, 2 * BP), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_q4_shared_sum<DT, GATED, BP>), dim3(blocks, 2 * BP, tokens), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -892,32 +894,16 @@ hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
     if (a.m == 2) return run_rows<DT, 2, GATED>(a, s);
     return run_rows<DT, 4, GATED>(a, s);
   }
-  // the few tokens of k_q4_shared where they lie if their rows are whole 16-byte
-  // pieces (a tile's, read 64 bytes of a row at a time, cost it a fifth of its time)
-  a.packed = r.bp > 4 || a.k % 8 != 0 || a.ldx % 8 != 0 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || a.ldx >= (1 << 22);
-  if (a.packed) {
-    const hipError_t e = launch_pack_x(a.x, a.ldx, a.m, a.k, ws, s);
-    if (e != hipSuccess) return e;
-    a.xt = ws;
-    a.x_panel = int64_t(a.steps64) * 2048;
-    a.x_row = 16;
-    a.x_unit = 256;
-    a.x_step = 2048;
-    a.x_half = 1024;
-  } else {
-    a.xt = reinterpret_cast<const char*>(a.x);
-    a.x_row = a.ldx * 2;
-    a.x_panel = 16 * a.x_row;
-    a.x_unit = 16;
-    a.x_step = 128;
-    a.x_half = 64;
-  }
+  a.ws = reinterpret_cast<f32x4_t*>(ws + q4_pack_bytes(r, a.k, a.m));
   a.parts = r.parts;
   a.whole = int32_t(r.whole);
-  a.ws = reinterpret_cast<f32x4_t*>(ws + q4_pack_bytes(r, a.k, a.m));
   if (r.bp == 1) return run_shared<DT, GATED, 1>(a, s);
   if (r.bp == 2) return run_shared<DT, GATED, 2>(a, s);
   if (r.bp == 4) return run_shared<DT, GATED, 4>(a, s);
+  const hipError_t e = launch_pack_x(a.x, a.ldx, a.m, a.k, ws, s);
+  if (e != hipSuccess) return e;
+  a.xt = ws;
+  a.x_panel = int64_t(a.steps64) * 2048;
   if (r.bp == 8) return run_tile<DT, GATED, 16, 8, 4, 2>(a, s);
   return run_tile<DT, GATED, 16, 16, 2, 4>(a, s);
 }

@@ -23,8 +23,7 @@ inline int64_t q4_quads(int64_t k) { return (q4_steps(k) + 3) / 4; }
 inline int64_t q4_rows16(int64_t rows) { return (rows + 15) / 16 * 16; }
 
 // How a product runs.  bp = 0: the register-fed kernel (few tokens).  bp = 1, 2
-// or 4 token panels: k_q4_shared, k cut into `parts` for every eight weight
-// panels.  Else LDS-fed tiles of ap weight panels x bp token panels, of which the
+// or 4 token panels: k_q4_shared (ap = 8), k cut into `parts`.  Else LDS-fed tiles of ap weight panels x bp token panels, of which the
 // first `whole` run over all of k and the others are cut into `parts`.  A gated
 // product (`matrices` = 2) takes half of a tile's ap panels from each weight.
 struct Q4Route {
@@ -35,8 +34,7 @@ struct Q4Route {
 Q4Route q4_route(int64_t n, int64_t k, int64_t m, int matrices, int64_t cus);
 // Workgroups of a route's product (0 for the register-fed kernel).
 int64_t q4_groups(const Q4Route& r, int64_t n, int64_t m, int matrices);
-// Workspace: activations as panels (not for the register-fed kernel), then the
-// parts' sums.
+// Workspace: a tile's activations as panels, then the parts' sums.
 size_t q4_pack_bytes(const Q4Route& r, int64_t k, int64_t m);
 size_t q4_part_bytes(const Q4Route& r, int64_t n, int64_t m, int matrices);
 

@@ -12,7 +12,7 @@ constexpr int64_t kRowsTokens = 4;
 constexpr int64_t kSharedTokens = 64;
 
 int64_t tiles_of(const Q4Route& r, int64_t n, int64_t m, int matrices) {
-  return r.ap == 8 ? up(n, 128) : up(n, 16 * r.ap / matrices) * up(m, 16 * r.bp);
+  return (r.ap == 8 ? up(n, 128) : up(n, 16 * r.ap / matrices)) * up(m, 16 * r.bp);
 }
 
 }  // namespace
@@ -63,7 +63,7 @@ int64_t q4_groups(const Q4Route& r, int64_t n, int64_t m, int matrices) {
 }
 
 size_t q4_pack_bytes(const Q4Route& r, int64_t k, int64_t m) {
-  return r.bp == 0 ? 0 : size_t(up(m, 16)) * size_t(up(k, 64)) * 2048;
+  return r.ap != 16 ? 0 : size_t(up(m, 16)) * size_t(up(k, 64)) * 2048;
 }
 
 size_t q4_part_bytes(const Q4Route& r, int64_t n, int64_t m, int matrices) {
