@@ -279,6 +279,26 @@ __device__ __forceinline__ uint4 load8_16(const uint16_t* row, int32_t c0, int32
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight columns moved down by `by` (none if it is not positive), zeros behind.
+__device__ __forceinline__ uint4 move_down(uint4 u, int by) {
+  if (by >= 8) return make_uint4(0, 0, 0, 0);
+  if (by > 0) {
+    if (by & 4) u = make_uint4(u.z, u.w, 0, 0);
+    if (by & 2) u = make_uint4(u.y, u.z, u.w, 0);
+    if (by & 1)
+      u = make_uint4(u.x >> 16 | u.y << 16, u.y >> 16 | u.z << 16, u.z >> 16 | u.w << 16, u.w >> 16);
+  }
+  return u;
+}
+
+// Sets of registers that a wavefront's codes of 512 columns take turns in: the
+// next are loaded whole ahead of the products (two), or, with two weights, step by
+// step into the registers that the products have done with (one: the gated kernels
+// would need 145 registers, and 17408x5120 at 32 tokens takes 36.8 us instead of
+// 31.9; a single weight's with one 8192x28672 at 64 tokens 67.9 instead of 60.2).
+template <int P>
+constexpr int kRing = P == 1 ? 2 : 1;
+
 // Few tokens: one workgroup per panel (of each weight, gated), its wavefronts
 // cut k.  A lane loads 16 bytes of codes a step (32 codes of its row, eight for
 // each of four matrix instructions), 16 bytes of scales per four steps, and the
@@ -306,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
     scale_at[p] = a.w[p].scales + row * 16;
     lift[p] = DT == HYB_F16 ? kTopLift - int(a.w[p].tops[row]) : 0;
   }
-  uint4 code[2][P][4], scale[2][P], xr[MT];
+  uint4 code[kRing<P>][P][4], scale[2][P], xr[MT];
   f32x4_t acc[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -316,27 +336,38 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
     for (int t = 0; t < MT; ++t)
       xr[t] = tok0 + t < a.m ? load8_16(a.x + (tok0 + t) * a.ldx, q * 512 + lane * 8, a.k) : make_uint4(0, 0, 0, 0);
   };
-  auto load_w = [&](int32_t q, uint4 (&c)[P][4], uint4 (&sc)[P]) {
+  auto load_scale = [&](int32_t q, uint4 (&sc)[P]) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+    for (int p = 0; p < P; ++p) sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+  };
+  auto load_step = [&](int32_t step, uint4 (&c)[P][4], int s) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)  // (steps behind the last lie behind the resource: zeros)
-        c[p][s] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], (q * 4 + s) * 1024 + lane * 16, 0, HYB_W_AUX));
-    }
+    for (int p = 0; p < P; ++p)  // (steps behind the last lie behind the resource: zeros)
+      c[p][s] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], step * 1024 + lane * 16, 0, HYB_W_AUX));
   };
   const int t16 = lane & 15;
   const char* xb = xs + (t16 < MT ? t16 : MT - 1) * kRow + (lane >> 4) * 16;
-  auto step = [&](int32_t q, auto buf) {
-    constexpr int B = decltype(buf)::value;
+  if (q0 < q1) {
+    load_x(q0);
+    load_scale(q0, scale[0]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load_step(q0 * 4 + s, code[0], s);
+  }
+  auto quad = [&](int32_t q, auto turn) {
+    constexpr int T = decltype(turn)::value, B = kRing<P> == 2 ? T : 0;
+    const bool more = q + 1 < q1;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int t = 0; t < MT; ++t) *reinterpret_cast<uint4*>(xs + t * kRow + lane * 16) = xr[t];
     __builtin_amdgcn_wave_barrier();
-    if (q + 1 < q1) {
+    if (more) {
       load_x(q + 1);
-      load_w(q + 1, code[1 - B], scale[1 - B]);
+      load_scale(q + 1, scale[1 - T]);
+      if constexpr (kRing<P> == 2) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) load_step(q * 4 + 4 + s, code[1 - B], s);
+      }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -347,20 +378,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
       for (int p = 0; p < P; ++p) {
         const uint4 cw = code[B][p][s];
         const uint32_t c[4] = {cw.x, cw.y, cw.z, cw.w};
-        const uint32_t sw = s == 0 ? scale[B][p].x : s == 1 ? scale[B][p].y : s == 2 ? scale[B][p].z : scale[B][p].w;
+        const uint32_t sw = s == 0 ? scale[T][p].x : s == 1 ? scale[T][p].y : s == 2 ? scale[T][p].z : scale[T][p].w;
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           acc[p] = mfma16x16x32<DT>(widen_codes4<DT>(c[h], group_scale<DT>(sw, h, lift[p])), b[h], acc[p]);
       }
+      if (kRing<P> == 1 && more) load_step(q * 4 + 4 + s, code[0], s);
     }
   };
-  if (q0 < q1) {
-    load_x(q0);
-    load_w(q0, code[0], scale[0]);
-  }
   for (int32_t q = q0; q < q1; q += 2) {
-    step(q, std::integral_constant<int, 0>());
-    if (q + 1 < q1) step(q + 1, std::integral_constant<int, 1>());
+    quad(q, std::integral_constant<int, 0>());
+    if (q + 1 < q1) quad(q + 1, std::integral_constant<int, 1>());
   }
   // sums of the wavefronts, in order: [wave][weight][token][row]
   __builtin_amdgcn_wave_barrier();
@@ -487,39 +515,59 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
 #pragma unroll
     for (int t = 0; t < kLoads; ++t) {
       const int c = wave * kLoads + t;
+      // (a lane behind the last token or at the row's end loads the last token's or
+      // the row's last eight columns, so that no load branches)
       const int64_t tok = tok0 + (c >> 4) * 16 + (lane & 15);
       const int32_t col = q * 512 + (c & 15) * 32 + (lane >> 4) * 8;
-      xr[t] = tok < a.m ? load8_16(a.x + tok * a.ldx, col, a.k) : make_uint4(0, 0, 0, 0);
+      const Bytes16 u = *reinterpret_cast<const Bytes16*>(a.x + (tok < a.m ? tok : a.m - 1) * a.ldx +
+                                                          (col < a.k - 8 ? col : a.k - 8));
+      xr[t] = make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
     }
   };
   auto store_x = [&](int32_t q) {
+    if ((q + 1) * 512 > a.k) {
+#pragma unroll
+      for (int t = 0; t < kLoads; ++t)
+        xr[t] = move_down(xr[t], q * 512 + ((wave * kLoads + t) & 15) * 32 + (lane >> 4) * 8 - (a.k - 8));
+    }
 #pragma unroll
     for (int t = 0; t < kLoads; ++t)
       *reinterpret_cast<uint4*>(q4_smem + (q & 1) * kX + (wave * kLoads + t) * 1024 + lane * 16) = xr[t];
   };
-  uint4 code[2][P][4], scale[2][P];
-  auto load_w = [&](int32_t q, uint4 (&c)[P][4], uint4 (&sc)[P]) {
+  uint4 code[kRing<P>][P][4], scale[2][P];
+  auto load_scale = [&](int32_t q, uint4 (&sc)[P]) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+    for (int p = 0; p < P; ++p) sc[p] = *reinterpret_cast<const uint4*>(scale_at[p] + int64_t(q) * a.rows16 * 16);
+  };
+  auto load_step = [&](int32_t step, uint4 (&c)[P][4], int s) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)  // (steps behind the last lie behind the resource: zeros)
-        c[p][s] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], (q * 4 + s) * 1024 + lane * 16, 0, HYB_W_AUX));
-    }
+    for (int p = 0; p < P; ++p)
+      c[p][s] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(code_rsrc[p], step * 1024 + lane * 16, 0, HYB_W_AUX));
   };
   f32x4_t acc[P][BP];
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < BP; ++j) acc[p][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int32_t q, auto buf) {
-    constexpr int B = decltype(buf)::value;
-    // the other half of the LDS was read ahead of the last barrier
+  if (q0 < q1) {
+    load_x(q0);
+    load_scale(q0, scale[0]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load_step(q0 * 4 + s, code[0], s);
+  }
+  auto quad = [&](int32_t q, auto turn) {
+    constexpr int T = decltype(turn)::value, B = kRing<P> == 2 ? T : 0;
+    const bool more = q + 1 < q1;
+    // (this half of the LDS was read ahead of the last barrier)
     store_x(q);
-    if (q + 1 < q1) {
+    if (more) {
       load_x(q + 1);
-      load_w(q + 1, code[1 - B], scale[1 - B]);
+      load_scale(q + 1, scale[1 - T]);
+      if constexpr (kRing<P> == 2) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) load_step(q * 4 + 4 + s, code[1 - B], s);
+      }
     }
     __syncthreads();
     const char* xs = q4_smem + (q & 1) * kX + lane * 16;
@@ -534,21 +582,18 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
         for (int p = 0; p < P; ++p) {
           const uint4 cw = code[B][p][s];
           const uint32_t c = h == 0 ? cw.x : h == 1 ? cw.y : h == 2 ? cw.z : cw.w;
-          const uint32_t sw = s == 0 ? scale[B][p].x : s == 1 ? scale[B][p].y : s == 2 ? scale[B][p].z : scale[B][p].w;
+          const uint32_t sw = s == 0 ? scale[T][p].x : s == 1 ? scale[T][p].y : s == 2 ? scale[T][p].z : scale[T][p].w;
           const uint4 w = widen_codes4<DT>(c, group_scale<DT>(sw, h, lift[p]));
 #pragma unroll
           for (int j = 0; j < BP; ++j) acc[p][j] = mfma16x16x32<DT>(w, b[j], acc[p][j]);
         }
       }
+      if (kRing<P> == 1 && more) load_step(q * 4 + 4 + s, code[0], s);
     }
   };
-  if (q0 < q1) {
-    load_x(q0);
-    load_w(q0, code[0], scale[0]);
-  }
   for (int32_t q = q0; q < q1; q += 2) {
-    step(q, std::integral_constant<int, 0>());
-    if (q + 1 < q1) step(q + 1, std::integral_constant<int, 1>());
+    quad(q, std::integral_constant<int, 0>());
+    if (q + 1 < q1) quad(q + 1, std::integral_constant<int, 1>());
   }
   const int64_t block = int64_t(blockIdx.z) * gridDim.x + blockIdx.x;
   if (a.parts > 1) {
