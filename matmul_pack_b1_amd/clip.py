@@ -9,6 +9,7 @@ Argument marshalling only, as in binding.py.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -23,6 +24,12 @@ class HybTensor(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldo", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
+# One descriptor as the binding packs it (its last word is the type and padding).
+_WORDS = 7
+assert ctypes.sizeof(HybTensor) == 8 * _WORDS
+_PER_LAUNCH = 64            # tensors of one launch, and the partial sums of one
+_SUM_BYTES = 2048 * 8
+
 _ready = False
 
 
@@ -30,7 +37,7 @@ def lib() -> ctypes.CDLL:
     global _ready
     L = hb.lib()
     if not _ready:
-        P, I64, SZ, T = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(HybTensor)
+        P, I64, SZ, T = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
         L.hyb_clip_workspace_size.argtypes = [I64, T, ctypes.POINTER(SZ)]
         L.hyb_norm.argtypes = [I64, T, P, P, SZ, P]
         L.hyb_clip.argtypes = [I64, T, ctypes.c_float, P, P, SZ, P]
@@ -44,45 +51,63 @@ def _rows(t, name):
     """(rows, columns, row stride) of a tensor that is contiguous, or 2-D with
     unit column stride and rows apart."""
     if t.is_contiguous():
-        return 1, t.numel(), t.numel()
+        n = t.numel()
+        return 1, n, n
     if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
         return t.shape[0], t.shape[1], t.stride(0)
     raise ValueError(f"{name} must be contiguous, or 2-D with unit column stride")
 
 
+def _refuse(i, t, out, index):
+    """What is wrong with a tensor and its output, of which something is."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"tensor {i} is a {type(t).__name__}")
+    if t.dtype not in _CODES:
+        raise TypeError(f"tensor {i} is {t.dtype}: float16, bfloat16 or float32")
+    _rows(t, f"tensor {i}")
+    if not isinstance(out, torch.Tensor) or out.shape != t.shape:
+        raise ValueError(f"outs[{i}] must be a tensor of shape {tuple(t.shape)}")
+    if out.dtype != t.dtype:
+        raise TypeError(f"outs[{i}] is {out.dtype}, expected {t.dtype}")
+    _rows(out, f"outs[{i}]")
+    device = None if index is None else torch.device("cuda", index)
+    hb._check_gpu(t, f"tensor {i}", device)
+    hb._check_gpu(out, f"outs[{i}]", t.device)
+    raise ValueError(f"tensor {i} cannot be used")
+
+
 def _list(tensors, outs):
-    """(count, C array, device)."""
+    """(count, C array as bytes, device).  The checks of each tensor come first
+    in one condition (a step has many tensors, and its time is the host's)."""
     tensors = list(tensors)
-    if outs is not None:
-        outs = list(outs)
-        if len(outs) != len(tensors):
-            raise ValueError(f"{len(outs)} outs for {len(tensors)} tensors")
-    array = (HybTensor * max(len(tensors), 1))()
-    device = None
+    outs = tensors if outs is None else list(outs)
+    if len(outs) != len(tensors):
+        raise ValueError(f"{len(outs)} outs for {len(tensors)} tensors")
+    words, index, Tensor = [], None, torch.Tensor
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"tensor {i} is a {type(t).__name__}")
-        code = _CODES.get(t.dtype)
+        out = outs[i]
+        code = _CODES.get(t.dtype) if isinstance(t, Tensor) else None
         if code is None:
-            raise TypeError(f"tensor {i} is {t.dtype}: float16, bfloat16 or float32")
+            _refuse(i, t, out, index)
+        at = t.get_device()
+        if at < 0 or (at != index and index is not None):
+            _refuse(i, t, out, index)
+        index = at
+        if out is not t and (not isinstance(out, Tensor) or out.dtype is not t.dtype or out.shape != t.shape
+                             or out.get_device() != at):
+            _refuse(i, t, out, index)
+        if t.is_contiguous() and (out is t or out.is_contiguous()):
+            n = t.numel()
+            words += (t.data_ptr(), out.data_ptr(), 1, n, n, n, code)
+            continue
         rows, cols, lda = _rows(t, f"tensor {i}")
-        out, ldo = t, lda
-        if outs is not None:
-            out = outs[i]
-            if not isinstance(out, torch.Tensor) or out.shape != t.shape:
-                raise ValueError(f"outs[{i}] must be a tensor of shape {tuple(t.shape)}")
-            if out.dtype != t.dtype:
-                raise TypeError(f"outs[{i}] is {out.dtype}, expected {t.dtype}")
-            orows, ocols, ldo = _rows(out, f"outs[{i}]")
-            if (orows, ocols) != (rows, cols):   # one of the two is contiguous: take it as rows too
-                rows, cols = t.shape
-                lda, ldo = (s.stride(0) if not s.is_contiguous() else cols for s in (t, out))
-        hb._check_gpu(t, f"tensor {i}", device)
-        device = t.device
-        if out is not t:
-            hb._check_gpu(out, f"outs[{i}]", device)
-        array[i] = HybTensor(hb._ptr(t), hb._ptr(out), rows, cols, lda, ldo, code)
-    return len(tensors), array, device
+        orows, _, ldo = _rows(out, f"outs[{i}]")
+        if orows != rows:   # one of the two is contiguous: take it as rows too
+            rows, cols = t.shape
+            lda, ldo = (s.stride(0) if not s.is_contiguous() else cols for s in (t, out))
+        words += (t.data_ptr(), out.data_ptr(), rows, cols, lda, ldo, code)
+    return (len(tensors), struct.pack(f"<{len(words)}Q", *words),
+            None if index is None else torch.device("cuda", index))
 
 
 def _run(tensors, outs, max_norm, out, workspace):
@@ -94,10 +119,8 @@ def _run(tensors, outs, max_norm, out, workspace):
             raise ValueError("out must hold one float32")
         hb._check_gpu(out, "out", device)
     with _on(device):
-        if workspace is None:
-            nbytes = ctypes.c_size_t(0)
-            hb.check(lib().hyb_clip_workspace_size(count, array, ctypes.byref(nbytes)), "hyb_clip_workspace_size")
-            nbytes = int(nbytes.value)
+        if workspace is None:   # the most that so many tensors need
+            nbytes = -(-count // _PER_LAUNCH) * _SUM_BYTES
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
             hb._check_gpu(workspace, "workspace", device)

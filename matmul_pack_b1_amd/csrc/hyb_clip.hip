@@ -10,19 +10,23 @@
 namespace hyb {
 namespace {
 
-// The tensors of one launch; tensor i has chunks start[i] .. start[i + 1] - 1,
-// rows' chunks one after the other.
+// The tensors of one launch, at most N; tensor i has chunks start[i] ..
+// start[i + 1] - 1, rows' chunks one after the other.  (A short list has a small
+// table: the host copies it for every launch.)
+template <int N>
 struct ClipTable {
-  const char* data[kClipTensors];
-  char* out[kClipTensors];
-  int64_t cols[kClipTensors], lda[kClipTensors], ldo[kClipTensors];
-  int64_t start[kClipTensors + 1];
-  uint8_t dtype[kClipTensors];
+  const char* data[N];
+  char* out[N];
+  int64_t cols[N], lda[N], ldo[N];
+  int64_t start[N + 1];
+  uint8_t dtype[N];
   int32_t count;
 };
-static_assert(sizeof(ClipTable) + 64 <= 4096, "kernel arguments");
+static_assert(sizeof(ClipTable<kClipTensors>) + 64 <= 4096, "kernel arguments");
+constexpr int kClipFew = 12;
 
-__device__ __forceinline__ int clip_find(const ClipTable& t, int64_t chunk) {
+template <int N>
+__device__ __forceinline__ int clip_find(const ClipTable<N>& t, int64_t chunk) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -78,12 +82,12 @@ __device__ __forceinline__ double clip_chunk(const char* p, int32_t n) {
   const int32_t whole = n / kEach;
   double s = 0.0;
   int32_t i = threadIdx.x;
-  for (; i + 768 < whole; i += 1024) {
-    Bytes16 b[4];
+  for (; i + 1792 < whole; i += 2048) {
+    Bytes16 b[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
+    for (int u = 0; u < 8; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s += clip_squares<DT>(b[u]);
+    for (int u = 0; u < 8; ++u) s += clip_squares<DT>(b[u]);
   }
   for (; i < whole; i += 256) s += clip_squares<DT>(reinterpret_cast<const Bytes16*>(p)[i]);
   const int32_t at = whole * kEach + int32_t(threadIdx.x);
@@ -95,8 +99,8 @@ __device__ __forceinline__ double clip_chunk(const char* p, int32_t n) {
 }
 
 // Chunk `chunk` of tensor i: f(data, out, elements).
-template <typename F>
-__device__ __forceinline__ void clip_at(const ClipTable& t, int i, int64_t chunk, F f) {
+template <int N, typename F>
+__device__ __forceinline__ void clip_at(const ClipTable<N>& t, int i, int64_t chunk, F f) {
   const int64_t per = (t.cols[i] + kClipChunk - 1) / kClipChunk, c = chunk - t.start[i];
   const int64_t row = c / per, col = (c - row * per) * kClipChunk;
   const int32_t n = int32_t(t.cols[i] - col < kClipChunk ? t.cols[i] - col : kClipChunk);
@@ -104,14 +108,13 @@ __device__ __forceinline__ void clip_at(const ClipTable& t, int i, int64_t chunk
   f(t.data[i] + (row * t.lda[i] + col) * size, t.out[i] + (row * t.ldo[i] + col) * size, n);
 }
 
-__global__ __launch_bounds__(256) void k_clip_squares(ClipTable t, double* __restrict__ sums) {
+template <int N>
+__global__ __launch_bounds__(256) void k_clip_squares(ClipTable<N> t, double* __restrict__ sums) {
   __shared__ double lds[4];
   const int64_t all = t.start[t.count];
-  const int64_t c0 = all * blockIdx.x / gridDim.x, c1 = all * (blockIdx.x + 1) / gridDim.x;
-  int i = clip_find(t, c0);
   double s = 0.0;
-  for (int64_t c = c0; c < c1; ++c) {
-    while (c >= t.start[i + 1]) ++i;
+  for (int64_t c = blockIdx.x; c < all; c += gridDim.x) {
+    const int i = clip_find(t, c);
     clip_at(t, i, c, [&](const char* p, char*, int32_t n) {
       if (t.dtype[i] == HYB_F32)
         s += clip_chunk<HYB_F32>(p, n);
@@ -155,12 +158,12 @@ __device__ __forceinline__ void clip_scale(const char* p, char* q, int32_t n, fl
     return r;
   };
   int32_t i = threadIdx.x;
-  for (; i + 768 < whole; i += 1024) {
-    Bytes16 b[4];
+  for (; i + 1792 < whole; i += 2048) {
+    Bytes16 b[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
+    for (int u = 0; u < 8; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) reinterpret_cast<Bytes16*>(q)[i + 256 * u] = scaled(b[u]);
+    for (int u = 0; u < 8; ++u) reinterpret_cast<Bytes16*>(q)[i + 256 * u] = scaled(b[u]);
   }
   for (; i < whole; i += 256) reinterpret_cast<Bytes16*>(q)[i] = scaled(reinterpret_cast<const Bytes16*>(p)[i]);
   const int32_t at = whole * kEach + int32_t(threadIdx.x);
@@ -175,18 +178,19 @@ __device__ __forceinline__ void clip_scale(const char* p, char* q, int32_t n, fl
 
 // Every workgroup takes the norm from the sums itself (they lie in the caches),
 // which saves a launch.
-__global__ __launch_bounds__(256) void k_clip_scale(ClipTable t, const double* __restrict__ sums, int64_t count,
+template <int N>
+__global__ __launch_bounds__(256) void k_clip_scale(ClipTable<N> t, const double* __restrict__ sums, int64_t count,
                                                     float max_norm, float* __restrict__ norm) {
   __shared__ double lds[4];
   const double v = clip_norm(sums, count, lds);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(v);
   const double r = double(max_norm) / (v + 1e-6);
   const float f = r < 1.0 || r != r ? float(r) : 1.f;
+  // from the last chunk to the first: what the squares read last lies in the
+  // last-level cache
   const int64_t all = t.start[t.count];
-  const int64_t c0 = all * blockIdx.x / gridDim.x, c1 = all * (blockIdx.x + 1) / gridDim.x;
-  int i = clip_find(t, c0);
-  for (int64_t c = c0; c < c1; ++c) {
-    while (c >= t.start[i + 1]) ++i;
+  for (int64_t c = all - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+    const int i = clip_find(t, c);
     if (f == 1.f && t.out[i] == t.data[i]) continue;
     clip_at(t, i, c, [&](const char* p, char* q, int32_t n) {
       if (t.dtype[i] == HYB_F32)
@@ -199,9 +203,11 @@ __global__ __launch_bounds__(256) void k_clip_scale(ClipTable t, const double* _
   }
 }
 
-ClipTable table_of(const std::vector<hyb_tensor>& tensors, const ClipLaunch& l) {
-  ClipTable t{};
+template <int N>
+ClipTable<N> table_of(const std::vector<hyb_tensor>& tensors, const ClipLaunch& l) {
+  ClipTable<N> t;
   t.count = l.count;
+  t.start[0] = 0;
   for (int j = 0; j < l.count; ++j) {
     const hyb_tensor& x = tensors[l.first + j];
     t.data[j] = static_cast<const char*>(x.data);
@@ -218,7 +224,12 @@ ClipTable table_of(const std::vector<hyb_tensor>& tensors, const ClipLaunch& l) 
 hipError_t launch_squares(const std::vector<hyb_tensor>& tensors, const std::vector<ClipLaunch>& plan, double* ws,
                           hipStream_t s) {
   for (const ClipLaunch& l : plan) {
-    hipLaunchKernelGGL(k_clip_squares, dim3(unsigned(l.groups)), dim3(256), 0, s, table_of(tensors, l), ws + l.sum0);
+    const dim3 grid(unsigned(l.groups));
+    if (l.count <= kClipFew)
+      hipLaunchKernelGGL((k_clip_squares<kClipFew>), grid, dim3(256), 0, s, table_of<kClipFew>(tensors, l), ws + l.sum0);
+    else
+      hipLaunchKernelGGL((k_clip_squares<kClipTensors>), grid, dim3(256), 0, s, table_of<kClipTensors>(tensors, l),
+                         ws + l.sum0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -241,9 +252,15 @@ hipError_t launch_clip(const std::vector<hyb_tensor>& tensors, float max_norm, f
   int64_t sums;
   const std::vector<ClipLaunch> plan = clip_plan(tensors, &sums);
   hipError_t e = launch_squares(tensors, plan, ws, s);
-  for (size_t i = 0; i < plan.size() && e == hipSuccess; ++i) {
-    hipLaunchKernelGGL(k_clip_scale, dim3(unsigned(plan[i].groups)), dim3(256), 0, s, table_of(tensors, plan[i]), ws, sums,
-                       max_norm, i == 0 ? norm : nullptr);
+  for (size_t i = plan.size(); i-- > 0 && e == hipSuccess;) {
+    const dim3 grid(unsigned(plan[i].groups));
+    float* to = i == 0 ? norm : nullptr;
+    if (plan[i].count <= kClipFew)
+      hipLaunchKernelGGL((k_clip_scale<kClipFew>), grid, dim3(256), 0, s, table_of<kClipFew>(tensors, plan[i]), ws, sums,
+                         max_norm, to);
+    else
+      hipLaunchKernelGGL((k_clip_scale<kClipTensors>), grid, dim3(256), 0, s, table_of<kClipTensors>(tensors, plan[i]), ws,
+                         sums, max_norm, to);
     e = hipGetLastError();
   }
   return e;
