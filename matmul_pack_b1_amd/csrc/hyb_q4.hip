@@ -11,37 +11,75 @@ namespace {
 
 // ------------------------------------------------------ quantise, read back --
 
-// Eight columns c0.. of one row as fp32; columns from k on are zero.
+// Eight columns of one row, as loaded: two elements to a word, or one for fp32.
 template <int DT>
-__device__ __forceinline__ void load8_f32(const void* a, int64_t base, int32_t c0, int32_t k, float (&v)[8]) {
-  if (c0 + 8 <= k) {
-    if constexpr (DT == HYB_F32) {
-      const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const float*>(a) + base + c0);
-      const Bytes16 lo = p[0], hi = p[1];
+struct Eight4 {
+  uint32_t w[DT == HYB_F32 ? 8 : 4];
+};
+
+// Columns c0.. of the row at element `base`.  A lane at or behind the row's end
+// loads the row's last eight columns (k >= 8), so that a wavefront's loads need no
+// branches and are all under way at once; trim4 then moves its columns into place
+// and zeros the rest.
+template <int DT>
+__device__ __forceinline__ Eight4<DT> load4(const void* a, int64_t base, int32_t c0, int32_t k) {
+  Eight4<DT> r;
+  constexpr int kWords = DT == HYB_F32 ? 8 : 4;
+  if (k < 8) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __builtin_bit_cast(float, lo.w[i]);
-        v[4 + i] = __builtin_bit_cast(float, hi.w[i]);
-      }
-    } else {
-      const Bytes16 u = *reinterpret_cast<const Bytes16*>(static_cast<const uint16_t*>(a) + base + c0);
+    for (int i = 0; i < kWords; ++i) r.w[i] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = widen16<DT>(u.w[i] & 0xFFFFu);
-        v[2 * i + 1] = widen16<DT>(u.w[i] >> 16);
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < k) {
+        if constexpr (DT == HYB_F32)
+          r.w[i] = static_cast<const uint32_t*>(a)[base + c0 + i];
+        else
+          r.w[i / 2] |= uint32_t(static_cast<const uint16_t*>(a)[base + c0 + i]) << (16 * (i & 1));
       }
-    }
-    return;
+    return r;
   }
+  const int64_t at = base + (c0 < k - 8 ? c0 : k - 8);
+  const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.f;
-    if (c0 + i < k) {
-      if constexpr (DT == HYB_F32)
-        v[i] = static_cast<const float*>(a)[base + c0 + i];
-      else
-        v[i] = widen16<DT>(static_cast<const uint16_t*>(a)[base + c0 + i]);
-    }
+  for (int i = 0; i < kWords / 4; ++i) {
+    const Bytes16 u = p[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[4 * i + j] = u.w[j];
+  }
+  return r;
+}
+
+// Eight 16-bit columns moved down by `by` (none if it is not positive), zeros
+// behind.
+__device__ __forceinline__ uint4 move_down(uint4 u, int by) {
+  if (by >= 8) return make_uint4(0, 0, 0, 0);
+  if (by > 0) {
+    if (by & 4) u = make_uint4(u.z, u.w, 0, 0);
+    if (by & 2) u = make_uint4(u.y, u.z, u.w, 0);
+    if (by & 1)
+      u = make_uint4(u.x >> 16 | u.y << 16, u.y >> 16 | u.z << 16, u.z >> 16 | u.w << 16, u.w >> 16);
+  }
+  return u;
+}
+
+template <int DT>
+__device__ __forceinline__ void trim4(Eight4<DT>& r, int32_t c0, int32_t k) {
+  if (k < 8) return;
+  const int32_t by = c0 - (k - 8);
+  if constexpr (DT == HYB_F32) {
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (by > 0 && (by & d)) r.w[i] = i + d < 8 ? r.w[i + d < 8 ? i + d : 0] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = by >= 8 ? 0 : r.w[i];
+  } else {
+    const uint4 u = move_down(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]), by);
+    r.w[0] = u.x;
+    r.w[1] = u.y;
+    r.w[2] = u.z;
+    r.w[3] = u.w;
   }
 }
 
@@ -55,58 +93,81 @@ __device__ __forceinline__ uint32_t group_byte(uint32_t top) {
   return uint32_t(e < 2 ? 2 : e > 252 ? 252 : e);
 }
 
-// One workgroup per panel, a wavefront per four steps at a time: a load covers
-// 128 columns of four rows (8 columns per lane, 16 lanes to a row, four to a
-// group), codes and scales are put into the stream's order in LDS.
+// One workgroup per panel, a wavefront per 512 columns at a time: a load covers
+// them in one row (8 columns per lane, four lanes to a group), codes and scales are
+// put into the stream's order in LDS.
 template <int DT>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a, int64_t n, int32_t k, int64_t lda,
                                                      int32_t steps, int64_t rows16, char* __restrict__ codes,
                                                      char* __restrict__ scales) {
-  __shared__ __attribute__((aligned(16))) char stage[4][4096 + 256];
+  // units and steps 4 and 16 banks apart: a row's 64 words lie on 64 banks
+  constexpr int kUnit = 256 + 16, kStep = 4 * kUnit;
+  constexpr int kRows = DT == HYB_F32 ? 4 : 8;  // loaded at once
+  __shared__ __attribute__((aligned(16))) char stage[4][4 * kStep + 256];
   __shared__ uint32_t tops[4][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t panel = blockIdx.x;
   const int32_t quads = (steps + 3) / 4;
-  const int j = lane & 15, rr = lane >> 4;
-  uint32_t best[4] = {0, 0, 0, 0};  // of rows 4 i + rr
+  const int live = n - panel * 16 < 16 ? int(n - panel * 16) : 16;  // rows
+  const int j = lane & 15;
   char* mine = stage[wave];
+  char* at = mine + (lane >> 4) * kStep + (j & 3) * kUnit + (j >> 2) * 4;
+  uint32_t best[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) best[r] = 0;
+  // two sets of registers take turns, so that loads are under way during the
+  // arithmetic
+  Eight4<DT> regs[2][kRows];
+  auto load = [&](Eight4<DT> (&in)[kRows], int32_t q, int r0) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      in[r] = load4<DT>(a, (panel * 16 + (r0 + r < live ? r0 + r : live - 1)) * lda, q * 512 + lane * 8, k);
+  };
+  if (wave < quads) load(regs[0], wave, 0);
   for (int32_t q = wave; q < quads; q += 4) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int r0 = 0; r0 < 16; r0 += kRows) {
+      Eight4<DT> (&in)[kRows] = regs[r0 / kRows & 1];
+      if (r0 + kRows < 16)
+        load(regs[(r0 / kRows + 1) & 1], q, r0 + kRows);
+      else if (q + 4 < quads)
+        load(regs[(r0 / kRows + 1) & 1], q + 4, 0);
+      if ((q + 1) * 512 > k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * i + rr;
-        const int64_t row = panel * 16 + r;
-        const int32_t c0 = (q * 4 + s) * 128 + j * 8;
+        for (int r = 0; r < kRows; ++r) trim4<DT>(in[r], q * 512 + lane * 8, k);
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
         float v[8];
-        if (row < n) {
-          load8_f32<DT>(a, row * lda, c0, k, v);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = in[r].w[DT == HYB_F32 ? e : e / 2];
+          v[e] = DT == HYB_F32 ? __builtin_bit_cast(float, w)
+                               : widen16<DT == HYB_F32 ? HYB_BF16 : DT>(e & 1 ? w >> 16 : w & 0xFFFFu);
         }
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu;
+          const float f = v[e];
+          const uint32_t b = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
           top = b > top ? b : top;
         }
-        uint32_t o = __shfl_xor(top, 1);
+        // over the four lanes of the group
+        uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(top), 0xB1, 0xF, 0xF, true));
         top = o > top ? o : top;
-        o = __shfl_xor(top, 2);
-        top = o > top ? o : top;
+        o = uint32_t(__builtin_amdgcn_update_dpp(0, int(top), 0x4E, 0xF, 0xF, true));
+        top = r0 + r < live ? (o > top ? o : top) : 0;
         const uint32_t byte = group_byte(top);
         const float scale = __builtin_bit_cast(float, byte << 23);
         uint32_t code = 0;
-        if (byte != 255u) {
-          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[0], v[1], scale, 0);
-          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[2], v[3], scale, 1);
-          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[4], v[5], scale, 2);
-          code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[6], v[7], scale, 3);
-        }
-        *reinterpret_cast<uint32_t*>(mine + s * 1024 + (j & 3) * 256 + r * 16 + (j >> 2) * 4) = code;
-        if ((j & 3) == 0) mine[4096 + r * 16 + s * 4 + (j >> 2)] = char(byte);
-        if (byte != 255u && top != 0 && byte > best[i]) best[i] = byte;
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[0], v[1], scale, 0);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[2], v[3], scale, 1);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[4], v[5], scale, 2);
+        code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(code, v[6], v[7], scale, 3);
+        code = r0 + r < live && byte != 255u ? code : 0;
+        *reinterpret_cast<uint32_t*>(at + (r0 + r) * 16) = code;
+        if ((j & 3) == 0) mine[4 * kStep + (r0 + r) * 16 + (lane >> 2)] = char(byte);
+        if (byte != 255u && top != 0 && byte > best[r0 + r]) best[r0 + r] = byte;
       }
     }
     // one wavefront writes and reads its own part: its accesses done suffices
@@ -115,20 +176,20 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a,
     for (int s = 0; s < 4; ++s)
       if (q * 4 + s < steps)
         *reinterpret_cast<uint4*>(codes + (panel * steps + q * 4 + s) * kQ4StepBytes + lane * 16) =
-            *reinterpret_cast<const uint4*>(mine + s * 1024 + lane * 16);
+            *reinterpret_cast<const uint4*>(mine + s * kStep + (lane >> 4) * kUnit + j * 16);
     *reinterpret_cast<uint32_t*>(scales + (q * rows16 + panel * 16) * 16 + lane * 4) =
-        *reinterpret_cast<const uint32_t*>(mine + 4096 + lane * 4);
+        *reinterpret_cast<const uint32_t*>(mine + 4 * kStep + lane * 4);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t b = best[i];
+  for (int r = 0; r < 16; ++r) {
+    uint32_t b = best[r];
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
+    for (int d = 1; d < 64; d *= 2) {
       const uint32_t o = __shfl_xor(b, d);
       b = o > b ? o : b;
     }
-    if (j == 0) tops[wave][4 * i + rr] = b;
+    if (lane == 0) tops[wave][r] = b;
   }
   __syncthreads();
   if (threadIdx.x < 16) {
@@ -277,18 +338,6 @@ __device__ __forceinline__ uint4 load8_16(const uint16_t* row, int32_t c0, int32
   for (int i = 0; i < 8; ++i)
     if (c0 + i < k) w[i >> 1] |= uint32_t(row[c0 + i]) << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight columns moved down by `by` (none if it is not positive), zeros behind.
-__device__ __forceinline__ uint4 move_down(uint4 u, int by) {
-  if (by >= 8) return make_uint4(0, 0, 0, 0);
-  if (by > 0) {
-    if (by & 4) u = make_uint4(u.z, u.w, 0, 0);
-    if (by & 2) u = make_uint4(u.y, u.z, u.w, 0);
-    if (by & 1)
-      u = make_uint4(u.x >> 16 | u.y << 16, u.y >> 16 | u.z << 16, u.z >> 16 | u.w << 16, u.w >> 16);
-  }
-  return u;
 }
 
 // Sets of registers that a wavefront's codes of 512 columns take turns in: the
