@@ -38,11 +38,13 @@ struct GatedOut {
 // Four outputs j.. of a token; fp32 rows may be at any 4-byte aligned address.
 template <int DT>
 __device__ __forceinline__ void gated_put(const GatedOut& o, int64_t tok, int32_t j, f32x4_t g, f32x4_t u) {
-  f32x4_t h;
+  with_act(o.act, [&](auto act) {
+    f32x4_t h;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = act_value(o.act, g[e]) * u[e];
-  const uint2 r = round16x4<DT>(h[0], h[1], h[2], h[3]);
-  *reinterpret_cast<Bytes8*>(o.h + tok * o.ldh + j) = Bytes8{{r.x, r.y}};
+    for (int e = 0; e < 4; ++e) h[e] = act_value<decltype(act)::value>(g[e]) * u[e];
+    const uint2 r = round16x4<DT>(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<Bytes8*>(o.h + tok * o.ldh + j) = Bytes8{{r.x, r.y}};
+  });
 }
 __device__ __forceinline__ void gated_keep(float* p, f32x4_t v) {
   const u32x4_t b = __builtin_bit_cast(u32x4_t, v);
@@ -116,18 +118,20 @@ __global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, Pan
     }
   }
   __syncthreads();  // the tile's LDS stages are free
-  panel_rows16<kOut, T::kB>(
-      gated_smem + wave * (kOut * T::kB * 512), lane, lane & 15,
-      [&](int i, int j) {
-        f32x4_t v;
+  with_act(o.act, [&](auto act) {
+    panel_rows16<kOut, T::kB>(
+        gated_smem + wave * (kOut * T::kB * 512), lane, lane & 15,
+        [&](int i, int j) {
+          f32x4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = act_value(o.act, acc[i][j][e]) * acc[i + kOut][j][e];
-        return round16x4<DT>(v[0], v[1], v[2], v[3]);
-      },
-      [&](int r, int c, uint4 v) {
-        const int32_t row = row0 + r, col = col0 + c;
-        if (row < o.m && col < o.n) *reinterpret_cast<Bytes16*>(o.h + row * o.ldh + col) = Bytes16{{v.x, v.y, v.z, v.w}};
-      });
+          for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(act)::value>(acc[i][j][e]) * acc[i + kOut][j][e];
+          return round16x4<DT>(v[0], v[1], v[2], v[3]);
+        },
+        [&](int r, int c, uint4 v) {
+          const int32_t row = row0 + r, col = col0 + c;
+          if (row < o.m && col < o.n) *reinterpret_cast<Bytes16*>(o.h + row * o.ldh + col) = Bytes16{{v.x, v.y, v.z, v.w}};
+        });
+  });
 }
 
 // Adds the parts of the tiles that were cut, in order: one thread per four
@@ -176,22 +180,23 @@ struct GatedGrad {
 };
 
 // dG and dU of one output.
-__device__ __forceinline__ void gated_grad1(int act, float g, float u, float dh, float* dg, float* du) {
+template <int ACT>
+__device__ __forceinline__ void gated_grad1(float g, float u, float dh, float* dg, float* du) {
   float a;
-  const float slope = act_slope(act, g, &a);
+  const float slope = act_slope<ACT>(g, &a);
   *dg = dh * u * slope;
   *du = dh * a;
 }
 
 // Four outputs' dG and dU, from column c on of the rows' starts.
-template <int DT>
-__device__ __forceinline__ void gated_grad4(int act, const float* g, const float* u, const uint16_t* dh, int64_t c,
+template <int DT, int ACT>
+__device__ __forceinline__ void gated_grad4(const float* g, const float* u, const uint16_t* dh, int64_t c,
                                             float* dg, float* du) {
   const Bytes16 gb = *reinterpret_cast<const Bytes16*>(g + c), ub = *reinterpret_cast<const Bytes16*>(u + c);
   const Bytes8 db = *reinterpret_cast<const Bytes8*>(dh + c);
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    gated_grad1(act, __builtin_bit_cast(float, gb.w[e]), __builtin_bit_cast(float, ub.w[e]),
+    gated_grad1<ACT>(__builtin_bit_cast(float, gb.w[e]), __builtin_bit_cast(float, ub.w[e]),
                 widen16<DT>((db.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu), dg + e, du + e);
 }
 
@@ -216,7 +221,9 @@ __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
     const int32_t c = int32_t(blockIdx.x) * 256 + threadIdx.x;
     if (c >= per) break;
     float dg[4], du[4];
-    gated_grad4<DT>(o.act, o.g + t * o.ldg, o.u + t * o.ldu, o.dh + t * o.lddh, int64_t(c) * 4, dg, du);
+    with_act(o.act, [&](auto act) {
+      gated_grad4<DT, decltype(act)::value>(o.g + t * o.ldg, o.u + t * o.ldu, o.dh + t * o.lddh, int64_t(c) * 4, dg, du);
+    });
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t a = __builtin_bit_cast(uint32_t, dg[e]) & 0x7FFFFFFFu;
@@ -258,8 +265,10 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
       float dg[8], du[8];
       const float *g = o.g + tok * o.ldg, *u = o.u + tok * o.ldu;
       const uint16_t* dh = o.dh + tok * o.lddh;
-      gated_grad4<DT>(o.act, g, u, dh, c, dg, du);
-      gated_grad4<DT>(o.act, g, u, dh, c + 8, dg + 4, du + 4);
+      with_act(o.act, [&](auto act) {
+        gated_grad4<DT, decltype(act)::value>(g, u, dh, c, dg, du);
+        gated_grad4<DT, decltype(act)::value>(g, u, dh, c + 8, dg + 4, du + 4);
+      });
       a = make_uint4(round16x2<DT>(dg[0] * lift, dg[1] * lift), round16x2<DT>(dg[2] * lift, dg[3] * lift),
                      round16x2<DT>(dg[4] * lift, dg[5] * lift), round16x2<DT>(dg[6] * lift, dg[7] * lift));
       b = make_uint4(round16x2<DT>(du[0] * lift, du[1] * lift), round16x2<DT>(du[2] * lift, du[3] * lift),

@@ -361,22 +361,24 @@ __device__ __forceinline__ void gemv_slab(const uint4* __restrict__ dense, const
   }
   __syncthreads();
   if constexpr (PAIR) {
-    for (int i = threadIdx.x; i < MT * 16; i += blockDim.x) {
-      const int m = i >> 4, r = i & 15;
-      if (m >= d.m) continue;
-      float g = sm.red[0][m][r], u = sm.red[WAVES][m][r];
+    with_act(o->act, [&](auto act) {
+      for (int i = threadIdx.x; i < MT * 16; i += blockDim.x) {
+        const int m = i >> 4, r = i & 15;
+        if (m >= d.m) continue;
+        float g = sm.red[0][m][r], u = sm.red[WAVES][m][r];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) {
-        g += sm.red[w][m][r];
-        u += sm.red[WAVES + w][m][r];
+        for (int w = 1; w < WAVES; ++w) {
+          g += sm.red[w][m][r];
+          u += sm.red[WAVES + w][m][r];
+        }
+        const int64_t row = slab * 16 + r;
+        if (o->g) {
+          o->g[m * o->ldg + row] = g;
+          o->u[m * o->ldu + row] = u;
+        }
+        o->h[m * o->ldh + row] = round16<DT>(act_value<decltype(act)::value>(g) * u);
       }
-      const int64_t row = slab * 16 + r;
-      if (o->g) {
-        o->g[m * o->ldg + row] = g;
-        o->u[m * o->ldu + row] = u;
-      }
-      o->h[m * o->ldh + row] = round16<DT>(act_value(o->act, g) * u);
-    }
+    });
     return;
   }
   for (int i = threadIdx.x; i < MT * 16; i += blockDim.x) {

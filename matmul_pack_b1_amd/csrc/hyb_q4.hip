@@ -340,6 +340,15 @@ __device__ __forceinline__ uint4 load8_16(const uint16_t* row, int32_t c0, int32
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// with_act for a gated product; f runs once with any activation for others.
+template <bool GATED, typename F>
+__device__ __forceinline__ void with_gated(int act, F f) {
+  if constexpr (GATED)
+    with_act(act, f);
+  else
+    f(std::integral_constant<int, HYB_ACT_SILU>());
+}
+
 // Sets of registers that a wavefront's codes of 512 columns take turns in: the
 // next are loaded whole ahead of the products (two), or, with two weights, step by
 // step into the registers that the products have done with (one: the gated kernels
@@ -448,20 +457,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_q4_rows(Q4Args a) {
       *reinterpret_cast<f32x4_t*>(red + (p * MT + t16) * 16 + (lane >> 4) * 4) = acc[p];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 16; i += 64 * WAVES) {
-    const int t = i >> 4, r = i & 15;
-    if (tok0 + t >= a.m || panel * 16 + r >= a.n) continue;
-    float v[P];
+  with_gated<GATED>(a.act, [&](auto act) {
+    for (int i = threadIdx.x; i < MT * 16; i += 64 * WAVES) {
+      const int t = i >> 4, r = i & 15;
+      if (tok0 + t >= a.m || panel * 16 + r >= a.n) continue;
+      float v[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      v[p] = 0.f;
+      for (int p = 0; p < P; ++p) {
+        v[p] = 0.f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) v[p] += reinterpret_cast<const float*>(smem + w * kOwn)[(p * MT + t) * 16 + r];
-      if constexpr (DT == HYB_F16) v[p] = __builtin_ldexpf(v[p], int(a.w[p].tops[panel * 16 + r]) - kTopLift);
+        for (int w = 0; w < WAVES; ++w) v[p] += reinterpret_cast<const float*>(smem + w * kOwn)[(p * MT + t) * 16 + r];
+        if constexpr (DT == HYB_F16) v[p] = __builtin_ldexpf(v[p], int(a.w[p].tops[panel * 16 + r]) - kTopLift);
+      }
+      const float out = GATED ? act_value<decltype(act)::value>(v[0]) * v[P - 1] : v[0];
+      store_out(a.y, a.ydt, (tok0 + t) * a.ldy + panel * 16 + r, out);
     }
-    const float out = GATED ? act_value(a.act, v[0]) * v[P - 1] : v[0];
-    store_out(a.y, a.ydt, (tok0 + t) * a.ldy + panel * 16 + r, out);
-  }
+  });
 }
 
 // Activations as panels (hyb_panel.h), rows behind m and columns behind k zero
@@ -515,13 +526,13 @@ __device__ __forceinline__ f32x4_t q4_lift(const Q4Args& a, int p, int64_t j0, f
   return v;
 }
 
-template <int DT, bool GATED>
+template <int DT, bool GATED, int ACT>
 __device__ __forceinline__ f32x4_t q4_finish(const Q4Args& a, int64_t j0, f32x4_t v, f32x4_t u) {
   v = q4_lift<DT>(a, 0, j0, v);
   if constexpr (GATED) {
     u = q4_lift<DT>(a, 1, j0, u);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = act_value(a.act, v[e]) * u[e];
+    for (int e = 0; e < 4; ++e) v[e] = act_value<ACT>(v[e]) * u[e];
   }
   return v;
 }
@@ -655,9 +666,12 @@ __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
   }
   if (mine >= panels) return;
   const int64_t j0 = panel * 16 + (lane >> 4) * 4;
+  with_gated<GATED>(a.act, [&](auto act) {
 #pragma unroll
-  for (int j = 0; j < BP; ++j)
-    q4_store4(a, tok0 + j * 16 + (lane & 15), j0, q4_finish<DT, GATED>(a, j0, acc[0][j], acc[P - 1][j]));
+    for (int j = 0; j < BP; ++j)
+      q4_store4(a, tok0 + j * 16 + (lane & 15), j0,
+                q4_finish<DT, GATED, decltype(act)::value>(a, j0, acc[0][j], acc[P - 1][j]));
+  });
 }
 
 // Adds the parts of k_q4_shared in order: one thread per four outputs.
@@ -682,7 +696,9 @@ __global__ __launch_bounds__(256) void k_q4_shared_sum(Q4Args a) {
     }
     v[p] = sum;
   }
-  q4_store4(a, tok, j0, q4_finish<DT, GATED>(a, j0, v[0], v[P - 1]));
+  with_gated<GATED>(a.act, [&](auto act) {
+    q4_store4(a, tok, j0, q4_finish<DT, GATED, decltype(act)::value>(a, j0, v[0], v[P - 1]));
+  });
 }
 
 // More tokens: AP panels of codes x BP panels of tokens through LDS, WA x WB
@@ -864,38 +880,40 @@ __global__ __launch_bounds__(64 * WA * WB) void k_q4_tile(Q4Args a) {
   }
   const int64_t col0 = (int64_t(ab) * T::kPanels + wa * T::kOutA) * 16;
   const int64_t row0 = (int64_t(bb) * BP + wb * T::kB) * 16;
-  if (a.ydt == HYB_F32) {
+  with_gated<GATED>(a.act, [&](auto act) {
+    auto value = [&](int i, int j) {
+      return q4_finish<DT, GATED, decltype(act)::value>(a, col0 + i * 16 + (lane >> 4) * 4, acc[i][j],
+                                                        acc[GATED ? i + T::kA / 2 : i][j]);
+    };
+    if (a.ydt == HYB_F32) {
 #pragma unroll
-    for (int j = 0; j < T::kB; ++j)
+      for (int j = 0; j < T::kB; ++j)
 #pragma unroll
-      for (int i = 0; i < T::kOutA; ++i) {
-        const int64_t j0 = col0 + i * 16 + (lane >> 4) * 4;
-        q4_store4(a, row0 + j * 16 + (lane & 15), j0,
-                  q4_finish<DT, GATED>(a, j0, acc[i][j], acc[GATED ? i + T::kA / 2 : i][j]));
-      }
-    return;
-  }
-  __syncthreads();  // the tile's LDS stages are free
-  const bool bf = a.ydt == HYB_BF16;
-  panel_rows16<T::kOutA, T::kB>(
-      q4_smem + wave * (T::kOutA * T::kB * 512), lane, lane & 15,
-      [&](int i, int j) {
-        const f32x4_t v = q4_finish<DT, GATED>(a, col0 + i * 16 + (lane >> 4) * 4, acc[i][j],
-                                               acc[GATED ? i + T::kA / 2 : i][j]);
-        return bf ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3]) : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
-      },
-      [&](int r, int c, uint4 u) {
-        const int64_t tok = row0 + r, col = col0 + c;
-        if (tok >= a.m || col >= a.n) return;
-        uint16_t* p = static_cast<uint16_t*>(a.y) + tok * a.ldy + col;
-        if (col + 8 <= a.n) {
-          *reinterpret_cast<Bytes16*>(p) = Bytes16{{u.x, u.y, u.z, u.w}};
-        } else {
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          for (int e = 0; e < 8; ++e)
-            if (col + e < a.n) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
-        }
-      });
+        for (int i = 0; i < T::kOutA; ++i)
+          q4_store4(a, row0 + j * 16 + (lane & 15), col0 + i * 16 + (lane >> 4) * 4, value(i, j));
+      return;
+    }
+    __syncthreads();  // the tile's LDS stages are free
+    const bool bf = a.ydt == HYB_BF16;
+    panel_rows16<T::kOutA, T::kB>(
+        q4_smem + wave * (T::kOutA * T::kB * 512), lane, lane & 15,
+        [&](int i, int j) {
+          const f32x4_t v = value(i, j);
+          return bf ? round16x4<HYB_BF16>(v[0], v[1], v[2], v[3]) : round16x4<HYB_F16>(v[0], v[1], v[2], v[3]);
+        },
+        [&](int r, int c, uint4 u) {
+          const int64_t tok = row0 + r, col = col0 + c;
+          if (tok >= a.m || col >= a.n) return;
+          uint16_t* p = static_cast<uint16_t*>(a.y) + tok * a.ldy + col;
+          if (col + 8 <= a.n) {
+            *reinterpret_cast<Bytes16*>(p) = Bytes16{{u.x, u.y, u.z, u.w}};
+          } else {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int e = 0; e < 8; ++e)
+              if (col + e < a.n) p[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+          }
+        });
+  });
 }
 
 // Adds the parts of a tile in order and stores the outputs: one thread per four
@@ -929,7 +947,9 @@ __global__ __launch_bounds__(256) void k_q4_sum(Q4Args a) {
     }
     v[p] = sum;
   }
-  q4_store4(a, tok, j0, q4_finish<DT, GATED>(a, j0, v[0], v[GATED ? 1 : 0]));
+  with_gated<GATED>(a.act, [&](auto act) {
+    q4_store4(a, tok, j0, q4_finish<DT, GATED, decltype(act)::value>(a, j0, v[0], v[GATED ? 1 : 0]));
+  });
 }
 
 // Zeros (k = 0).
