@@ -179,26 +179,29 @@ struct GatedGrad {
   uint32_t* top;  // fp16: bits of the largest finite |dG|, |dU|
 };
 
-// dG and dU of one output.
-template <int ACT>
-__device__ __forceinline__ void gated_grad1(float g, float u, float dh, float* dg, float* du) {
-  float a;
-  const float slope = act_slope<ACT>(g, &a);
-  *dg = dh * u * slope;
-  *du = dh * a;
-}
-
-// Four outputs' dG and dU, from column c on of the rows' starts.
-template <int DT, int ACT>
-__device__ __forceinline__ void gated_grad4(const float* g, const float* u, const uint16_t* dh, int64_t c,
-                                            float* dg, float* du) {
-  const Bytes16 gb = *reinterpret_cast<const Bytes16*>(g + c), ub = *reinterpret_cast<const Bytes16*>(u + c);
-  const Bytes8 db = *reinterpret_cast<const Bytes8*>(dh + c);
+// Four outputs' G, U (fp32) and dH, as loaded from any element-aligned address,
+// and their dG and dU.
+template <int DT>
+struct Gated4 {
+  Bytes16 g, u;
+  Bytes8 dh;
+  __device__ __forceinline__ Gated4() {}
+  __device__ __forceinline__ Gated4(const float* gp, const float* up, const uint16_t* dp)
+      : g(*reinterpret_cast<const Bytes16*>(gp)),
+        u(*reinterpret_cast<const Bytes16*>(up)),
+        dh(*reinterpret_cast<const Bytes8*>(dp)) {}
+  template <int ACT>
+  __device__ __forceinline__ void gradients(float* dg, float* du) const {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    gated_grad1<ACT>(__builtin_bit_cast(float, gb.w[e]), __builtin_bit_cast(float, ub.w[e]),
-                widen16<DT>((db.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu), dg + e, du + e);
-}
+    for (int e = 0; e < 4; ++e) {
+      float a;
+      const float slope = act_slope<ACT>(__builtin_bit_cast(float, g.w[e]), &a);
+      const float d = widen16<DT>((dh.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+      dg[e] = d * __builtin_bit_cast(float, u.w[e]) * slope;
+      du[e] = d * a;
+    }
+  }
+};
 
 // The power of two that brings a magnitude of these bits to [2^13, 2^14) (1 for
 // zero), and its reciprocal.
@@ -221,9 +224,8 @@ __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
     const int32_t c = int32_t(blockIdx.x) * 256 + threadIdx.x;
     if (c >= per) break;
     float dg[4], du[4];
-    with_act(o.act, [&](auto act) {
-      gated_grad4<DT, decltype(act)::value>(o.g + t * o.ldg, o.u + t * o.ldu, o.dh + t * o.lddh, int64_t(c) * 4, dg, du);
-    });
+    const Gated4<DT> in(o.g + t * o.ldg + c * 4, o.u + t * o.ldu + c * 4, o.dh + t * o.lddh + c * 4);
+    with_act(o.act, [&](auto act) { in.template gradients<decltype(act)::value>(dg, du); });
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t a = __builtin_bit_cast(uint32_t, dg[e]) & 0x7FFFFFFFu;
@@ -256,28 +258,35 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
   const int64_t panel = blockIdx.x, tok = panel * 16 + (lane & 15);
   float back;
   const float lift = DT == HYB_F16 ? gated_lift(*o.top, &back) : 1.f;
+  // (a lane behind the last token loads the last one's, so that no load branches
+  // and all are under way at once)
   const int u4 = lane >> 4;
+  const int64_t row = tok < o.m ? tok : o.m - 1, col = s * 64 + 16 * (u4 >> 1) + 4 * (u4 & 1);
+  const float *g = o.g + row * o.ldg + col, *u = o.u + row * o.ldu + col;
+  const uint16_t* dh = o.dh + row * o.lddh + col;
+  Gated4<DT> in[2][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
-    if (tok < o.m) {
-      const int32_t c = s * 64 + h * 32 + 16 * (u4 >> 1) + 4 * (u4 & 1);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) in[h][p] = Gated4<DT>(g + h * 32 + p * 8, u + h * 32 + p * 8, dh + h * 32 + p * 8);
+  const bool live = tok < o.m;
+  with_act(o.act, [&](auto act) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       float dg[8], du[8];
-      const float *g = o.g + tok * o.ldg, *u = o.u + tok * o.ldu;
-      const uint16_t* dh = o.dh + tok * o.lddh;
-      with_act(o.act, [&](auto act) {
-        gated_grad4<DT, decltype(act)::value>(g, u, dh, c, dg, du);
-        gated_grad4<DT, decltype(act)::value>(g, u, dh, c + 8, dg + 4, du + 4);
-      });
-      a = make_uint4(round16x2<DT>(dg[0] * lift, dg[1] * lift), round16x2<DT>(dg[2] * lift, dg[3] * lift),
-                     round16x2<DT>(dg[4] * lift, dg[5] * lift), round16x2<DT>(dg[6] * lift, dg[7] * lift));
-      b = make_uint4(round16x2<DT>(du[0] * lift, du[1] * lift), round16x2<DT>(du[2] * lift, du[3] * lift),
-                     round16x2<DT>(du[4] * lift, du[5] * lift), round16x2<DT>(du[6] * lift, du[7] * lift));
+      in[h][0].template gradients<decltype(act)::value>(dg, du);
+      in[h][1].template gradients<decltype(act)::value>(dg + 4, du + 4);
+      const int64_t at = (panel * o.steps + s) * kPanelStep + h * 1024 + lane * 16;
+      auto put = [&](char* to, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(to + at) =
+            live ? make_uint4(round16x2<DT>(v[0] * lift, v[1] * lift), round16x2<DT>(v[2] * lift, v[3] * lift),
+                              round16x2<DT>(v[4] * lift, v[5] * lift), round16x2<DT>(v[6] * lift, v[7] * lift))
+                 : make_uint4(0, 0, 0, 0);
+      };
+      put(o.out[0], dg);
+      put(o.out[1], du);
     }
-    const int64_t at = (panel * o.steps + s) * kPanelStep + h * 1024 + lane * 16;
-    *reinterpret_cast<uint4*>(o.out[0] + at) = a;
-    *reinterpret_cast<uint4*>(o.out[1] + at) = b;
-  }
+  });
 }
 
 struct GatedDx {
@@ -437,11 +446,9 @@ PanelOperand weight_operand(const hyb_layout& L, const hyb_packed& P, const char
 hipError_t expand_pair(const hyb_gated_pair& w, const GatedPlan& p, char* ws, hipStream_t s, PanelOperand (&out)[2]) {
   const hyb_layout* L[2] = {w.gate_layout, w.up_layout};
   const hyb_packed* P[2] = {w.gate, w.up};
-  for (int i = 0; i < 2; ++i) {
-    if (L[i]->n_sparse > 0) HYB_TRY(launch_expand_tiles(*L[i], *P[i], ws + p.w[i], s));
-    out[i] = weight_operand(*L[i], *P[i], ws + p.w[i]);
-  }
-  return hipSuccess;
+  for (int i = 0; i < 2; ++i) out[i] = weight_operand(*L[i], *P[i], ws + p.w[i]);
+  if (L[0]->n_sparse == 0 && L[1]->n_sparse == 0) return hipSuccess;
+  return launch_expand_pair(*L[0], *P[0], ws + p.w[0], *L[1], *P[1], ws + p.w[1], s);
 }
 
 // x as panels.
