@@ -66,15 +66,15 @@ __global__ __launch_bounds__(256) void k_gated_act(GatedOut o) {
 }
 
 // AP / 2 panels of each weight x BP panels of tokens.
-template <int DT, int AP, int BP, int WA, int WB>
+template <int DT, int AP, int BP, int WA, int WB, int STAGES>
 struct GatedTile {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, false, false, true, false, true> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, STAGES, false, false, true, false, true> T;
   static constexpr int kRows = 16 * AP / 2, kOut = T::kA / 2;
 };
 
-template <int DT, int AP, int BP, int WA, int WB>
+template <int DT, int AP, int BP, int WA, int WB, int STAGES>
 __global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, PanelOperand U, PanelOperand X, GatedOut o) {
-  typedef GatedTile<DT, AP, BP, WA, WB> D;
+  typedef GatedTile<DT, AP, BP, WA, WB, STAGES> D;
   typedef typename D::T T;
   constexpr int kOut = D::kOut;
   extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
@@ -136,9 +136,9 @@ __global__ __launch_bounds__(64 * WA * WB) void k_gated_tile(PanelOperand G, Pan
 
 // Adds the parts of the tiles that were cut, in order: one thread per four
 // outputs, in the order of the tile's registers.
-template <int DT, int AP, int BP, int WA, int WB>
+template <int DT, int AP, int BP, int WA, int WB, int STAGES>
 __global__ __launch_bounds__(256) void k_gated_sum(int32_t na, int32_t nb, GatedOut o) {
-  typedef GatedTile<DT, AP, BP, WA, WB> D;
+  typedef GatedTile<DT, AP, BP, WA, WB, STAGES> D;
   typedef typename D::T T;
   int32_t ab, bb;
   panel_block(o.whole + int32_t(blockIdx.x), na, nb, ab, bb);
@@ -176,7 +176,8 @@ struct GatedGrad {
   int32_t m, n, steps;
   int act;
   char* out[2];   // dG, dU panels: tokens x outputs
-  uint32_t* top;  // fp16: bits of the largest finite |dG|, |dU|
+  uint32_t* top;  // fp16: bits of the largest finite |dG|, |dU|, then each group's
+  int32_t groups;
 };
 
 // Four outputs' G, U (fp32) and dH, as loaded from any element-aligned address,
@@ -212,17 +213,17 @@ __device__ __forceinline__ float gated_lift(uint32_t top, float* back) {
   return __builtin_bit_cast(float, uint32_t(127 + e) << 23);
 }
 
-__global__ void k_gated_clear(uint32_t* top) { *top = 0; }
-
-// Largest finite |dG|, |dU| (fp16).
+// Largest finite |dG|, |dU| (fp16) of each workgroup's outputs.
+constexpr int kTopGroups = 512;
 template <int DT>
 __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
   __shared__ uint32_t tops[4];
   uint32_t best = 0;
   const int32_t per = o.n / 4;  // a packed weight's n is a multiple of 64
-  for (int64_t t = blockIdx.y; t < o.m; t += gridDim.y) {
-    const int32_t c = int32_t(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= per) break;
+  const int64_t all = int64_t(o.m) * per;
+#pragma unroll 2
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t t = i / per, c = i - t * per;
     float dg[4], du[4];
     const Gated4<DT> in(o.g + t * o.ldg + c * 4, o.u + t * o.ldu + c * 4, o.dh + t * o.lddh + c * 4);
     with_act(o.act, [&](auto act) { in.template gradients<decltype(act)::value>(dg, du); });
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 4; ++i) best = tops[i] > best ? tops[i] : best;
-    if (best > 0) atomicMax(o.top, best);  // (the largest, whatever the order)
+    o.top[1 + blockIdx.x] = best;
   }
 }
 
@@ -254,10 +255,26 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  float lift = 1.f;
+  if constexpr (DT == HYB_F16) {
+    // the largest of the groups' (every workgroup takes it itself)
+    __shared__ uint32_t tops[4];
+    uint32_t top = 0;
+    for (int32_t i = threadIdx.x; i < o.groups; i += 256) top = o.top[1 + i] > top ? o.top[1 + i] : top;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const uint32_t v = __shfl_xor(top, d);
+      top = v > top ? v : top;
+    }
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    for (int i = 0; i < 4; ++i) top = tops[i] > top ? tops[i] : top;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *o.top = top;
+    float back;
+    lift = gated_lift(top, &back);
+  }
   if (s >= o.steps) return;
   const int64_t panel = blockIdx.x, tok = panel * 16 + (lane & 15);
-  float back;
-  const float lift = DT == HYB_F16 ? gated_lift(*o.top, &back) : 1.f;
   // (a lane behind the last token loads the last one's, so that no load branches
   // and all are under way at once)
   const int u4 = lane >> 4;
@@ -299,10 +316,10 @@ struct GatedDx {
 
 // dX[token, column] = sum over the outputs of dG W_g' + dU W_u' (A = W' read
 // transposed, B = the panels).  A part takes the same steps of both.
-template <int DT, int AP, int BP, int WA, int WB>
+template <int DT, int AP, int BP, int WA, int WB, int STAGES>
 __global__ __launch_bounds__(64 * WA * WB) void k_gated_dx(PanelOperand G, PanelOperand U, PanelOperand DG,
                                                            PanelOperand DU, int32_t steps, int parts, GatedDx o) {
-  typedef PanelTile<DT, AP, BP, WA, WB, 2, true, false, true> T;
+  typedef PanelTile<DT, AP, BP, WA, WB, STAGES, true, false, true> T;
   extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
   const int32_t na = (G.steps * 4 + AP - 1) / AP, nb = (DG.rows16 / 16 + BP - 1) / BP;
   int32_t ab, bb;
@@ -457,20 +474,20 @@ hipError_t pack_x(const GatedPlan& p, const void* x, int64_t ldx, char* ws, hipS
   return launch_pack_x(static_cast<const uint16_t*>(x), ldx, p.m, p.k, ws + p.x, s);
 }
 
-template <int DT, int BP, int WA, int WB>
+template <int DT, int BP, int WA, int WB, int STAGES>
 hipError_t run_forward_tile(const PanelOperand (&W)[2], const PanelOperand& X, const GatedOut& o, hipStream_t s) {
-  typedef GatedTile<DT, 16, BP, WA, WB> D;
+  typedef GatedTile<DT, 16, BP, WA, WB, STAGES> D;
   typedef typename D::T T;
-  HYB_TRY(allow_lds(&k_gated_tile<DT, 16, BP, WA, WB>, T::kLds));
+  HYB_TRY(allow_lds(&k_gated_tile<DT, 16, BP, WA, WB, STAGES>, T::kLds));
   const int64_t na = (W[0].rows16 + 127) / 128, nb = (X.rows16 + 16 * BP - 1) / (16 * BP), rest = na * nb - o.whole;
-  hipLaunchKernelGGL((k_gated_tile<DT, 16, BP, WA, WB>), dim3(unsigned(o.whole + rest * o.parts)), dim3(64 * WA * WB),
-                     T::kLds, s, W[0], W[1], X, o);
+  hipLaunchKernelGGL((k_gated_tile<DT, 16, BP, WA, WB, STAGES>), dim3(unsigned(o.whole + rest * o.parts)),
+                     dim3(64 * WA * WB), T::kLds, s, W[0], W[1], X, o);
   HYB_TRY(hipGetLastError());
   if (rest == 0) return hipSuccess;
   constexpr int kEach = T::kWaves * D::kOut * T::kB;  // of 64 lanes, a tile
   static_assert(kEach % 4 == 0, "whole workgroups");
-  hipLaunchKernelGGL((k_gated_sum<DT, 16, BP, WA, WB>), dim3(unsigned(rest), kEach / 4), dim3(256), 0, s, int32_t(na),
-                     int32_t(nb), o);
+  hipLaunchKernelGGL((k_gated_sum<DT, 16, BP, WA, WB, STAGES>), dim3(unsigned(rest), kEach / 4), dim3(256), 0, s,
+                     int32_t(na), int32_t(nb), o);
   return hipGetLastError();
 }
 
@@ -514,16 +531,17 @@ hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, c
   o.ws = reinterpret_cast<f32x4_t*>(ws + p.gu);
   o.whole = int32_t(p.whole);
   o.parts = p.parts;
-  if (p.bp == 16) return run_forward_tile<DT, 16, 2, 4>(W, X, o, s);
-  return run_forward_tile<DT, 8, 4, 2>(W, X, o, s);
+  if (p.bp == 16) return run_forward_tile<DT, 16, 2, 4, 2>(W, X, o, s);
+  if (p.bp == 8) return run_forward_tile<DT, 8, 4, 2, 2>(W, X, o, s);
+  return run_forward_tile<DT, 4, 4, 2, 4>(W, X, o, s);
 }
 
-template <int DT, int BP, int WA, int WB>
+template <int DT, int BP, int WA, int WB, int STAGES>
 hipError_t run_dx(const PanelOperand (&W)[2], const PanelOperand (&D)[2], int parts, const GatedDx& o, hipStream_t s) {
-  typedef PanelTile<DT, 16, BP, WA, WB, 2, true, false, true> T;
-  HYB_TRY(allow_lds(&k_gated_dx<DT, 16, BP, WA, WB>, T::kLds));
+  typedef PanelTile<DT, 16, BP, WA, WB, STAGES, true, false, true> T;
+  HYB_TRY(allow_lds(&k_gated_dx<DT, 16, BP, WA, WB, STAGES>, T::kLds));
   const int64_t na = (W[0].steps * 4 + 15) / 16, nb = (D[0].rows16 / 16 + BP - 1) / BP;
-  hipLaunchKernelGGL((k_gated_dx<DT, 16, BP, WA, WB>), dim3(unsigned(na * nb), unsigned(parts)), dim3(64 * WA * WB),
+  hipLaunchKernelGGL((k_gated_dx<DT, 16, BP, WA, WB, STAGES>), dim3(unsigned(na * nb), unsigned(parts)), dim3(64 * WA * WB),
                      T::kLds, s, W[0], W[1], D[0], D[1], D[0].steps, parts, o);
   return hipGetLastError();
 }
@@ -557,11 +575,9 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
   g.out[1] = ws + p.g[1];
   g.top = top;
   if (DT == HYB_F16) {
-    hipLaunchKernelGGL(k_gated_clear, dim3(1), dim3(1), 0, s, top);
-    HYB_TRY(hipGetLastError());
-    const unsigned across = unsigned((p.n / 4 + 255) / 256);
-    const int64_t down = 2048 / across + 1;
-    hipLaunchKernelGGL((k_gated_top<DT>), dim3(across, unsigned(p.m < down ? p.m : down)), dim3(256), 0, s, g);
+    const int64_t want = (p.m * (p.n / 4) + 255) / 256;
+    g.groups = int32_t(want < kTopGroups ? want : kTopGroups);
+    hipLaunchKernelGGL((k_gated_top<DT>), dim3(unsigned(g.groups)), dim3(256), 0, s, g);
     HYB_TRY(hipGetLastError());
   }
   hipLaunchKernelGGL((k_gated_grad<DT>), dim3(unsigned(p.m16 / 16), unsigned((g.steps + 3) / 4)), dim3(256), 0, s, g);
@@ -573,9 +589,9 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
     HYB_TRY(expand_pair(w, p, ws, s, W));
     const GatedDx o{reinterpret_cast<float*>(ws + p.dx), static_cast<uint16_t*>(b.dx), b.lddx, int32_t(p.m),
                     int32_t(p.k), top};
-    HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4>(W, D, p.parts, o, s))
-            : p.bp == 8 ? (run_dx<DT, 8, 4, 2>(W, D, p.parts, o, s))
-                        : (run_dx<DT, 4, 4, 2>(W, D, p.parts, o, s)));
+    HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4, 2>(W, D, p.parts, o, s))
+            : p.bp == 8 ? (run_dx<DT, 8, 4, 2, 2>(W, D, p.parts, o, s))
+                        : (run_dx<DT, 4, 4, 2, 4>(W, D, p.parts, o, s)));
     if (p.parts > 1) {
       hipLaunchKernelGGL((k_gated_dx_sum<DT>), dim3(unsigned(p.m), unsigned((p.k + 1023) / 1024)), dim3(256), 0, s,
                          p.parts, o);
@@ -588,7 +604,7 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
     const GatedDw o{{static_cast<uint16_t*>(b.dw[0]), static_cast<uint16_t*>(b.dw[1])}, {b.lddw[0], b.lddw[1]},
                     int32_t(p.n), int32_t(p.k), top};
     const int32_t steps = int32_t(p.m64 / 64);
-    HYB_TRY(p.m <= 256 ? (run_dw<DT, 8, 8, 2, 4>(X, D, steps, o, s)) : (run_dw<DT, 16, 16, 2, 4>(X, D, steps, o, s)));
+    HYB_TRY(p.small_dw ? (run_dw<DT, 8, 8, 2, 4>(X, D, steps, o, s)) : (run_dw<DT, 16, 16, 2, 4>(X, D, steps, o, s)));
   }
   return hipSuccess;
 }

@@ -8,6 +8,14 @@ namespace {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
+// Tiles of 256 rows x 16 bp tokens: microseconds of four 64-column steps on a
+// compute unit, and of what comes before and after them.
+struct Tile {
+  int bp;
+  double quad, start;
+};
+constexpr Tile kTiles[] = {{4, 2.4, 3.0}, {8, 5.0, 5.0}, {16, 7.0, 10.0}};
+
 }  // namespace
 
 GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) {
@@ -48,11 +56,7 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
     // are cut into parts.
     const int64_t quads = (p.k / 64 + 3) / 4;
     double least = 1e300;
-    struct Tile {
-      int bp;
-      double step;
-    };
-    for (const Tile& c : {Tile{8, 0.55}, Tile{16, 1.0}}) {
+    for (const Tile& c : kTiles) {
       const int64_t tiles = up(p.n, 128) / 128 * (up(m, 16 * c.bp) / (16 * c.bp));
       const int64_t whole = tiles / cus * cus, rest = tiles - whole;
       auto offer = [&](int64_t first, int64_t parts, double cost) {
@@ -63,34 +67,43 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
           p.parts = int(parts);
         }
       };
-      offer(tiles, 1, double(up(tiles, cus) / cus * quads) * c.step);
-      for (int64_t parts = 2; rest > 0 && parts <= quads && parts <= 32 && rest * parts <= 2 * cus; ++parts)
+      offer(tiles, 1, double(up(tiles, cus) / cus) * (double(quads) * c.quad + c.start));
+      for (int64_t parts = 2; rest > 0 && parts <= quads && parts <= 32 && rest * parts <= 2 * cus; ++parts) {
+        const double sums = 3.0 + double(rest * parts) * 256 * 16 * c.bp * 8 / 7.0e6;
         offer(whole, parts,
-              double(whole / cus * quads + up(rest * parts, cus) / cus * (up(quads, parts) / parts)) * c.step + 2.0 +
-                  0.004 * double(rest * parts) * c.bp / 16);
+              double(whole / cus) * (double(quads) * c.quad + c.start) +
+                  double(up(rest * parts, cus) / cus) * (double(quads) / double(parts) * c.quad + c.start) + sums);
+      }
     }
     if (p.parts > 1) {
       const int64_t tiles = up(p.n, 128) / 128 * (up(m, 16 * p.bp) / (16 * p.bp));
       p.gu = take((tiles - p.whole) * p.parts * 16 * p.bp * 1024);
     }
   } else {
-    p.misc = take(256);
+    p.misc = take(4 + 512 * 4);  // the largest gradient, and that of each workgroup
     for (int i = 0; i < 2; ++i) p.g[i] = take(p.m16 * p.n * 2);
-    p.bp = m <= 64 ? 4 : m <= 128 ? 8 : 16;
+    p.small_dw = m <= 256 || up(p.n, 256) / 256 * (up(p.k, 256) / 256) * 2 <= cus;
   }
   if (!dx || dw) p.x = take(p.m16 * p.k * 2);
   if (!dw || dx)
     for (int i = 0; i < 2; ++i)
       if (both[i]->n_sparse > 0) p.w[i] = take(p.n * p.k * 2);
   if (dx) {
-    const int64_t tiles = up(p.k, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp));
-    const int64_t slots = p.bp == 4 ? 2 * cus : cus, quads = up(p.n, 256) / 256;
+    // (k / 256) x (m / 16 bp) tiles, whose 2 n outputs are cut into parts
+    const int64_t quads = up(p.n, 256) / 256;  // of four steps of each weight
     double least = 1e300;
-    for (int parts = 1; parts <= 32 && parts <= quads; ++parts) {
-      const double cost = double(up(tiles * parts, slots) / slots) / parts * (1.0 + 0.01 * parts);
-      if (cost < least) {
-        least = cost;
-        p.parts = parts;
+    for (const Tile& c : kTiles) {
+      const int64_t tiles = up(p.k, 256) / 256 * (up(p.m16, 16 * c.bp) / (16 * c.bp));
+      for (int parts = 1; parts <= 32 && parts <= quads; ++parts) {
+        if (parts > 1 && tiles * parts > 4 * cus) break;
+        const double rounds = double(up(tiles * parts, cus) / cus);
+        const double sums = parts > 1 ? 3.0 + double(parts) * double(m) * double(p.k) * 8 / 7.0e6 : 0.0;
+        const double cost = rounds * (2.0 * double(up(quads, parts) / parts) * c.quad + c.start) + sums;
+        if (cost < least) {
+          least = cost;
+          p.parts = parts;
+          p.bp = c.bp;
+        }
       }
     }
     if (p.parts > 1) p.dx = take(int64_t(p.parts) * m * p.k * 4);

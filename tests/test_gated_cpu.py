@@ -136,12 +136,12 @@ def test_forward_refusals(args, status):
 
 @pytest.mark.parametrize("args,status", [
     (dict(act=9), 1), (dict(dt=hb.HYB_F32), 3), (dict(x=P16 + 1), 1), (dict(ldx=255), 1), (dict(h=None), 1),
-    (dict(ldh=7), 1), (dict(g=P16, u=P16), 4), (dict(g=P16), 1), (dict(m=40, ws=None), 1), (dict(m=40, nbytes=5), 1),
+    (dict(ldh=7), 1), (dict(g=P16, u=P16), 4), (dict(g=P16), 1), (dict(k=4, m=40, ws=None), 1), (dict(k=4, m=40, nbytes=5), 1),
 ])
 def test_forward_4bit_refusals(args, status):
-    d = dict(act=1, x=P16, dt=hb.HYB_BF16, m=2, ldx=256, h=P16, ldh=8, g=None, u=None, ws=P16, nbytes=1 << 40)
+    d = dict(act=1, x=P16, dt=hb.HYB_BF16, m=2, k=256, ldx=256, h=P16, ldh=8, g=None, u=None, ws=P16, nbytes=1 << 40)
     d.update(args)
-    st = gated.lib().hyb_gated(ctypes.byref(_q4_pair()), d["act"], d["x"], d["dt"], d["m"], d["ldx"], d["h"], d["ldh"],
+    st = gated.lib().hyb_gated(ctypes.byref(_q4_pair(k=d["k"])), d["act"], d["x"], d["dt"], d["m"], d["ldx"], d["h"], d["ldh"],
                                d["g"], 8, d["u"], 8, d["ws"], d["nbytes"], None)
     assert _status(st) == status
 
@@ -184,8 +184,8 @@ def test_workspace_sizes():
     dz = 2 * 208 * 128 * 2                                     # dG and dU of 200 tokens
     assert need(200, gated.DX) >= dz and need(200, gated.DW) >= dz
     assert need(200, gated.DX | gated.DW) >= max(need(200, gated.DX), need(200, gated.DW))
-    four = ctypes.byref(_q4_pair())
-    assert need(1, 0, four) == need(4, 0, four) == 0 and need(40, 0, four) >= 48 * 256 * 2
+    four, narrow = ctypes.byref(_q4_pair()), ctypes.byref(_q4_pair(k=4))
+    assert need(1, 0, four) == need(4, 0, four) == 0 and need(40, 0, narrow) >= 48 * 64 * 2
 
 
 def test_empty_calls_do_nothing():

@@ -102,7 +102,7 @@ def test_quantise_refusals(args, status):
     (dict(dt=hb.HYB_F32), 3), (dict(dt=0), 3), (dict(y_dtype=0), 3), (dict(n=-1), 2), (dict(k=(1 << 22) + 1), 2),
     (dict(m=-1), 2), (dict(m=(1 << 22) + 1), 2), (dict(x=None), 1), (dict(x=P16 + 1), 1), (dict(ldx=255), 1),
     (dict(y=None), 1), (dict(y=P16 + 2), 1), (dict(ldy=7), 1), (dict(w=(None, P16)), 1), (dict(w=(P16, None)), 1),
-    (dict(w=(P16 + 1, P16)), 1), (dict(m=5, ws=None), 1), (dict(m=40, ws=None), 1), (dict(m=40, ws=P16 + 8), 1), (dict(m=40, nbytes=100), 1),
+    (dict(w=(P16 + 1, P16)), 1), (dict(k=4, m=5, ws=None), 1), (dict(k=4, m=40, ws=P16 + 8), 1), (dict(k=4, m=40, nbytes=100), 1),
     (dict(n=2 ** 27 - 16, m=2 ** 22, ldy=2 ** 31, nbytes=1 << 62), 4),
 ])
 def test_gemm_refusals(args, status):
