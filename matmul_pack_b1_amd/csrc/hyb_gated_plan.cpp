@@ -9,12 +9,27 @@ namespace {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 // Tiles of 256 rows x 16 bp tokens: microseconds of four 64-column steps on a
-// compute unit, and of what comes before and after them.
+// compute unit, and of what comes before and after them.  `sums` and `sum_rate`
+// (bytes a microsecond) price the joining of cut tiles; no order of tiles is
+// faster than `weight_rate` over the expanded weights.  Fitted to timings of
+// every tile and cut that fits at 96 (forward) and 98 (dX) sizes from 1024 x 4096
+// to 17408 x 5120, 1 to 4096 tokens: the tile taken is at most 7% slower than
+// the best one there, and 0.1% on average (tiles of one size are up to 60% slower).
 struct Tile {
   int bp;
   double quad, start;
 };
-constexpr Tile kTiles[] = {{4, 2.4, 3.0}, {8, 5.0, 5.0}, {16, 7.0, 10.0}};
+struct Costs {
+  Tile tiles[3];
+  double sums, sum_rate, weight_rate;
+};
+constexpr Costs kForward = {{{4, 3.2, 2.6}, {8, 4.8, 5.3}, {16, 6.9, 10.0}}, 4.0, 5.6e6, 4.5e6};
+constexpr Costs kInput = {{{4, 3.7, 2.0}, {8, 4.4, 4.8}, {16, 5.3, 8.2}}, 2.2, 9.2e6, 1.0e7};
+
+// Up to this many tokens the forward pass runs the two products of the sparse
+// kernels and joins them: 14336 x 4096, 30% sparse, 128 tokens 72 against 89 us,
+// 4096 x 4096 37 against 40; at 333 tokens 165 against 136 and 60 against 57.
+constexpr int64_t kRowsTokens = 128;
 
 }  // namespace
 
@@ -38,7 +53,7 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
   if (!dx && !dw) {
     p.decode = m <= kGemvCrossoverM;
     if (p.decode) return p;
-    p.rows = m <= 64;
+    p.rows = m <= kRowsTokens;
     p.grouped = m <= kMaxGemvM && gemv_preferred(L, int(m));
     if (p.rows) {
       p.gu = take(2 * m * p.n * 4);
@@ -56,7 +71,8 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
     // are cut into parts.
     const int64_t quads = (p.k / 64 + 3) / 4;
     double least = 1e300;
-    for (const Tile& c : kTiles) {
+    const double weights = double(4 * p.n * p.k) / kForward.weight_rate;
+    for (const Tile& c : kForward.tiles) {
       const int64_t tiles = up(p.n, 128) / 128 * (up(m, 16 * c.bp) / (16 * c.bp));
       const int64_t whole = tiles / cus * cus, rest = tiles - whole;
       auto offer = [&](int64_t first, int64_t parts, double cost) {
@@ -67,12 +83,14 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
           p.parts = int(parts);
         }
       };
-      offer(tiles, 1, double(up(tiles, cus) / cus) * (double(quads) * c.quad + c.start));
+      auto longer = [&](double t) { return t > weights ? t : weights; };
+      offer(tiles, 1, longer(double(up(tiles, cus) / cus) * (double(quads) * c.quad + c.start)));
       for (int64_t parts = 2; rest > 0 && parts <= quads && parts <= 32 && rest * parts <= 2 * cus; ++parts) {
-        const double sums = 3.0 + double(rest * parts) * 256 * 16 * c.bp * 8 / 7.0e6;
+        const double sums = kForward.sums + double(rest * parts) * 256 * 16 * c.bp * 8 / kForward.sum_rate;
         offer(whole, parts,
-              double(whole / cus) * (double(quads) * c.quad + c.start) +
-                  double(up(rest * parts, cus) / cus) * (double(quads) / double(parts) * c.quad + c.start) + sums);
+              longer(double(whole / cus) * (double(quads) * c.quad + c.start) +
+                     double(up(rest * parts, cus) / cus) * (double(quads) / double(parts) * c.quad + c.start)) +
+                  sums);
       }
     }
     if (p.parts > 1) {
@@ -92,13 +110,16 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
     // (k / 256) x (m / 16 bp) tiles, whose 2 n outputs are cut into parts
     const int64_t quads = up(p.n, 256) / 256;  // of four steps of each weight
     double least = 1e300;
-    for (const Tile& c : kTiles) {
+    const double weights = double(4 * p.n * p.k) / kInput.weight_rate;
+    for (const Tile& c : kInput.tiles) {
       const int64_t tiles = up(p.k, 256) / 256 * (up(p.m16, 16 * c.bp) / (16 * c.bp));
       for (int parts = 1; parts <= 32 && parts <= quads; ++parts) {
         if (parts > 1 && tiles * parts > 4 * cus) break;
         const double rounds = double(up(tiles * parts, cus) / cus);
-        const double sums = parts > 1 ? 3.0 + double(parts) * double(m) * double(p.k) * 8 / 7.0e6 : 0.0;
-        const double cost = rounds * (2.0 * double(up(quads, parts) / parts) * c.quad + c.start) + sums;
+        const double sums =
+            parts > 1 ? kInput.sums + double(parts) * double(m) * double(p.k) * 8 / kInput.sum_rate : 0.0;
+        const double tile = rounds * (2.0 * double(up(quads, parts) / parts) * c.quad + c.start);
+        const double cost = (tile > weights ? tile : weights) + sums;
         if (cost < least) {
           least = cost;
           p.parts = parts;
