@@ -78,7 +78,7 @@ hyb_status hyb_q4_dequantize(const hyb_q4* src, int64_t n, int64_t k, void* a, i
  *       are rounded to nearest even from the fp32 sum), row stride ldy >= n,
  *       element-aligned.  k = 0 gives zeros.
  * The workspace (device, 16-byte aligned, no initial contents, the bytes of
- * hyb_q4_gemm_workspace_size for the current device; 0 up to 4 tokens) holds
+ * hyb_q4_gemm_workspace_size for the current device; may be 0) holds
  * activations laid out for the matrix units and the fp32 sums of products whose
  * k is cut into parts, which are added in a fixed order; calls that overlap on
  * one buffer race. */

@@ -100,6 +100,7 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
   } else {
     p.misc = take(4 + 512 * 4);  // the largest gradient, and that of each workgroup
     for (int i = 0; i < 2; ++i) p.g[i] = take(p.m16 * p.n * 2);
+    // (figures at k_gated_dw)
     p.small_dw = m <= 256 || up(p.n, 256) / 256 * (up(p.k, 256) / 256) * 2 <= cus;
   }
   if (!dx || dw) p.x = take(p.m16 * p.k * 2);

