@@ -9,10 +9,10 @@
 #include <type_traits>
 
 #include "hyb_act.h"
+#include "hyb_expand.h"
 #include "hyb_gated_internal.h"
 #include "hyb_panel.h"
 #include "hyb_q4_internal.h"
-#include "hyb_xent_internal.h"
 
 namespace hyb {
 namespace {
@@ -258,11 +258,12 @@ __global__ __launch_bounds__(256) void k_gated_top(GatedGrad o) {
 // dG and dU as panels, in the column order in which a lane of the dX product
 // holds the rows of a W' that is read transposed (hyb_panel.h): unit u of a half
 // has columns 16 (u / 2) + 4 (u % 2) + {0..3, 8..11}.  Rows behind m are zero.
-// Bound by memory: 4096 x 14336, 587 MB read and 235 written, 182 us (4.5 TB/s).
+// Bound by memory: 4096 x 14336, 587 MB read and 235 written, 182 us alone (4.5 TB/s;
+// in k_gated_prepare the panels of some tokens first, 228 us in all instead of 206).
 template <int DT>
-__global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
+__device__ __forceinline__ void gated_grad(const GatedGrad& o, int64_t panel, int32_t quad) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int32_t s = int32_t(blockIdx.y) * 4 + wave;
+  const int32_t s = quad * 4 + wave;
   float lift = 1.f;
   if constexpr (DT == HYB_F16) {
     // the largest of the groups' (every workgroup takes it itself)
@@ -277,12 +278,12 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
     if (lane == 0) tops[wave] = top;
     __syncthreads();
     for (int i = 0; i < 4; ++i) top = tops[i] > top ? tops[i] : top;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *o.top = top;
+    if (panel == 0 && quad == 0 && threadIdx.x == 0) *o.top = top;
     float back;
     lift = gated_lift(top, &back);
   }
   if (s >= o.steps) return;
-  const int64_t panel = blockIdx.x, tok = panel * 16 + (lane & 15);
+  const int64_t tok = panel * 16 + (lane & 15);
   // (a lane behind the last token loads the last one's, so that no load branches
   // and all are under way at once)
   const int u4 = lane >> 4;
@@ -312,6 +313,62 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGrad o) {
       put(o.out[1], du);
     }
   });
+}
+
+// What the products read, in one launch (its parts wait for nothing of each
+// other, and small calls are the depth of their launches): workgroups of dG and dU
+// (backward only), of each weight's sparse tiles, and of x as panels.  2816x1024, 333
+// tokens, forward and backward 68 us, with a launch each 76; 14336x4096, 4096 tokens,
+// backward 206 us for 1.0 GB (4.9 TB/s), with a launch each 227.
+struct GatedPrepare {
+  GatedGrad grad;
+  Expand w[2];
+  const uint16_t* x;
+  int64_t ldx;
+  char* xt;
+  int32_t m, k, steps;         // x: tokens, columns, steps of 64
+  int32_t grads, weights[2], xs;  // workgroups of each part
+};
+
+// x (16-byte aligned rows, k a multiple of 64): a wavefront per panel and four
+// steps, whose eight loads are under way at once; rows behind m are zero.
+__device__ __forceinline__ void gated_pack_x(const GatedPrepare& o, int64_t panel, int32_t s, int lane) {
+  const int64_t row = panel * 16 + (lane & 15);
+  const int32_t c0 = s * 64 + (lane >> 4) * 8;
+  uint4 u[8];
+#pragma unroll
+  for (int h = 0; h < 8; ++h)
+    u[h] = row < o.m && c0 + h * 32 < o.k ? *reinterpret_cast<const uint4*>(o.x + row * o.ldx + c0 + h * 32)
+                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int h = 0; h < 8; ++h)
+    if (s + h / 2 < o.steps)
+      *reinterpret_cast<uint4*>(o.xt + (panel * o.steps + s) * kPanelStep + h * 1024 + lane * 16) = u[h];
+}
+
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(256) void k_gated_prepare(GatedPrepare o, int32_t first) {
+  int32_t id = first + int32_t(blockIdx.x);
+  if constexpr (GRAD) {
+    if (id < o.grads) {
+      const int32_t quads = (o.grad.steps + 3) / 4;
+      return gated_grad<DT>(o.grad, id / quads, id % quads);
+    }
+    id -= o.grads;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t across = (o.steps + 15) / 16;
+  const bool x = id >= o.weights[0] + o.weights[1], second = !x && id >= o.weights[0];
+  if (x || second) id -= o.weights[0];
+  if (x) id -= o.weights[1];
+  const int64_t panel = id / across;
+  const int32_t s = (id % across * 4 + wave) * 4;
+  if (s >= o.steps) return;
+  if (x)
+    gated_pack_x(o, panel, s, lane);
+  else
+    expand4(second ? o.w[1] : o.w[0], panel, s, lane);
 }
 
 struct GatedDx {
@@ -472,18 +529,38 @@ PanelOperand weight_operand(const hyb_layout& L, const hyb_packed& P, const char
   return o;
 }
 
-hipError_t expand_pair(const hyb_gated_pair& w, const GatedPlan& p, char* ws, hipStream_t s, PanelOperand (&out)[2]) {
+// Both weights' tiles, and x as panels, as the launch below leaves them.
+void weight_pair(const hyb_gated_pair& w, const GatedPlan& p, char* ws, GatedPrepare* o, PanelOperand (&out)[2]) {
   const hyb_layout* L[2] = {w.gate_layout, w.up_layout};
   const hyb_packed* P[2] = {w.gate, w.up};
-  for (int i = 0; i < 2; ++i) out[i] = weight_operand(*L[i], *P[i], ws + p.w[i]);
-  if (L[0]->n_sparse == 0 && L[1]->n_sparse == 0) return hipSuccess;
-  return launch_expand_pair(*L[0], *P[0], ws + p.w[0], *L[1], *P[1], ws + p.w[1], s);
+  for (int i = 0; i < 2; ++i) {
+    out[i] = weight_operand(*L[i], *P[i], ws + p.w[i]);
+    o->w[i] = Expand{static_cast<const char*>(P[i]->val), static_cast<const char*>(P[i]->meta), P[i]->tidx,
+                     int32_t(L[i]->n_dense), int32_t(L[i]->n_sparse), L[i]->b1, L[i]->b2, L[i]->meta,
+                     int32_t(L[i]->tiles_k), int32_t(p.k / 64), ws + p.w[i]};
+    if (L[i]->n_sparse > 0) o->weights[i] = int32_t(p.n / 16 * ((p.k / 64 + 15) / 16));
+  }
+}
+PanelOperand x_panels(const GatedPlan& p, const void* x, int64_t ldx, char* ws, GatedPrepare* o) {
+  o->x = static_cast<const uint16_t*>(x);
+  o->ldx = ldx;
+  o->xt = ws + p.x;
+  o->xs = int32_t(p.m16 / 16 * ((p.k / 64 + 15) / 16));
+  return PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.k / 64), nullptr, 0};
 }
 
-// x as panels.
-hipError_t pack_x(const GatedPlan& p, const void* x, int64_t ldx, char* ws, hipStream_t s, PanelOperand* out) {
-  *out = PanelOperand{ws + p.x, int32_t(p.m16), int32_t(p.k / 64), nullptr, 0};
-  return launch_pack_x(static_cast<const uint16_t*>(x), ldx, p.m, p.k, ws + p.x, s);
+template <int DT, bool GRAD>
+hipError_t prepare(const GatedPlan& p, GatedPrepare& o, hipStream_t s) {
+  o.m = int32_t(p.m);
+  o.k = int32_t(p.k);
+  o.steps = int32_t(p.k / 64);
+  const int32_t all = o.grads + o.weights[0] + o.weights[1] + o.xs, most = 1 << 23;
+  for (int32_t first = 0; first < all; first += most) {  // (a launch stays below 2^32 threads)
+    const int32_t count = all - first < most ? all - first : most;
+    hipLaunchKernelGGL((k_gated_prepare<DT, GRAD>), dim3(unsigned(count)), dim3(256), 0, s, o, first);
+    HYB_TRY(hipGetLastError());
+  }
+  return hipSuccess;
 }
 
 template <int DT, int BP, int WA, int WB, int STAGES>
@@ -537,9 +614,11 @@ hipError_t forward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, c
     hipLaunchKernelGGL((k_gated_act<DT>), dim3(unsigned((p.n + 1023) / 1024), unsigned(p.m)), dim3(256), 0, s, o);
     return hipGetLastError();
   }
-  PanelOperand W[2], X;
-  HYB_TRY(expand_pair(w, p, ws, s, W));
-  HYB_TRY(pack_x(p, x, ldx, ws, s, &X));
+  PanelOperand W[2];
+  GatedPrepare first{};
+  weight_pair(w, p, ws, &first, W);
+  const PanelOperand X = x_panels(p, x, ldx, ws, &first);
+  HYB_TRY((prepare<DT, false>(p, first, s)));
   o.ws = reinterpret_cast<f32x4_t*>(ws + p.gu);
   o.whole = int32_t(p.whole);
   o.parts = p.parts;
@@ -572,7 +651,8 @@ template <int DT>
 hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int64_t ldx,
                           const GatedBackward& b, char* ws, hipStream_t s) {
   uint32_t* top = reinterpret_cast<uint32_t*>(ws + p.misc);
-  GatedGrad g{};
+  GatedPrepare first{};
+  GatedGrad& g = first.grad;
   g.g = b.g;
   g.u = b.u;
   g.dh = static_cast<const uint16_t*>(b.dh);
@@ -592,13 +672,14 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
     hipLaunchKernelGGL((k_gated_top<DT>), dim3(unsigned(g.groups)), dim3(256), 0, s, g);
     HYB_TRY(hipGetLastError());
   }
-  hipLaunchKernelGGL((k_gated_grad<DT>), dim3(unsigned(p.m16 / 16), unsigned((g.steps + 3) / 4)), dim3(256), 0, s, g);
-  HYB_TRY(hipGetLastError());
+  first.grads = int32_t(p.m16 / 16 * ((g.steps + 3) / 4));
+  PanelOperand W[2], X;
+  if (b.dx) weight_pair(w, p, ws, &first, W);
+  if (b.dw[0]) X = x_panels(p, x, ldx, ws, &first);
+  HYB_TRY((prepare<DT, true>(p, first, s)));
   const PanelOperand D[2] = {PanelOperand{ws + p.g[0], int32_t(p.m16), g.steps, nullptr, 0},
                              PanelOperand{ws + p.g[1], int32_t(p.m16), g.steps, nullptr, 0}};
   if (b.dx) {
-    PanelOperand W[2];
-    HYB_TRY(expand_pair(w, p, ws, s, W));
     const GatedDx o{reinterpret_cast<float*>(ws + p.dx), static_cast<uint16_t*>(b.dx), b.lddx, int32_t(p.m),
                     int32_t(p.k), top};
     HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4, 2>(W, D, p.parts, o, s))
@@ -611,8 +692,6 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
     }
   }
   if (b.dw[0]) {
-    PanelOperand X;
-    HYB_TRY(pack_x(p, x, ldx, ws, s, &X));
     const GatedDw o{{static_cast<uint16_t*>(b.dw[0]), static_cast<uint16_t*>(b.dw[1])}, {b.lddw[0], b.lddw[1]},
                     int32_t(p.n), int32_t(p.k), top};
     const int32_t steps = int32_t(p.m64 / 64);

@@ -1022,7 +1022,9 @@ hipError_t run_product(Q4Args& a, const Q4Route& r, char* ws, hipStream_t s) {
   if (r.bp == 1) return run_shared<DT, GATED, 1>(a, s);
   if (r.bp == 2) return run_shared<DT, GATED, 2>(a, s);
   if (r.bp == 4) return run_shared<DT, GATED, 4>(a, s);
-  const hipError_t e = launch_pack_x(a.x, a.ldx, a.m, a.k, ws, s);
+  hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((a.m + 15) / 16), unsigned((a.steps64 + 15) / 16)), dim3(256), 0, s, a.x,
+                     a.ldx, a.m, a.k, a.steps64, ws);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.xt = ws;
   a.x_panel = int64_t(a.steps64) * 2048;
@@ -1067,13 +1069,6 @@ hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a
     hipLaunchKernelGGL((k_q4_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
   else
     hipLaunchKernelGGL((k_q4_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_pack_x(const uint16_t* x, int64_t ldx, int64_t m, int64_t k, char* out, hipStream_t s) {
-  const int32_t steps64 = int32_t((k + 63) / 64);
-  hipLaunchKernelGGL(k_q4_pack_x, dim3(unsigned((m + 15) / 16), unsigned((steps64 + 15) / 16)), dim3(256), 0, s, x, ldx, m,
-                     int32_t(k), steps64, out);
   return hipGetLastError();
 }
 

@@ -42,9 +42,6 @@ hipError_t launch_q4_quantize(const void* a, int dtype, int64_t n, int64_t k, in
                               hipStream_t s);
 hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a, int dtype, int64_t lda,
                                 hipStream_t s);
-// x (m x k, 16 bits) as panels of hyb_panel.h: ceil(m / 16) of ceil(k / 64) steps,
-// rows behind m and columns behind k zero.
-hipError_t launch_pack_x(const uint16_t* x, int64_t ldx, int64_t m, int64_t k, char* out, hipStream_t s);
 // Y = X W^T, or with `up` act(X W^T) * (X up^T).
 hipError_t launch_q4_product(const hyb_q4& w, const hyb_q4* up, int act, int64_t n, int64_t k, const void* x,
                              int x_dtype, int64_t m, int64_t ldx, void* y, int y_dtype, int64_t ldy, char* ws,

@@ -11,6 +11,7 @@
 // (W', X and, for dW, G) are transposed on their way out of LDS.
 #include <type_traits>
 
+#include "hyb_expand.h"
 #include "hyb_panel.h"
 #include "hyb_xent_internal.h"
 
@@ -72,15 +73,6 @@ __global__ __launch_bounds__(256) void k_xent_pack_x(const uint16_t* __restrict_
   }
 }
 
-// Sixteen columns 16 q.. of a row (q = lane / 16) as the two 16-byte pieces of
-// the panel order: half q / 2, units 2 (q % 2) and 2 (q % 2) + 1.
-__device__ __forceinline__ void store_row16(char* step, int lane, const uint32_t (&e)[8]) {
-  const int q = lane >> 4, r = lane & 15;
-  char* p = step + (q >> 1) * 1024 + (2 * (q & 1)) * 256;
-  *reinterpret_cast<uint4*>(p + r * 16) = make_uint4(e[0], e[1], e[2], e[3]);
-  *reinterpret_cast<uint4*>(p + 256 + r * 16) = make_uint4(e[4], e[5], e[6], e[7]);
-}
-
 // The tiles of rows v0.. (a multiple of b1) of a packed matrix that are not
 // multiplied where they lie, into `out` in tile order (one wavefront per panel
 // and step): sparse ones expanded from their values and codes, those of a tile
@@ -137,76 +129,6 @@ __global__ __launch_bounds__(256) void k_xent_expand(const uint4* __restrict__ d
     }
   }
   store_row16(dst, lane, e);
-}
-
-struct ExpandOne {
-  const char* val;
-  const char* meta;
-  const int32_t* tidx;
-  int32_t n_dense, n_sparse;
-  char* out;
-};
-struct ExpandPair {
-  ExpandOne w[2];
-  int b1, b2, meta_kind;
-  int32_t tiles_k, steps;
-};
-
-// The same for two whole matrices in one launch (its third dimension), a wavefront
-// per panel and four steps, whose loads are under way at once: 17408 x 5120, 60% of
-// the tiles sparse, 56 us (one step a wavefront, a launch each, 79 us).
-__global__ __launch_bounds__(256) void k_expand_pair(ExpandPair e) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool second = blockIdx.z != 0;
-  const ExpandOne w = second ? e.w[1] : e.w[0];
-  if (w.n_sparse == 0) return;
-  const int32_t s0 = (int32_t(blockIdx.y) * 4 + wave) * 4;
-  if (s0 >= e.steps) return;
-  const int64_t r0 = int64_t(blockIdx.x) * 16, tn = r0 / e.b1;
-  const int rs = int(r0 - tn * e.b1) / 16, spt = e.b2 / 64;
-  int32_t ti[4];
-  uint4 val[4];
-  uint32_t code[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) ti[i] = s0 + i < e.steps ? w.tidx[tn * e.tiles_k + (s0 + i) / spt] : 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // (a tile that is not sparse, or has no slot: an empty resource, zeros)
-    const int64_t slot = ~ti[i];
-    const bool in = ti[i] < 0 && slot < w.n_sparse && s0 + i < e.steps;
-    const int c = (s0 + i) % spt;
-    const int64_t at = (in ? slot * e.b1 * e.b2 : 0) + rs * 16 * e.b2;
-    const __amdgpu_buffer_rsrc_t vr = make_rsrc(w.val + at + c * 1024, in ? 1024 : 0);
-    const __amdgpu_buffer_rsrc_t mr = make_rsrc(w.meta + at / 8, in ? 2 * e.b2 : 0);
-    val[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(vr, lane * 16, 0, 0));
-    code[i] = __builtin_amdgcn_raw_buffer_load_b16(mr, (lane * spt + c) * 2, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t s = s0 + i;
-    if (s >= e.steps || (ti[i] >= 0 && ti[i] < w.n_dense)) continue;
-    const bool in = ti[i] < 0 && ~ti[i] < w.n_sparse;
-    const uint32_t v[4] = {val[i].x, val[i].y, val[i].z, val[i].w};
-    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in && e.meta_kind == HYB_META_MASK8) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[4 * g + j] = __builtin_amdgcn_perm(v[2 * g + 1], v[2 * g], expand8_selector((code[i] >> (8 * g)) & 0xFFu, j));
-    } else if (in) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t i0, i1;
-        nibble_positions((code[i] >> (4 * g)) & 0xFu, e.meta_kind, i0, i1);
-        x[2 * g] = __builtin_amdgcn_perm(0u, v[g], scatter_selector(0, i0, i1));
-        x[2 * g + 1] = __builtin_amdgcn_perm(0u, v[g], scatter_selector(2, i0, i1));
-      }
-    }
-    store_row16(w.out + (tn * e.tiles_k + s / spt) * e.b1 * e.b2 * 2 + int64_t(rs) * 32 * e.b2 + s % spt * kPanelStep,
-                lane, x);
-  }
 }
 
 // Largest exponent byte of an 8-bit head's scales (rows < n_vocab); *top starts
@@ -974,23 +896,6 @@ hipError_t backward_typed(const hyb_head& head, const XentPlan& p, int64_t n_voc
 }
 
 }  // namespace
-
-hipError_t launch_expand_pair(const hyb_layout& L0, const hyb_packed& P0, char* out0, const hyb_layout& L1,
-                              const hyb_packed& P1, char* out1, hipStream_t s) {
-  auto one = [](const hyb_layout& L, const hyb_packed& P, char* out) {
-    return ExpandOne{static_cast<const char*>(P.val), static_cast<const char*>(P.meta), P.tidx,
-                     int32_t(L.n_dense),              int32_t(L.n_sparse),              out};
-  };
-  const ExpandPair e{{one(L0, P0, out0), one(L1, P1, out1)},
-                     L0.b1,
-                     L0.b2,
-                     L0.meta,
-                     int32_t(L0.tiles_k),
-                     int32_t(L0.k / 64)};
-  const dim3 grid(unsigned(L0.n / 16), unsigned((e.steps + 15) / 16), 2);
-  hipLaunchKernelGGL(k_expand_pair, grid, dim3(256), 0, s, e);
-  return hipGetLastError();
-}
 
 hipError_t launch_xent(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype, int64_t ldx,
                        const int64_t* target, int64_t ignore, float* loss, float* lse, char* ws, hipStream_t s) {

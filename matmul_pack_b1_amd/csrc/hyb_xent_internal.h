@@ -27,12 +27,6 @@ struct XentPlan {
 };
 XentPlan xent_plan(const hyb_head& head, int64_t m, int what, int64_t cus);
 
-// The tiles of two packed matrices of one shape that a PanelOperand calls spare
-// (all but the dense ones with a slot), each at its place in tile order, n k
-// 16-bit elements.  A matrix without sparse tiles is left out.
-hipError_t launch_expand_pair(const hyb_layout& L0, const hyb_packed& P0, char* out0, const hyb_layout& L1,
-                              const hyb_packed& P1, char* out1, hipStream_t s);
-
 hipError_t launch_xent(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype, int64_t ldx,
                        const int64_t* target, int64_t ignore, float* loss, float* lse, char* ws, hipStream_t s);
 hipError_t launch_xent_backward(const hyb_head& head, const XentPlan& p, int64_t n_vocab, const void* x, int dtype,
