@@ -69,8 +69,8 @@ hyb_status hyb_gated_workspace_size(const hyb_gated_pair* w, int32_t m, int32_t 
  *   g, u  device m x n fp32, row strides ldg, ldu >= n, element-aligned:
  *         receive G and U for hyb_gated_backward; both or neither (NULL), and
  *         neither with 4-bit weights (HYB_ERR_UNSUPPORTED)
- * 0 <= m <= 2^22; 1 <= n <= 2^27 - 16 and 1 <= k <= 2^21 for packed weights,
- * 0 <= n and 0 <= k <= 2^22 for 4-bit ones (k = 0 gives zeros). */
+ * 0 <= m <= 2^22; 1 <= n, k <= 2^21 for packed weights, 0 <= n <= 2^27 - 16
+ * and 0 <= k <= 2^22 for 4-bit ones (k = 0 gives zeros). */
 hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
                      void* h, int64_t ldh, float* g, int64_t ldg, float* u, int64_t ldu, void* workspace,
                      size_t workspace_bytes, void* stream);

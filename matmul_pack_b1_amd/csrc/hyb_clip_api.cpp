@@ -1,7 +1,7 @@
 // Host side of the norm and the clipping (include/hyb_clip.h): argument checks
 // and planning, then the launches.
 #include <algorithm>
-#include <new>
+#include <exception>
 
 #include "hyb_clip_internal.h"
 
@@ -65,6 +65,9 @@ hyb_status read_list(int64_t count, const hyb_tensor* list, bool data, bool out,
       if (t.rows > 1 && (ld < t.cols || ld > most))
         return fail(HYB_ERR_INVALID_ARG, "tensor %lld: row stride %lld outside [%lld, 2^40]", (long long)i, (long long)ld,
                     (long long)t.cols);
+      else if (t.rows > 1 && ld > (int64_t(1) << 44) / (t.rows - 1))  // (addresses stay within 64 bits)
+        return fail(HYB_ERR_INVALID_ARG, "tensor %lld: %lld rows of stride %lld reach over 2^44 elements", (long long)i,
+                    (long long)t.rows, (long long)ld);
     if (data && (!t.data || !aligned(t.data, elem_size(t.dtype))))
       return fail(HYB_ERR_INVALID_ARG, "tensor %lld: data is NULL or not aligned to its element", (long long)i);
     if (data && out && (!t.out || !aligned(t.out, elem_size(t.dtype))))
@@ -145,7 +148,7 @@ template <typename F>
 hyb_status guarded(F f) {
   try {
     return f();
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {
     return fail(HYB_ERR_INVALID_ARG, "out of host memory");
   }
 }

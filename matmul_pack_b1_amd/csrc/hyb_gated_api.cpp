@@ -159,6 +159,7 @@ hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_
   if (g) {
     if ((st = check_rows(g, n, ldg, "g", 4)) != HYB_OK) return st;
     if ((st = check_rows(u, n, ldu, "u", 4)) != HYB_OK) return st;
+    if (g == u) return fail(HYB_ERR_INVALID_ARG, "g and u are one buffer");
   }
   if (k > 0 && (st = check_x(x, k, ldx, dtype != 0)) != HYB_OK) return st;
   if ((st = check_ws(workspace, workspace_bytes, need)) != HYB_OK) return st;
@@ -194,6 +195,7 @@ hyb_status hyb_gated_backward(const hyb_gated_pair* w, int32_t act, const void* 
   if (dw_gate) {
     if ((st = check_rows(dw_gate, k, lddw_gate, "dw_gate")) != HYB_OK) return st;
     if ((st = check_rows(dw_up, k, lddw_up, "dw_up")) != HYB_OK) return st;
+    if (dw_gate == dw_up) return fail(HYB_ERR_INVALID_ARG, "dw_gate and dw_up are one buffer");
   }
   size_t need = 0;
   if ((st = hyb_gated_workspace_size(w, m, what, &need)) != HYB_OK) return st;

@@ -45,6 +45,7 @@ def call_clip(ts, max_norm=1.0, norm=64, ws=P16 // 2, nbytes=1 << 20, count=None
 @pytest.mark.parametrize("args,status", [
     (dict(dtype=0), 3), (dict(dtype=4), 3), (dict(rows=-1), 2), (dict(cols=-1), 2), (dict(rows=1 << 21, cols=1 << 20), 2),
     (dict(cols=(1 << 40) + 1), 2), (dict(lda=7), 1), (dict(ldo=7), 1), (dict(ldo=-9), 1), (dict(lda=(1 << 40) + 1), 1),
+    (dict(rows=1 << 10, lda=1 << 35), 1), (dict(rows=1 << 10, ldo=1 << 35), 1),
     (dict(data=None), 1), (dict(out=None), 1), (dict(data=P16 + 2), 1), (dict(out=P16 + 1), 1),
     (dict(out=P16 + 16), 1), (dict(out=P16 - 16), 1), (dict(out=P16, ldo=9), 1), (dict(data=32), 1), (dict(out=60), 1),
 ])

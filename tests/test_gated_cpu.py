@@ -120,13 +120,13 @@ FORWARD = [
     (dict(m=(1 << 22) + 1), 2), (dict(x=None), 1), (dict(x=P16 + 8), 1), (dict(ldx=255), 1), (dict(ldx=260), 1),
     (dict(ldx=1 << 22), 4), (dict(h=None), 1), (dict(h=P16 + 1), 1), (dict(ldh=127), 1), (dict(ldh=2 ** 31 + 1), 4),
     (dict(g=None), 1), (dict(u=None), 1), (dict(g=P16 + 2), 1), (dict(ldu=100), 1), (dict(ws=None), 1),
-    (dict(ws=P16 + 8), 1), (dict(nbytes=64), 1),
+    (dict(ws=P16 + 8), 1), (dict(nbytes=64), 1), (dict(u=P16), 1),
 ]
 
 
 @pytest.mark.parametrize("args,status", FORWARD)
 def test_forward_refusals(args, status):
-    d = dict(act=1, x=P16, dt=hb.HYB_BF16, m=200, ldx=256, h=P16, ldh=128, g=P16, ldg=128, u=P16, ldu=128, ws=P16,
+    d = dict(act=1, x=P16, dt=hb.HYB_BF16, m=200, ldx=256, h=P16, ldh=128, g=P16, ldg=128, u=3 * P16, ldu=128, ws=P16,
              nbytes=1 << 40)
     d.update(args)
     st = gated.lib().hyb_gated(ctypes.byref(_packed_pair()), d["act"], d["x"], d["dt"], d["m"], d["ldx"], d["h"],
@@ -150,11 +150,11 @@ def test_forward_4bit_refusals(args, status):
     (dict(act=0), 1), (dict(dt=hb.HYB_F16), 3), (dict(m=-1), 2), (dict(x=P16 + 8), 1), (dict(ldx=257), 1),
     (dict(g=None), 1), (dict(u=None), 1), (dict(dh=None), 1), (dict(dh=P16 + 1), 1), (dict(lddh=100), 1),
     (dict(dx=P16 + 1), 1), (dict(lddx=200), 1), (dict(dwg=None), 1), (dict(dwu=None), 1), (dict(dwu=P16 + 1), 1),
-    (dict(lddw=200), 1), (dict(ws=None), 1), (dict(nbytes=64), 1),
+    (dict(lddw=200), 1), (dict(ws=None), 1), (dict(nbytes=64), 1), (dict(dwu=P16), 1),
 ])
 def test_backward_refusals(args, status):
     d = dict(act=1, x=P16, dt=hb.HYB_BF16, m=20, ldx=256, g=P16, u=P16, dh=P16, lddh=128, dx=P16, lddx=256, dwg=P16,
-             dwu=P16, lddw=256, ws=P16, nbytes=1 << 40)
+             dwu=3 * P16, lddw=256, ws=P16, nbytes=1 << 40)
     d.update(args)
     st = gated.lib().hyb_gated_backward(ctypes.byref(_packed_pair()), d["act"], d["x"], d["dt"], d["m"], d["ldx"],
                                         d["g"], 128, d["u"], 128, d["dh"], d["lddh"], d["dx"], d["lddx"], d["dwg"],
