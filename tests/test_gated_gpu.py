@@ -342,3 +342,23 @@ def test_workspace_of_the_caller():
         assert torch.equal(a, b)
     with pytest.raises(hb.HybError):
         gated.backward(G, U, x, g, u, dh, need_dw=True, workspace=ws[:1024])
+
+
+def test_more_than_2_31_outputs():
+    """G, U, H and the gradients' panels lie beyond 2^31 elements; only the last
+    tokens have a gradient."""
+    m, n, k, last = 160000, 14336, 64, slice(159700, 160000)
+    G, wg, U, wu = weights("packed", 7, n, k, "bf16")
+    x = normal(8, m, k, "bf16")
+    h, g, u = gated.forward(G, U, x, save=True)
+    xv = as64(x[last])
+    for got, w in ((g, wg), (u, wu)):
+        close(got[last], xv @ w.T, k * 2.0 ** -23 * (np.abs(xv) @ np.abs(w).T))
+    a = go.act(as64(g[last]), "silu")[0]
+    ref = a * as64(u[last])
+    close(h[last], ref, (2.0 ** -8 + 2.0 ** -20) * np.abs(ref) + act_error(as64(g[last])) * np.abs(as64(u[last])))
+    dh = torch.zeros_like(h)
+    dh[last] = normal(9, 300, n, "bf16")
+    dx, dwg, dwu = gated.backward(G, U, x, g, u, dh, need_dw=True)
+    assert not dx[:159700].any()
+    check_backward(G, wg, U, wu, x[last], g[last], u[last], dh[last], "bf16", "silu", (dx[last], dwg, dwu))
