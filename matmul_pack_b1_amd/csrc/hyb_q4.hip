@@ -5,6 +5,7 @@
 #include "hyb_act.h"
 #include "hyb_panel.h"
 #include "hyb_q4_internal.h"
+#include "hyb_stream.h"
 
 namespace hyb {
 namespace {
@@ -42,7 +43,7 @@ __device__ __forceinline__ Eight4<DT> load4(const void* a, int64_t base, int32_t
   const Bytes16* p = reinterpret_cast<const Bytes16*>(static_cast<const char*>(a) + at * (DT == HYB_F32 ? 4 : 2));
 #pragma unroll
   for (int i = 0; i < kWords / 4; ++i) {
-    const Bytes16 u = p[i];
+    const Bytes16 u = stream_load(p + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.w[4 * i + j] = u.w[j];
   }
@@ -96,7 +97,8 @@ __device__ __forceinline__ uint32_t group_byte(uint32_t top) {
 // One workgroup per panel, a wavefront per 512 columns at a time: a load covers
 // them in one row (8 columns per lane, four lanes to a group), codes and scales are
 // put into the stream's order in LDS.  Bound by memory: 28672x8192 bf16, 470 MB read
-// and 125 MB written, 166 us (3.6 TB/s; with 128 columns of four rows to a load 186).
+// and 125 MB written, 111-128 us (4.6-5.4 TB/s; with loads that the caches keep 166, and
+// so with 128 columns of four rows to a load 186).
 template <int DT>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a, int64_t n, int32_t k, int64_t lda,
                                                      int32_t steps, int64_t rows16, char* __restrict__ codes,
@@ -201,8 +203,9 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a,
 }
 
 // One wavefront per panel and step: codes through LDS into rows, 8 columns per
-// lane.  Bound by memory: 28672x8192, 595 MB, 112 us (5.3 TB/s).
-template <int DT>
+// lane.  Bound by memory: 28672x8192, 595 MB, 94 us (6.3 TB/s; with stores that the
+// caches keep 111, and the quantising of the next weight 128 instead of 111).
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ codes,
                                                        const char* __restrict__ scales, int64_t n, int32_t k,
                                                        int64_t lda, int32_t steps, int64_t rows16,
@@ -243,8 +246,13 @@ __global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ 
         Bytes16 u[2];
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e >> 2].w[e & 3] = __builtin_bit_cast(uint32_t, v[e]);
-        reinterpret_cast<Bytes16*>(p)[0] = u[0];
-        reinterpret_cast<Bytes16*>(p)[1] = u[1];
+        if constexpr (STREAM) {
+          stream_store(p, u[0]);
+          stream_store(p + 4, u[1]);
+        } else {
+          reinterpret_cast<Bytes16*>(p)[0] = u[0];
+          reinterpret_cast<Bytes16*>(p)[1] = u[1];
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -256,7 +264,10 @@ __global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ 
         Bytes16 u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) u.w[e] = round16x2<DT>(v[2 * e], v[2 * e + 1]);
-        *reinterpret_cast<Bytes16*>(p) = u;
+        if constexpr (STREAM)
+          stream_store(p, u);
+        else
+          *reinterpret_cast<Bytes16*>(p) = u;
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -1063,12 +1074,16 @@ hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a
   const dim3 grid(unsigned(rows16 / 16), unsigned((steps + 3) / 4));
   const char* codes = static_cast<const char*>(src.codes);
   const char* scales = static_cast<const char*>(src.scales);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+  };
+  const bool stream = n * k * (dtype == HYB_F32 ? 4 : 2) > kStreamBytes;
   if (dtype == HYB_F32)
-    hipLaunchKernelGGL((k_q4_dequantize<HYB_F32>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+    stream ? go(&k_q4_dequantize<HYB_F32, true>) : go(&k_q4_dequantize<HYB_F32, false>);
   else if (dtype == HYB_BF16)
-    hipLaunchKernelGGL((k_q4_dequantize<HYB_BF16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+    stream ? go(&k_q4_dequantize<HYB_BF16, true>) : go(&k_q4_dequantize<HYB_BF16, false>);
   else
-    hipLaunchKernelGGL((k_q4_dequantize<HYB_F16>), grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
+    stream ? go(&k_q4_dequantize<HYB_F16, true>) : go(&k_q4_dequantize<HYB_F16, false>);
   return hipGetLastError();
 }
 
