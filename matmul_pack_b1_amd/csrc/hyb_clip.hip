@@ -1,13 +1,16 @@
 // Kernels of the 2-norm over a list of tensors and their scaling
-// (include/hyb_clip.h).  Bound by memory: 872 MB of gradients are read in 167 us (5.2
-// TB/s) and scaled in 313 (5.6); nine small ones take the depth of two launches, 4.5
-// and 5.7 us.
+// (include/hyb_clip.h).  Bound by memory: 872 MB of gradients are read in 129 us
+// (6.7 TB/s) and scaled in 317 (5.5), 450 in all (491 with loads and stores that the
+// caches keep); nine small ones take the depth of two launches, 4.7 and 6.2 us.
 //
 // Squares are fp64: the converting and the fused multiply-add of an element take
 // less of the vector unit than its bytes take of memory, and no sum overflows or
 // loses what is small beside it.
+#include <type_traits>
+
 #include "hyb_clip_internal.h"
 #include "hyb_panel.h"
+#include "hyb_stream.h"
 
 namespace hyb {
 namespace {
@@ -77,8 +80,24 @@ __device__ __forceinline__ float clip_read(const char* p, int64_t i) {
     return widen16<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
 }
 
+// Lists beyond kStreamBytes (STREAM) are read and written around the caches.
+template <bool STREAM>
+__device__ __forceinline__ Bytes16 clip_load(const char* p) {
+  if constexpr (STREAM)
+    return stream_load(p);
+  else
+    return *reinterpret_cast<const Bytes16*>(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void clip_store(char* p, const Bytes16& b) {
+  if constexpr (STREAM)
+    stream_store(p, b);
+  else
+    *reinterpret_cast<Bytes16*>(p) = b;
+}
+
 // A thread's share of the squares of `n` elements at p.
-template <int DT>
+template <int DT, bool STREAM>
 __device__ __forceinline__ double clip_chunk(const char* p, int32_t n) {
   constexpr int kEach = DT == HYB_F32 ? 4 : 8;  // of 16 bytes
   const int32_t whole = n / kEach;
@@ -87,7 +106,7 @@ __device__ __forceinline__ double clip_chunk(const char* p, int32_t n) {
   for (; i + 1792 < whole; i += 2048) {
     Bytes16 b[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
+    for (int u = 0; u < 8; ++u) b[u] = clip_load<STREAM>(p + (i + 256 * u) * 16);
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += clip_squares<DT>(b[u]);
   }
@@ -110,7 +129,7 @@ __device__ __forceinline__ void clip_at(const ClipTable<N>& t, int i, int64_t ch
   f(t.data[i] + (row * t.lda[i] + col) * size, t.out[i] + (row * t.ldo[i] + col) * size, n);
 }
 
-template <int N>
+template <int N, bool STREAM>
 __global__ __launch_bounds__(256) void k_clip_squares(ClipTable<N> t, double* __restrict__ sums) {
   __shared__ double lds[4];
   const int64_t all = t.start[t.count];
@@ -119,11 +138,11 @@ __global__ __launch_bounds__(256) void k_clip_squares(ClipTable<N> t, double* __
     const int i = clip_find(t, c);
     clip_at(t, i, c, [&](const char* p, char*, int32_t n) {
       if (t.dtype[i] == HYB_F32)
-        s += clip_chunk<HYB_F32>(p, n);
+        s += clip_chunk<HYB_F32, STREAM>(p, n);
       else if (t.dtype[i] == HYB_BF16)
-        s += clip_chunk<HYB_BF16>(p, n);
+        s += clip_chunk<HYB_BF16, STREAM>(p, n);
       else
-        s += clip_chunk<HYB_F16>(p, n);
+        s += clip_chunk<HYB_F16, STREAM>(p, n);
     });
   }
   s = clip_block_sum(s, lds);
@@ -144,7 +163,7 @@ __global__ __launch_bounds__(256) void k_clip_norm(const double* __restrict__ su
   if (threadIdx.x == 0) *norm = float(v);
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __device__ __forceinline__ void clip_scale(const char* p, char* q, int32_t n, float f) {
   constexpr int kEach = DT == HYB_F32 ? 4 : 8;
   const int32_t whole = n / kEach;
@@ -163,9 +182,9 @@ __device__ __forceinline__ void clip_scale(const char* p, char* q, int32_t n, fl
   for (; i + 1792 < whole; i += 2048) {
     Bytes16 b[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) b[u] = reinterpret_cast<const Bytes16*>(p)[i + 256 * u];
+    for (int u = 0; u < 8; ++u) b[u] = clip_load<STREAM>(p + (i + 256 * u) * 16);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) reinterpret_cast<Bytes16*>(q)[i + 256 * u] = scaled(b[u]);
+    for (int u = 0; u < 8; ++u) clip_store<STREAM>(q + (i + 256 * u) * 16, scaled(b[u]));
   }
   for (; i < whole; i += 256) reinterpret_cast<Bytes16*>(q)[i] = scaled(reinterpret_cast<const Bytes16*>(p)[i]);
   const int32_t at = whole * kEach + int32_t(threadIdx.x);
@@ -180,7 +199,7 @@ __device__ __forceinline__ void clip_scale(const char* p, char* q, int32_t n, fl
 
 // Every workgroup takes the norm from the sums itself (they lie in the caches),
 // which saves a launch.
-template <int N>
+template <int N, bool STREAM>
 __global__ __launch_bounds__(256) void k_clip_scale(ClipTable<N> t, const double* __restrict__ sums, int64_t count,
                                                     float max_norm, float* __restrict__ norm) {
   __shared__ double lds[4];
@@ -189,18 +208,18 @@ __global__ __launch_bounds__(256) void k_clip_scale(ClipTable<N> t, const double
   const double r = double(max_norm) / (v + 1e-6);
   const float f = r < 1.0 || r != r ? float(r) : 1.f;
   // from the last chunk to the first: what the squares read last lies in the
-  // last-level cache (872 MB 492 us, from the first on 522)
+  // last-level cache (872 MB, kept by the caches, 492 us, from the first on 522)
   const int64_t all = t.start[t.count];
   for (int64_t c = all - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = clip_find(t, c);
     if (f == 1.f && t.out[i] == t.data[i]) continue;
     clip_at(t, i, c, [&](const char* p, char* q, int32_t n) {
       if (t.dtype[i] == HYB_F32)
-        clip_scale<HYB_F32>(p, q, n, f);
+        clip_scale<HYB_F32, STREAM>(p, q, n, f);
       else if (t.dtype[i] == HYB_BF16)
-        clip_scale<HYB_BF16>(p, q, n, f);
+        clip_scale<HYB_BF16, STREAM>(p, q, n, f);
       else
-        clip_scale<HYB_F16>(p, q, n, f);
+        clip_scale<HYB_F16, STREAM>(p, q, n, f);
     });
   }
 }
@@ -223,15 +242,32 @@ ClipTable<N> table_of(const std::vector<hyb_tensor>& tensors, const ClipLaunch& 
   return t;
 }
 
+template <typename F>
+void with_table(int count, F f) {
+  if (count <= kClipFew)
+    f(std::integral_constant<int, kClipFew>());
+  else
+    f(std::integral_constant<int, kClipTensors>());
+}
+
+// More bytes than the last-level cache holds?
+bool streamed(const std::vector<hyb_tensor>& tensors) {
+  int64_t bytes = 0;
+  for (const hyb_tensor& t : tensors) bytes += t.rows * t.cols * (t.dtype == HYB_F32 ? 4 : 2);
+  return bytes > kStreamBytes;
+}
+
 hipError_t launch_squares(const std::vector<hyb_tensor>& tensors, const std::vector<ClipLaunch>& plan, double* ws,
-                          hipStream_t s) {
+                          bool stream, hipStream_t s) {
   for (const ClipLaunch& l : plan) {
-    const dim3 grid(unsigned(l.groups));
-    if (l.count <= kClipFew)
-      hipLaunchKernelGGL((k_clip_squares<kClipFew>), grid, dim3(256), 0, s, table_of<kClipFew>(tensors, l), ws + l.sum0);
-    else
-      hipLaunchKernelGGL((k_clip_squares<kClipTensors>), grid, dim3(256), 0, s, table_of<kClipTensors>(tensors, l),
+    auto go = [&](auto kernel, auto few) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(l.groups)), dim3(256), 0, s, table_of<decltype(few)::value>(tensors, l),
                          ws + l.sum0);
+    };
+    with_table(l.count, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      stream ? go(&k_clip_squares<N, true>, n) : go(&k_clip_squares<N, false>, n);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -243,7 +279,7 @@ hipError_t launch_squares(const std::vector<hyb_tensor>& tensors, const std::vec
 hipError_t launch_norm(const std::vector<hyb_tensor>& tensors, float* norm, double* ws, hipStream_t s) {
   int64_t sums;
   const std::vector<ClipLaunch> plan = clip_plan(tensors, &sums);
-  const hipError_t e = launch_squares(tensors, plan, ws, s);
+  const hipError_t e = launch_squares(tensors, plan, ws, streamed(tensors), s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_clip_norm, dim3(1), dim3(256), 0, s, ws, sums, norm);
   return hipGetLastError();
@@ -253,16 +289,19 @@ hipError_t launch_clip(const std::vector<hyb_tensor>& tensors, float max_norm, f
   if (tensors.empty()) return launch_norm(tensors, norm, ws, s);
   int64_t sums;
   const std::vector<ClipLaunch> plan = clip_plan(tensors, &sums);
-  hipError_t e = launch_squares(tensors, plan, ws, s);
+  const bool stream = streamed(tensors);
+  hipError_t e = launch_squares(tensors, plan, ws, stream, s);
   for (size_t i = plan.size(); i-- > 0 && e == hipSuccess;) {
-    const dim3 grid(unsigned(plan[i].groups));
+    const ClipLaunch& l = plan[i];
     float* to = i == 0 ? norm : nullptr;
-    if (plan[i].count <= kClipFew)
-      hipLaunchKernelGGL((k_clip_scale<kClipFew>), grid, dim3(256), 0, s, table_of<kClipFew>(tensors, plan[i]), ws, sums,
-                         max_norm, to);
-    else
-      hipLaunchKernelGGL((k_clip_scale<kClipTensors>), grid, dim3(256), 0, s, table_of<kClipTensors>(tensors, plan[i]), ws,
+    auto go = [&](auto kernel, auto few) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(l.groups)), dim3(256), 0, s, table_of<decltype(few)::value>(tensors, l), ws,
                          sums, max_norm, to);
+    };
+    with_table(l.count, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      stream ? go(&k_clip_scale<N, true>, n) : go(&k_clip_scale<N, false>, n);
+    });
     e = hipGetLastError();
   }
   return e;
