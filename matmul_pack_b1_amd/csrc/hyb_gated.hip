@@ -13,6 +13,7 @@
 #include "hyb_gated_internal.h"
 #include "hyb_panel.h"
 #include "hyb_q4_internal.h"
+#include "hyb_stream.h"
 
 namespace hyb {
 namespace {
@@ -46,9 +47,11 @@ __device__ __forceinline__ void gated_put(const GatedOut& o, int64_t tok, int32_
     *reinterpret_cast<Bytes8*>(o.h + tok * o.ldh + j) = Bytes8{{r.x, r.y}};
   });
 }
+// (G and U wait for the backward pass: around the caches, 14336x4096, 4096 tokens,
+// forward and backward 2530 us instead of 2585, and 2816x1024, 333 tokens 68 either way.)
 __device__ __forceinline__ void gated_keep(float* p, f32x4_t v) {
   const u32x4_t b = __builtin_bit_cast(u32x4_t, v);
-  *reinterpret_cast<Bytes16*>(p) = Bytes16{{b[0], b[1], b[2], b[3]}};
+  stream_store(p, Bytes16{{b[0], b[1], b[2], b[3]}});
 }
 
 // H from fp32 G and U, which the products left in memory: four outputs a thread
@@ -67,10 +70,9 @@ __global__ __launch_bounds__(256) void k_gated_act(GatedOut o) {
 
 // AP / 2 panels of each weight x BP panels of tokens.  Bound by the matrix units:
 // 17408x5120, 2048 tokens 708 us, 1.03 Pflop/s, of which ten a round of tiles are their
-// start, activation and outputs; 14336x4096, 4096 tokens with 470 MB of G and U 925.
+// start, activation and outputs; 14336x4096, 4096 tokens with 470 MB of G and U 870-910.
 // (A priority above its neighbours' around the matrix instructions: no gain;
-// addresses prepared a step earlier 680 against 675 us; outputs stored around the
-// caches: no gain.)
+// addresses prepared a step earlier 680 against 675 us.)
 template <int DT, int AP, int BP, int WA, int WB, int STAGES>
 struct GatedTile {
   typedef PanelTile<DT, AP, BP, WA, WB, STAGES, false, false, true, false, true> T;
@@ -319,7 +321,7 @@ __device__ __forceinline__ void gated_grad(const GatedGrad& o, int64_t panel, in
 // other, and small calls are the depth of their launches): workgroups of dG and dU
 // (backward only), of each weight's sparse tiles, and of x as panels.  2816x1024, 333
 // tokens, forward and backward 68 us, with a launch each 76; 14336x4096, 4096 tokens,
-// backward 206 us for 1.0 GB (4.9 TB/s), with a launch each 227.
+// backward 206 us, with a launch each 227 (182, 5.5 TB/s, with G and U past the caches).
 struct GatedPrepare {
   GatedGrad grad;
   Expand w[2];
