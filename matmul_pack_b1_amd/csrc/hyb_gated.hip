@@ -385,14 +385,13 @@ struct GatedDx {
 // transposed, B = the panels).  A part takes the same steps of both.  14336x4096,
 // 4096 tokens 760 us, 1.27 Pflop/s (a library's product 4096 x 14336 x 4096: 1.29).
 template <int DT, int AP, int BP, int WA, int WB, int STAGES>
-__global__ __launch_bounds__(64 * WA * WB) void k_gated_dx(PanelOperand G, PanelOperand U, PanelOperand DG,
-                                                           PanelOperand DU, int32_t steps, int parts, GatedDx o) {
+__device__ __forceinline__ void gated_dx(const PanelOperand& G, const PanelOperand& U, const PanelOperand& DG,
+                                         const PanelOperand& DU, int32_t steps, int parts, const GatedDx& o, int32_t id,
+                                         int32_t part, char* gated_smem) {
   typedef PanelTile<DT, AP, BP, WA, WB, STAGES, true, false, true> T;
-  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
   const int32_t na = (G.steps * 4 + AP - 1) / AP, nb = (DG.rows16 / 16 + BP - 1) / BP;
   int32_t ab, bb;
-  const int32_t part = int32_t(blockIdx.y);
-  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
+  panel_block(panel_order(id, na * nb), na, nb, ab, bb);
   const int32_t quads = (steps + 3) / 4;  // a part is a whole number of four steps
   const int32_t s0 = int32_t(int64_t(quads) * part / parts) * 4;
   const int32_t s1 = part + 1 == parts ? steps : int32_t(int64_t(quads) * (part + 1) / parts) * 4;
@@ -432,6 +431,14 @@ __global__ __launch_bounds__(64 * WA * WB) void k_gated_dx(PanelOperand G, Panel
       });
 }
 
+template <int DT, int AP, int BP, int WA, int WB, int STAGES>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_dx(PanelOperand G, PanelOperand U, PanelOperand DG,
+                                                           PanelOperand DU, int32_t steps, int parts, GatedDx o) {
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  gated_dx<DT, AP, BP, WA, WB, STAGES>(G, U, DG, DU, steps, parts, o, int32_t(blockIdx.x), int32_t(blockIdx.y),
+                                       gated_smem);
+}
+
 // dX = the sum of the parts, in order, rounded once.
 template <int DT>
 __global__ __launch_bounds__(256) void k_gated_dx_sum(int parts, GatedDx o) {
@@ -464,14 +471,12 @@ struct GatedDw {
 // 840 against 775).  Small products take tiles of 128 x 128: 2816x1024, 333 tokens, with
 // the gradients' pass 22.6 against 25.3 us; 4096x4096, 1024 tokens 92.5 against 82.6.
 template <int DT, int AP, int BP, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB) void k_gated_dw(PanelOperand X, PanelOperand DG, PanelOperand DU,
-                                                           int32_t steps, GatedDw o) {
+__device__ __forceinline__ void gated_dw(const PanelOperand& X, const PanelOperand& DG, const PanelOperand& DU,
+                                         int32_t steps, const GatedDw& o, int32_t id, bool second, char* gated_smem) {
   typedef PanelTile<DT, AP, BP, WA, WB, 2, true, true> T;
-  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
   const int32_t na = (X.steps * 4 + AP - 1) / AP, nb = (DG.steps * 4 + BP - 1) / BP;
   int32_t ab, bb;
-  panel_block(panel_order(int32_t(blockIdx.x), na * nb), na, nb, ab, bb);
-  const bool second = blockIdx.y != 0;
+  panel_block(panel_order(id, na * nb), na, nb, ab, bb);
   PanelOperand D = DG;
   if (second) D.data = DU.data;
   f32x4_t acc[T::kA][T::kB];
@@ -496,6 +501,29 @@ __global__ __launch_bounds__(64 * WA * WB) void k_gated_dw(PanelOperand X, Panel
         const int32_t row = row0 + r, col = col0 + c;
         if (row < o.n && col < o.k) *reinterpret_cast<Bytes16*>(y + row * ld + col) = Bytes16{{u.x, u.y, u.z, u.w}};
       });
+}
+
+template <int DT, int AP, int BP, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB) void k_gated_dw(PanelOperand X, PanelOperand DG, PanelOperand DU,
+                                                           int32_t steps, GatedDw o) {
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  gated_dw<DT, AP, BP, WA, WB>(X, DG, DU, steps, o, int32_t(blockIdx.x), blockIdx.y != 0, gated_smem);
+}
+
+// Small products, of which neither fills the compute units: dX's tiles and, behind
+// them, dW's 128 x 128 ones in one launch (figures at the plan's choice of it).
+template <int DT, int BP, int WA, int WB, int STAGES>
+__global__ __launch_bounds__(512) void k_gated_both(PanelOperand G, PanelOperand U, PanelOperand DG, PanelOperand DU,
+                                                    PanelOperand X, int32_t steps, int parts, GatedDx dx, int32_t tiles,
+                                                    int32_t steps_m, GatedDw dw, int32_t tiles_w) {
+  extern __shared__ __attribute__((aligned(1024))) char gated_smem[];
+  int32_t id = int32_t(blockIdx.x);
+  if (id < tiles * parts) {
+    gated_dx<DT, 16, BP, WA, WB, STAGES>(G, U, DG, DU, steps, parts, dx, id % tiles, id / tiles, gated_smem);
+    return;
+  }
+  id -= tiles * parts;
+  gated_dw<DT, 8, 8, 2, 4>(X, DG, DU, steps_m, dw, id % tiles_w, id >= tiles_w, gated_smem);
 }
 
 // dW of an empty batch.
@@ -649,6 +677,21 @@ hipError_t run_dw(const PanelOperand& X, const PanelOperand (&D)[2], int32_t ste
   return hipGetLastError();
 }
 
+template <int DT, int BP, int WA, int WB, int STAGES>
+hipError_t run_both(const PanelOperand (&W)[2], const PanelOperand (&D)[2], const PanelOperand& X, int parts,
+                    const GatedDx& dx, int32_t steps_m, const GatedDw& dw, hipStream_t s) {
+  typedef PanelTile<DT, 16, BP, WA, WB, STAGES, true, false, true> T;
+  typedef PanelTile<DT, 8, 8, 2, 4, 2, true, true> V;
+  constexpr int kLds = T::kLds > V::kLds ? T::kLds : V::kLds;
+  static_assert(WA * WB == 8, "one size of workgroup");
+  HYB_TRY(allow_lds(&k_gated_both<DT, BP, WA, WB, STAGES>, kLds));
+  const int64_t tiles = int64_t((W[0].steps * 4 + 15) / 16) * ((D[0].rows16 / 16 + BP - 1) / BP);
+  const int64_t tiles_w = int64_t((X.steps * 4 + 7) / 8) * ((D[0].steps * 4 + 7) / 8);
+  hipLaunchKernelGGL((k_gated_both<DT, BP, WA, WB, STAGES>), dim3(unsigned(tiles * parts + 2 * tiles_w)), dim3(512), kLds, s,
+                     W[0], W[1], D[0], D[1], X, D[0].steps, parts, dx, int32_t(tiles), steps_m, dw, int32_t(tiles_w));
+  return hipGetLastError();
+}
+
 template <int DT>
 hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, const void* x, int64_t ldx,
                           const GatedBackward& b, char* ws, hipStream_t s) {
@@ -681,24 +724,28 @@ hipError_t backward_typed(const hyb_gated_pair& w, const GatedPlan& p, int act, 
   HYB_TRY((prepare<DT, true>(p, first, s)));
   const PanelOperand D[2] = {PanelOperand{ws + p.g[0], int32_t(p.m16), g.steps, nullptr, 0},
                              PanelOperand{ws + p.g[1], int32_t(p.m16), g.steps, nullptr, 0}};
-  if (b.dx) {
-    const GatedDx o{reinterpret_cast<float*>(ws + p.dx), static_cast<uint16_t*>(b.dx), b.lddx, int32_t(p.m),
-                    int32_t(p.k), top};
-    HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4, 2>(W, D, p.parts, o, s))
-            : p.bp == 8 ? (run_dx<DT, 8, 4, 2, 2>(W, D, p.parts, o, s))
-                        : (run_dx<DT, 4, 4, 2, 4>(W, D, p.parts, o, s)));
-    if (p.parts > 1) {
-      hipLaunchKernelGGL((k_gated_dx_sum<DT>), dim3(unsigned(p.m), unsigned((p.k + 1023) / 1024)), dim3(256), 0, s,
-                         p.parts, o);
-      HYB_TRY(hipGetLastError());
-    }
+  const GatedDx dx{reinterpret_cast<float*>(ws + p.dx), static_cast<uint16_t*>(b.dx), b.lddx, int32_t(p.m),
+                   int32_t(p.k), top};
+  const GatedDw dw{{static_cast<uint16_t*>(b.dw[0]), static_cast<uint16_t*>(b.dw[1])}, {b.lddw[0], b.lddw[1]},
+                   int32_t(p.n), int32_t(p.k), top};
+  const int32_t steps = int32_t(p.m64 / 64);
+  const bool both = b.dx && b.dw[0] && p.both;
+  if (both) {
+    HYB_TRY(p.bp == 16  ? (run_both<DT, 16, 2, 4, 2>(W, D, X, p.parts, dx, steps, dw, s))
+            : p.bp == 8 ? (run_both<DT, 8, 4, 2, 2>(W, D, X, p.parts, dx, steps, dw, s))
+                        : (run_both<DT, 4, 4, 2, 4>(W, D, X, p.parts, dx, steps, dw, s)));
+  } else if (b.dx) {
+    HYB_TRY(p.bp == 16  ? (run_dx<DT, 16, 2, 4, 2>(W, D, p.parts, dx, s))
+            : p.bp == 8 ? (run_dx<DT, 8, 4, 2, 2>(W, D, p.parts, dx, s))
+                        : (run_dx<DT, 4, 4, 2, 4>(W, D, p.parts, dx, s)));
   }
-  if (b.dw[0]) {
-    const GatedDw o{{static_cast<uint16_t*>(b.dw[0]), static_cast<uint16_t*>(b.dw[1])}, {b.lddw[0], b.lddw[1]},
-                    int32_t(p.n), int32_t(p.k), top};
-    const int32_t steps = int32_t(p.m64 / 64);
-    HYB_TRY(p.small_dw ? (run_dw<DT, 8, 8, 2, 4>(X, D, steps, o, s)) : (run_dw<DT, 16, 16, 2, 4>(X, D, steps, o, s)));
+  if (b.dx && p.parts > 1) {
+    hipLaunchKernelGGL((k_gated_dx_sum<DT>), dim3(unsigned(p.m), unsigned((p.k + 1023) / 1024)), dim3(256), 0, s, p.parts,
+                       dx);
+    HYB_TRY(hipGetLastError());
   }
+  if (b.dw[0] && !both)
+    HYB_TRY(p.small_dw ? (run_dw<DT, 8, 8, 2, 4>(X, D, steps, dw, s)) : (run_dw<DT, 16, 16, 2, 4>(X, D, steps, dw, s)));
   return hipSuccess;
 }
 

@@ -21,6 +21,7 @@ struct GatedPlan {
   bool grouped;  // ... from the grouped decode kernel, or the matrix-core ones
   int bp;       // token panels per tile
   bool small_dw;  // dW in tiles of 128 x 128
+  bool both;      // dX and dW in one launch
   int64_t whole;  // forward tiles that run over all of k; the others are cut
   int parts;      // parts of those, or cuts of n in the dX product
   size_t x, w[2], g[2], gu, split, split_bytes, dx, misc, total;

@@ -128,6 +128,13 @@ GatedPlan gated_plan(const hyb_gated_pair& w, int64_t m, int what, int64_t cus) 
         }
       }
     }
+    // dX's and dW's tiles side by side, one a compute unit (dW's alone: two).  Both
+    // gradients in us, a launch each and one: 512x512 333 tokens 28.7, 23.0;
+    // 2816x1024 333 tokens 46.4, 39.0, 1024 tokens 65.0, 68.5; 1024x4096 200 tokens
+    // 40.3, 38.7, 1024 tokens 65.5, 71.7; 4096x4096 200 tokens 80.7, 87.8.
+    const int64_t units = up(p.k, 256) / 256 * (up(p.m16, 16 * p.bp) / (16 * p.bp)) * p.parts;
+    const int64_t units_w = 2 * (up(p.n, 128) / 128) * (up(p.k, 128) / 128);
+    p.both = dw && p.small_dw && (units + units_w <= cus || (units_w <= 2 * cus && m <= 512));
     if (p.parts > 1) p.dx = take(int64_t(p.parts) * m * p.k * 4);
   }
   p.total = at;
