@@ -31,7 +31,8 @@ extern "C" {
  * device addresses aligned to the element.  A contiguous tensor of any shape is
  * one row.  `out` may be `data` itself (with ldo = lda); else the addresses from
  * its first to its last element hold no element of another data or out of the
- * list, nor of rows between them.  0 <= rows, cols and rows * cols <= 2^40. */
+ * list, nor of rows between them.  0 <= rows, cols and rows * cols <= 2^40;
+ * the rows reach over at most 2^44 elements. */
 typedef struct {
   const void* data;
   void* out;

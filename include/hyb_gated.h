@@ -26,9 +26,10 @@
  * rounded once.
  *
  * Conventions as in hyb.h and hyb_q4.h: host checks first, work enqueued on
- * `stream`, no allocation, capturable.  The caller's workspace (device, 16-byte
- * aligned, no initial contents) holds the bytes that hyb_gated_workspace_size
- * gives; calls that overlap on one workspace race.
+ * `stream`, no allocation, capturable; outputs overlap neither the inputs nor
+ * each other.  The caller's workspace (device, 16-byte aligned, no initial
+ * contents) holds the bytes that hyb_gated_workspace_size gives; calls that
+ * overlap on one workspace race.
  */
 #ifndef HYB_GATED_H_
 #define HYB_GATED_H_
