@@ -309,14 +309,15 @@ constexpr int kTopLift = 139;
 
 // The scale of group h of a word's four: its byte as the exponent of a float.
 // (The conversion reads only the exponent: bits of the bytes around it may lie
-// in the sign and the mantissa.)  For fp16 `lift` is kTopLift - top.
+// in the sign and the mantissa.)  For fp16 `lift` is kTopLift - top; the byte of a
+// group of zeros may lie far above top, and stays short of 255, a NaN.
 template <int DT>
 __device__ __forceinline__ float group_scale(uint32_t word, int h, int lift) {
   if constexpr (DT == HYB_BF16) {
     return __builtin_bit_cast(float, h < 3 ? word << (23 - 8 * h) : word >> 1);
   } else {
     const int b = (word >> (8 * h)) & 0xFFu;
-    const int e = b + lift < 0 ? 0 : b + lift;
+    const int e = b + lift < 0 ? 0 : b + lift > 254 ? 254 : b + lift;
     return __builtin_bit_cast(float, uint32_t(b == 255 ? 255 : e) << 23);
   }
 }
