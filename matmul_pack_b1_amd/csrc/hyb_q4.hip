@@ -303,9 +303,10 @@ struct Q4Args {
   int32_t whole, parts;
 };
 
-// fp16 operands carry a row's values divided by 2^(top - 139): at most 6 * 2^12,
-// normal numbers for scales down to 2^-25 of the row's largest.
-constexpr int kTopLift = 139;
+// fp16 operands carry a row's values divided by 2^(top - 140): at most 6 * 2^13 (below
+// fp16's 65504), and 2^-24, its smallest number, for half of a scale of 2^-36 of the
+// row's largest.
+constexpr int kTopLift = 140;
 
 // The scale of group h of a word's four: its byte as the exponent of a float.
 // (The conversion reads only the exponent: bits of the bytes around it may lie

@@ -1,5 +1,5 @@
 """fp16 products over 4-bit weights at the ends of what hyb_q4.h promises: rows of
-any scale beside groups of zeros."""
+any scale beside groups of zeros, and groups far below their row's largest."""
 import pytest
 import torch
 
@@ -58,3 +58,52 @@ def test_gated_rows_of_any_scale_beside_zeros(k, live, m):
         assert not bool(h.isnan().any())
         fits = (ref.abs() < 60000) & (g.abs() < 8)
         assert bool(((h - ref).abs() <= (2.0 ** -11 + 2.0 ** -17) * ref.abs() + 2.0 ** -25)[fits].all())
+
+
+# As above, with the columns of the two groups.
+FAR = [(64, 1), (64, 3), (64, 4), (64, 16), (320, 40), (5000, 30), (64, 70), (64, 64)]
+
+
+@pytest.mark.parametrize("k,m", FAR)
+@pytest.mark.parametrize("below", [26, 30, 35, 36])
+def test_groups_far_below_their_row(k, m, below):
+    """Scales of 2^-36 of the row's largest and above are exact: one activation a
+    token, in the small group."""
+    w = torch.zeros(70, k, dtype=torch.float64)
+    for r in range(70):
+        sign = 1 - 2 * (torch.arange(32) % 2)
+        w[r, :32] = 6.0 * 2.0 ** (r - 20)
+        w[r, 32:64] = GRID[(torch.arange(32) + r) % 7] * sign * 2.0 ** (r - 20 - below)
+        w[r, 32 + (r + 3) % 32] = 6.0 * 2.0 ** (r - 20 - below)
+    Q = q4.pack(w.float().cuda())
+    assert torch.equal(q4.unpack(Q, out_dtype=torch.float32).double().cpu(), w)
+    x = torch.zeros(m, k, dtype=torch.float64)
+    x[torch.arange(m), 32 + torch.arange(m) % 32] = 1.0 + torch.arange(m).double() / 1024
+    y = q4.gemm(Q, x.half().cuda()).double().cpu()
+    assert torch.equal(y, x @ w.t())
+
+
+@pytest.mark.parametrize("m", [333, 901])
+@pytest.mark.parametrize("below", [26, 35, 36])
+def test_groups_far_below_their_row_in_tiles(m, below):
+    """The same in the LDS-fed tiles (128 and 256 tokens; gated whole and cut)."""
+    n, k = 12003, 515
+    w = torch.zeros(n, k, dtype=torch.float64, device="cuda")
+    w[:, :32] = 6.0
+    w[:, 480:512] = GRID.cuda()[(torch.arange(n, device="cuda")[:, None] + torch.arange(32, device="cuda")) % 7] * 2.0 ** -below
+    w[torch.arange(n), 480 + torch.arange(n) % 32] = 6.0 * 2.0 ** -below
+    Q = q4.pack(w.float())
+    x = torch.zeros(m, k, dtype=torch.float64, device="cuda")
+    x[torch.arange(m), 480 + torch.arange(m) % 32] = 1.0 + torch.arange(m, device="cuda").double() / 1024
+    ref = x @ w.t()
+    assert torch.equal(q4.gemm(Q, x.half()).double(), ref)
+    # the gated tiles: silu(32) is 32 in fp32
+    w2 = torch.zeros_like(w)
+    w2[:, 512] = 2.0
+    x[:, 512] = 16.0
+    big = 2.0 ** 31
+    x[:, 480:512] *= 2.0 ** 10
+    up = w * big / 2.0 ** 10
+    h = gated.forward(q4.pack(w2.float()), q4.pack(up.float()), x.half()).double()
+    want = (32.0 * (x @ up.t())).half().double()
+    assert torch.equal(h, want)
