@@ -21,7 +21,7 @@
  * (rounded to 16 bits they would add as much to the gradients' errors as the
  * roundings below do); dG and dU are rounded once to the 16-bit type of its
  * products (bf16; or fp16, scaled by the power of two that brings the
- * largest finite one to [2^13, 2^14), so that they neither overflow nor, down
+ * largest finite one to [2^14, 2^15), so that they neither overflow nor, down
  * to 2^-28 of the largest, lose bits) and the gradients are summed in fp32 and
  * rounded once.
  *
