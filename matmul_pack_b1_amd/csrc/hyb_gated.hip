@@ -213,10 +213,11 @@ struct Gated4 {
 
 // The power of two that brings a magnitude of these bits to [2^14, 2^15) (1 for
 // zero), and its reciprocal: below fp16's 65504, and 2^-28 of it and above are normal
-// numbers (from 2^-14 on).
+// numbers (from 2^-14 on).  (A largest below 2^-112, whose factor would not be a
+// number, gives zeros in fp16 whatever it is multiplied by.)
 __device__ __forceinline__ float gated_lift(uint32_t top, float* back) {
   int e = top == 0 ? 0 : 14 + 127 - int(top >> 23);
-  e = e > 100 ? 100 : e < -100 ? -100 : e;
+  e = e > 126 ? 126 : e;  // (-113 at least, for a finite one)
   *back = __builtin_bit_cast(float, uint32_t(127 - e) << 23);
   return __builtin_bit_cast(float, uint32_t(127 + e) << 23);
 }

@@ -39,3 +39,25 @@ def test_smallest_fp16_gradients(below, top, m):
     assert not dwg.any() and not dwu[:, :77].any() and not dwu[:, 78:].any()
     # (dX is rounded to fp16, whose normal numbers end at 2^-14)
     assert torch.equal(dx[m - 1].cpu(), small.half())
+
+
+@pytest.mark.parametrize("m", [2, 300])
+@pytest.mark.parametrize("size", [2.0 ** -125, 2.0 ** -80, 2.0 ** 80, 2.0 ** 112])
+def test_largest_of_any_size(size, m):
+    """A largest dG anywhere in fp32: finite, so that it adds nothing where it meets
+    zeros, and right where an output holds it (infinite beyond fp16, 0 below it)."""
+    n = k = 128
+    P = hb.pack(torch.eye(n, dtype=torch.float16, device="cuda"), np.zeros((2, 2), dtype=np.uint8), 64, 64, "idx2")
+    g, u = torch.full((m, n), 32.0, device="cuda"), torch.zeros(m, n, device="cuda")
+    dh = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+    dh[0], u[0] = 2.0 ** 15, size / 2.0 ** 2     # dG = 2^13 size, dU = 2^20
+    dh[0, 1:] = 0.0
+    x = torch.zeros(m, k, dtype=torch.float16, device="cuda")
+    x[0, 3] = 2.0 ** -10
+    dx, dwg, dwu = gated.backward(P, P, x, g, u, dh, need_dw=True)
+    dg = 2.0 ** 13 * size
+    assert not dwg[1:].any() and not dwg[0, :3].any() and not dwg[0, 4:].any()
+    assert float(dwg[0, 3]) == float(torch.tensor(dg * 2.0 ** -10, dtype=torch.float64).half())
+    assert not dx[1:].any() and not dx[0, 1:].any() and float(dx[0, 0]) == float("inf")
+    if size < 1:
+        assert float(dwu[0, 3]) == 2.0 ** 10
