@@ -40,8 +40,9 @@ typedef struct {
   int32_t dtype;
 } hyb_tensor;
 
-/* Workspace bytes for `count` >= 0 tensors of these sizes (data and out are not
- * looked at) on the current device.  Host only. */
+/* Workspace bytes for `count` >= 0 tensors of these sizes, of hyb_norm or of
+ * hyb_clip.  Host only.  data and out are not looked at; an ldo that hyb_clip would
+ * refuse, as where a norm's tensors have no out, counts as lda. */
 hyb_status hyb_clip_workspace_size(int64_t count, const hyb_tensor* tensors, size_t* bytes);
 
 /* norm: device fp32, one element, 4-byte aligned.  `tensors` is host memory,

@@ -46,8 +46,14 @@ Range range_of(const void* p, const hyb_tensor& t, int64_t ld) {
 
 bool cross(const Range& a, const Range& b) { return a.from < b.to && b.from < a.to; }
 
+// May rows of `cols` elements lie `ld` apart, and their addresses within 64 bits?
+bool reach(int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && ld <= (int64_t(1) << 40) && ld <= (int64_t(1) << 44) / (rows - 1);
+}
+
 // Checks the list and keeps the tensors that have elements, rows joined where
-// they are contiguous.
+// they are contiguous.  Without `data` (sizes are asked for, of a norm or of a
+// scaling) an `ldo` that no call could take counts as lda.
 hyb_status read_list(int64_t count, const hyb_tensor* list, bool data, bool out, std::vector<hyb_tensor>* kept) {
   if (count < 0) return fail(HYB_ERR_SHAPE, "count = %lld is negative", (long long)count);
   if (count > 0 && !list) return fail(HYB_ERR_INVALID_ARG, "tensors is NULL");
@@ -60,6 +66,7 @@ hyb_status read_list(int64_t count, const hyb_tensor* list, bool data, bool out,
       return fail(HYB_ERR_SHAPE, "tensor %lld is %lld x %lld: need 0 <= rows, cols and at most 2^40 elements",
                   (long long)i, (long long)t.rows, (long long)t.cols);
     if (t.rows == 0 || t.cols == 0) continue;
+    if (!data && t.rows > 1 && !reach(t.rows, t.cols, t.ldo)) t.ldo = t.lda;
     const int64_t most = int64_t(1) << 40;
     for (const int64_t ld : {t.lda, out ? t.ldo : t.lda})
       if (t.rows > 1 && (ld < t.cols || ld > most))
