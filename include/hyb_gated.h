@@ -71,7 +71,12 @@ hyb_status hyb_gated_workspace_size(const hyb_gated_pair* w, int32_t m, int32_t 
  *         receive G and U for hyb_gated_backward; both or neither (NULL), and
  *         neither with 4-bit weights (HYB_ERR_UNSUPPORTED)
  * 0 <= m <= 2^22; 1 <= n, k <= 2^21 for packed weights, 0 <= n <= 2^27 - 16
- * and 0 <= k <= 2^22 for 4-bit ones (k = 0 gives zeros). */
+ * and 0 <= k <= 2^22 for 4-bit ones (k = 0 gives zeros).  A launch bounds their
+ * products, and what is beyond is HYB_ERR_UNSUPPORTED: for packed weights
+ * ceil(n/128) ceil(m/64), ceil(k/128) ceil(m/64) and ceil(n/128) ceil(k/128) stay
+ * below 2^22 (2.4 million tokens of 14336 outputs), for 4-bit ones ceil(n/128)
+ * ceil(m/16) below 2^23 suffices.  Row strides of h, g, u, dh, dx, dw_gate and dw_up
+ * are at most 2^31. */
 hyb_status hyb_gated(const hyb_gated_pair* w, int32_t act, const void* x, int32_t x_dtype, int32_t m, int64_t ldx,
                      void* h, int64_t ldh, float* g, int64_t ldg, float* u, int64_t ldu, void* workspace,
                      size_t workspace_bytes, void* stream);

@@ -107,11 +107,11 @@ hyb_status check_ws(const void* ws, size_t bytes, size_t need) {
   return HYB_OK;
 }
 
-// Tiles of any launch stay below 2^32 threads in one grid dimension, and the
-// decode and elementwise kernels' rows too.
+// Tiles of any launch (G and U, dX, dW) stay below 2^32 threads in one grid
+// dimension, and the elementwise kernels' rows too.
 hyb_status check_launch(int64_t n, int64_t k, int64_t m) {
-  const int64_t side = n > k ? n : k;
-  if ((side + 127) / 128 * ((m + 63) / 64) >= (int64_t(1) << 22) || (side + 127) / 128 * ((k + 127) / 128) >= (int64_t(1) << 22))
+  const int64_t tn = (n + 127) / 128, tk = (k + 127) / 128, tm = (m + 63) / 64, most = int64_t(1) << 22;
+  if (tn * tm >= most || tk * tm >= most || tn * tk >= most)
     return fail(HYB_ERR_UNSUPPORTED, "n x k x m = %lld x %lld x %lld is too large for one launch", (long long)n,
                 (long long)k, (long long)m);
   return HYB_OK;
