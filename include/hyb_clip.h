@@ -6,11 +6,12 @@
  *   out   = a * min(1, max_norm / (norm + 1e-6))
  *
  * Squares are taken and summed in 64 bits, in an order that depends on the
- * tensors' sizes and the device alone; the norm is rounded once to fp32 (an
+ * tensors' sizes and strides alone; the norm is rounded once to fp32 (an
  * infinity where it lies beyond fp32), the factor is computed in 64 bits and
  * rounded to fp32, each product rounded to fp32 and then to the tensor's type.
  * A NaN anywhere makes the norm, and every element scaled, NaN; an infinity
- * makes the norm infinite and the factor 0 (and the infinities NaN).
+ * makes the norm infinite and the factor 0 (and the infinities NaN), or NaN where
+ * max_norm is infinite too.
  *
  * Conventions as in hyb.h: host checks first, work enqueued on `stream`, no
  * allocation, capturable.  The caller's workspace (device, 16-byte aligned, no
