@@ -203,8 +203,10 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ a,
 }
 
 // One wavefront per panel and step: codes through LDS into rows, 8 columns per
-// lane.  Bound by memory: 28672x8192, 595 MB, 94 us (6.3 TB/s; with stores that the
-// caches keep 111, and the quantising of the next weight 128 instead of 111).
+// lane.  Bound by memory: 28672x8192 to bf16, 595 MB, 94 us (6.3 TB/s; with stores that
+// the caches keep 111, and the quantising of the next weight 128 instead of 111).  To
+// fp32, whose 32 bytes a lane leave in two stores, the caches put the halves together:
+// 277 us (3.8 TB/s; around them 491).
 template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ codes,
                                                        const char* __restrict__ scales, int64_t n, int32_t k,
@@ -246,13 +248,8 @@ __global__ __launch_bounds__(256) void k_q4_dequantize(const char* __restrict__ 
         Bytes16 u[2];
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e >> 2].w[e & 3] = __builtin_bit_cast(uint32_t, v[e]);
-        if constexpr (STREAM) {
-          stream_store(p, u[0]);
-          stream_store(p + 4, u[1]);
-        } else {
-          reinterpret_cast<Bytes16*>(p)[0] = u[0];
-          reinterpret_cast<Bytes16*>(p)[1] = u[1];
-        }
+        reinterpret_cast<Bytes16*>(p)[0] = u[0];
+        reinterpret_cast<Bytes16*>(p)[1] = u[1];
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -1092,9 +1089,9 @@ hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
   };
-  const bool stream = n * k * (dtype == HYB_F32 ? 4 : 2) > kStreamBytes;
+  const bool stream = n * k * 2 > kStreamBytes;
   if (dtype == HYB_F32)
-    stream ? go(&k_q4_dequantize<HYB_F32, true>) : go(&k_q4_dequantize<HYB_F32, false>);
+    go(&k_q4_dequantize<HYB_F32, false>);
   else if (dtype == HYB_BF16)
     stream ? go(&k_q4_dequantize<HYB_BF16, true>) : go(&k_q4_dequantize<HYB_BF16, false>);
   else
