@@ -1089,7 +1089,10 @@ hipError_t launch_q4_dequantize(const hyb_q4& src, int64_t n, int64_t k, void* a
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, codes, scales, n, int32_t(k), lda, steps, rows16, a);
   };
-  const bool stream = n * k * 2 > kStreamBytes;
+  // 16-bit rows that begin within 64 bytes leave parts of lines at both ends, which the
+  // caches join: 28672x8192, row stride 8193 164 us (around them 196), 8200 168 (178);
+  // 8224 182 (143), 8192 144 (95)
+  const bool stream = n * k * 2 > kStreamBytes && (reinterpret_cast<uintptr_t>(a) | uintptr_t(lda * 2)) % 64 == 0;
   if (dtype == HYB_F32)
     go(&k_q4_dequantize<HYB_F32, false>);
   else if (dtype == HYB_BF16)

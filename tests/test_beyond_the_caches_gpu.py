@@ -65,18 +65,21 @@ def test_clip(few):
     assert all(torch.equal(o, a) for o, a in zip(outs, again))
 
 
+# columns, row stride and first element: rows that begin anywhere, or at 64 bytes
+@pytest.mark.parametrize("k,pitch,offset", [(8195, 8197, 1), (8195, 8224, 32), (8192, 8192, 0)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
-def test_q4_read_back(dtype):
+def test_q4_read_back(dtype, k, pitch, offset):
     """The same values as from slices of the rows, which are read back through the
-    caches, at every alignment of a row."""
-    k = 8195
+    caches."""
     n = (256 << 20) // (k * dtype.itemsize) + 3
     w = torch.randn(n, k, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
-    out = torch.full((n + 1, k + 2), 7.0, dtype=dtype, device="cuda")
-    q4.unpack(q4.pack(w), out=out[:n, 1:k + 1])
+    base = torch.full((n * pitch + offset + 99,), 7.0, dtype=dtype, device="cuda")
+    assert base.data_ptr() % 64 == 0
+    out = torch.as_strided(base, (n, k), (pitch, 1), offset)
+    q4.unpack(q4.pack(w), out=out)
     for r in range(0, n, 5000):
         part = q4.unpack(q4.pack(w[r:r + 5000]), out_dtype=dtype)
         assert part.numel() * part.element_size() <= 256 << 20
-        assert torch.equal(out[r:min(r + 5000, n), 1:k + 1], part)
-    out[:n, 1:k + 1] = 7.0
-    assert bool((out == 7.0).all())
+        assert torch.equal(out[r:r + 5000], part)
+    out.fill_(7.0)
+    assert bool((base == 7.0).all())
