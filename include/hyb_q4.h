@@ -71,7 +71,9 @@ hyb_status hyb_q4_quantize(const void* a, int32_t dtype, int64_t n, int64_t k, i
 hyb_status hyb_q4_dequantize(const hyb_q4* src, int64_t n, int64_t k, void* a, int32_t dtype, int64_t lda,
                              void* stream);
 
-/* Y = X W^T for any number 0 <= m <= 2^22 of tokens, one included.
+/* Y = X W^T for any number 0 <= m <= 2^22 of tokens, one included.  (A launch bounds n
+ * m: ceil(n/128) ceil(m/16) below 2^23 is always taken, what is beyond may be
+ * HYB_ERR_UNSUPPORTED.)  Row strides, here and above, are at most 2^31.
  *   x   device m x k of x_dtype (HYB_BF16 or HYB_F16), row stride ldx >= k,
  *       element-aligned (16-byte aligned rows are read fastest)
  *   y   device m x n of y_dtype (HYB_F32, HYB_BF16 or HYB_F16; 16-bit outputs

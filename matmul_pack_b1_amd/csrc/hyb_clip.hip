@@ -1,7 +1,8 @@
 // Kernels of the 2-norm over a list of tensors and their scaling
-// (include/hyb_clip.h).  Bound by memory: 872 MB of gradients are read in 129 us
-// (6.7 TB/s) and scaled in 317 (5.5), 450 in all (491 with loads and stores that the
-// caches keep); nine small ones take the depth of two launches, 4.7 and 6.2 us.
+// (include/hyb_clip.h).  Bound by memory: 872 MB of gradients are read in 129-145 us
+// (6.0-6.7 TB/s) and scaled in 317-332 (5.3-5.5), 450 in all in a loop (491 with loads and
+// stores that the caches keep); nine small ones take the depth of two launches, 4.6 and 6.1
+// us.
 //
 // Squares are fp64: the converting and the fused multiply-add of an element take
 // less of the vector unit than its bytes take of memory, and no sum overflows or
@@ -16,8 +17,10 @@ namespace hyb {
 namespace {
 
 // The tensors of one launch, at most N; tensor i has chunks start[i] ..
-// start[i + 1] - 1, rows' chunks one after the other.  (A short list has a small
-// table: the host copies it for every launch.)
+// start[i + 1] - 1, rows' chunks one after the other.  A list of up to twelve has a
+// small table, since the host copies it for every launch: nine tensors 15.3-17.0 us a call,
+// with the large one 16.3-17.4 (in each of four processes; 20 tensors with a table of 32 or
+// of 64 differ by less than the processes do).
 template <int N>
 struct ClipTable {
   const char* data[N];

@@ -23,8 +23,8 @@ struct ClipLaunch {
   int count;
   int64_t chunks, groups, sum0;
 };
-// The launches over the tensors that have elements (`index` their numbers in
-// the list); *sums is the number of partial sums.
+// The launches over the tensors, which all have elements; *sums is the number of
+// partial sums.
 std::vector<ClipLaunch> clip_plan(const std::vector<hyb_tensor>& tensors, int64_t* sums);
 
 hipError_t launch_norm(const std::vector<hyb_tensor>& tensors, float* norm, double* ws, hipStream_t s);

@@ -1,5 +1,6 @@
-// Sparse tiles of a packed matrix as dense ones, in panels (hyb_panel.h), shared by
-// the cross entropy and the gated projection.
+// Sparse tiles of a packed matrix as dense ones, in panels (hyb_panel.h): the order of
+// the stores, which the cross entropy's expanding of a piece of the vocabulary has too, and
+// the gated projection's expanding.
 #ifndef HYB_EXPAND_H_
 #define HYB_EXPAND_H_
 

@@ -69,8 +69,9 @@ __global__ __launch_bounds__(256) void k_gated_act(GatedOut o) {
 }
 
 // AP / 2 panels of each weight x BP panels of tokens.  Bound by the matrix units:
-// 17408x5120, 2048 tokens 708 us, 1.03 Pflop/s, of which ten a round of tiles are their
-// start, activation and outputs; 14336x4096, 4096 tokens with 470 MB of G and U 870-910.
+// 17408x5120, 2048 tokens 672-696 us in a kernel trace, 1.05-1.09 Pflop/s, of which ten a
+// round of tiles are their start, activation and outputs (the whole call takes 652-672 in a
+// loop, whose clock is higher); 14336x4096, 4096 tokens with 470 MB of G and U 870-910.
 // (A priority above its neighbours' around the matrix instructions: no gain;
 // addresses prepared a step earlier 680 against 675 us.)
 template <int DT, int AP, int BP, int WA, int WB, int STAGES>
@@ -223,7 +224,8 @@ __device__ __forceinline__ float gated_lift(uint32_t top, float* back) {
 }
 
 // Largest finite |dG|, |dU| (fp16) of each workgroup's outputs: one pass over G, U
-// and dH more, 5.5 us at 2816x1024 and 333 tokens.  (Maxima: their order does not
+// and dH more, 5.7 us at 2816x1024 and 333 tokens, 122 at 14336x4096 and 4096 (587 MB, 4.8
+// TB/s; forward and backward 2702 us, in bf16 2510).  (Maxima: their order does not
 // matter.)
 constexpr int kTopGroups = 512;
 template <int DT>

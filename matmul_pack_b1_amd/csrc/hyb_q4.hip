@@ -555,9 +555,10 @@ __device__ __forceinline__ f32x4_t q4_finish(const Q4Args& a, int64_t j0, f32x4_
 // BP tokens' activations, 512 columns at a time, come through LDS for all eight
 // (from registers, in which a row at any alignment and the end of k cost nothing
 // more).  The k of a workgroup's panels may be cut into parts, a workgroup each.
-// Bound by memory with one block of tokens: 8192x28672, 13 tokens, eight parts 23.6 us
-// for 125 MB (5.3 TB/s), and 4.1 for the sums; gated 17408x5120, 16 tokens 21.0 and
-// 4.0 (every wavefront with its own activations, as in k_q4_rows, 413 and 194).
+// Bound by memory with one block of tokens: 8192x28672, 13 tokens, eight parts 23.6-24.8
+// us for 125 MB (5.0-5.3 TB/s), and 4.1 for the sums; gated 17408x5120, 16 tokens 21.0-22.4
+// and 4.0.  With 64 tokens by the LDS, where each panel reads them all: 58 and 5, gated 43
+// and 5 (every wavefront with its own activations, as in k_q4_rows, 413 and 194).
 template <int DT, bool GATED, int BP>
 __global__ __launch_bounds__(512) void k_q4_shared(Q4Args a) {
   constexpr int P = GATED ? 2 : 1;
@@ -722,8 +723,9 @@ __global__ __launch_bounds__(256) void k_q4_shared_sum(Q4Args a) {
 // worth of eight are widened, scale included, for every BP / WB x 2 matrix
 // instructions they feed.  A step is 64 columns of x; codes come 128 columns at
 // a time (half the panels in each of two steps), scales 512.  Bound by the matrix
-// units and LDS: 17408x5120, 2048 tokens 285 us, 1.28 Pflop/s (a dense bf16 product
-// of 8192 cubed reaches 1.51).
+// units and LDS: 17408x5120, 2048 tokens 273-292 us in a kernel trace, 1.25-1.34 Pflop/s
+// (the whole call takes 262-284 in a loop; a dense bf16 product of 8192 cubed reaches
+// 1.51), gated 556 (522 the call), fp16 697 (612).
 template <int DT, bool GATED, int AP, int BP, int WA, int WB>
 struct Q4Tile {
   static constexpr int kWaves = WA * WB;
